@@ -213,7 +213,8 @@ def _quantised(x):
     part, e = torch.frexp(x.abs().amax(-1))
     e = (e - 8 - (part <= 0.875).int()).clamp(-124, 120).int()
     scale = torch.where(part == 0, 1.0, ((e + 127) << 23).view(torch.float32))  # 2^e, exactly
-    return (x / scale[..., None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn), scale
+    top = torch.where(e == 120, 240.0, 448.0)[..., None]  # larger codes times 2^120 are no bf16 values
+    return (x / scale[..., None]).clamp(-top, top).to(torch.float8_e4m3fn), scale
 
 
 def _places(s, rows, have, first, bs):
@@ -301,9 +302,9 @@ def _power(e):
 
 
 def _e4m3(x):
-    """x in 64 bits rounded to the nearest e4m3 value, ties to the even one; 448 at most."""
+    """x in 64 bits rounded to the nearest e4m3 value, ties to the even one (all are below 448 here)."""
     unit = _power(torch.frexp(x.abs().clamp_min(2.0 ** -6))[1] - 4)
-    return (torch.round(x / unit) * unit).clamp(-448.0, 448.0)
+    return torch.round(x / unit) * unit
 
 
 def _exact_write(s):
