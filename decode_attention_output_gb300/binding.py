@@ -24,7 +24,8 @@ _DTYPES = {torch.bfloat16: DA_DTYPE_BF16, torch.float32: DA_DTYPE_F32, torch.int
 
 # every symbol declared in include/decode_attn.h
 EXPORTS = ("decode_attn_fwd", "decode_attn_only", "decode_attn_only_noalloc", "decode_attn_fwd_paged",
-           "decode_attn_only_paged", "decode_attn_fwd_fp8", "decode_attn_only_fp8", "decode_attn_scores", "decode_attn_oproj", "decode_attn_set_option", "decode_attn_get_option", "decode_attn_last_device_error", "decode_attn_device_error",
+           "decode_attn_only_paged", "decode_attn_fwd_fp8", "decode_attn_only_fp8", "decode_attn_fwd_paged_fp8", "decode_attn_only_paged_fp8",
+           "decode_attn_prefill", "decode_attn_cache_write", "decode_attn_cache_read", "decode_attn_scores", "decode_attn_oproj", "decode_attn_set_option", "decode_attn_get_option", "decode_attn_last_device_error", "decode_attn_device_error",
            "decode_attn_release", "decode_attn_status_str")
 
 
@@ -58,6 +59,11 @@ def load_library(path: str) -> ctypes.CDLL:
     lib.decode_attn_only_paged.argtypes = [P, P, P, P, P, P, f32, vp]
     lib.decode_attn_fwd_fp8.argtypes = [P, P, P, P, P, P, f32, f32, f32, vp]
     lib.decode_attn_only_fp8.argtypes = [P, P, P, P, P, f32, f32, f32, vp]
+    lib.decode_attn_fwd_paged_fp8.argtypes = [P, P, P, P, P, P, P, P, f32, vp]
+    lib.decode_attn_only_paged_fp8.argtypes = [P, P, P, P, P, P, P, f32, vp]
+    lib.decode_attn_prefill.argtypes = [P, P, P, P, P, P, f32, vp]
+    lib.decode_attn_cache_write.argtypes = [P, P, P, P, P, P, P, P, vp]
+    lib.decode_attn_cache_read.argtypes = [P, P, P, P, P, P, P, vp]
     lib.decode_attn_scores.argtypes = [P, P, P, P, vp]
     lib.decode_attn_oproj.argtypes = [P, P, P, vp]
     lib.decode_attn_set_option.argtypes = [ctypes.c_char_p, i64]
@@ -217,6 +223,54 @@ def decode_attn_only_fp8(q, k_cache, v_cache, seq_lens, attn_out, scale: float, 
     _check("decode_attn_only_fp8", lib.decode_attn_only_fp8(*ds, float(scale), float(k_scale),
                                                             float(v_scale), _stream(stream)))
     return attn_out
+
+
+def decode_attn_fwd_paged_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, o_weight, out, scale: float,
+                              stream=None) -> torch.Tensor:
+    """decode_attn_fwd_paged over a paged fp8 cache: k_pages / v_pages [num_blocks, Hkv, block_size, 128]
+    torch.float8_e4m3fn, kv_scales [num_blocks, Hkv, 2, block_size] fp32, the keys and values being code * scale
+    of their token and head (see decode_attn_cache_write); returns ``out``."""
+    lib = _lib or load()  # the lock only until the library is loaded
+    ds = [_ref(x) for x in (q, k_pages, v_pages, kv_scales, block_table, seq_lens, o_weight, out)]
+    _check("decode_attn_fwd_paged_fp8", lib.decode_attn_fwd_paged_fp8(*ds, float(scale), _stream(stream)))
+    return out
+
+
+def decode_attn_only_paged_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, attn_out, scale: float,
+                               stream=None) -> torch.Tensor:
+    """decode_attn_only_paged over a paged fp8 cache (see decode_attn_fwd_paged_fp8); returns ``attn_out``."""
+    lib = _lib or load()  # the lock only until the library is loaded
+    ds = [_ref(x) for x in (q, k_pages, v_pages, kv_scales, block_table, seq_lens, attn_out)]
+    _check("decode_attn_only_paged_fp8", lib.decode_attn_only_paged_fp8(*ds, float(scale), _stream(stream)))
+    return attn_out
+
+
+def decode_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, out, scale: float, stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts: q and out [Tq, Hq, 128], k and v [Tk, Hkv, 128], offsets [B + 1]
+    int32 of the sequences in each; the queries of a sequence are its last tokens. Returns ``out``."""
+    lib = _lib or load()  # the lock only until the library is loaded
+    ds = [_ref(x) for x in (q, k, v, cu_seqlens_q, cu_seqlens_k, out)]
+    _check("decode_attn_prefill", lib.decode_attn_prefill(*ds, float(scale), _stream(stream)))
+    return out
+
+
+def decode_attn_cache_write(k, v, cu_seqlens, block_table, seq_lens, k_pages, v_pages, kv_scales=None,
+                            stream=None) -> None:
+    """The new tokens' k and v [T, Hkv, D] (packed: rows cu_seqlens[b] .. cu_seqlens[b + 1] are the last tokens of
+    the seq_lens[b] of sequence b) into the pages that block_table names: bf16 pools take copies, e4m3 pools codes
+    with a power-of-two scale per token and head in kv_scales [num_blocks, Hkv, 2, block_size] fp32."""
+    lib = _lib or load()  # the lock only until the library is loaded
+    ds = [_ref(x) for x in (k, v, cu_seqlens, block_table, seq_lens, k_pages, v_pages, kv_scales)]
+    _check("decode_attn_cache_write", lib.decode_attn_cache_write(*ds, _stream(stream)))
+
+
+def decode_attn_cache_read(k_pages, v_pages, kv_scales, block_table, cu_seqlens, k_out, v_out, stream=None):
+    """The first tokens of each sequence out of a paged cache (kv_scales None: bf16 pools) into the packed
+    k_out and v_out [T, Hkv, D] bf16; returns ``(k_out, v_out)``."""
+    lib = _lib or load()  # the lock only until the library is loaded
+    ds = [_ref(x) for x in (k_pages, v_pages, kv_scales, block_table, cu_seqlens, k_out, v_out)]
+    _check("decode_attn_cache_read", lib.decode_attn_cache_read(*ds, _stream(stream)))
+    return k_out, v_out
 
 
 def decode_attn_scores(q, k_cache, seq_lens, scores, stream=None) -> torch.Tensor:

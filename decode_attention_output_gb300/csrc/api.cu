@@ -182,6 +182,54 @@ int encode_table_map(CUtensorMap* map, const void* base, int64_t entries) {
   return r == CUDA_SUCCESS ? DA_OK : DA_ERR_UNSUPPORTED;
 }
 
+// Map over the scales of a paged fp8 cache, [num_blocks][Hkv][2][block_size] fp32; box =
+// box_tokens scales of K and of V.
+int encode_scales_map(CUtensorMap* map, const da_tensor_t* t, int box_tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return DA_ERR_CUDA;
+  const int64_t NB = t->shape[0], H = t->shape[1], BS = t->shape[3];
+  const int64_t st = t->stride[2];
+  const int64_t sh = H == 1 ? 2 * st : t->stride[1];
+  const int64_t sb = NB == 1 ? sh * H : t->stride[0];
+  cuuint64_t dims[4] = {(cuuint64_t)BS, 2, (cuuint64_t)H, (cuuint64_t)NB};
+  cuuint64_t strides[3] = {(cuuint64_t)(st * 4), (cuuint64_t)(sh * 4), (cuuint64_t)(sb * 4)};
+  cuuint32_t box[4] = {(cuuint32_t)box_tokens, 2, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, t->data, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DA_OK : DA_ERR_UNSUPPORTED;
+}
+
+// 4-D map over packed tokens [T][H][128] bf16, the dims in two halves of 64 (128-byte rows,
+// 128-byte swizzle). K and V: one box = 128 tokens of a head, both halves ({dim, token, half,
+// head}). Queries (heads_box > 0): one half of box_tokens tokens x heads_box heads, a token's
+// heads in consecutive rows ({dim, head, token, half}).
+int encode_packed_map(CUtensorMap* map, const da_tensor_t* t, int box_tokens, int heads_box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return DA_ERR_CUDA;
+  const cuuint64_t T = (cuuint64_t)t->shape[0], H = (cuuint64_t)t->shape[1];
+  // a stride of an extent-1 dimension is never used; give it a harmless legal value
+  const cuuint64_t sh = (cuuint64_t)(H == 1 ? 128 : t->stride[1]) * 2, st = T == 1 ? sh * H : (cuuint64_t)t->stride[0] * 2;
+  cuuint64_t dims[4] = {64, T, 2, H}, strides[3] = {st, 128, sh};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, 2, 1}, estr[4] = {1, 1, 1, 1};
+  if (heads_box > 0) {
+    dims[1] = H;
+    dims[2] = T;
+    dims[3] = 2;
+    strides[0] = sh;
+    strides[1] = st;
+    strides[2] = 128;
+    box[1] = (cuuint32_t)heads_box;
+    box[2] = (cuuint32_t)box_tokens;
+    box[3] = 1;
+  }
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DA_OK : DA_ERR_UNSUPPORTED;
+}
+
 // 2-D map over a row-major bf16 matrix [rows][cols] with row stride `ld` elements;
 // box = 64 columns x box_rows rows, 128-byte swizzle.
 int encode_2d_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
@@ -282,13 +330,26 @@ struct PagedShape {
   const int* table;
   long long table_stride, table_entries;  // row stride; flat extent (B-1)*stride + max_blocks
   int block_size, num_blocks;
+  const da_tensor_t* scales;  // e4m3 pools: [num_blocks][Hkv][2][block_size] fp32, else null
 };
 
+// kv_scales of an e4m3 pool kp: a scale per token and KV head for K and for V.
+int check_scales(const da_tensor_t* scales, const da_tensor_t* kp) {
+  DA_TRY(check_tensor(scales, DA_DTYPE_F32, 4, kInput16));
+  if (scales->shape[0] != kp->shape[0] || scales->shape[1] != kp->shape[1] || scales->shape[2] != 2 ||
+      scales->shape[3] != kp->shape[2])
+    return DA_ERR_SHAPE;
+  return DA_OK;
+}
+
 int check_paged_inputs(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp,
-                       const da_tensor_t* table, const da_tensor_t* lens, AttnShape* s, PagedShape* ps) {
+                       const da_tensor_t* table, const da_tensor_t* lens, AttnShape* s, PagedShape* ps,
+                       const da_tensor_t* scales = nullptr, int kv_dtype = DA_DTYPE_BF16) {
+  const bool kv8 = kv_dtype == DA_DTYPE_E4M3;
   DA_TRY(check_tensor(q, DA_DTYPE_BF16, 3, kInput16));
-  DA_TRY(check_tensor(kp, DA_DTYPE_BF16, 4, kInput16));
-  DA_TRY(check_tensor(vp, DA_DTYPE_BF16, 4, kInput16));
+  DA_TRY(check_tensor(kp, kv_dtype, 4, kInput16));
+  DA_TRY(check_tensor(vp, kv_dtype, 4, kInput16));
+  if (kv8) DA_TRY(check_scales(scales, kp));
   if (!table || !lens) return DA_ERR_NULL;
   if (table->dtype != DA_DTYPE_I32 || lens->dtype != DA_DTYPE_I32) return DA_ERR_DTYPE;
   if (table->ndim != 2 || lens->ndim != 1) return DA_ERR_SHAPE;
@@ -301,7 +362,8 @@ int check_paged_inputs(const da_tensor_t* q, const da_tensor_t* kp, const da_ten
   if (table->shape[0] != B || lens->shape[0] != B) return DA_ERR_SHAPE;
   if (Hq <= 0 || Hkv <= 0 || NB <= 0 || BS <= 0 || MB <= 0) return DA_ERR_SHAPE;
   if (Hq % Hkv) return DA_ERR_SHAPE;
-  if (!paged_block_ok((int)std::min<int64_t>(BS, 1 << 30), (int)D)) return DA_ERR_UNSUPPORTED;
+  if (kv8 && D != kHeadDim) return DA_ERR_UNSUPPORTED;  // fp8 caches: D = 128
+  if (!paged_block_ok((int)std::min<int64_t>(BS, 1 << 30), (int)D, kv8)) return DA_ERR_UNSUPPORTED;
   if (Hq / Hkv > kMaxGroup) return DA_ERR_UNSUPPORTED;
   if (B > DA_MAX_BATCH) return DA_ERR_UNSUPPORTED;
   if (B * Hkv > (int64_t)kMaxCounters) return DA_ERR_UNSUPPORTED;
@@ -330,6 +392,81 @@ int check_paged_inputs(const da_tensor_t* q, const da_tensor_t* kp, const da_ten
   ps->table_entries = B > 0 ? (B - 1) * ps->table_stride + MB : 0;
   ps->block_size = (int)BS;
   ps->num_blocks = (int)NB;
+  ps->scales = scales;
+  return DA_OK;
+}
+
+// The pools, block table and packed tokens of decode_attn_cache_write / _read. `lens` null: reading.
+int check_cache(const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cu, const da_tensor_t* table,
+                const da_tensor_t* lens, bool write, const da_tensor_t* kp, const da_tensor_t* vp,
+                const da_tensor_t* scales, CacheParams* p) {
+  DA_TRY(check_tensor(k, DA_DTYPE_BF16, 3, kInput16));
+  DA_TRY(check_tensor(v, DA_DTYPE_BF16, 3, kInput16));
+  if (!kp || !vp || !cu || !table || (write && !lens)) return DA_ERR_NULL;
+  const int kv_dtype = kp->dtype;
+  if (kv_dtype != DA_DTYPE_BF16 && kv_dtype != DA_DTYPE_E4M3) return DA_ERR_DTYPE;
+  const bool kv8 = kv_dtype == DA_DTYPE_E4M3;
+  DA_TRY(check_tensor(kp, kv_dtype, 4, kInput16));
+  DA_TRY(check_tensor(vp, kv_dtype, 4, kInput16));
+  if (kv8) DA_TRY(check_scales(scales, kp));
+  else if (scales) return DA_ERR_DTYPE;  // a bf16 pool has no scales
+  if (cu->dtype != DA_DTYPE_I32 || table->dtype != DA_DTYPE_I32 || (write && lens->dtype != DA_DTYPE_I32))
+    return DA_ERR_DTYPE;
+  if (cu->ndim != 1 || table->ndim != 2 || (write && lens->ndim != 1)) return DA_ERR_SHAPE;
+  const int64_t T = k->shape[0], H = k->shape[1], D = k->shape[2];
+  const int64_t NB = kp->shape[0], BS = kp->shape[2], B = table->shape[0], MB = table->shape[1];
+  if (D != kHeadDim && D != kHeadDimWide) return DA_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if (v->shape[i] != k->shape[i]) return DA_ERR_SHAPE;
+  for (int i = 0; i < 4; ++i)
+    if (vp->shape[i] != kp->shape[i]) return DA_ERR_SHAPE;
+  if (kp->shape[1] != H || kp->shape[3] != D) return DA_ERR_SHAPE;
+  if (cu->shape[0] != B + 1 || (write && lens->shape[0] != B)) return DA_ERR_SHAPE;
+  if (H <= 0 || NB <= 0 || BS <= 0 || MB <= 0) return DA_ERR_SHAPE;
+  if (kv8 && D != kHeadDim) return DA_ERR_UNSUPPORTED;
+  if (!paged_block_ok((int)std::min<int64_t>(BS, 1 << 30), (int)D, kv8)) return DA_ERR_UNSUPPORTED;
+  if (B > DA_MAX_BATCH || H > kMaxCounters || T >= ((int64_t)1 << 31) || NB >= ((int64_t)1 << 31) || MB > ((int64_t)1 << 30) ||
+      MB * BS > ((int64_t)1 << 30))
+    return DA_ERR_UNSUPPORTED;
+  if (B > 0) {
+    if (!cu->data || !table->data || (write && !lens->data)) return DA_ERR_NULL;
+    if (cu->stride[0] != 1 || (write && B > 1 && lens->stride[0] != 1)) return DA_ERR_STRIDE;
+    if (MB > 1 && table->stride[1] != 1) return DA_ERR_STRIDE;
+    if (B > 1 && table->stride[0] < MB) return DA_ERR_STRIDE;
+    for (const da_tensor_t* t : {cu, table, lens})
+      if (t && reinterpret_cast<uintptr_t>(t->data) % 4) return DA_ERR_ALIGN;
+  }
+  memset(p, 0, sizeof(*p));
+  p->k = static_cast<const __nv_bfloat16*>(k->data);
+  p->v = static_cast<const __nv_bfloat16*>(v->data);
+  p->k_st = k->stride[0];
+  p->k_sh = k->stride[1];
+  p->v_st = v->stride[0];
+  p->v_sh = v->stride[1];
+  p->cu = static_cast<const int*>(cu->data);
+  p->table = static_cast<const int*>(table->data);
+  p->bt_stride = B > 1 ? table->stride[0] : MB;
+  p->seq_lens = write ? static_cast<const int*>(lens->data) : nullptr;
+  p->k_pages = kp->data;
+  p->v_pages = vp->data;
+  p->kp_sb = kp->stride[0];
+  p->kp_sh = kp->stride[1];
+  p->kp_sr = kp->stride[2];
+  p->vp_sb = vp->stride[0];
+  p->vp_sh = vp->stride[1];
+  p->vp_sr = vp->stride[2];
+  if (kv8) {
+    p->scales = static_cast<float*>(scales->data);
+    p->sc_sb = scales->stride[0];
+    p->sc_sh = scales->stride[1];
+    p->sc_st = scales->stride[2];
+  }
+  p->B = (int)B;
+  p->Hkv = (int)H;
+  p->T = (int)T;
+  p->max_blocks = (int)MB;
+  p->num_blocks = (int)NB;
+  while ((1 << p->block_shift) < BS) ++p->block_shift;
   return DA_OK;
 }
 
@@ -692,7 +829,9 @@ int run_attention(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t*
     p.units = fused->plan->units;
   }
 
-  const int box_tokens = paged ? std::min(paged->block_size, tile_tokens(s.D)) : (kv8 ? kTileFp8 : 0);
+  const bool paged8 = paged && paged->scales;
+  const int tile_tok = kv8 || paged8 ? kTileFp8 : tile_tokens(s.D);
+  const int box_tokens = paged ? std::min(paged->block_size, tile_tok) : (kv8 ? kTileFp8 : 0);
   DA_TRY(encode_kv_map(&p.tm_k, k, box_tokens));
   if (v) DA_TRY(encode_kv_map(&p.tm_v, v, box_tokens));
   else p.tm_v = p.tm_k;
@@ -705,6 +844,7 @@ int run_attention(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t*
     p.block_shift = 0;
     while ((1 << p.block_shift) < paged->block_size) ++p.block_shift;
     DA_TRY(encode_table_map(&p.tm_table, paged->table, paged->table_entries));
+    if (paged8) DA_TRY(encode_scales_map(&p.tm_scales, paged->scales, box_tokens));
   }
   p.q = static_cast<const __nv_bfloat16*>(q->data);
   p.q_sb = q->stride[0];
@@ -742,7 +882,8 @@ int run_attention(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t*
     const int flat = std::min(grid, p.attn_workers);
     set_split_divisor(p, 0, flat);
     set_split_divisor(p, 1, p.cluster > 1 ? (int)std::min<long long>(flat, (long long)s.B * s.Hkv * p.cluster) : flat);
-    return kv8     ? launch_attention_fp8(p, grid, pl.nb, stream)
+    return paged8  ? launch_attention_paged_fp8(p, grid, pl.nb, stream)
+           : kv8   ? launch_attention_fp8(p, grid, pl.nb, stream)
            : paged ? launch_attention_paged(p, grid, pl.nb, s.D, stream)
                    : launch_attention(p, grid, pl.nb, s.D, scores != nullptr, stream, fused ? fused->plan->npad : 0);
   };
@@ -770,7 +911,8 @@ int only_checked(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* 
   if (!std::isfinite(scale)) return DA_ERR_UNSUPPORTED;
   if (s.B == 0) return DA_OK;
   const Options o = options_snapshot();
-  const AttnPlan pl = plan_attention(s, o, kv8 ? kTileFp8 : 0, false, cluster_use_only(o));
+  const bool fp8 = kv8 || (paged && paged->scales);
+  const AttnPlan pl = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_only(o));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = nullptr;
   DA_TRY(workspace_get(pl.bytes, st, &ws));
@@ -793,7 +935,8 @@ int fwd_checked(const da_tensor_t* q, const da_tensor_t* k_cache, const da_tenso
   if (!std::isfinite(scale)) return DA_ERR_UNSUPPORTED;
   if (s.B == 0) return DA_OK;
   const Options o = options_snapshot();
-  const AttnPlan ap = plan_attention(s, o, kv8 ? kTileFp8 : 0, false, cluster_use_fwd(o));
+  const bool fp8 = kv8 || (paged && paged->scales);
+  const AttnPlan ap = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_fwd(o));
   const size_t attn_bytes = align_up((size_t)s.B * K * 2, 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const AttnPlan fap = plan_attention(s, o, 0, true);
@@ -825,6 +968,16 @@ int fwd_checked(const da_tensor_t* q, const da_tensor_t* k_cache, const da_tenso
                        gp.onchip ? 0 : (int)o.attn_trigger));
   return run_projection(attn, K, o_weight, out, s.B, (int)K, (int)N, ws, scratch + ap.bytes + attn_bytes, gp,
                         o.pdl != 0, st);
+}
+
+// decode_attn_cache_write / _read after their checks: one launch.
+int run_cache(CacheParams& p, int dim, bool kv8, bool write, void* stream) {
+  if (p.T == 0 || p.B == 0) return DA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = nullptr;
+  DA_TRY(workspace_get(0, st, &ws));
+  p.err = reinterpret_cast<int*>(ws + kErrOff);
+  return launch_cache(p, dim, kv8, write, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1042,6 +1195,100 @@ int decode_attn_fwd_paged(const da_tensor_t* q, const da_tensor_t* k_pages, cons
   PagedShape ps;
   DA_TRY(check_paged_inputs(q, k_pages, v_pages, block_table, seq_lens, &s, &ps));
   return fwd_checked(q, k_pages, v_pages, seq_lens, o_weight, out, scale, stream, s, &ps);
+}
+
+int decode_attn_only_paged_fp8(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages,
+                               const da_tensor_t* kv_scales, const da_tensor_t* block_table,
+                               const da_tensor_t* seq_lens, const da_tensor_t* attn_out, float scale, void* stream) {
+  AttnShape s;
+  PagedShape ps;
+  DA_TRY(check_paged_inputs(q, k_pages, v_pages, block_table, seq_lens, &s, &ps, kv_scales, DA_DTYPE_E4M3));
+  return only_checked(q, k_pages, v_pages, seq_lens, attn_out, scale, stream, s, &ps);
+}
+
+int decode_attn_fwd_paged_fp8(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages,
+                              const da_tensor_t* kv_scales, const da_tensor_t* block_table,
+                              const da_tensor_t* seq_lens, const da_tensor_t* o_weight, const da_tensor_t* out,
+                              float scale, void* stream) {
+  AttnShape s;
+  PagedShape ps;
+  DA_TRY(check_paged_inputs(q, k_pages, v_pages, block_table, seq_lens, &s, &ps, kv_scales, DA_DTYPE_E4M3));
+  return fwd_checked(q, k_pages, v_pages, seq_lens, o_weight, out, scale, stream, s, &ps);
+}
+
+int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v,
+                        const da_tensor_t* cu_seqlens_q, const da_tensor_t* cu_seqlens_k, const da_tensor_t* out,
+                        float scale, void* stream) {
+  DA_TRY(check_tensor(q, DA_DTYPE_BF16, 3, kInput16));
+  DA_TRY(check_tensor(k, DA_DTYPE_BF16, 3, kInput16));
+  DA_TRY(check_tensor(v, DA_DTYPE_BF16, 3, kInput16));
+  DA_TRY(check_tensor(out, DA_DTYPE_BF16, 3, kInput16));  // rows leave in 16-byte stores
+  const da_tensor_t *cq = cu_seqlens_q, *ck = cu_seqlens_k;
+  if (!cq || !ck) return DA_ERR_NULL;
+  if (cq->dtype != DA_DTYPE_I32 || ck->dtype != DA_DTYPE_I32) return DA_ERR_DTYPE;
+  if (cq->ndim != 1 || ck->ndim != 1) return DA_ERR_SHAPE;
+  const int64_t Tq = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
+  if (D != kHeadDim && D != kHeadDimWide) return DA_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if (out->shape[i] != q->shape[i] || v->shape[i] != k->shape[i]) return DA_ERR_SHAPE;
+  if (k->shape[2] != D || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return DA_ERR_SHAPE;
+  const int64_t B = cq->shape[0] - 1;
+  if (B < 0 || ck->shape[0] != B + 1) return DA_ERR_SHAPE;
+  if (D != kHeadDim || Hq / Hkv > kMaxGroup || B > DA_MAX_BATCH) return DA_ERR_UNSUPPORTED;
+  if (Tq > (1 << 30) || Tk > (1 << 30) || Hq > (1 << 20)) return DA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale)) return DA_ERR_UNSUPPORTED;
+  for (const da_tensor_t* t : {cq, ck}) {
+    if (!t->data) return DA_ERR_NULL;
+    if (B > 0 && t->stride[0] != 1) return DA_ERR_STRIDE;
+    if (reinterpret_cast<uintptr_t>(t->data) % 4) return DA_ERR_ALIGN;
+  }
+  if (B == 0 || Tq == 0) return DA_OK;
+  PrefillParams p;
+  memset(&p, 0, sizeof(p));
+  p.G = (int)(Hq / Hkv);
+  p.npos = 128 / p.G;
+  // items: 2 * npos positions of one sequence and KV head, at most one ragged per sequence
+  const int64_t items = ((Tq + 2 * p.npos - 1) / (2 * p.npos) + B - 1) * Hkv;
+  if (items >= ((int64_t)1 << 31) - 4096) return DA_ERR_UNSUPPORTED;
+  DA_TRY(encode_packed_map(&p.tm_q, q, p.npos, p.G));
+  if (Tk > 0) {
+    DA_TRY(encode_packed_map(&p.tm_k, k, 128, 0));
+    DA_TRY(encode_packed_map(&p.tm_v, v, 128, 0));
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = nullptr;
+  DA_TRY(workspace_get(0, st, &ws));
+  p.err = reinterpret_cast<int*>(ws + kErrOff);
+  p.out = static_cast<__nv_bfloat16*>(out->data);
+  p.o_st = out->stride[0];
+  p.o_sh = out->stride[1];
+  p.cu_q = static_cast<const int*>(cq->data);
+  p.cu_k = static_cast<const int*>(ck->data);
+  p.B = (int)B;
+  p.Hkv = (int)Hkv;
+  p.Tq = (int)Tq;
+  p.Tk = (int)Tk;
+  // the kernel masks with infinities: a scale of 0 becomes one that leaves every weight 1
+  p.scale_log2 = scale * 1.4426950408889634f;
+  if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;
+  const int grid = (int)std::min<int64_t>(std::max(1, sm_count()), items);
+  return launch_prefill(p, grid, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int decode_attn_cache_write(const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cu_seqlens,
+                            const da_tensor_t* block_table, const da_tensor_t* seq_lens, const da_tensor_t* k_pages,
+                            const da_tensor_t* v_pages, const da_tensor_t* kv_scales, void* stream) {
+  CacheParams p;
+  DA_TRY(check_cache(k, v, cu_seqlens, block_table, seq_lens, true, k_pages, v_pages, kv_scales, &p));
+  return run_cache(p, (int)k->shape[2], k_pages->dtype == DA_DTYPE_E4M3, true, stream);
+}
+
+int decode_attn_cache_read(const da_tensor_t* k_pages, const da_tensor_t* v_pages, const da_tensor_t* kv_scales,
+                           const da_tensor_t* block_table, const da_tensor_t* cu_seqlens, const da_tensor_t* k_out,
+                           const da_tensor_t* v_out, void* stream) {
+  CacheParams p;
+  DA_TRY(check_cache(k_out, v_out, cu_seqlens, block_table, nullptr, false, k_pages, v_pages, kv_scales, &p));
+  return run_cache(p, (int)k_out->shape[2], k_pages->dtype == DA_DTYPE_E4M3, false, stream);
 }
 
 int decode_attn_last_device_error(void* stream, int32_t* host_code) {

@@ -1,7 +1,7 @@
 // attn_decode.cuh -- persistent split-KV decode attention for sm_103a (the kernel
 // template; attn_decode.cu instantiates head dim 128 and the fused step,
 // attn_decode_d256.cu head dim 256, attn_decode_paged.cu the paged cache,
-// attn_decode_fp8.cu the fp8 cache).
+// attn_decode_fp8.cu the fp8 cache, attn_decode_paged_fp8.cu the paged fp8 cache).
 //
 // Computes, for every batch row b and query head h (KV head j = h / G),
 //   S = q . K^T over t < L_b (the page's scores_fp32, fp32),
@@ -56,6 +56,12 @@
 //    thread stay those of D = 128 except the q fragments, which double.
 //  * fp8 (e4m3) cache: a warp owns 32 tokens (two 16-row halves, one softmax update);
 //    codes are widened to f16 in registers (exact) for f16 MMAs, q and P in f16.
+//  * Paged fp8 cache: a scale per (token, KV head) for K and one for V, copied with each box
+//    of the tile. With V's scale 2^e m (1 <= m < 2) and x the scaled log2 score, the kernel
+//    takes w = 2^(x + e - r), r the running maximum of x + e: w m (f16) enters P.V with the
+//    codes, and w 2^-e enters the sum. A token's weight in P.V is then never small because
+//    some other token's V is large, the exponents cost no instruction (two multiplies become
+//    fused multiply-adds), and partial states merge as they do elsewhere, r in m's place.
 #pragma once
 #include <type_traits>
 
@@ -120,6 +126,27 @@ __device__ __forceinline__ int cta_of(long long x, long long T, int P) {
 }
 
 __device__ __forceinline__ int clamp_len(int L, int Lcap) { return L < 0 ? 0 : (L > Lcap ? Lcap : L); }
+
+// What the scales (ks, vs) of one token of a paged fp8 cache do to its weight: the scaled
+// log2 score is x = s * k with k = ks * scale * log2 e; with vs = 2^e m the weight in P.V is
+// 2^(x + e - r) m and the share in the sum 2^(x + e - r) * inv with inv = 2^-e. e is kept at
+// -100 at least (below it m shrinks instead), so that inv and a sum of 2^20 tokens stay finite
+// in fp32; a zero scale gives m = 0. Whatever bits stand past a sequence's end, m and inv are
+// finite: their weight 0 stays 0.
+struct TokenScale {
+  float k, e, m, inv;
+};
+__device__ __forceinline__ TokenScale token_scale(float ks, float vs, float sl2) {
+  const uint32_t bits = __float_as_uint(vs);
+  const uint32_t ef = vs == 0.f ? 127u : min(max((bits >> 23) & 0xffu, 27u), 254u);  // e + 127
+  TokenScale t;
+  t.k = ks * sl2;
+  t.e = __uint_as_float(0x4b000000u | ef) - (8388608.f + 127.f);  // 2^23 + ef, exactly
+  t.inv = __uint_as_float((254u - ef) << 23);
+  const float m = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
+  t.m = (bits & 0x7f800000u) >= (27u << 23) ? m : vs * 0x1p100f;
+  return t;
+}
 
 // Keep the bf16 halves of v whose token index (tok for the low half, tok + 1 for
 // the high half) is below `valid`.
@@ -352,28 +379,29 @@ __device__ void fused_epilogue(const AttnParams& p, uint64_t* bars, uint32_t tme
 // fetched but are never used; boxes that start at or past the sequence's length are
 // not loaded (the consumers mask those tokens). A block id outside [0, num_blocks) is
 // recorded in the error word and read past the pool's end, which TMA fills with zeros.
-template <int S, int DIM>
-__device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t ring, uint8_t* q_slots, size_t q_slot,
-                                               uint64_t* bars, int* flags, const int* prefix, const int* lens,
+template <int S, int DIM, bool KV8>
+__device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t ring, uint32_t scales, uint8_t* q_slots,
+                                               size_t q_slot, uint64_t* bars, int* flags, const int* prefix, const int* lens,
                                                int* ids, long long start, long long end, const Cursor& c_start,
                                                int role) {
   // This lane shares its SM sub-partition with two busy consumer warps, so every
   // instruction per tile costs: block sizes are powers of two (shifts, no divisions),
   // and all but the copies is done before waiting for the stage.
-  constexpr int kT = tile_tokens(DIM), kQRow = q_row_bytes(DIM);
-  constexpr int kLogT = kT == 64 ? 6 : 5;
+  constexpr int kT = KV8 ? kTileFp8 : tile_tokens(DIM), kQRow = q_row_bytes(DIM);
+  constexpr int kLogT = kT == 128 ? 7 : (kT == 64 ? 6 : 5);
   static_assert((1 << kLogT) == kT, "tile tokens are a power of two");
+  constexpr uint32_t kTokenBytes = KV8 ? DIM : DIM * 2;  // of K (or V)
   constexpr int PF = AttnSmem::kIdTiles, kRow = AttnSmem::kIdRow, kStride = AttnSmem::kIdStride;
   static_assert(kStride * 4 % 128 == 0, "ring rows must start 128-byte aligned");
   static_assert((PF & (PF - 1)) == 0, "ring rows are a power of two");
-  constexpr int kMaxSub = kT / 8;  // boxes per tile at the smallest block size
+  constexpr int kMaxSub = kT / (KV8 ? kMinBlockFp8 : kMinBlock);  // boxes per tile at the smallest block size
   static_assert(kMaxSub + 3 <= kRow, "a tile's ids fit one row after rounding down to 16 bytes");
   if (start >= end) return;
   const int B = p.B, Hkv = p.Hkv, G = p.G;
   const int lbs = p.block_shift;
   const int lsub = lbs < kLogT ? lbs : kLogT;  // log2 of the tokens per box
   const int nsub = 1 << (kLogT - lsub);        // boxes per 64-dim column of a tile
-  const uint32_t sub_bytes = (128u * (DIM / 64)) << lsub;  // one box row of K (or V)
+  const uint32_t sub_bytes = kTokenBytes << lsub;  // one box of K (or V)
   const unsigned nblk = (unsigned)p.num_blocks;
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   auto empty_bar = [&](int s) { return smem_u32(bars + S + s); };
@@ -388,6 +416,7 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
   prefetch_tensormap(&p.tm_k);
   prefetch_tensormap(&p.tm_v);
   prefetch_tensormap(&p.tm_table);
+  if (KV8) prefetch_tensormap(&p.tm_scales);
   const uint64_t kv_policy = l2_policy_evict_first();
   // Two producers (one per consumer group) share the work: this one issues the tiles whose
   // index in the range has parity `role`, i.e. the stages of group `role` and the block-id
@@ -429,7 +458,7 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
     const uint32_t fb = full_bar(stage);
     const uint32_t kdst = ring + stage * kStageBytes;
     mbar_wait_bounded(empty_bar(stage), ((it / S) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
-    mbar_arrive_expect_tx(fb, 2 * n_load * sub_bytes + (with_q ? G * DIM * 2 : 0));
+    mbar_arrive_expect_tx(fb, n_load * (2 * sub_bytes + (KV8 ? 8u << lsub : 0u)) + (with_q ? G * DIM * 2 : 0));
 #pragma unroll
     for (int s = 0; s < kMaxSub; ++s) {
       if (s >= n_load) break;
@@ -439,9 +468,12 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
         bk = (int)nblk;
       }
       // one copy per tensor: box s = all D/64 dim boxes of its rows ([box][dim box][rows])
-      const uint32_t off = (uint32_t)(s * 128 * (DIM / 64)) << lsub;
+      const uint32_t off = (uint32_t)(s * kTokenBytes) << lsub;
       tma_load_5d_hint(kdst + off, &p.tm_k, fb, 0, row, 0, c.kvh, bk, kv_policy);
       tma_load_5d_hint(kdst + kKTileBytes + off, &p.tm_v, fb, 0, row, 0, c.kvh, bk, kv_policy);
+      if (KV8)  // box s: its K scales, then its V scales
+        tma_load_4d_hint(scales + stage * AttnSmem::kScaleStageBytes + ((uint32_t)s << (lsub + 3)), &p.tm_scales, fb, row, 0,
+                         c.kvh, bk, kv_policy);
     }
     if (with_q) {
       const uint32_t qdst = smem_u32(q_slots + stage * q_slot);
@@ -471,8 +503,8 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
   constexpr bool kWide = DIM == kHeadDimWide;
   static_assert(DIM == kHeadDim || (kWide && !kFused), "head dim 128, or 256 without the fused step");
   static_assert(!PAGED || (!kFused && !SCORES), "the paged variant computes attention only");
-  static_assert(!KV8 || (DIM == kHeadDim && !kFused && !SCORES && !PAGED),
-                "the fp8-cache variant: head dim 128, attention only, contiguous cache");
+  static_assert(!KV8 || (DIM == kHeadDim && !kFused && !SCORES), "the fp8-cache variants: head dim 128, attention only");
+  constexpr bool kScaled = PAGED && KV8;  // scales per token and KV head
   // Stage: K tile then V tile, 32 KB (bf16: 64 tokens x 256 B each; fp8: 128 tokens x 128 B).
   constexpr int kSB = kStageBytes;
   constexpr int kKB = kSB / 2;
@@ -503,6 +535,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
   float* cpart_ml = cpart_o + 2 * HP * DIM;                                   // [2][HP][2]
   int* duty = reinterpret_cast<int*>(cpart_ml + 2 * HP * 2);  // [2][4] merges to share
   const uint32_t ring = smem_u32(smem);
+  const float* scales = reinterpret_cast<const float*>(smem + (kScaled ? lay.off_scales(p.cluster > 1) : 0));
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   auto empty_bar = [&](int s) { return smem_u32(bars + S + s); };
   // Guards of the bounds-checked build (constant true otherwise): an index against the
@@ -722,7 +755,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
     // ------------------------------------------------------------ producer(s)
     if constexpr (PAGED) {
       if (lane == 0)
-        paged_producer<S, DIM>(p, ring, q_slots, kFixed.q_slot(), bars, flags, prefix, lens,
+        paged_producer<S, DIM, KV8>(p, ring, smem_u32(scales), q_slots, kFixed.q_slot(), bars, flags, prefix, lens,
                                reinterpret_cast<int*>(smem + lay.off_ids()), start, end, c_start,
                                warp - kGroups * kGroupWarps);
     } else if (lane == 0) {
@@ -933,6 +966,19 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
             }
             // ---- online softmax over the 32 tokens (element i of half hh: token
             // 16hh + g + 8(i>>1), head 8nb + 2t + (i&1)); P rounded to f16 for P.V
+            // (paged: the factors of this lane's four tokens; see TokenScale)
+            TokenScale ts[2][2];
+            if constexpr (kScaled) {
+              const float* sc = scales + stage * (AttnSmem::kScaleStageBytes / 4);
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const int tok = tb + 16 * hh + g + 8 * r;
+                  const int at = ((tok >> lbox) << (lbox + 1)) + (tok & ((1 << lbox) - 1));
+                  ts[hh][r] = token_scale(sc[at], sc[at + (1 << lbox)], sl2);
+                }
+            }
             float xv[NB][2][4];
             bool grow = false;
 #pragma unroll
@@ -940,10 +986,17 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
                 const bool v0 = 16 * hh + g < vw, v1 = 16 * hh + g + 8 < vw;
-                xv[nb][hh][0] = v0 ? sa[hh][nb][0] * sl2 : kNegInf;
-                xv[nb][hh][1] = v0 ? sa[hh][nb][1] * sl2 : kNegInf;
-                xv[nb][hh][2] = v1 ? sa[hh][nb][2] * sl2 : kNegInf;
-                xv[nb][hh][3] = v1 ? sa[hh][nb][3] * sl2 : kNegInf;
+                if constexpr (kScaled) {
+                  xv[nb][hh][0] = v0 ? fmaf(sa[hh][nb][0], ts[hh][0].k, ts[hh][0].e) : kNegInf;
+                  xv[nb][hh][1] = v0 ? fmaf(sa[hh][nb][1], ts[hh][0].k, ts[hh][0].e) : kNegInf;
+                  xv[nb][hh][2] = v1 ? fmaf(sa[hh][nb][2], ts[hh][1].k, ts[hh][1].e) : kNegInf;
+                  xv[nb][hh][3] = v1 ? fmaf(sa[hh][nb][3], ts[hh][1].k, ts[hh][1].e) : kNegInf;
+                } else {
+                  xv[nb][hh][0] = v0 ? sa[hh][nb][0] * sl2 : kNegInf;
+                  xv[nb][hh][1] = v0 ? sa[hh][nb][1] * sl2 : kNegInf;
+                  xv[nb][hh][2] = v1 ? sa[hh][nb][2] * sl2 : kNegInf;
+                  xv[nb][hh][3] = v1 ? sa[hh][nb][3] * sl2 : kNegInf;
+                }
                 grow |= fmaxf(xv[nb][hh][0], xv[nb][hh][2]) > m_run[nb][0] + kSlack;
                 grow |= fmaxf(xv[nb][hh][1], xv[nb][hh][3]) > m_run[nb][1] + kSlack;
               }
@@ -979,10 +1032,20 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
               float ls0 = 0.f, ls1 = 0.f;
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh) {
-                const uint32_t r0 = pack_f16x2(fast_exp2(xv[nb][hh][0] - m0), fast_exp2(xv[nb][hh][1] - m1));
-                const uint32_t r1 = pack_f16x2(fast_exp2(xv[nb][hh][2] - m0), fast_exp2(xv[nb][hh][3] - m1));
-                ls0 += f16lo_to_f32(r0) + f16lo_to_f32(r1);  // the weights that enter P.V
-                ls1 += f16hi_to_f32(r0) + f16hi_to_f32(r1);
+                uint32_t r0, r1;
+                if constexpr (kScaled) {
+                  const float w0 = fast_exp2(xv[nb][hh][0] - m0), w1 = fast_exp2(xv[nb][hh][1] - m1);
+                  const float w2 = fast_exp2(xv[nb][hh][2] - m0), w3 = fast_exp2(xv[nb][hh][3] - m1);
+                  ls0 = fmaf(w0, ts[hh][0].inv, fmaf(w2, ts[hh][1].inv, ls0));
+                  ls1 = fmaf(w1, ts[hh][0].inv, fmaf(w3, ts[hh][1].inv, ls1));
+                  r0 = pack_f16x2(w0 * ts[hh][0].m, w1 * ts[hh][0].m);
+                  r1 = pack_f16x2(w2 * ts[hh][1].m, w3 * ts[hh][1].m);
+                } else {
+                  r0 = pack_f16x2(fast_exp2(xv[nb][hh][0] - m0), fast_exp2(xv[nb][hh][1] - m1));
+                  r1 = pack_f16x2(fast_exp2(xv[nb][hh][2] - m0), fast_exp2(xv[nb][hh][3] - m1));
+                  ls0 += f16lo_to_f32(r0) + f16lo_to_f32(r1);  // the weights that enter P.V
+                  ls1 += f16hi_to_f32(r0) + f16hi_to_f32(r1);
+                }
                 pb[hh][nb][0] = movmatrix_trans(r0);  // P[head g][tokens 16hh + 2t, +1]
                 pb[hh][nb][1] = movmatrix_trans(r1);  // P[head g][tokens 16hh + 2t + 8, +9]
               }
@@ -1242,7 +1305,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
             lsum += f * merge_ml[(w * HP + h) * 2 + 1];
             acc += f * merge_o[(w * HP + h) * kMergeRow + dl];
           }
-          if constexpr (KV8) acc *= p.v_scale;  // V = v_cache * v_scale (linear through every merge)
+          if constexpr (KV8 && !kScaled) acc *= p.v_scale;  // V = v_cache * v_scale (linear through every merge)
           if (on_chip) {
             if (ok(cslot >= 0 && cslot < 2 && h < HP) && sm_ok(smem_u32(cpart_ml + (cslot * HP + h) * 2), 8)) {
               cpart_o[(cslot * HP + h) * DIM + d] = acc;
@@ -1429,7 +1492,8 @@ cudaError_t launch_one(const AttnParams& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(attn_threads(attn_producers(PAGED, NPAD > 0, SCORES)));
-  cfg.dynamicSmemBytes = attn_smem_bytes(p.B, NB, S, DIM, kStageBytes, p.cluster > 1);
+  cfg.dynamicSmemBytes = PAGED && KV8 ? AttnSmem(NB, p.B, S, DIM).total_scaled(p.cluster > 1)
+                                      : attn_smem_bytes(p.B, NB, S, DIM, kStageBytes, p.cluster > 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   if (NPAD > 0) {

@@ -78,6 +78,15 @@ struct AttnSmem {
   __host__ __device__ constexpr size_t total(bool cluster = false) const {
     return 1024 + off_cpart() + (cluster ? cpart_bytes() : 0);
   }
+  // paged fp8 caches: the scales of each stage's 128 tokens, after everything else (one
+  // box's K scales then its V scales, 128-byte aligned for the tensor copies)
+  __host__ __device__ constexpr size_t off_scales(bool cluster) const {
+    return (off_cpart() + (cluster ? cpart_bytes() : 0) + 127) & ~(size_t)127;
+  }
+  __host__ __device__ constexpr size_t total_scaled(bool cluster = false) const {
+    return 1024 + off_scales(cluster) + (size_t)stages * kScaleStageBytes;
+  }
+  static constexpr int kScaleStageBytes = 2 * 128 * 4;
   static constexpr int kIdTiles = 8;
   static constexpr int kIdRow = 16;     // entries a row receives
   static constexpr int kIdStride = 32;  // entries between rows (128 bytes)
@@ -91,6 +100,8 @@ constexpr size_t attn_smem_bytes(int batch, int nb, int stages, int dim = kHeadD
 // fp8 (e4m3) caches: a tile is 128 tokens (128 x 128 dims x 1 byte of K and of V), so a
 // stage holds the same 32 KB and the ring the same 4 stages as for bf16.
 constexpr int kTileFp8 = 128;
+static_assert(AttnSmem(2, kMaxBatch, 4).total_scaled() <= kMaxDynSmem && AttnSmem(2, 128, 4).total_scaled(true) <= kMaxDynSmem,
+              "attention kernel (paged fp8) exceeds 227 KB of shared memory");
 static_assert(AttnSmem(2, kMaxBatch, 4).total() <= kMaxDynSmem, "attention kernel exceeds 227 KB of shared memory");
 // Cluster mode needs room for two parked states: every group width at D = 128, up to
 // eight heads per group at D = 256 (the host checks each launch; wider groups at D = 256
@@ -156,6 +167,9 @@ struct AttnParams {
   CUtensorMap tm_table;  // the table as one flat int32 array (one row), box 16 entries
   // fp8 (e4m3) caches only: K = k_cache * k_scale, V = v_cache * v_scale
   float k_scale, v_scale;
+  // paged fp8 caches: a scale per token and KV head instead, [num_blocks][Hkv][2][block_size]
+  // fp32 (K's, then V's), box min(block size, 128) tokens x 2
+  CUtensorMap tm_scales;
   // Cluster mode (> 1): the grid is launched in clusters of `cluster` consecutive CTAs; the
   // tiles are split over the CTAs as always, and a sequence whose parts all lie in one
   // cluster merges them in distributed shared memory (the others through L2).
@@ -174,8 +188,11 @@ constexpr int kMaxAttnCluster = 8;  // portable cluster size
 
 // Paged caches: a power of two from 8 tokens (tiles are cut into blocks, or blocks hold
 // whole tiles; the producer's index arithmetic is shifts and masks).
-__host__ __device__ constexpr bool paged_block_ok(int block_size, int dim) {
-  return block_size >= 8 && block_size <= (1 << 20) && (block_size & (block_size - 1)) == 0 && dim > 0;
+// A paged fp8 cache: from 16 (a tile of 128 tokens then has at most eight boxes, whose ids
+// fit a row of the id ring, and a box's scales are a multiple of 128 bytes).
+constexpr int kMinBlock = 8, kMinBlockFp8 = 16;
+__host__ __device__ constexpr bool paged_block_ok(int block_size, int dim, bool kv8 = false) {
+  return block_size >= (kv8 ? kMinBlockFp8 : kMinBlock) && block_size <= (1 << 20) && (block_size & (block_size - 1)) == 0 && dim > 0;
 }
 
 constexpr int kProjWBytes = 2 * 64 * 128;  // one stage of W_o: 128 columns x 64 k-rows
@@ -197,9 +214,46 @@ cudaError_t launch_attention_d256(const AttnParams& p, int grid, int nb, bool sc
 cudaError_t launch_attention_paged(const AttnParams& p, int grid, int nb, int dim, cudaStream_t stream);
 // Attention over an fp8 (e4m3) cache, D = 128 (p.k_scale, p.v_scale set).
 cudaError_t launch_attention_fp8(const AttnParams& p, int grid, int nb, cudaStream_t stream);
+// Attention over a paged fp8 cache with a scale per token and KV head, D = 128 (p.block_table,
+// p.tm_scales set).
+cudaError_t launch_attention_paged_fp8(const AttnParams& p, int grid, int nb, cudaStream_t stream);
 // Clusters of `cluster` attention CTAs (one per SM) that can be resident at once on the
 // current device (the GPCs' SM counts leave some SMs out); 0 if the query fails.
 int attn_max_active_clusters(int cluster);
+
+// ------------------------------------------------------------ prompt attention
+struct PrefillParams {
+  CUtensorMap tm_q;  // q [Tq][Hq][128] bf16: box 64 dims x G heads x npos tokens, 128B swizzle
+  CUtensorMap tm_k;  // k, v [Tk][Hkv][128]: box 64 dims x 128 tokens x both halves of the dims
+  CUtensorMap tm_v;
+  __nv_bfloat16* out;  // [Tq][Hq][128]
+  long long o_st, o_sh;
+  const int *cu_q, *cu_k;  // [B + 1]
+  int* err;
+  int B, Hkv, G, Tq, Tk;
+  int npos;            // query positions per tile, floor(128 / G)
+  float scale_log2;    // scale * log2(e), never 0
+};
+// grid = persistent CTAs, one per SM or as many as there can be work items.
+cudaError_t launch_prefill(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream);
+
+// ------------------------------------------------ paged cache: writing and reading
+struct CacheParams {
+  const __nv_bfloat16 *k, *v;  // [T][Hkv][D] packed tokens (read: the destinations)
+  long long k_st, k_sh, v_st, v_sh;
+  const int* cu;               // [B + 1] offsets of the sequences in the packed tokens
+  const int* table;            // [B][max_blocks]
+  long long bt_stride;
+  const int* seq_lens;         // [B] tokens of each sequence, the new ones among them (write only)
+  void *k_pages, *v_pages;     // [num_blocks][Hkv][block_size][D] bf16 or e4m3
+  long long kp_sb, kp_sh, kp_sr, vp_sb, vp_sh, vp_sr;
+  float* scales;               // [num_blocks][Hkv][2][block_size] (e4m3 pools)
+  long long sc_sb, sc_sh, sc_st;
+  int* err;
+  int B, Hkv, T, max_blocks, block_shift, num_blocks;
+  int head_groups;             // set by the launcher
+};
+cudaError_t launch_cache(CacheParams& p, int dim, bool kv8, bool write, bool pdl, cudaStream_t stream);
 
 // ------------------------------------------------------- projection: GEMV path
 constexpr int kGemvThreads = 256;

@@ -1,0 +1,475 @@
+// prefill.cu -- causal attention over packed prompts on the 5th-generation tensor cores.
+//
+// For query i of a sequence (Lq queries, the last of its Lk tokens) and query head h:
+//   S_ij = q_i . k_j (KV head h / G),  j < i + Lk - Lq + 1
+//   O_i  = sum_j 2^(s S_ij - m_i) v_j / sum_j 2^(s S_ij - m_i),   s = scale * log2 e.
+//
+// Work item: 256 rows of one (sequence, KV head), as two tiles of 128: a tile's rows are
+// npos = floor(128 / G) query positions x the G heads that share the KV head, so both tiles
+// use every K and V tile that is brought in, whatever G is, and short prompts fill tiles.
+// Items are taken heaviest (last positions) first within each sequence.
+//
+//  * tcgen05.mma M = N = 128: S = Q K^T from shared memory into TMEM, then O += P V with P in
+//    TMEM over the columns its S was read from, and V as the N-major B operand. TMEM: two S
+//    and two O accumulators of 128 columns, all 512.
+//  * A warpgroup per tile does the softmax with one row per thread: no shuffles, the row's
+//    maximum, sum and O correction are one thread's. While it works on its S, the tensor cores
+//    work for the other tile: per K/V tile they run PV0, S0, PV1, S1 (of the next K tile). In
+//    this order an MMA never overwrites an S or P that an earlier one still needs, and one
+//    barrier each way per tile and step is enough.
+//  * The running maximum lags as in the decode kernel: O in TMEM is only rescaled when a row's
+//    maximum grows by more than 2^8, by the thread that owns the row; when S(j) has
+//    arrived, PV(j - 1) is complete, so this needs no barrier of its own.
+//  * One producer lane streams K and V tiles (32 KB) by TMA through a ring of five stages; the
+//    producer warp also finds the items (a scan of the offsets) and passes them on.
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace da {
+namespace {
+
+constexpr int kN = 128;                         // keys per tile
+constexpr int kStagesP = 5;                     // K / V ring
+constexpr uint32_t kHalf = 128 * 128;           // 128 rows x 64 dims bf16
+constexpr uint32_t kTileP = 2 * kHalf;          // 128 rows x 128 dims
+constexpr int kSoftWarps = 8;                   // four per tile
+// two softmax warpgroups and a third whose first two warps are the producer and the MMA issuer
+constexpr int kThreadsP = (kSoftWarps + 4) * 32;
+// registers a thread: 168 at launch; the third warpgroup gives 80 of its own to the softmax,
+// whose threads hold a row of 128 scores (2 * 208 + 88 = 3 * 168)
+constexpr int kRegsSoft = 208, kRegsRest = 88;
+constexpr float kSlackP = 8.f;                  // log2 units the maximum may lag
+constexpr float kNegInfP = -__builtin_huge_valf();
+
+struct Item {  // in shared memory, as ints
+  int lq, lk, q0, k0, p0, kvh;  // lq < 0: no more items
+};
+constexpr size_t kOffRing = 2 * kTileP;
+constexpr size_t kOffBars = kOffRing + (size_t)kStagesP * kTileP;
+enum Bar { kQFull, kQEmpty, kVFix, kItemFull, kItemEmpty = kItemFull + 2, kSFull = kItemEmpty + 2, kPFull = kSFull + 2,
+           kOFull = kPFull + 2, kKvFull = kOFull + 2, kKvEmpty = kKvFull + kStagesP, kBars = kKvEmpty + kStagesP };
+constexpr size_t kOffItems = kOffBars + kBars * 8;
+constexpr size_t kOffFlags = kOffItems + 2 * sizeof(Item);
+constexpr size_t kSmemP = 1024 + kOffFlags + 16;
+static_assert(kSmemP <= kMaxDynSmem, "prefill kernel exceeds 227 KB of shared memory");
+
+// K/V tiles that tile w of an item needs: those up to its last row's last key.
+__device__ __forceinline__ int kv_tiles(const Item& it, int w, int npos) {
+  const int first = it.p0 + w * npos;
+  if (first >= it.lq) return 0;
+  const int last = min(first + npos, it.lq) - 1;
+  return max(0, last + it.lk - it.lq + kN) / kN;
+}
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]),
+      "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+      "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
+      "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
+      "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(taddr)
+      : "memory");
+}
+// Waits for the thread's TMEM loads; their 32 registers are read behind the wait only.
+__device__ __forceinline__ void tmem_ld_wait_x32(float* r) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(r[i]));
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] x B[smem]; issued by one thread.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// (x, y) * (a, a) + (c, c)
+__device__ __forceinline__ float2 fma2(float2 x, float a, float c) {
+  unsigned long long r, xx = *reinterpret_cast<unsigned long long*>(&x), aa, cc;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(a));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(xx), "l"(aa), "l"(cc));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<unsigned long long*>(&x)), "l"(*reinterpret_cast<unsigned long long*>(&y)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+__global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
+  constexpr uint32_t kIdescS = umma_idesc_bf16(128, kN, /*A MN-major*/ false, /*B MN-major*/ false);
+  constexpr uint32_t kIdescO = umma_idesc_bf16(128, 128, /*A MN-major*/ false, /*B MN-major*/ true);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
+  Item* items = reinterpret_cast<Item*>(smem + kOffItems);
+  int* flags = reinterpret_cast<int*>(smem + kOffFlags);  // [0] abort, [1] TMEM address
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const uint32_t q_smem = smem_u32(smem), ring = q_smem + kOffRing;
+  const int G = p.G, npos = p.npos;
+
+  if (warp == kSoftWarps + 1) {
+    tmem_alloc(smem_u32(flags + 1), 512);
+    tmem_relinquish();
+  } else if (tid == kSoftWarps * 32) {
+    prefetch_tensormap(&p.tm_q);
+    if (p.Tk > 0) {
+      prefetch_tensormap(&p.tm_k);
+      prefetch_tensormap(&p.tm_v);
+    }
+    for (int i = 0; i < kBars; ++i) {
+      const bool soft = i == kPFull || i == kPFull + 1;
+      mbar_init(bar(i), soft ? 4 : (i == kItemEmpty || i == kItemEmpty + 1 ? kSoftWarps + 1 : 1));
+    }
+    flags[0] = 0;
+    fence_barrier_init();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = (uint32_t)flags[1];
+  pdl_wait_primary();
+
+  if (warp == kSoftWarps) {
+    // ------------------------------------------------------------ producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    int base = 0, b0 = 0;  // items of the sequences before b0 (a multiple of 32) and b0
+    int kv = 0, qn = 0;
+    auto load_kv = [&](const CUtensorMap* map, const Item& it, int j, bool fix) {
+      const int s = kv % kStagesP;
+      mbar_wait_bounded(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+      const uint32_t dst = ring + s * kTileP, full = bar(kKvFull + s);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(fix ? bar(kVFix) : full, kTileP);
+        tma_load_4d(dst, map, fix ? bar(kVFix) : full, 0, it.k0 + j * kN, 0, it.kvh);
+      }
+      ++kv;
+      return s;
+    };
+    int fixes = 0;
+    for (int n = 0, x = blockIdx.x;; ++n, x += gridDim.x) {
+      // the sequence that holds row block x / Hkv: 32 sequences at a time
+      Item it;
+      const int mb = x / p.Hkv;
+      it.kvh = x - mb * p.Hkv;
+      it.lq = -1;
+      it.lk = it.q0 = it.k0 = it.p0 = 0;
+      while (b0 < p.B) {
+        const int b = b0 + lane;
+        int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+        if (b < p.B) {
+          q0 = min(max(__ldg(p.cu_q + b), 0), p.Tq);
+          q1 = min(max(__ldg(p.cu_q + b + 1), q0), p.Tq);
+          k0 = min(max(__ldg(p.cu_k + b), 0), p.Tk);
+          k1 = min(max(__ldg(p.cu_k + b + 1), k0), p.Tk);
+        }
+        const int nb = (q1 - q0 + 2 * npos - 1) / (2 * npos);
+        int end = nb;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, end, off);
+          if (lane >= off) end += o;
+        }
+        const unsigned after = __ballot_sync(0xffffffffu, base + end > mb);
+        if (after) {
+          const int src = __ffs(after) - 1;
+          it.lq = __shfl_sync(0xffffffffu, q1 - q0, src);
+          it.lk = __shfl_sync(0xffffffffu, k1 - k0, src);
+          it.q0 = __shfl_sync(0xffffffffu, q0, src);
+          it.k0 = __shfl_sync(0xffffffffu, k0, src);
+          it.p0 = (__shfl_sync(0xffffffffu, base + end, src) - 1 - mb) * 2 * npos;  // last block first
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, end, 31);
+        b0 += 32;
+      }
+      const int slot = n & 1;
+      mbar_wait_bounded(bar(kItemEmpty + slot), ((n >> 1) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+      if (lane == 0) {
+        items[slot] = it;
+        mbar_arrive(bar(kItemFull + slot));
+      }
+      if (it.lq < 0 || *(volatile int*)flags) break;
+      const int n0 = kv_tiles(it, 0, npos), n1 = kv_tiles(it, 1, npos), nt = max(n0, n1);
+      for (int j = 0; j < nt && !*(volatile int*)flags; ++j) {
+        load_kv(&p.tm_k, it, j, false);
+        if (j == 0) {  // the queries of both tiles (the second may have none)
+          mbar_wait_bounded(bar(kQEmpty), (qn & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+          ++qn;
+          if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(npos * G) * 128;
+            mbar_arrive_expect_tx(bar(kQFull), bytes * ((n0 > 0 ? 2 : 0) + (n1 > 0 ? 2 : 0)));
+            for (int w = 0; w < 2; ++w)
+              if ((w ? n1 : n0) > 0)
+                for (int c = 0; c < 2; ++c)
+                  tma_load_4d(q_smem + w * kTileP + c * kHalf, &p.tm_q, bar(kQFull), 0, it.kvh * G,
+                              it.q0 + it.p0 + w * npos, c);
+          }
+        }
+        // A V tile that ends inside another sequence's rows: their weights are 0, but 0 times
+        // a NaN or infinity there is not, so those rows are cleared before the MMA sees them.
+        const int valid = it.lk - j * kN;
+        const bool fix = valid < kN && it.k0 + it.lk < p.Tk;
+        const int s = load_kv(&p.tm_v, it, j, fix);
+        if (fix) {
+          mbar_wait_bounded(bar(kVFix), fixes & 1, p.err, kErrWaitFull, flags);
+          ++fixes;
+          uint4* tile = reinterpret_cast<uint4*>(smem + kOffRing + s * kTileP);
+          for (int i = valid * 8 + lane; i < kN * 8; i += 32) {
+            tile[i] = make_uint4(0, 0, 0, 0);
+            tile[i + kHalf / 16] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kKvFull + s));
+        }
+      }
+    }
+    // every stage released (all MMAs that read them done, and so every copy) before the CTA may end
+    for (int i = kv > kStagesP ? kv - kStagesP : 0; i < kv; ++i)
+      mbar_wait_bounded(bar(kKvEmpty + i % kStagesP), (i / kStagesP) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
+    if (qn) mbar_wait_bounded(bar(kQEmpty), (qn - 1) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
+  } else if (warp == kSoftWarps + 1) {
+    // ---------------------------------------------------------- MMA issuer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (lane == 0) {
+      int kv = 0, qn = 0, pn[2] = {0, 0};
+      auto stage_wait = [&](int i) {
+        mbar_wait_bounded(bar(kKvFull + i % kStagesP), (i / kStagesP) & 1, p.err, kErrWaitFull, flags);
+        tc_fence_after_sync();
+        return ring + (i % kStagesP) * kTileP;
+      };
+      auto scores = [&](int w, uint32_t k_smem) {  // S_w = Q_w K^T
+        const uint32_t a = q_smem + w * kTileP;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_bf16(tmem + w * 128, umma_smem_desc(a + off, 16, 1024), umma_smem_desc(k_smem + off, 16, 1024), kIdescS,
+                    kk != 0);
+        }
+        umma_commit(bar(kSFull + w));
+      };
+      for (int n = 0;; ++n) {
+        const int slot = n & 1;
+        mbar_wait_bounded(bar(kItemFull + slot), (n >> 1) & 1, p.err, kErrWaitFull, flags);
+        const Item it = items[slot];
+        mbar_arrive(bar(kItemEmpty + slot));
+        if (it.lq < 0 || *(volatile int*)flags) break;
+        const int nt[2] = {kv_tiles(it, 0, npos), kv_tiles(it, 1, npos)};
+        const int top = max(nt[0], nt[1]);
+        if (top == 0) continue;
+        uint32_t k_smem = stage_wait(kv);
+        mbar_wait_bounded(bar(kQFull), qn & 1, p.err, kErrWaitFull, flags);
+        ++qn;
+        tc_fence_after_sync();
+        for (int w = 0; w < 2; ++w)
+          if (nt[w] > 0) scores(w, k_smem);
+        umma_commit(bar(kKvEmpty + kv % kStagesP));
+        if (top == 1) umma_commit(bar(kQEmpty));
+        for (int j = 0; j < top; ++j) {
+          const int v_it = kv + 1, k_it = kv + 2;
+          const uint32_t v_smem = stage_wait(v_it);
+          k_smem = 0;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (j < nt[w]) {  // O_w += P_w V
+              mbar_wait_bounded(bar(kPFull + w), pn[w] & 1, p.err, kErrWaitMma, flags);
+              ++pn[w];
+              tc_fence_after_sync();
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                umma_bf16_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8,
+                             umma_smem_desc(v_smem + kk * 16 * 128, kHalf, 1024), kIdescO, j > 0 || kk > 0);
+              if (j == nt[w] - 1) umma_commit(bar(kOFull + w));
+            }
+            if (j + 1 < nt[w]) {
+              if (!k_smem) k_smem = stage_wait(k_it);
+              scores(w, k_smem);
+            }
+          }
+          umma_commit(bar(kKvEmpty + v_it % kStagesP));
+          if (j + 1 < top) {
+            umma_commit(bar(kKvEmpty + k_it % kStagesP));
+            if (j + 2 == top) umma_commit(bar(kQEmpty));
+          }
+          kv += 2;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < kSoftWarps) {
+    // ------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    const int w = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row of it (= TMEM lane)
+    const uint32_t s_tmem = tmem + w * 128 + ((uint32_t)((warp & 3) * 32) << 16), o_tmem = s_tmem + 256;
+    const int off = r / G, g = r - off * G;               // position in the tile, head of the group
+    const int off0 = (warp & 3) * 32 / G;                 // of the warp's first row
+    const float sl2 = p.scale_log2;
+    const bool neg = sl2 < 0.f;
+    int sn = 0, on = 0;
+    for (int n = 0;; ++n) {
+      const int slot = n & 1;
+      mbar_wait_bounded(bar(kItemFull + slot), (n >> 1) & 1, p.err, kErrWaitFull, flags);
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kItemEmpty + slot));
+      if (it.lq < 0 || *(volatile int*)flags) break;
+      const int first = it.p0 + w * npos, pos = first + off;
+      const bool row_ok = off < npos && pos < it.lq;
+      const int lim = min(it.lk, pos + it.lk - it.lq + 1);            // keys of this row
+      const int lim0 = min(it.lk, first + off0 + it.lk - it.lq + 1);  // the least of the warp's rows
+      const int nt = kv_tiles(it, w, npos);
+      float m = kNegInfP, l = 0.f;
+      for (int j = 0; j < nt; ++j) {
+        mbar_wait_bounded(bar(kSFull + w), sn & 1, p.err, kErrWaitMma, flags);
+        ++sn;
+        tc_fence_after_sync();
+        float s[kN];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_x32(s_tmem + c * 32, s + c * 32);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait_x32(s + c * 32);
+        if ((j + 1) * kN > lim0) {  // some row of the warp ends inside this tile
+          const float none = neg ? -kNegInfP : kNegInfP;
+          const int left = lim - j * kN;
+#pragma unroll
+          for (int c = 0; c < kN; ++c) s[c] = c < left ? s[c] : none;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = s[c];
+        if (!neg) {
+#pragma unroll
+          for (int c = 4; c < kN; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+          mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        } else {
+#pragma unroll
+          for (int c = 4; c < kN; ++c) mx[c & 3] = fminf(mx[c & 3], s[c]);
+          mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
+        }
+        const float xm = mx[0] * sl2;
+        const bool grow = row_ok && xm > m + kSlackP;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float al = grow ? fast_exp2(m - xm) : 1.f;
+          m = grow ? xm : m;
+          l *= al;
+          if (j > 0) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              tmem_ld_x32(o_tmem + c * 32, o);
+              tmem_ld_wait_x32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= al;
+              tmem_st_x32(o_tmem + c * 32, reinterpret_cast<uint32_t*>(o));
+            }
+          }
+        }
+        const float mr = m == kNegInfP ? 0.f : -m;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float2 x = fma2(make_float2(s[h * 64 + 2 * i], s[h * 64 + 2 * i + 1]), sl2, mr);
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+            sum[i & 1] = add2(sum[i & 1], x);
+            pk[i] = pack_bf16x2(x.x, x.y);
+          }
+          tmem_st_x32(s_tmem + h * 32, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + w));
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      }
+      __nv_bfloat16* out = p.out + (long long)(it.q0 + pos) * p.o_st + (long long)(it.kvh * G + g) * p.o_sh;
+      if (nt > 0) {
+        mbar_wait_bounded(bar(kOFull + w), on & 1, p.err, kErrWaitMma, flags);
+        ++on;
+        tc_fence_after_sync();
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tmem_ld_x32(o_tmem + c * 32, o);
+          tmem_ld_wait_x32(o);
+          if (row_ok) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                y[k] = l == 0.f ? 0u : pack_bf16x2(o[i * 8 + 2 * k] * inv, o[i * 8 + 2 * k + 1] * inv);
+              *reinterpret_cast<uint4*>(out + c * 32 + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+        }
+      } else if (row_ok) {  // no key at all
+#pragma unroll
+        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(out + i * 8) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kSoftWarps + 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream) {
+  static int configured[64] = {0};  // the shared-memory opt-in, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemP);
+    if (e != cudaSuccess) return e;
+    configured[dev] = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreadsP);
+  cfg.dynamicSmemBytes = kSmemP;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, prefill_kernel, p);
+}
+
+}  // namespace da

@@ -215,6 +215,103 @@ int decode_attn_only_fp8(const da_tensor_t* q, const da_tensor_t* k_cache, const
                          float v_scale, void* stream);
 
 /*
+ * decode_attn_fwd_paged_fp8 / decode_attn_only_paged_fp8 -- decode_attn_fwd_paged /
+ * decode_attn_only_paged over a paged fp8 cache with a scale for every token and KV head, the
+ * cache that decode_attn_cache_write fills:
+ *
+ *   K[b, j, t, :] = k_pages[i, j, r, :] * kv_scales[i, j, 0, r]
+ *   V[b, j, t, :] = v_pages[i, j, r, :] * kv_scales[i, j, 1, r]
+ *   i = block_table[b, t / block_size],  r = t % block_size
+ *
+ *   k_pages, v_pages [num_blocks, Hkv, block_size, 128] e4m3; strides multiples of 16 elements
+ *   kv_scales [num_blocks, Hkv, 2, block_size] fp32 (K's scales, then V's); strides multiples
+ *             of 4 elements. Any finite values; V's between 2^-100 and 2^100 in magnitude keep
+ *             the accuracy of the other entry points (smaller ones lose it gradually), 0 makes
+ *             the row zero.
+ *   other arguments as decode_attn_fwd_paged / decode_attn_only_paged
+ * block_size: a power of two from 16 to 2^20. Head dim 128 only (D = 256 returns
+ * DA_ERR_UNSUPPORTED). q and the softmax weights as in decode_attn_fwd_fp8. A table entry
+ * outside the pool sets bit 64 of the error word and its block reads as zeros.
+ */
+int decode_attn_fwd_paged_fp8(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages,
+                              const da_tensor_t* kv_scales, const da_tensor_t* block_table,
+                              const da_tensor_t* seq_lens, const da_tensor_t* o_weight, const da_tensor_t* out,
+                              float scale, void* stream);
+int decode_attn_only_paged_fp8(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages,
+                               const da_tensor_t* kv_scales, const da_tensor_t* block_table,
+                               const da_tensor_t* seq_lens, const da_tensor_t* attn_out, float scale, void* stream);
+
+/*
+ * decode_attn_prefill -- causal attention over whole prompts: the queries of B packed sequences
+ * of different lengths (tokens laid end to end, no padding) over their keys and values.
+ *
+ *   q [Tq, Hq, 128] bf16, k and v [Tk, Hkv, 128] bf16; out [Tq, Hq, 128] bf16, written
+ *   cu_seqlens_q, cu_seqlens_k [B + 1] int32 (device): sequence b holds rows
+ *     cu_seqlens_q[b] .. cu_seqlens_q[b + 1] of q and out, and rows cu_seqlens_k[b] ..
+ *     cu_seqlens_k[b + 1] of k and v: Lq queries, which are the LAST Lq of its Lk tokens
+ *     (Lq < Lk: a prompt whose beginning is cached already, see decode_attn_cache_read)
+ *   scale  softmax scale, any finite float
+ *
+ * Query i of a sequence (0 <= i < Lq) attends keys j <= i + Lk - Lq; query head h attends with
+ * KV head h / (Hq / Hkv). A query without a key (Lk < Lq: the first Lq - Lk ones) gives a row
+ * of zeros. Rows of q that belong to no sequence are left as they were in out. Offsets are
+ * clamped to [0, Tq] and [0, Tk]; a sequence whose end is not after its start is empty.
+ * Other sequences' rows never reach a sequence's output, whatever they hold; a NaN or infinity
+ * in a sequence's own k or v can make any output row of that sequence and KV head non-finite.
+ * Requires Hq % Hkv == 0, Hq / Hkv <= 16, B <= 1024, D = 128 (256 returns DA_ERR_UNSUPPORTED);
+ * out 16-byte aligned with strides multiples of 8 elements, like the inputs.
+ * The softmax weights enter P.V as bf16, unnormalised; sums and the accumulation are fp32.
+ */
+int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v,
+                        const da_tensor_t* cu_seqlens_q, const da_tensor_t* cu_seqlens_k, const da_tensor_t* out,
+                        float scale, void* stream);
+
+/*
+ * decode_attn_cache_write -- the keys and values of new tokens into a paged cache, as
+ * decode_attn_*_paged (bf16 pools: copied) or decode_attn_*_paged_fp8 (e4m3 pools: quantised)
+ * read them.
+ *
+ *   k, v        [T, Hkv, D] bf16: the new tokens of B packed sequences
+ *   cu_seqlens  [B + 1] int32 (device): sequence b holds rows cu_seqlens[b] .. cu_seqlens[b + 1]
+ *   block_table [B, max_blocks] int32 (device), rows contiguous
+ *   seq_lens    [B] int32 (device): tokens of each sequence, the new ones among them: its n
+ *               rows are tokens seq_lens[b] - n .. seq_lens[b] - 1 (a decode step after its
+ *               token: n = 1 and the same seq_lens that its attention takes)
+ *   k_pages, v_pages [num_blocks, Hkv, block_size, D] bf16 (D = 128 or 256) or e4m3 (D = 128),
+ *               any strides obeying the conventions; written
+ *   kv_scales   [num_blocks, Hkv, 2, block_size] fp32, written, for e4m3 pools; NULL for bf16
+ *
+ * e4m3: per token and head, of K and of V alike, scale = 2^e with the least e for which the
+ * row's largest finite magnitude is at most 448 * 2^e (e in [-124, 120]; 1 for a row of
+ * zeros), code = e4m3(x / scale), rounded to nearest even; infinities become the largest code,
+ * +-448, NaN the NaN code. Every code * scale is a bf16 value (under 2^120, for rows that pass
+ * 2.98e38, codes end at +-240 for that).
+ * Nothing else in the pools is touched. Rows that belong to no sequence, and tokens before a
+ * sequence's first (a negative position), are not written; a token past max_blocks *
+ * block_size, or whose table entry lies outside the pool, is not written and sets bit 64 of the
+ * device error word. Two tokens of one call must not share a place (a block that two
+ * sequences share is for reading only): what such a row holds afterwards is unspecified.
+ * block_size: a power of two from 8 (e4m3: 16) to 2^20. B <= 1024.
+ */
+int decode_attn_cache_write(const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cu_seqlens,
+                            const da_tensor_t* block_table, const da_tensor_t* seq_lens, const da_tensor_t* k_pages,
+                            const da_tensor_t* v_pages, const da_tensor_t* kv_scales, void* stream);
+
+/*
+ * decode_attn_cache_read -- the first tokens of B sequences out of a paged cache (bf16 or
+ * e4m3), packed: row cu_seqlens[b] + t of k_out and v_out [T, Hkv, D] bf16 is token t of
+ * sequence b, 0 <= t < cu_seqlens[b + 1] - cu_seqlens[b] (e4m3: code * scale, rounded once to
+ * bf16; exact for what decode_attn_cache_write wrote). The k and v of decode_attn_prefill for
+ * prompts whose beginning is cached. Other arguments and limits as decode_attn_cache_write;
+ * rows that belong to no sequence are left as they were; a token past max_blocks * block_size,
+ * or whose table entry lies outside the pool, reads as zeros and sets bit 64.
+ * k_out, v_out 16-byte aligned with strides multiples of 8 elements.
+ */
+int decode_attn_cache_read(const da_tensor_t* k_pages, const da_tensor_t* v_pages, const da_tensor_t* kv_scales,
+                           const da_tensor_t* block_table, const da_tensor_t* cu_seqlens, const da_tensor_t* k_out,
+                           const da_tensor_t* v_out, void* stream);
+
+/*
  * decode_attn_scores -- the first contraction alone: the page's `scores_fp32`
  * (q_grouped . k_cache^T, b_trans=True), unscaled, in fp32.
  *   scores [B, Hq, Lcap] fp32: scores[b, h, t] is written for t < seq_lens[b]

@@ -1,0 +1,199 @@
+"""decode_attn_only_paged_fp8 / decode_attn_fwd_paged_fp8 (a scale per token and KV head) against the formula in 64
+bits, within the bounds of prompt_helpers."""
+import math
+
+import pytest
+import torch
+
+import decode_attention_output_gb300 as da
+from prompt_helpers import F64, assert_within, token_ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+SCALE = 1 / math.sqrt(128)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    from decode_attention_output_gb300 import build
+
+    build.build()
+    da.load()
+    torch.cuda.set_device(0)
+    yield
+    assert da.decode_attn_last_device_error() == 0
+
+
+def case(B, Hq, Hkv, lens, bs, seed=0, spread=1.0, max_blocks=None, pow2=True):
+    """q, pools with unused rows of garbage (NaN codes and scales), table, lens."""
+    g = torch.Generator().manual_seed(seed)
+    most = max_blocks or max(1, max(-(-n // bs) for n in lens))
+    blocks = B * most + 2
+    table = torch.randperm(blocks, generator=g)[: B * most].view(B, most)
+    k, v = ((torch.randn((blocks, Hkv, bs, 128), generator=g) * 60).to(torch.float8_e4m3fn) for _ in range(2))
+    size = torch.randn((blocks, Hkv, 2, bs), generator=g) * spread - 6
+    scales = torch.exp2(torch.round(size) if pow2 else size).float()
+    used = torch.zeros((blocks, bs), dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for t in range(min(max(n, 0), most * bs)):
+            used[table[b, t // bs], t % bs] = True
+    for p in (k, v):
+        p.view(torch.uint8).masked_fill_(~used[:, None, :, None], 0x7F)
+    scales.masked_fill_(~used[:, None, None, :], float("nan"))
+    q = torch.randn((B, Hq, 128), generator=g).to(torch.bfloat16)
+    return q, k, v, scales, table, list(lens)
+
+
+def on(x):
+    q, k, v, scales, table, lens = x
+    return [q.to(DEV), k.to(DEV), v.to(DEV), scales.to(DEV), table.to(torch.int32).to(DEV),
+            torch.tensor(lens, dtype=torch.int32, device=DEV)]
+
+
+def check(x, what, scale=SCALE):
+    ref, tol = token_ref(*x, scale)
+    out = torch.full(x[0].shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    da.decode_attn_only_paged_fp8(*on(x), out, scale)
+    torch.cuda.synchronize()
+    assert da.decode_attn_last_device_error() == 0
+    assert_within(out.cpu(), ref, tol, what)
+    return out, tol
+
+
+CASES = [
+    ("one_token", (1, 4, 1, [1], 16)),
+    ("g4", (3, 8, 2, [320, 1, 129], 16)),
+    ("zero_and_odd", (4, 16, 4, [0, 127, 128, 300], 32)),
+    ("g8_bs64", (2, 16, 2, [224, 65], 64)),
+    ("g16_bs128", (2, 32, 2, [256, 127], 128)),
+    ("g12_bs32", (2, 24, 2, [500, 33], 32)),
+    ("g1_bs256", (2, 4, 4, [300, 512], 256)),
+    ("bs1024", (2, 4, 2, [1500, 700], 1024)),
+    ("many", (40, 8, 1, [(i * 37) % 130 for i in range(40)], 16)),
+    ("clusters_equal", (4, 32, 8, [2048] * 4, 64)),
+    ("clusters_ragged", (8, 32, 8, [2048, 0, 1, 1500, 64, 2000, 777, 129], 16)),
+]
+
+
+@pytest.mark.parametrize("name,args", CASES, ids=[c[0] for c in CASES])
+def test_parity(name, args):
+    check(case(*args, seed=1), name)
+    check(case(*args, seed=2, pow2=False), name + ", any scales")
+
+
+@pytest.mark.parametrize("spread", [4.0, 12.0])
+def test_scales_of_very_different_size(spread):
+    """Values whose size differs by factors of thousands and more from token to token."""
+    check(case(3, 16, 2, [700, 64, 3], 16, seed=3, spread=spread), f"spread {spread}")
+    x = case(2, 8, 2, [400, 300], 32, seed=4)
+    x[3][:, :, 1] *= torch.exp2(torch.linspace(-40, 40, x[3].shape[0]).round())[:, None, None]  # V
+    check(x, "values from 2^-46 to 2^34")
+
+
+def test_negative_scale_zero_scales_and_large_scores():
+    x = case(2, 8, 2, [200, 150], 16, seed=5)
+    check(x, "negative softmax scale", -0.05)
+    check(x, "weights all alike", 0.0)
+    check(x, "one weight only", 3.0)
+    x[3][::2, :, 1] = 0.0  # every other block's values are zero
+    check(x, "zero value scales")
+    x[3][::3, :, 0] = 0.0
+    check(x, "zero key scales")
+
+
+@pytest.mark.parametrize("ctas", [1, 5, 300])
+def test_split_counts(ctas):
+    old = da.decode_attn_get_option("attn_ctas")
+    da.decode_attn_set_option("attn_ctas", ctas)
+    try:
+        check(case(3, 16, 2, [640, 333, 17], 16, seed=6), f"{ctas} CTAs")
+    finally:
+        da.decode_attn_set_option("attn_ctas", old)
+
+
+def test_token_major_pool_views_and_padded_table():
+    x = case(2, 8, 2, [250, 100], 32, seed=7)
+    out, _ = check(x, "plain")
+    q, k, v, scales, table, lens = on(x)
+    k2, v2 = (p.transpose(1, 2).contiguous().transpose(1, 2) for p in (k, v))
+    wide = torch.zeros((*scales.shape[:2], 3, 64), dtype=torch.float32, device=DEV)
+    wide[:, :, :2, 16:48] = scales
+    big = torch.full((2, 20), 1 << 30, dtype=torch.int32, device=DEV)
+    big[:, : table.shape[1]] = table
+    out2 = torch.empty_like(out)
+    da.decode_attn_only_paged_fp8(q, k2, v2, wide[:, :, :2, 16:48], big[:, : table.shape[1]], lens, out2, SCALE)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2)
+
+
+def test_block_outside_the_pool_reads_as_zeros():
+    x = case(2, 8, 2, [64, 64], 16, seed=8)
+    x[4][1, 2] = x[1].shape[0] + 7
+    ref, tol = token_ref(*x, SCALE)
+    out = torch.empty(x[0].shape, dtype=torch.bfloat16, device=DEV)
+    da.decode_attn_only_paged_fp8(*on(x), out, SCALE)
+    assert da.decode_attn_last_device_error() == 64
+    assert_within(out.cpu(), ref, tol, "zeros")
+
+
+def test_lengths_past_the_table_are_clamped():
+    x = case(2, 8, 2, [96, 96], 32, seed=9)
+    out, _ = check(x, "full")
+    a = on(x)
+    a[5] = torch.tensor([1 << 30, 97], dtype=torch.int32, device=DEV)
+    out2 = torch.empty_like(out)
+    da.decode_attn_only_paged_fp8(*a, out2, SCALE)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2)
+
+
+@pytest.mark.parametrize("B,N", [(1, 256), (5, 1032), (33, 512)])
+def test_whole_step(B, N):
+    Hq, Hkv = 16, 4
+    x = case(B, Hq, Hkv, [(i * 97) % 400 + 1 for i in range(B)], 16, seed=10)
+    ref, tol = token_ref(*x, SCALE)
+    g = torch.Generator().manual_seed(11)
+    w = (torch.randn((Hq * 128, N), generator=g) / math.sqrt(Hq * 128)).to(torch.bfloat16)
+    out = torch.empty((B, N), dtype=torch.bfloat16, device=DEV)
+    a = on(x)
+    da.decode_attn_fwd_paged_fp8(*a, w.to(DEV), out, SCALE)
+    torch.cuda.synchronize()
+    assert da.decode_attn_last_device_error() == 0
+    ref, tol, w = ref.reshape(B, -1), tol.reshape(B, -1), w.to(F64)
+    want = ref @ w
+    # the attention's bound through W, K = 2048 products in fp32 (2^-23 of each partial sum), the output's bf16
+    bound = tol @ w.abs() + Hq * 128 * 2.0 ** -23 * (ref.abs() @ w.abs()) + 2.0 ** -8 * want.abs()
+    assert_within(out.cpu(), want, bound * 1.01, "step")
+
+
+def test_captured_and_other_stream():
+    x = case(3, 32, 8, [900, 5, 400], 64, seed=12, max_blocks=16)
+    a = on(x)
+    out, tol = check(x, "eager")
+    s = torch.cuda.Stream()
+    out2 = torch.empty_like(out)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        da.decode_attn_only_paged_fp8(*a, out2, SCALE)
+    s.synchronize()
+    assert torch.equal(out, out2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        da.decode_attn_only_paged_fp8(*a, out2, SCALE)
+    for n in ([900, 3, 17], [0, 5, 400]):  # shorter lengths: the rows that `case` filled
+        a[5].copy_(torch.tensor(n, dtype=torch.int32))
+        out2.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, tol = token_ref(*x[:5], n, SCALE)
+        assert_within(out2.cpu(), ref, tol, "replayed")
+
+
+def test_empty_batch():
+    q = torch.empty((0, 8, 128), dtype=torch.bfloat16, device=DEV)
+    kp = torch.zeros((4, 2, 16, 128), device=DEV).to(torch.float8_e4m3fn)
+    sc = torch.ones((4, 2, 2, 16), device=DEV)
+    da.decode_attn_only_paged_fp8(q, kp, kp, sc, torch.empty((0, 3), dtype=torch.int32, device=DEV),
+                                  torch.empty((0,), dtype=torch.int32, device=DEV), q.clone(), 0.1)
+    torch.cuda.synchronize()
