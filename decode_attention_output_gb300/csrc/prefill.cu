@@ -90,16 +90,38 @@ __device__ __forceinline__ void tmem_ld_wait_x32(float* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] x B[smem]; issued by one thread.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// One thread's work of a converged warp. The whole warp runs the issuing code and each
+// instruction elects its thread, so that descriptors stay in uniform registers: issued from a
+// branch that one lane takes, an MMA cost about 100 cycles against the 64 it computes for.
+#define DA_ELECT "elect.sync _|e, 0xffffffff;\n\t"
+
+// D[tmem] (+)= A[smem] x B[smem]
+__device__ __forceinline__ void warp_umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t" DA_ELECT
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] x B[smem]
+__device__ __forceinline__ void warp_umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t" DA_ELECT
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ void warp_umma_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t" DA_ELECT
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // (x, y) * (a, a) + (c, c)
 __device__ __forceinline__ float2 fma2(float2 x, float a, float c) {
@@ -254,71 +276,78 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
   } else if (warp == kSoftWarps + 1) {
     // ---------------------------------------------------------- MMA issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (lane == 0) {
-      int kv = 0, qn = 0, pn[2] = {0, 0};
-      auto stage_wait = [&](int i) {
-        mbar_wait_bounded(bar(kKvFull + i % kStagesP), (i / kStagesP) & 1, p.err, kErrWaitFull, flags);
-        tc_fence_after_sync();
-        return ring + (i % kStagesP) * kTileP;
-      };
-      auto scores = [&](int w, uint32_t k_smem) {  // S_w = Q_w K^T
-        const uint32_t a = q_smem + w * kTileP;
+    auto wait = [&](int b, int parity, int code) {
+      mbar_wait_bounded(bar(b), parity, p.err, code, flags);
+      __syncwarp();
+      tc_fence_after_sync();
+    };
+    const uint64_t q_desc = umma_smem_desc(q_smem, 16, 1024);
+    const uint64_t k_desc = umma_smem_desc(ring, 16, 1024), v_desc = umma_smem_desc(ring, kHalf, 1024);
+    int ks = 0, kph = 0;  // ring position of the next K or V tile
+    int qn = 0, pn[2] = {0, 0};
+    auto next_stage = [&] {  // waits for the next tile, returns its stage
+      const int s = ks;
+      wait(kKvFull + s, kph, kErrWaitFull);
+      if (++ks == kStagesP) {
+        ks = 0;
+        kph ^= 1;
+      }
+      return s;
+    };
+    auto scores = [&](int w, int stage) {  // S_w = Q_w K^T
+      const uint64_t a = q_desc + (uint64_t)(w * (kTileP >> 4)), b = k_desc + (uint64_t)(stage * (kTileP >> 4));
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-          umma_bf16(tmem + w * 128, umma_smem_desc(a + off, 16, 1024), umma_smem_desc(k_smem + off, 16, 1024), kIdescS,
-                    kk != 0);
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+        warp_umma_ss(tmem + w * 128, a + off, b + off, kIdescS, kk != 0);
+      }
+      warp_umma_commit(bar(kSFull + w));
+    };
+    for (int n = 0;; ++n) {
+      const int slot = n & 1;
+      mbar_wait_bounded(bar(kItemFull + slot), (n >> 1) & 1, p.err, kErrWaitFull, flags);
+      __syncwarp();
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kItemEmpty + slot));
+      __syncwarp();
+      if (uniform(it.lq < 0 || *(volatile int*)flags)) break;
+      const int nt[2] = {uniform(kv_tiles(it, 0, npos)), uniform(kv_tiles(it, 1, npos))};
+      const int top = max(nt[0], nt[1]);
+      if (top == 0) continue;
+      int k_stage = next_stage();
+      wait(kQFull, qn & 1, kErrWaitFull);
+      ++qn;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (nt[w] > 0) scores(w, k_stage);
+      warp_umma_commit(bar(kKvEmpty + k_stage));
+      if (top == 1) warp_umma_commit(bar(kQEmpty));
+      for (int j = 0; j < top; ++j) {
+        const int v_stage = next_stage();
+        const bool more = j + 1 < top;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (j < nt[w]) {  // O_w += P_w V
+            wait(kPFull + w, pn[w] & 1, kErrWaitMma);
+            ++pn[w];
+            const uint64_t b = v_desc + (uint64_t)(v_stage * (kTileP >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              warp_umma_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO,
+                           j > 0 || kk > 0);
+            if (j == nt[w] - 1) warp_umma_commit(bar(kOFull + w));
+          }
+          if (w == 0 && more) k_stage = next_stage();
+          if (j + 1 < nt[w]) scores(w, k_stage);
         }
-        umma_commit(bar(kSFull + w));
-      };
-      for (int n = 0;; ++n) {
-        const int slot = n & 1;
-        mbar_wait_bounded(bar(kItemFull + slot), (n >> 1) & 1, p.err, kErrWaitFull, flags);
-        const Item it = items[slot];
-        mbar_arrive(bar(kItemEmpty + slot));
-        if (it.lq < 0 || *(volatile int*)flags) break;
-        const int nt[2] = {kv_tiles(it, 0, npos), kv_tiles(it, 1, npos)};
-        const int top = max(nt[0], nt[1]);
-        if (top == 0) continue;
-        uint32_t k_smem = stage_wait(kv);
-        mbar_wait_bounded(bar(kQFull), qn & 1, p.err, kErrWaitFull, flags);
-        ++qn;
-        tc_fence_after_sync();
-        for (int w = 0; w < 2; ++w)
-          if (nt[w] > 0) scores(w, k_smem);
-        umma_commit(bar(kKvEmpty + kv % kStagesP));
-        if (top == 1) umma_commit(bar(kQEmpty));
-        for (int j = 0; j < top; ++j) {
-          const int v_it = kv + 1, k_it = kv + 2;
-          const uint32_t v_smem = stage_wait(v_it);
-          k_smem = 0;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (j < nt[w]) {  // O_w += P_w V
-              mbar_wait_bounded(bar(kPFull + w), pn[w] & 1, p.err, kErrWaitMma, flags);
-              ++pn[w];
-              tc_fence_after_sync();
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_bf16_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8,
-                             umma_smem_desc(v_smem + kk * 16 * 128, kHalf, 1024), kIdescO, j > 0 || kk > 0);
-              if (j == nt[w] - 1) umma_commit(bar(kOFull + w));
-            }
-            if (j + 1 < nt[w]) {
-              if (!k_smem) k_smem = stage_wait(k_it);
-              scores(w, k_smem);
-            }
-          }
-          umma_commit(bar(kKvEmpty + v_it % kStagesP));
-          if (j + 1 < top) {
-            umma_commit(bar(kKvEmpty + k_it % kStagesP));
-            if (j + 2 == top) umma_commit(bar(kQEmpty));
-          }
-          kv += 2;
+        warp_umma_commit(bar(kKvEmpty + v_stage));
+        if (more) {
+          warp_umma_commit(bar(kKvEmpty + k_stage));
+          if (j + 2 == top) warp_umma_commit(bar(kQEmpty));
         }
       }
     }
-    __syncwarp();
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
