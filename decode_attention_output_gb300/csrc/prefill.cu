@@ -9,19 +9,22 @@
 // use every K and V tile that is brought in, whatever G is, and short prompts fill tiles.
 // Items are taken heaviest (last positions) first within each sequence.
 //
-//  * tcgen05.mma M = N = 128: S = Q K^T from shared memory into TMEM, then O += P V with P in
-//    TMEM over the columns its S was read from, and V as the N-major B operand. TMEM: two S
-//    and two O accumulators of 128 columns, all 512.
-//  * A warpgroup per tile does the softmax with one row per thread: no shuffles, the row's
-//    maximum, sum and O correction are one thread's. While it works on its S, the tensor cores
-//    work for the other tile: per K/V tile they run PV0, S0, PV1, S1 (of the next K tile). In
-//    this order an MMA never overwrites an S or P that an earlier one still needs, and one
-//    barrier each way per tile and step is enough.
+//  * tcgen05.mma M = N = 128: S = Q K^T from shared memory into TMEM, then O += P V with P
+//    (bf16) in TMEM and V as the N-major B operand. TMEM, all 512 columns: one S (128), a P
+//    for each tile (64 each), an O for each tile (128 each).
+//  * The work is a stream of steps (item, K/V tile) that runs on across items, through four
+//    parties that only wait for data: one warp issues S = Q K^T for the two tiles in turn, a
+//    warpgroup per tile does the softmax, another warp issues O += P V, a producer loads. A
+//    softmax thread holds one row (no shuffles; the row's maximum, sum and O correction are
+//    one thread's), takes its S into registers and frees it at once. With one issuing warp and
+//    P over its S (PV(r), then S(r + 1)) a step took 2860 cycles, of which its MMAs compute for
+//    2048: each side waited for the other in turn, and each wait costs an issuing warp some
+//    200 cycles in which nothing else was issued. An item's O is stored when its tile's next
+//    step has its weights.
 //  * The running maximum lags as in the decode kernel: O in TMEM is only rescaled when a row's
-//    maximum grows by more than 2^8, by the thread that owns the row; when S(j) has
-//    arrived, PV(j - 1) is complete, so this needs no barrier of its own.
-//  * One producer lane streams K and V tiles (32 KB) by TMA through a ring of five stages; the
-//    producer warp also finds the items (a scan of the offsets) and passes them on.
+//    maximum grows by more than 2^8, by the thread that owns the row.
+//  * One producer warp streams K and V tiles (32 KB) by TMA through a ring of five stages, in
+//    the order of their use; it also finds the items (a scan of the offsets) and passes them on.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -33,7 +36,7 @@ constexpr int kStagesP = 5;                     // K / V ring
 constexpr uint32_t kHalf = 128 * 128;           // 128 rows x 64 dims bf16
 constexpr uint32_t kTileP = 2 * kHalf;          // 128 rows x 128 dims
 constexpr int kSoftWarps = 8;                   // four per tile
-// two softmax warpgroups and a third whose first two warps are the producer and the MMA issuer
+// two softmax warpgroups and a third: the producer, the issuers of S and of PV, and a spare warp
 constexpr int kThreadsP = (kSoftWarps + 4) * 32;
 // registers a thread: 168 at launch; the third warpgroup gives 80 of its own to the softmax,
 // whose threads hold a row of 128 scores (2 * 208 + 88 = 3 * 168)
@@ -46,10 +49,22 @@ struct Item {  // in shared memory, as ints
 };
 constexpr size_t kOffRing = 2 * kTileP;
 constexpr size_t kOffBars = kOffRing + (size_t)kStagesP * kTileP;
-enum Bar { kQFull, kQEmpty, kVFix, kItemFull, kItemEmpty = kItemFull + 2, kSFull = kItemEmpty + 2, kPFull = kSFull + 2,
-           kOFull = kPFull + 2, kKvFull = kOFull + 2, kKvEmpty = kKvFull + kStagesP, kBars = kKvEmpty + kStagesP };
+constexpr int kItems = 4;  // items on their way from the producer
+enum Bar {
+  kQFull,                          // per tile: queries landed / free
+  kQEmpty = kQFull + 2,
+  kSFull = kQEmpty + 2,            // per tile: its S is in TMEM
+  kPFull = kSFull + 2,             // per tile: its P is in TMEM, O is corrected
+  kPvDone = kPFull + 2,            // per tile: its PV has completed
+  kSFree = kPvDone + 2,            // the S columns have been read
+  kVFix,                           // a V tile that needs clearing has landed
+  kItemFull, kItemEmpty = kItemFull + kItems,
+  kKvFull = kItemEmpty + kItems, kKvEmpty = kKvFull + kStagesP,
+  kBars = kKvEmpty + kStagesP
+};
+constexpr uint32_t kTmemP = 128, kTmemO = 256;  // columns: S, P0, P1, O0, O1
 constexpr size_t kOffItems = kOffBars + kBars * 8;
-constexpr size_t kOffFlags = kOffItems + 2 * sizeof(Item);
+constexpr size_t kOffFlags = kOffItems + kItems * sizeof(Item);
 constexpr size_t kSmemP = 1024 + kOffFlags + 16;
 static_assert(kSmemP <= kMaxDynSmem, "prefill kernel exceeds 227 KB of shared memory");
 
@@ -121,6 +136,21 @@ __device__ __forceinline__ void warp_umma_commit(uint32_t bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
+// mbar_wait_bounded in few instructions: the issuing warp's code competes with the softmax
+// loop for the instruction cache.
+__device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, int* err, int code, int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return;
+  const unsigned long long t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (*(volatile int*)abort_flag) return;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicOr(err, code);
+      *(volatile int*)abort_flag = 1;
+      return;
+    }
+  }
+}
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // (x, y) * (a, a) + (c, c)
@@ -130,6 +160,11 @@ __device__ __forceinline__ float2 fma2(float2 x, float a, float c) {
   asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(xx), "l"(aa), "l"(cc));
   return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   unsigned long long r;
@@ -162,8 +197,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       prefetch_tensormap(&p.tm_v);
     }
     for (int i = 0; i < kBars; ++i) {
-      const bool soft = i == kPFull || i == kPFull + 1;
-      mbar_init(bar(i), soft ? 4 : (i == kItemEmpty || i == kItemEmpty + 1 ? kSoftWarps + 1 : 1));
+      const bool soft = i == kPFull || i == kPFull + 1 || i == kSFree;  // an arrival per warp of a tile
+      mbar_init(bar(i), soft ? 4 : (i >= kItemEmpty && i < kItemEmpty + kItems ? kSoftWarps + 2 : 1));
     }
     flags[0] = 0;
     fence_barrier_init();
@@ -178,19 +213,32 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     // ------------------------------------------------------------ producer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     int base = 0, b0 = 0;  // items of the sequences before b0 (a multiple of 32) and b0
-    int kv = 0, qn = 0;
-    auto load_kv = [&](const CUtensorMap* map, const Item& it, int j, bool fix) {
+    int kv = 0, fixes = 0, qn[2] = {0, 0};
+    auto load_kv = [&](const CUtensorMap* map, int row, int kvh, int valid, bool is_v) {  // valid: the sequence's tokens from row on
       const int s = kv % kStagesP;
       mbar_wait_bounded(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
-      const uint32_t dst = ring + s * kTileP, full = bar(kKvFull + s);
-      if (lane == 0) {
-        mbar_arrive_expect_tx(fix ? bar(kVFix) : full, kTileP);
-        tma_load_4d(dst, map, fix ? bar(kVFix) : full, 0, it.k0 + j * kN, 0, it.kvh);
-      }
       ++kv;
-      return s;
+      // A V tile that ends inside another sequence's rows: their weights are 0, but 0 times a
+      // NaN or infinity there is not, so those rows are cleared before the MMA sees them.
+      const bool fix = is_v && valid < kN && row + valid < p.Tk;
+      const int full = fix ? kVFix : kKvFull + s;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(full), kTileP);
+        tma_load_4d(ring + s * kTileP, map, bar(full), 0, row, 0, kvh);
+      }
+      if (fix) {
+        mbar_wait_bounded(bar(kVFix), fixes & 1, p.err, kErrWaitFull, flags);
+        ++fixes;
+        uint4* tile = reinterpret_cast<uint4*>(smem + kOffRing + s * kTileP);
+        for (int i = valid * 8 + lane; i < kN * 8; i += 32) {
+          tile[i] = make_uint4(0, 0, 0, 0);
+          tile[i + kHalf / 16] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kKvFull + s));
+      }
     };
-    int fixes = 0;
     for (int n = 0, x = blockIdx.x;; ++n, x += gridDim.x) {
       // the sequence that holds row block x / Hkv: 32 sequences at a time
       Item it;
@@ -227,140 +275,143 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         base += __shfl_sync(0xffffffffu, end, 31);
         b0 += 32;
       }
-      const int slot = n & 1;
-      mbar_wait_bounded(bar(kItemEmpty + slot), ((n >> 1) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+      const int slot = n % kItems;
+      mbar_wait_bounded(bar(kItemEmpty + slot), ((n / kItems) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
       if (lane == 0) {
         items[slot] = it;
         mbar_arrive(bar(kItemFull + slot));
       }
       if (it.lq < 0 || *(volatile int*)flags) break;
-      const int n0 = kv_tiles(it, 0, npos), n1 = kv_tiles(it, 1, npos), nt = max(n0, n1);
-      for (int j = 0; j < nt && !*(volatile int*)flags; ++j) {
-        load_kv(&p.tm_k, it, j, false);
-        if (j == 0) {  // the queries of both tiles (the second may have none)
-          mbar_wait_bounded(bar(kQEmpty), (qn & 1) ^ 1, p.err, kErrWaitEmpty, flags);
-          ++qn;
+      const int nt[2] = {kv_tiles(it, 0, npos), kv_tiles(it, 1, npos)};
+      for (int j = 0; j < max(nt[0], nt[1]) && !*(volatile int*)flags; ++j) {
+        const int row = it.k0 + j * kN, valid = it.lk - j * kN;
+        load_kv(&p.tm_k, row, it.kvh, valid, false);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (j > 0 || nt[w] == 0) continue;
+          mbar_wait_bounded(bar(kQEmpty + w), (qn[w] & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+          ++qn[w];
           if (lane == 0) {
-            const uint32_t bytes = (uint32_t)(npos * G) * 128;
-            mbar_arrive_expect_tx(bar(kQFull), bytes * ((n0 > 0 ? 2 : 0) + (n1 > 0 ? 2 : 0)));
-            for (int w = 0; w < 2; ++w)
-              if ((w ? n1 : n0) > 0)
-                for (int c = 0; c < 2; ++c)
-                  tma_load_4d(q_smem + w * kTileP + c * kHalf, &p.tm_q, bar(kQFull), 0, it.kvh * G,
-                              it.q0 + it.p0 + w * npos, c);
+            mbar_arrive_expect_tx(bar(kQFull + w), (uint32_t)(npos * G) * 256);
+            for (int c = 0; c < 2; ++c)
+              tma_load_4d(q_smem + w * kTileP + c * kHalf, &p.tm_q, bar(kQFull + w), 0, it.kvh * G,
+                          it.q0 + it.p0 + w * npos, c);
           }
         }
-        // A V tile that ends inside another sequence's rows: their weights are 0, but 0 times
-        // a NaN or infinity there is not, so those rows are cleared before the MMA sees them.
-        const int valid = it.lk - j * kN;
-        const bool fix = valid < kN && it.k0 + it.lk < p.Tk;
-        const int s = load_kv(&p.tm_v, it, j, fix);
-        if (fix) {
-          mbar_wait_bounded(bar(kVFix), fixes & 1, p.err, kErrWaitFull, flags);
-          ++fixes;
-          uint4* tile = reinterpret_cast<uint4*>(smem + kOffRing + s * kTileP);
-          for (int i = valid * 8 + lane; i < kN * 8; i += 32) {
-            tile[i] = make_uint4(0, 0, 0, 0);
-            tile[i + kHalf / 16] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kKvFull + s));
-        }
+        load_kv(&p.tm_v, row, it.kvh, valid, true);
       }
     }
     // every stage released (all MMAs that read them done, and so every copy) before the CTA may end
     for (int i = kv > kStagesP ? kv - kStagesP : 0; i < kv; ++i)
       mbar_wait_bounded(bar(kKvEmpty + i % kStagesP), (i / kStagesP) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
-    if (qn) mbar_wait_bounded(bar(kQEmpty), (qn - 1) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
-  } else if (warp == kSoftWarps + 1) {
-    // ---------------------------------------------------------- MMA issuer
+    for (int w = 0; w < 2; ++w)
+      if (qn[w]) mbar_wait_bounded(bar(kQEmpty + w), (qn[w] - 1) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
+  } else if (warp == kSoftWarps + 1 || warp == kSoftWarps + 2) {
+    // ------------------------------------------- MMA issuers: S = Q K^T; O += P V
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    const bool pv = warp == kSoftWarps + 2;
     auto wait = [&](int b, int parity, int code) {
-      mbar_wait_bounded(bar(b), parity, p.err, code, flags);
+      wait_bar(bar(b), parity, p.err, code, flags);
       __syncwarp();
-      tc_fence_after_sync();
     };
     const uint64_t q_desc = umma_smem_desc(q_smem, 16, 1024);
-    const uint64_t k_desc = umma_smem_desc(ring, 16, 1024), v_desc = umma_smem_desc(ring, kHalf, 1024);
-    int ks = 0, kph = 0;  // ring position of the next K or V tile
-    int qn = 0, pn[2] = {0, 0};
-    auto next_stage = [&] {  // waits for the next tile, returns its stage
-      const int s = ks;
-      wait(kKvFull + s, kph, kErrWaitFull);
-      if (++ks == kStagesP) {
-        ks = 0;
-        kph ^= 1;
-      }
-      return s;
-    };
-    auto scores = [&](int w, int stage) {  // S_w = Q_w K^T
-      const uint64_t a = q_desc + (uint64_t)(w * (kTileP >> 4)), b = k_desc + (uint64_t)(stage * (kTileP >> 4));
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-        warp_umma_ss(tmem + w * 128, a + off, b + off, kIdescS, kk != 0);
-      }
-      warp_umma_commit(bar(kSFull + w));
-    };
+    const uint64_t kv_desc = pv ? umma_smem_desc(ring, kHalf, 1024) : umma_smem_desc(ring, 16, 1024);
+    int ks = pv ? 1 : 0, kph = 0;  // ring position of the next V or K tile (they alternate)
+    int tn = 0;                    // bit w: the parity that tile w's P (or Q) completes next
+    int sn = 0;
     for (int n = 0;; ++n) {
-      const int slot = n & 1;
-      mbar_wait_bounded(bar(kItemFull + slot), (n >> 1) & 1, p.err, kErrWaitFull, flags);
-      __syncwarp();
+      const int slot = n % kItems;
+      wait(kItemFull + slot, (n / kItems) & 1, kErrWaitFull);
       const Item it = items[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kItemEmpty + slot));
       __syncwarp();
       if (uniform(it.lq < 0 || *(volatile int*)flags)) break;
-      const int nt[2] = {uniform(kv_tiles(it, 0, npos)), uniform(kv_tiles(it, 1, npos))};
-      const int top = max(nt[0], nt[1]);
-      if (top == 0) continue;
-      int k_stage = next_stage();
-      wait(kQFull, qn & 1, kErrWaitFull);
-      ++qn;
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        if (nt[w] > 0) scores(w, k_stage);
-      warp_umma_commit(bar(kKvEmpty + k_stage));
-      if (top == 1) warp_umma_commit(bar(kQEmpty));
-      for (int j = 0; j < top; ++j) {
-        const int v_stage = next_stage();
-        const bool more = j + 1 < top;
-#pragma unroll
+      const int nt0 = uniform(kv_tiles(it, 0, npos)), nt1 = uniform(kv_tiles(it, 1, npos));
+      for (int j = 0; j < max(nt0, nt1); ++j) {
+        const int stage = ks;
+        wait(kKvFull + stage, kph, kErrWaitFull);
+        ks += 2;
+        if (ks >= kStagesP) {
+          ks -= kStagesP;
+          kph ^= 1;
+        }
+        const uint64_t b = kv_desc + (uint64_t)(stage * (kTileP >> 4));
+#pragma unroll 1
         for (int w = 0; w < 2; ++w) {
-          if (j < nt[w]) {  // O_w += P_w V
-            wait(kPFull + w, pn[w] & 1, kErrWaitMma);
-            ++pn[w];
-            const uint64_t b = v_desc + (uint64_t)(v_stage * (kTileP >> 4));
+          const int nt = w ? nt1 : nt0;
+          if (j >= nt) continue;
+          if (pv) {  // O_w += P_w V
+            wait(kPFull + w, tn >> w & 1, kErrWaitMma);
+            tn ^= 1 << w;
+            tc_fence_after_sync();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              warp_umma_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO,
-                           j > 0 || kk > 0);
-            if (j == nt[w] - 1) warp_umma_commit(bar(kOFull + w));
+              warp_umma_ts(tmem + kTmemO + w * 128, tmem + kTmemP + w * 64 + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO,
+                           kk > 0 || j > 0);
+            warp_umma_commit(bar(kPvDone + w));
+          } else {  // S = Q_w K^T
+            if (j == 0) {
+              wait(kQFull + w, tn >> w & 1, kErrWaitFull);
+              tn ^= 1 << w;
+            }
+            wait(kSFree, (sn & 1) ^ 1, kErrWaitMma);
+            ++sn;
+            tc_fence_after_sync();
+            const uint64_t a = q_desc + (uint64_t)(w * (kTileP >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+              warp_umma_ss(tmem, a + off, b + off, kIdescS, kk != 0);
+            }
+            warp_umma_commit(bar(kSFull + w));
+            if (j == nt - 1) warp_umma_commit(bar(kQEmpty + w));
           }
-          if (w == 0 && more) k_stage = next_stage();
-          if (j + 1 < nt[w]) scores(w, k_stage);
         }
-        warp_umma_commit(bar(kKvEmpty + v_stage));
-        if (more) {
-          warp_umma_commit(bar(kKvEmpty + k_stage));
-          if (j + 2 == top) warp_umma_commit(bar(kQEmpty));
-        }
+        warp_umma_commit(bar(kKvEmpty + stage));
       }
     }
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int w = warp >> 2, r = (warp & 3) * 32 + lane;  // tile, row of it (= TMEM lane)
-    const uint32_t s_tmem = tmem + w * 128 + ((uint32_t)((warp & 3) * 32) << 16), o_tmem = s_tmem + 256;
+    const uint32_t s_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t p_tmem = s_tmem + kTmemP + w * 64, o_tmem = s_tmem + kTmemO + w * 128;
     const int off = r / G, g = r - off * G;               // position in the tile, head of the group
     const int off0 = (warp & 3) * 32 / G;                 // of the warp's first row
     const float sl2 = p.scale_log2;
     const bool neg = sl2 < 0.f;
-    int sn = 0, on = 0;
+    int step = 0;
+    float m = kNegInfP, l = 0.f;
+    __nv_bfloat16* out = nullptr;  // this row of the item in work (null: no such row)
+    // The O of the tile's last item, complete with PV of its last step (waited for here)
+    auto pv_done = [&] {
+      if (step > 0) wait_bar(bar(kPvDone + w), (step - 1) & 1, p.err, kErrWaitMma, flags);
+      tc_fence_after_sync();
+    };
+    auto store = [&](__nv_bfloat16* to, float sum) {
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tmem_ld_x32(o_tmem + c * 32, o);
+        tmem_ld_wait_x32(o);
+        if (to) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              y[k] = sum == 0.f ? 0u : pack_bf16x2(o[i * 8 + 2 * k] * inv, o[i * 8 + 2 * k + 1] * inv);
+            *reinterpret_cast<uint4*>(to + c * 32 + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+    };
     for (int n = 0;; ++n) {
-      const int slot = n & 1;
-      mbar_wait_bounded(bar(kItemFull + slot), (n >> 1) & 1, p.err, kErrWaitFull, flags);
+      const int slot = n % kItems;
+      wait_bar(bar(kItemFull + slot), (n / kItems) & 1, p.err, kErrWaitFull, flags);
+      __syncwarp();
       const Item it = items[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kItemEmpty + slot));
@@ -370,16 +421,22 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       const int lim = min(it.lk, pos + it.lk - it.lq + 1);            // keys of this row
       const int lim0 = min(it.lk, first + off0 + it.lk - it.lq + 1);  // the least of the warp's rows
       const int nt = kv_tiles(it, w, npos);
-      float m = kNegInfP, l = 0.f;
-      for (int j = 0; j < nt; ++j) {
-        mbar_wait_bounded(bar(kSFull + w), sn & 1, p.err, kErrWaitMma, flags);
-        ++sn;
+      __nv_bfloat16* to = row_ok ? p.out + (long long)(it.q0 + pos) * p.o_st + (long long)(it.kvh * G + g) * p.o_sh : nullptr;
+      if (nt == 0 && to) {  // no key at all
+#pragma unroll
+        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(to + i * 8) = make_uint4(0, 0, 0, 0);
+      }
+      for (int j = 0; j < nt; ++j, ++step) {
+        wait_bar(bar(kSFull + w), step & 1, p.err, kErrWaitMma, flags);
         tc_fence_after_sync();
         float s[kN];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_x32(s_tmem + c * 32, s + c * 32);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_wait_x32(s + c * 32);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSFree));
         if ((j + 1) * kN > lim0) {  // some row of the warp ends inside this tile
           const float none = neg ? -kNegInfP : kNegInfP;
           const int left = lim - j * kN;
@@ -391,79 +448,61 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         for (int c = 0; c < 4; ++c) mx[c] = s[c];
         if (!neg) {
 #pragma unroll
-          for (int c = 4; c < kN; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-          mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int c = 4; c < kN; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], s[c], s[c + 1]);
+          mx[0] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         } else {
 #pragma unroll
           for (int c = 4; c < kN; ++c) mx[c & 3] = fminf(mx[c & 3], s[c]);
           mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
         }
         const float xm = mx[0] * sl2;
-        const bool grow = row_ok && xm > m + kSlackP;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float al = grow ? fast_exp2(m - xm) : 1.f;
-          m = grow ? xm : m;
-          l *= al;
-          if (j > 0) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float o[32];
-              tmem_ld_x32(o_tmem + c * 32, o);
-              tmem_ld_wait_x32(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= al;
-              tmem_st_x32(o_tmem + c * 32, reinterpret_cast<uint32_t*>(o));
-            }
-          }
+        const float l_old = l;
+        if (j == 0) {
+          m = kNegInfP;
+          l = 0.f;
         }
+        const bool grow = row_ok && xm > m + kSlackP;
+        const bool any = __any_sync(0xffffffffu, grow);
+        const float al = grow ? fast_exp2(m - xm) : 1.f;
+        m = grow ? xm : m;
+        l *= al;
         const float mr = m == kNegInfP ? 0.f : -m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pk[64];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float2 x = fma2(make_float2(s[h * 64 + 2 * i], s[h * 64 + 2 * i + 1]), sl2, mr);
-            x.x = fast_exp2(x.x);
-            x.y = fast_exp2(x.y);
-            sum[i & 1] = add2(sum[i & 1], x);
-            pk[i] = pack_bf16x2(x.x, x.y);
-          }
-          tmem_st_x32(s_tmem + h * 32, pk);
+        for (int i = 0; i < 64; ++i) {
+          float2 x = fma2(make_float2(s[2 * i], s[2 * i + 1]), sl2, mr);
+          x.x = fast_exp2(x.x);
+          x.y = fast_exp2(x.y);
+          sum[i & 1] = add2(sum[i & 1], x);
+          pk[i] = pack_bf16x2(x.x, x.y);
         }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        pv_done();
+        if (j == 0) {
+          if (step > 0) store(out, l_old);
+          out = to;
+        } else if (any) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            tmem_ld_x32(o_tmem + c * 32, o);
+            tmem_ld_wait_x32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= al;
+            tmem_st_x32(o_tmem + c * 32, reinterpret_cast<uint32_t*>(o));
+          }
+        }
+        tmem_st_x32(p_tmem, pk);
+        tmem_st_x32(p_tmem + 32, pk + 32);
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kPFull + w));
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      }
-      __nv_bfloat16* out = p.out + (long long)(it.q0 + pos) * p.o_st + (long long)(it.kvh * G + g) * p.o_sh;
-      if (nt > 0) {
-        mbar_wait_bounded(bar(kOFull + w), on & 1, p.err, kErrWaitMma, flags);
-        ++on;
-        tc_fence_after_sync();
-        const float inv = 1.f / l;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          tmem_ld_x32(o_tmem + c * 32, o);
-          tmem_ld_wait_x32(o);
-          if (row_ok) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t y[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                y[k] = l == 0.f ? 0u : pack_bf16x2(o[i * 8 + 2 * k] * inv, o[i * 8 + 2 * k + 1] * inv);
-              *reinterpret_cast<uint4*>(out + c * 32 + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          }
-        }
-      } else if (row_ok) {  // no key at all
-#pragma unroll
-        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(out + i * 8) = make_uint4(0, 0, 0, 0);
       }
     }
+    pv_done();
+    if (step > 0) store(out, l);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
   }
