@@ -156,6 +156,13 @@ __device__ __forceinline__ uint32_t mask_tokens(uint32_t v, int tok, int valid) 
   return v & (lo | hi);
 }
 
+// Byte-permute selector for a pair of tokens (tok in the low half of the word, tok + 1 in the
+// high half, two dims each): their first dims, then their second ones; zeros (byte 4) for a
+// token at or past `valid`.
+__device__ __forceinline__ uint32_t pair_select(int tok, int valid) {
+  return (tok < valid ? 0x0100u : 0x0404u) | (tok + 1 < valid ? 0x3020u : 0x4040u);
+}
+
 // ---------------------------------------------------------------- fused step
 // Phase B of the fused step projects the attention output X [B][K] with W_o [K][N]
 // on tcgen05: y^T[n][b] = W_o^T[n][k] . X^T[k][b] (swap-AB: M = 128 hidden columns,
@@ -418,15 +425,15 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
   prefetch_tensormap(&p.tm_table);
   if (KV8) prefetch_tensormap(&p.tm_scales);
   const uint64_t kv_policy = l2_policy_evict_first();
-  // Two producers (one per consumer group) share the work: this one issues the tiles whose
-  // index in the range has parity `role`, i.e. the stages of group `role` and the block-id
-  // ring rows of the same parity (S and PF are even), and walks the same cursor to skip the
-  // others.
-  static_assert(S % 2 == 0 && PF % 2 == 0, "stages and id rows split by parity");
+  // The producers (two: one per consumer group; or four) share the work: this one issues the
+  // tiles whose index in the range is `role` modulo their number, i.e. the stages and the
+  // block-id ring rows of the same residue, and walks the same cursor to skip the others.
+  constexpr int NP = attn_producers(true, false, false, KV8);
+  static_assert(S % NP == 0 && PF % NP == 0, "stages and id rows split by residue");
   Cursor ca = c_start;  // the tile whose ids were fetched last
   for (int k = 0; k < PF && start + k < end; ++k) {
     if (k > 0) cursor_next(ca, prefix, B, Hkv);
-    if ((k & 1) == role) fetch(ca, k);
+    if (k % NP == role) fetch(ca, k);
   }
   Cursor c = c_start;
   long long seg0 = start;
@@ -436,7 +443,7 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
       cursor_next(c, prefix, B, Hkv);
       if (c.j == 0) seg0 = x;
     }
-    if ((it & 1) != role) {  // the other producer's tile: keep the id cursor in step
+    if (it % NP != role) {  // another producer's tile: keep the id cursor in step
       if (x + PF < end) cursor_next(ca, prefix, B, Hkv);
       continue;
     }
@@ -457,16 +464,14 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
     for (int s = 0; s < kMaxSub; ++s) blk[s] = idr[s];  // within the row; checked where used
     const uint32_t fb = full_bar(stage);
     const uint32_t kdst = ring + stage * kStageBytes;
+    bool bad = false;  // an id outside the pool
     mbar_wait_bounded(empty_bar(stage), ((it / S) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
     mbar_arrive_expect_tx(fb, n_load * (2 * sub_bytes + (KV8 ? 8u << lsub : 0u)) + (with_q ? G * DIM * 2 : 0));
 #pragma unroll
     for (int s = 0; s < kMaxSub; ++s) {
       if (s >= n_load) break;
-      int bk = blk[s];
-      if ((unsigned)bk >= nblk) {
-        atomicOr(p.err, kErrBlockTable);
-        bk = (int)nblk;
-      }
+      const int bk = (int)min((unsigned)blk[s], nblk);
+      bad |= (unsigned)bk == nblk;
       // one copy per tensor: box s = all D/64 dim boxes of its rows ([box][dim box][rows])
       const uint32_t off = (uint32_t)(s * kTokenBytes) << lsub;
       tma_load_5d_hint(kdst + off, &p.tm_k, fb, 0, row, 0, c.kvh, bk, kv_policy);
@@ -480,6 +485,7 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
       const __nv_bfloat16* qsrc = p.q + (long long)c.b * p.q_sb + (long long)(c.kvh * G) * p.q_sh;
       for (int h = 0; h < G; ++h) bulk_load(qdst + h * kQRow, qsrc + (long long)h * p.q_sh, DIM * 2, fb);
     }
+    if (bad) atomicOr(p.err, kErrBlockTable);
     // ids of tile x + PF into the row this tile has just read. The row's reads have
     // completed: their values are operands of the copies issued above, which precede
     // this refill in program order. (A proxy fence here would also wait for the copies
@@ -491,13 +497,13 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
   }
   // do not leave with copies in flight (every id row fetched was waited for above)
   for (int k = it > S ? it - S : 0; k < it; ++k)
-    if ((k & 1) == role) mbar_wait_bounded(full_bar(k % S), (k / S) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
+    if (k % NP == role) mbar_wait_bounded(full_bar(k % S), (k / S) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
 }
 
 template <int NB, bool SCORES, int S, int NPAD, int DIM, bool PAGED = false, bool KV8 = false>
-__global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, SCORES)), 1)
+__global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, SCORES, KV8)), 1)
     attn_decode_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kProducers = attn_producers(PAGED, NPAD > 0, SCORES);
+  constexpr int kProducers = attn_producers(PAGED, NPAD > 0, SCORES, KV8);
   constexpr int kThreads = attn_threads(kProducers);
   constexpr bool kFused = NPAD > 0;
   constexpr bool kWide = DIM == kHeadDimWide;
@@ -950,8 +956,9 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
                 ldsm_x4(kbase + row * 128 + ((chunk ^ (lane & 7)) << 4), m[0], m[1], m[2], m[3]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const uint32_t a[4] = {e4m3x2_to_f16x2(m[2 * h]), e4m3x2_to_f16x2(m[2 * h + 1]),
-                                         e4m3x2_to_f16x2(m[2 * h] >> 16), e4m3x2_to_f16x2(m[2 * h + 1] >> 16)};
+                  uint32_t a[4];
+                  e4m3x4_to_f16x4(m[2 * h], a[0], a[2]);
+                  e4m3x4_to_f16x4(m[2 * h + 1], a[1], a[3]);
 #pragma unroll
                   for (int nb = 0; nb < NB; ++nb) {
                     if (h) mma_f16_16816(so[nb], a, qf[nb][2 * kk + h][0], qf[nb][2 * kk + h][1]);
@@ -1063,6 +1070,9 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
               // are 0 too), with no branch on the count in the hot loop (measured 28.1 -> 27.5 us
               // for the batch-8 fp8 attention)
               const int vwh = vw - 16 * hh;
+              // the permute itself puts zeros in place of tokens past the sequence (which may hold
+              // anything; P is 0 there): byte 4 is the first of its zero operand
+              const uint32_t sel_lo = pair_select(2 * t, vwh), sel_hi = pair_select(2 * t + 8, vwh);
               const int row = tb + 16 * hh + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
               for (int mp = 0; mp < 4; ++mp) {
@@ -1071,12 +1081,9 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
                 ldsm_x4_trans(vbase + row * 128 + ((chunk ^ (lane & 7)) << 4), m[0], m[1], m[2], m[3]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  uint32_t lo = m[2 * h], hi = m[2 * h + 1];  // tokens 2t, 2t+1 and 2t+8, 2t+9
-                  lo = mask_tokens(lo, 2 * t, vwh);  // rows past the sequence may hold anything;
-                  hi = mask_tokens(hi, 2 * t + 8, vwh);  // P is 0 there
-                  const uint32_t pl = __byte_perm(lo, 0, 0x3120), ph = __byte_perm(hi, 0, 0x3120);
-                  const uint32_t a[4] = {e4m3x2_to_f16x2(pl), e4m3x2_to_f16x2(pl >> 16), e4m3x2_to_f16x2(ph),
-                                         e4m3x2_to_f16x2(ph >> 16)};
+                  uint32_t a[4];  // from tokens 2t, 2t+1 and 2t+8, 2t+9
+                  e4m3x4_to_f16x4(__byte_perm(m[2 * h], 0, sel_lo), a[0], a[1]);
+                  e4m3x4_to_f16x4(__byte_perm(m[2 * h + 1], 0, sel_hi), a[2], a[3]);
 #pragma unroll
                   for (int nb = 0; nb < NB; ++nb) mma_f16_16816(o[2 * mp + h][nb], a, pb[hh][nb][0], pb[hh][nb][1]);
                 }
@@ -1491,7 +1498,7 @@ cudaError_t launch_one(const AttnParams& p, int grid, cudaStream_t stream) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(attn_threads(attn_producers(PAGED, NPAD > 0, SCORES)));
+  cfg.blockDim = dim3(attn_threads(attn_producers(PAGED, NPAD > 0, SCORES, KV8)));
   cfg.dynamicSmemBytes = PAGED && KV8 ? AttnSmem(NB, p.B, S, DIM).total_scaled(p.cluster > 1)
                                       : attn_smem_bytes(p.B, NB, S, DIM, kStageBytes, p.cluster > 1);
   cfg.stream = stream;

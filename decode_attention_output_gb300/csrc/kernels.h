@@ -25,8 +25,10 @@ constexpr int kConsumerThreads = kGroups * kGroupWarps * 32;
 // its group's stages) for a paged cache, where small blocks mean several copies per tile and
 // one lane's issue rate set the pace; for a contiguous cache when kContigTwoProducers.
 constexpr bool kContigTwoProducers = true;
-__host__ __device__ constexpr int attn_producers(bool paged, bool fused, bool scores) {
-  return paged || (kContigTwoProducers && !fused && !scores) ? 2 : 1;
+// A paged fp8 cache has more and smaller copies (a third one per box for the scales, 2 KB of K
+// in a block of 16): four.
+__host__ __device__ constexpr int attn_producers(bool paged, bool fused, bool scores, bool kv8 = false) {
+  return paged && kv8 ? 4 : paged || (kContigTwoProducers && !fused && !scores) ? 2 : 1;
 }
 __host__ __device__ constexpr int attn_threads(int producers) { return kConsumerThreads + 32 * producers; }
 constexpr int kMaxStages = 6;                  // even stage counts: stage s always belongs to group s % 2
