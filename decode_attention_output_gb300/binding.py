@@ -3,13 +3,17 @@
 Argument marshalling only: each function turns ``torch.Tensor`` arguments into
 ``da_tensor_t`` descriptors (data pointer, dtype, shape, strides in elements),
 passes the current CUDA stream, and raises :class:`DecodeAttnError` on a
-nonzero status. Every step of the computation runs in the library's kernels.
+nonzero status. The entry points that take tensors go through ``_da_dispatch``
+(csrc/dispatch.cpp), which reads the tensors in C++; the others through ctypes.
+Every step of the computation runs in the library's kernels.
 The library must have been built (``decode_attention_output_gb300.build``);
 there is no fallback of any kind.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 import threading
@@ -41,6 +45,7 @@ class DecodeAttnError(RuntimeError):
 
 
 _lib = None
+_call = None  # _da_dispatch.call(address, stream, n, tensors ..., floats ...) -> status
 _lock = threading.Lock()
 
 
@@ -74,6 +79,7 @@ def load_library(path: str) -> ctypes.CDLL:
     lib.decode_attn_release.restype = None
     lib.decode_attn_status_str.argtypes = [ctypes.c_int]
     lib.decode_attn_status_str.restype = ctypes.c_char_p
+    lib.addr = {name: ctypes.cast(getattr(lib, name), vp).value for name in EXPORTS}
     for name in EXPORTS:
         if name not in ("decode_attn_release", "decode_attn_status_str"):
             getattr(lib, name).restype = ctypes.c_int
@@ -82,18 +88,32 @@ def load_library(path: str) -> ctypes.CDLL:
 
 def load(path: str | None = None) -> ctypes.CDLL:
     """Loads the library (once). Fails loudly if it has not been built."""
-    global _lib
+    global _lib, _call
     with _lock:
         if _lib is None:
+            if _call is None:
+                _call = _load_dispatch()
             _lib = load_library(path or _build.lib_path())
     return _lib
+
+
+def _load_dispatch():
+    path = _build.dispatch_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: run decode_attention_output_gb300.build.build() first")
+    loader = importlib.machinery.ExtensionFileLoader("_da_dispatch", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_da_dispatch", loader))
+    loader.exec_module(module)
+    return module.call
 
 
 def use_library(lib: ctypes.CDLL | None) -> ctypes.CDLL | None:
     """Makes ``lib`` (from :func:`load_library`) the library every entry point below calls
     and returns the previous one; the tests use it to run the bounds-checked build."""
-    global _lib
+    global _lib, _call
     with _lock:
+        if _call is None:
+            _call = _load_dispatch()
         prev, _lib = _lib, lib
     return prev
 
@@ -106,9 +126,7 @@ def describe(t: torch.Tensor | None) -> da_tensor_t | None:
 
 
 # da_tensor_t as bytes: data pointer, dtype, ndim, shape[4], stride[4] (little endian,
-# no padding: the C struct has none either). Packing the fields in one call costs a
-# third of filling a ctypes structure field by field, and the calls below are made
-# once per tensor per step.
+# no padding: the C struct has none either).
 _DESC = struct.Struct("<Qii4q4q")
 _PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
 assert _DESC.size == ctypes.sizeof(da_tensor_t)
@@ -124,11 +142,6 @@ def _pack(t: torch.Tensor) -> bytes:
         raise ValueError("at most 4 dimensions")
     pad = _PAD[n]
     return _DESC.pack(t.data_ptr() if t.numel() else 0, code, n, *shape, *pad, *t.stride(), *pad)
-
-
-def _ref(t):
-    """Argument for a `const da_tensor_t*` parameter: packed bytes, or NULL for None."""
-    return None if t is None else _pack(t)
 
 
 # The raw handle of the current stream without building a torch.cuda.Stream object
@@ -158,16 +171,16 @@ def status_str(code: int) -> str:
 def decode_attn_fwd(q, k_cache, v_cache, seq_lens, o_weight, out, scale: float, stream=None) -> torch.Tensor:
     """out[B, N] = (softmax(scale * q K^T) V)_flat . o_weight; returns ``out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_cache, v_cache, seq_lens, o_weight, out)]
-    _check("decode_attn_fwd", lib.decode_attn_fwd(*ds, float(scale), _stream(stream)))
+    _check("decode_attn_fwd",
+           _call(lib.addr["decode_attn_fwd"], _stream(stream), 6, q, k_cache, v_cache, seq_lens, o_weight, out, scale))
     return out
 
 
 def decode_attn_only(q, k_cache, v_cache, seq_lens, attn_out, scale: float, stream=None) -> torch.Tensor:
     """attn_out[B, Hq, D] = softmax(scale * q K^T) V (bf16); returns ``attn_out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_cache, v_cache, seq_lens, attn_out)]
-    _check("decode_attn_only", lib.decode_attn_only(*ds, float(scale), _stream(stream)))
+    _check("decode_attn_only",
+           _call(lib.addr["decode_attn_only"], _stream(stream), 5, q, k_cache, v_cache, seq_lens, attn_out, scale))
     return attn_out
 
 
@@ -178,9 +191,9 @@ def decode_attn_only_noalloc(q, k_cache, v_cache, seq_lens, attn_out, scale: flo
     fixed 8 MiB scratch array inside the library; calls that overlap on the GPU race
     on it. Raises DecodeAttnError (DA_ERR_SCRATCH) when a call needs more scratch."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_cache, v_cache, seq_lens, attn_out)]
     _check("decode_attn_only_noalloc",
-           lib.decode_attn_only_noalloc(*ds, float(scale), _stream(stream)))
+           _call(lib.addr["decode_attn_only_noalloc"], _stream(stream), 5,
+                 q, k_cache, v_cache, seq_lens, attn_out, scale))
     return attn_out
 
 
@@ -189,8 +202,9 @@ def decode_attn_fwd_paged(q, k_pages, v_pages, block_table, seq_lens, o_weight, 
     """decode_attn_fwd over a paged cache: k_pages / v_pages [num_blocks, Hkv, block_size, D],
     block_table [B, max_blocks] int32; returns ``out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_pages, v_pages, block_table, seq_lens, o_weight, out)]
-    _check("decode_attn_fwd_paged", lib.decode_attn_fwd_paged(*ds, float(scale), _stream(stream)))
+    _check("decode_attn_fwd_paged",
+           _call(lib.addr["decode_attn_fwd_paged"], _stream(stream), 7,
+                 q, k_pages, v_pages, block_table, seq_lens, o_weight, out, scale))
     return out
 
 
@@ -198,9 +212,9 @@ def decode_attn_only_paged(q, k_pages, v_pages, block_table, seq_lens, attn_out,
                            stream=None) -> torch.Tensor:
     """decode_attn_only over a paged cache (see decode_attn_fwd_paged); returns ``attn_out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_pages, v_pages, block_table, seq_lens, attn_out)]
     _check("decode_attn_only_paged",
-           lib.decode_attn_only_paged(*ds, float(scale), _stream(stream)))
+           _call(lib.addr["decode_attn_only_paged"], _stream(stream), 6,
+                 q, k_pages, v_pages, block_table, seq_lens, attn_out, scale))
     return attn_out
 
 
@@ -209,9 +223,9 @@ def decode_attn_fwd_fp8(q, k_cache, v_cache, seq_lens, o_weight, out, scale: flo
     """decode_attn_fwd over an fp8 cache: k_cache / v_cache torch.float8_e4m3fn, the keys
     and values being k_cache * k_scale and v_cache * v_scale; returns ``out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_cache, v_cache, seq_lens, o_weight, out)]
-    _check("decode_attn_fwd_fp8", lib.decode_attn_fwd_fp8(*ds, float(scale), float(k_scale),
-                                                          float(v_scale), _stream(stream)))
+    _check("decode_attn_fwd_fp8",
+           _call(lib.addr["decode_attn_fwd_fp8"], _stream(stream), 6,
+                 q, k_cache, v_cache, seq_lens, o_weight, out, scale, k_scale, v_scale))
     return out
 
 
@@ -219,9 +233,9 @@ def decode_attn_only_fp8(q, k_cache, v_cache, seq_lens, attn_out, scale: float, 
                          stream=None) -> torch.Tensor:
     """decode_attn_only over an fp8 cache (see decode_attn_fwd_fp8); returns ``attn_out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_cache, v_cache, seq_lens, attn_out)]
-    _check("decode_attn_only_fp8", lib.decode_attn_only_fp8(*ds, float(scale), float(k_scale),
-                                                            float(v_scale), _stream(stream)))
+    _check("decode_attn_only_fp8",
+           _call(lib.addr["decode_attn_only_fp8"], _stream(stream), 5,
+                 q, k_cache, v_cache, seq_lens, attn_out, scale, k_scale, v_scale))
     return attn_out
 
 
@@ -231,8 +245,9 @@ def decode_attn_fwd_paged_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_l
     torch.float8_e4m3fn, kv_scales [num_blocks, Hkv, 2, block_size] fp32, the keys and values being code * scale
     of their token and head (see decode_attn_cache_write); returns ``out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_pages, v_pages, kv_scales, block_table, seq_lens, o_weight, out)]
-    _check("decode_attn_fwd_paged_fp8", lib.decode_attn_fwd_paged_fp8(*ds, float(scale), _stream(stream)))
+    _check("decode_attn_fwd_paged_fp8",
+           _call(lib.addr["decode_attn_fwd_paged_fp8"], _stream(stream), 8,
+                 q, k_pages, v_pages, kv_scales, block_table, seq_lens, o_weight, out, scale))
     return out
 
 
@@ -240,8 +255,9 @@ def decode_attn_only_paged_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_
                                stream=None) -> torch.Tensor:
     """decode_attn_only_paged over a paged fp8 cache (see decode_attn_fwd_paged_fp8); returns ``attn_out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_pages, v_pages, kv_scales, block_table, seq_lens, attn_out)]
-    _check("decode_attn_only_paged_fp8", lib.decode_attn_only_paged_fp8(*ds, float(scale), _stream(stream)))
+    _check("decode_attn_only_paged_fp8",
+           _call(lib.addr["decode_attn_only_paged_fp8"], _stream(stream), 7,
+                 q, k_pages, v_pages, kv_scales, block_table, seq_lens, attn_out, scale))
     return attn_out
 
 
@@ -249,8 +265,8 @@ def decode_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, out, scale: float, 
     """Causal attention over packed prompts: q and out [Tq, Hq, 128], k and v [Tk, Hkv, 128], offsets [B + 1]
     int32 of the sequences in each; the queries of a sequence are its last tokens. Returns ``out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k, v, cu_seqlens_q, cu_seqlens_k, out)]
-    _check("decode_attn_prefill", lib.decode_attn_prefill(*ds, float(scale), _stream(stream)))
+    _check("decode_attn_prefill",
+           _call(lib.addr["decode_attn_prefill"], _stream(stream), 6, q, k, v, cu_seqlens_q, cu_seqlens_k, out, scale))
     return out
 
 
@@ -260,32 +276,33 @@ def decode_attn_cache_write(k, v, cu_seqlens, block_table, seq_lens, k_pages, v_
     the seq_lens[b] of sequence b) into the pages that block_table names: bf16 pools take copies, e4m3 pools codes
     with a power-of-two scale per token and head in kv_scales [num_blocks, Hkv, 2, block_size] fp32."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (k, v, cu_seqlens, block_table, seq_lens, k_pages, v_pages, kv_scales)]
-    _check("decode_attn_cache_write", lib.decode_attn_cache_write(*ds, _stream(stream)))
+    _check("decode_attn_cache_write",
+           _call(lib.addr["decode_attn_cache_write"], _stream(stream), 8,
+                 k, v, cu_seqlens, block_table, seq_lens, k_pages, v_pages, kv_scales))
 
 
 def decode_attn_cache_read(k_pages, v_pages, kv_scales, block_table, cu_seqlens, k_out, v_out, stream=None):
     """The first tokens of each sequence out of a paged cache (kv_scales None: bf16 pools) into the packed
     k_out and v_out [T, Hkv, D] bf16; returns ``(k_out, v_out)``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (k_pages, v_pages, kv_scales, block_table, cu_seqlens, k_out, v_out)]
-    _check("decode_attn_cache_read", lib.decode_attn_cache_read(*ds, _stream(stream)))
+    _check("decode_attn_cache_read",
+           _call(lib.addr["decode_attn_cache_read"], _stream(stream), 7,
+                 k_pages, v_pages, kv_scales, block_table, cu_seqlens, k_out, v_out))
     return k_out, v_out
 
 
 def decode_attn_scores(q, k_cache, seq_lens, scores, stream=None) -> torch.Tensor:
     """scores[B, Hq, Lcap] (fp32) = q K^T for t < seq_lens[b]; returns ``scores``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (q, k_cache, seq_lens, scores)]
-    _check("decode_attn_scores", lib.decode_attn_scores(*ds, _stream(stream)))
+    _check("decode_attn_scores",
+           _call(lib.addr["decode_attn_scores"], _stream(stream), 4, q, k_cache, seq_lens, scores))
     return scores
 
 
 def decode_attn_oproj(attn_flat, o_weight, out, stream=None) -> torch.Tensor:
     """out[B, N] = attn_flat[B, K] . o_weight[K, N] (bf16); returns ``out``."""
     lib = _lib or load()  # the lock only until the library is loaded
-    ds = [_ref(x) for x in (attn_flat, o_weight, out)]
-    _check("decode_attn_oproj", lib.decode_attn_oproj(*ds, _stream(stream)))
+    _check("decode_attn_oproj", _call(lib.addr["decode_attn_oproj"], _stream(stream), 3, attn_flat, o_weight, out))
     return out
 
 

@@ -1,4 +1,5 @@
-"""Builds libdecode_attn.so in-tree for sm_103a with nvcc (no cmake, no torch).
+"""Builds libdecode_attn.so in-tree for sm_103a with nvcc (no cmake, no torch), and beside it
+``_lib/_da_dispatch.so``, the binding's caller (csrc/dispatch.cpp, g++ with torch's headers).
 
 Each .cu file compiles in its own nvcc process (in parallel), then one link
 step produces ``_lib/libdecode_attn.so``. A stamp of the sources, headers and
@@ -16,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +31,7 @@ CHECKED_FLAGS = ["-DDA_BOUNDS_CHECK"]
 SOURCES = ["api.cu", "attn_decode.cu", "attn_decode_d256.cu", "attn_decode_paged.cu", "attn_decode_fp8.cu",
            "attn_decode_paged_fp8.cu", "kv_cache.cu", "prefill.cu",
            "oproj_gemv.cu", "oproj_umma.cu", "oproj_onchip.cu"]
+DISPATCH_SOURCE, DISPATCH_NAME = "dispatch.cpp", "_da_dispatch.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -47,15 +50,49 @@ def lib_path(checked: bool = False) -> str:
     return os.path.join(LIB_DIR, LIB_NAME)
 
 
+def dispatch_path() -> str:
+    return os.path.join(LIB_DIR, DISPATCH_NAME)
+
+
 def _stamp(extra=()) -> str:
     h = hashlib.sha1()
     for d in (CSRC, INCLUDE):
         for name in sorted(os.listdir(d)):
-            if name.endswith((".cu", ".cuh", ".h")):
+            if name.endswith((".cu", ".cuh", ".h", ".cpp")):
                 with open(os.path.join(d, name), "rb") as f:
                     h.update(name.encode() + f.read())
     h.update(" ".join(ARCH + NVCC_FLAGS + list(extra)).encode())
     return h.hexdigest()
+
+
+def build_dispatch(force: bool = False) -> str:
+    """Compile the binding's caller for this Python and torch; returns its path."""
+    import torch
+
+    out = dispatch_path()
+    base = os.path.dirname(torch.__file__)
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
+           "-isystem", os.path.join(base, "include"), "-isystem", os.path.join(base, "include/torch/csrc/api/include"),
+           "-isystem", sysconfig.get_paths()["include"], f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           os.path.join(CSRC, DISPATCH_SOURCE), f"-L{os.path.join(base, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    h = hashlib.sha1(" ".join([*cmd, sys.version, torch.__version__]).encode())
+    for path in (os.path.join(CSRC, DISPATCH_SOURCE), os.path.join(INCLUDE, "decode_attn.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    stamp, stamp_file = h.hexdigest(), out + ".stamp.txt"
+    os.makedirs(LIB_DIR, exist_ok=True)
+    if not force and os.path.exists(out) and os.path.exists(stamp_file):
+        with open(stamp_file) as f:
+            if f.read().strip() == stamp:
+                return out
+    tmp = out + f".tmp{os.getpid()}"
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {DISPATCH_SOURCE}:\n{r.stderr}")
+    os.replace(tmp, out)
+    with open(stamp_file, "w") as f:
+        f.write(stamp)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: bool = False) -> str:
@@ -71,6 +108,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
     if not force and os.path.exists(out) and os.path.exists(stamp_file):
         with open(stamp_file) as f:
             if f.read().strip() == stamp:
+                build_dispatch()
                 return out
     exe = nvcc()
 
@@ -86,8 +124,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        caller = ex.submit(build_dispatch, force)
         objs = list(ex.map(compile_one, SOURCES))
+        caller.result()
     tmp = out + f".tmp{os.getpid()}"
     cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
