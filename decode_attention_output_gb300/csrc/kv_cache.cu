@@ -16,10 +16,12 @@
 //
 // Read: the first cu[b + 1] - cu[b] tokens of each sequence, code * scale, packed to bf16.
 //
-// Bound by bytes (T * Hkv * 2 * (256 + 132) at D = 128). A warp takes one token and a few of
-// its heads: half a warp holds a 128-dim row (16 bytes of bf16 a lane), one half K and the
-// other V, so the maximum is four shuffles, rows leave as whole 128-byte lines and the token's
-// place (a search of cu, its block) is found once, while the rows are already on their way.
+// Bound by bytes (T * Hkv * 2 * (256 + 132) at D = 128) once the instructions are few: a warp
+// takes one token and as many as eight of its heads (a divisor of Hkv, so that no row needs a
+// test). Half a warp holds a 128-dim row (16 bytes of bf16 a lane), one half K and the other V:
+// the maximum is four shuffles of packed 16-bit maxima, rows leave as whole 128-byte lines, a
+// row's addresses are one addition from the last head's, and the token's place (a search of
+// cu, its block) is found once, while the rows are already on their way.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -60,16 +62,21 @@ __device__ __forceinline__ bool locate(const CacheParams& p, int t, int lane, in
   return !WRITE;  // such a token is not written, and reads as zeros
 }
 
-// Largest finite magnitude of eight bf16 values, as bf16 bits (order of the bits = order of
-// the magnitudes; infinities and NaN, from 0x7f80 up, count as zero).
+// Largest magnitudes of a lane's eight bf16 values, as two packed bf16 bit patterns (their
+// order is the magnitudes' order). Infinities and NaN, 0x7f80 and more, only with ALL.
+template <bool ALL>
 __device__ __forceinline__ unsigned amax_bits(const uint4& x) {
-  unsigned m = 0;
-  const unsigned w[4] = {x.x, x.y, x.z, x.w};
+  unsigned a[4] = {x.x & 0x7fff7fffu, x.y & 0x7fff7fffu, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu};
+  if (!ALL)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned a = w[i] & 0x7fff7fffu;
-    m = __vmaxu2(m, a & ~__vcmpgeu2(a, 0x7f807f80u));
-  }
+    for (int i = 0; i < 4; ++i) a[i] &= ~__vcmpgeu2(a[i], 0x7f807f80u);
+  return __vmaxu2(__vmaxu2(a[0], a[1]), __vmaxu2(a[2], a[3]));
+}
+// ... over the lanes of a row
+template <int LANES>
+__device__ __forceinline__ unsigned row_max(unsigned m) {
+#pragma unroll
+  for (int off = LANES / 2; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
   return max(m & 0xffffu, m >> 16);
 }
 
@@ -82,43 +89,51 @@ __device__ __forceinline__ unsigned e4m3x2(float lo, float hi) {
 
 template <int DIM, bool KV8, bool WRITE, int HG>
 __global__ void __launch_bounds__(kCacheWarps * 32) kv_cache_kernel(const CacheParams p) {
-  constexpr int kLanes = DIM / 8;         // lanes of a row, 8 elements each
-  constexpr int kRows = 32 / kLanes;      // rows a warp holds at once
-  constexpr int kIt = 2 * HG / kRows;     // K and V rows of HG heads
+  constexpr int kLanes = DIM / 8;      // lanes of a row, 8 elements each
+  constexpr int kPer = kLanes / 16;    // tensors a lane takes part in: K or V, or (D = 256) both
   static_assert(!KV8 || DIM == kHeadDim, "e4m3 pools: head dim 128");
   const int lane = threadIdx.x & 31, col = (lane % kLanes) * 8;
   pdl_wait_primary();
   const long long unit = (long long)blockIdx.x * kCacheWarps + (threadIdx.x >> 5);
   const int t = (int)(unit / p.head_groups), h0 = (int)(unit - (long long)t * p.head_groups) * HG;
   if (t >= p.T) return;
-  auto tensor = [&](int it) { return (it * kRows + lane / kLanes) & 1; };
-  auto head = [&](int it) { return h0 + ((it * kRows + lane / kLanes) >> 1); };
-  auto token_row = [&](int it) {
-    return (tensor(it) ? p.v + t * p.v_st + head(it) * p.v_sh : p.k + t * p.k_st + head(it) * p.k_sh) + col;
-  };
-  auto page_at = [&](int it, int block, int row) {  // element offset in the pool
-    return (tensor(it) ? block * p.vp_sb + head(it) * p.vp_sh + row * p.vp_sr
-                       : block * p.kp_sb + head(it) * p.kp_sh + row * p.kp_sr) + col;
-  };
-  auto scale_at = [&](int it, int block, int row) { return block * p.sc_sb + head(it) * p.sc_sh + tensor(it) * p.sc_st + row; };
   int block = 0, row = 0;
+  // Element offsets of this lane's share of the first head's row, and from head to head
+  const bool is_v[2] = {kPer == 1 && lane >= kLanes, true};
+  auto token_row = [&](int q) {
+    return is_v[q] ? const_cast<__nv_bfloat16*>(p.v) + t * p.v_st + h0 * p.v_sh + col
+                   : const_cast<__nv_bfloat16*>(p.k) + t * p.k_st + h0 * p.k_sh + col;
+  };
+  auto token_step = [&](int q) { return is_v[q] ? p.v_sh : p.k_sh; };
+  auto page_row = [&](int q) {
+    return is_v[q] ? block * p.vp_sb + h0 * p.vp_sh + row * p.vp_sr + col : block * p.kp_sb + h0 * p.kp_sh + row * p.kp_sr + col;
+  };
+  auto page_step = [&](int q) { return is_v[q] ? p.vp_sh : p.kp_sh; };
+  auto pool = [&](int q) { return is_v[q] ? p.v_pages : p.k_pages; };
   if (WRITE) {
-    uint4 x[kIt];
+    uint4 x[kPer][HG];
 #pragma unroll
-    for (int it = 0; it < kIt; ++it)
-      x[it] = head(it) < p.Hkv ? ldg_stream_v4(token_row(it)) : make_uint4(0, 0, 0, 0);
+    for (int q = 0; q < kPer; ++q) {
+      const __nv_bfloat16* from = token_row(q);
+      const long long step = token_step(q);
+#pragma unroll
+      for (int h = 0; h < HG; ++h, from += step) x[q][h] = ldg_stream_v4(from);
+    }
     if (!locate<true>(p, t, lane, &block, &row)) return;
+    if constexpr (KV8) {
+      uint8_t* to = static_cast<uint8_t*>(pool(0)) + page_row(0);
+      const long long step = page_step(0);
+      float* scale = p.scales + block * p.sc_sb + h0 * p.sc_sh + (is_v[0] ? p.sc_st : 0) + row;
 #pragma unroll
-    for (int it = 0; it < kIt; ++it) {
-      if constexpr (KV8) {
-        unsigned m = amax_bits(x[it]);
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      for (int h = 0; h < HG; ++h, to += step, scale += p.sc_sh) {
+        const uint4 y = x[0][h];
+        unsigned m = row_max<kLanes>(amax_bits<true>(y));
+        if (__any_sync(0xffffffffu, m >= 0x7f80u)) m = row_max<kLanes>(amax_bits<false>(y));
         // m = (1 + f / 128) 2^(E - 127); it fits 448 2^e = 1.75 2^(8 + e) with e = E - 135 when
         // f <= 96, else with one more: adding 31 carries into E exactly when f > 96
         const int e = m == 0 ? 0 : min(max((int)((m + 31u) >> 7) - 135, -124), 120);
         const float inv = __int_as_float((127 - e) << 23);
-        const unsigned w[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
+        const unsigned w[4] = {y.x, y.y, y.z, y.w};
         unsigned c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = e4m3x2(bf16lo_to_f32(w[i]) * inv, bf16hi_to_f32(w[i]) * inv);
@@ -131,60 +146,67 @@ __global__ void __launch_bounds__(kCacheWarps * 32) kv_cache_kernel(const CacheP
               if (mag > 0x77u && mag < 0x7fu) c[i] -= (mag - 0x77u) << b;
             }
         }
-        if (head(it) < p.Hkv) {
-          uint8_t* pool = static_cast<uint8_t*>(tensor(it) ? p.v_pages : p.k_pages);
-          *reinterpret_cast<uint2*>(pool + page_at(it, block, row)) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-          if (col == 0) p.scales[scale_at(it, block, row)] = __int_as_float((127 + e) << 23);
-        }
-      } else if (head(it) < p.Hkv) {
-        __nv_bfloat16* pool = static_cast<__nv_bfloat16*>(tensor(it) ? p.v_pages : p.k_pages);
-        *reinterpret_cast<uint4*>(pool + page_at(it, block, row)) = x[it];
+        *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+        if (col == 0) *scale = __int_as_float((127 + e) << 23);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(pool(q)) + page_row(q);
+        const long long step = page_step(q);
+#pragma unroll
+        for (int h = 0; h < HG; ++h, to += step) *reinterpret_cast<uint4*>(to) = x[q][h];
       }
     }
   } else {
     if (!locate<false>(p, t, lane, &block, &row)) return;
-    uint4 x[kIt];
-    float s[kIt];
+    if constexpr (KV8) {
+      uint2 x[HG];
+      float s[HG];
+      const uint8_t* from = static_cast<const uint8_t*>(pool(0)) + page_row(0);
+      const long long step = page_step(0);
+      const float* scale = p.scales + block * p.sc_sb + h0 * p.sc_sh + (is_v[0] ? p.sc_st : 0) + row;
 #pragma unroll
-    for (int it = 0; it < kIt; ++it) {
-      x[it] = make_uint4(0, 0, 0, 0);
-      s[it] = 0.f;
-      if (head(it) < p.Hkv && block >= 0) {
-        if constexpr (KV8) {
-          const uint8_t* pool = static_cast<const uint8_t*>(tensor(it) ? p.v_pages : p.k_pages);
-          const uint2 c = *reinterpret_cast<const uint2*>(pool + page_at(it, block, row));
-          x[it].x = c.x;
-          x[it].y = c.y;
-          s[it] = p.scales[scale_at(it, block, row)];
-        } else {
-          const __nv_bfloat16* pool = static_cast<const __nv_bfloat16*>(tensor(it) ? p.v_pages : p.k_pages);
-          x[it] = *reinterpret_cast<const uint4*>(pool + page_at(it, block, row));
-        }
+      for (int h = 0; h < HG; ++h, from += step, scale += p.sc_sh) {
+        x[h] = block >= 0 ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0, 0);
+        s[h] = block >= 0 ? __ldg(scale) : 0.f;
       }
-    }
+      __nv_bfloat16* to = token_row(0);
+      const long long to_step = token_step(0);
 #pragma unroll
-    for (int it = 0; it < kIt; ++it) {
-      if (KV8) {  // e4m3 -> f16 (exact) -> f32, times the scale, rounded once to bf16
-        const unsigned c[2] = {x[it].x, x[it].y};
-        unsigned o[4];
+      for (int h = 0; h < HG; ++h, to += to_step) {  // e4m3 -> f16 (exact) -> f32, times the scale, rounded once to bf16
+        uint32_t f[4], o[4];
+        e4m3x4_to_f16x4(x[h].x, f[0], f[1]);
+        e4m3x4_to_f16x4(x[h].y, f[2], f[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const unsigned h = e4m3x2_to_f16x2(c[i >> 1] >> (16 * (i & 1)));
-          o[i] = pack_bf16x2(f16lo_to_f32(h) * s[it], f16hi_to_f32(h) * s[it]);
-        }
-        x[it] = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(f16lo_to_f32(f[i]) * s[h], f16hi_to_f32(f[i]) * s[h]);
+        *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      if (head(it) < p.Hkv) *reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(token_row(it))) = x[it];
+    } else {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        uint4 x[HG];
+        const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(pool(q)) + page_row(q);
+        const long long step = page_step(q);
+#pragma unroll
+        for (int h = 0; h < HG; ++h, from += step)
+          x[h] = block >= 0 ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
+        __nv_bfloat16* to = token_row(q);
+        const long long to_step = token_step(q);
+#pragma unroll
+        for (int h = 0; h < HG; ++h, to += to_step) *reinterpret_cast<uint4*>(to) = x[h];
+      }
     }
   }
 }
 
 template <int DIM, bool KV8, bool WRITE>
 cudaError_t launch_heads(CacheParams& p, bool pdl, cudaStream_t stream) {
-  // A warp takes four heads of a token; one head where that would leave SMs without a warp
-  // (a decode step's few tokens).
-  const int hg = (long long)p.T * ((p.Hkv + 3) / 4) >= 4096 ? 4 : 1;
-  p.head_groups = (p.Hkv + hg - 1) / hg;
+  // A warp takes the most heads of a token that divide Hkv, up to eight; one where that would
+  // leave SMs without a warp (a decode step's few tokens).
+  int hg = 8;
+  while (p.Hkv % hg || (hg > 1 && (long long)p.T * (p.Hkv / hg) < 4096)) hg /= 2;
+  p.head_groups = p.Hkv / hg;
   const long long blocks = ((long long)p.T * p.head_groups + kCacheWarps - 1) / kCacheWarps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -196,8 +218,13 @@ cudaError_t launch_heads(CacheParams& p, bool pdl, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return hg == 4 ? cudaLaunchKernelEx(&cfg, kv_cache_kernel<DIM, KV8, WRITE, 4>, (const CacheParams)p)
-                 : cudaLaunchKernelEx(&cfg, kv_cache_kernel<DIM, KV8, WRITE, 1>, (const CacheParams)p);
+  const CacheParams& c = p;
+  switch (hg) {
+    case 8: return cudaLaunchKernelEx(&cfg, kv_cache_kernel<DIM, KV8, WRITE, 8>, c);
+    case 4: return cudaLaunchKernelEx(&cfg, kv_cache_kernel<DIM, KV8, WRITE, 4>, c);
+    case 2: return cudaLaunchKernelEx(&cfg, kv_cache_kernel<DIM, KV8, WRITE, 2>, c);
+    default: return cudaLaunchKernelEx(&cfg, kv_cache_kernel<DIM, KV8, WRITE, 1>, c);
+  }
 }
 
 }  // namespace
