@@ -1271,8 +1271,7 @@ int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_ten
   // the kernel masks with infinities: a scale of 0 becomes one that leaves every weight 1
   p.scale_log2 = scale * 1.4426950408889634f;
   if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;
-  const int grid = (int)std::min<int64_t>(std::max(1, sm_count()), items);
-  return launch_prefill(p, grid, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return launch_prefill(p, (int)items, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 int decode_attn_cache_write(const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cu_seqlens,

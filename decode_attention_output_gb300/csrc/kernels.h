@@ -236,7 +236,7 @@ struct PrefillParams {
   int npos;            // query positions per tile, floor(128 / G)
   float scale_log2;    // scale * log2(e), never 0
 };
-// grid = persistent CTAs, one per SM or as many as there can be work items.
+// grid = as many CTAs as there can be work items; those that run take over the others.
 cudaError_t launch_prefill(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream);
 
 // ------------------------------------------------ paged cache: writing and reading

@@ -7,7 +7,11 @@
 // Work item: 256 rows of one (sequence, KV head), as two tiles of 128: a tile's rows are
 // npos = floor(128 / G) query positions x the G heads that share the KV head, so both tiles
 // use every K and V tile that is brought in, whatever G is, and short prompts fill tiles.
-// Items are taken heaviest (last positions) first within each sequence.
+// Items are taken heaviest (last positions) first within each sequence: the grid has a CTA per
+// item, and a CTA that runs takes over the next one that has not started (cluster launch
+// control), so that items of very different length even out and set-up and pipeline carry on
+// across them (taking items blockIdx, blockIdx + gridDim, ... left 16 ragged prompts at 75 steps
+// on the longest CTA of 62 on average, 8192 tokens at 476 of 445).
 //
 //  * tcgen05.mma M = N = 128: S = Q K^T from shared memory into TMEM, then O += P V with P
 //    (bf16) in TMEM and V as the N-major B operand. TMEM, all 512 columns: one S (128), a P
@@ -58,13 +62,15 @@ enum Bar {
   kPvDone = kPFull + 2,            // per tile: its PV has completed
   kSFree = kPvDone + 2,            // the S columns have been read
   kVFix,                           // a V tile that needs clearing has landed
+  kNext,                           // the next item's index has been answered
   kItemFull, kItemEmpty = kItemFull + kItems,
   kKvFull = kItemEmpty + kItems, kKvEmpty = kKvFull + kStagesP,
   kBars = kKvEmpty + kStagesP
 };
 constexpr uint32_t kTmemP = 128, kTmemO = 256;  // columns: S, P0, P1, O0, O1
 constexpr size_t kOffItems = kOffBars + kBars * 8;
-constexpr size_t kOffFlags = kOffItems + kItems * sizeof(Item);
+constexpr size_t kOffNext = (kOffItems + kItems * sizeof(Item) + 15) & ~(size_t)15;  // answer to the request for the next item
+constexpr size_t kOffFlags = kOffNext + 16;
 constexpr size_t kSmemP = 1024 + kOffFlags + 16;
 static_assert(kSmemP <= kMaxDynSmem, "prefill kernel exceeds 227 KB of shared memory");
 
@@ -150,6 +156,27 @@ __device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, int* err
       return;
     }
   }
+}
+// Asks for a CTA of the grid that has not started, to run it here; the 16-byte answer lands at
+// `dst` and completes on `bar`.
+__device__ __forceinline__ void request_next_cta(uint32_t dst, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+               "r"(bar)
+               : "memory");
+}
+// The answer: that CTA's blockIdx.x, or -1: none is left (the request must not be repeated).
+__device__ __forceinline__ int next_cta(uint32_t src) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=&r"(x)
+      : "r"(src)
+      : "memory");
+  return x;
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -239,13 +266,30 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         if (lane == 0) mbar_arrive(bar(kKvFull + s));
       }
     };
-    for (int n = 0, x = blockIdx.x;; ++n, x += gridDim.x) {
+    const uint32_t next_smem = smem_u32(smem + kOffNext);
+    int x = blockIdx.x, n = 0, asked = 0;
+    auto ask = [&] {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(kNext), 16);
+        request_next_cta(next_smem, bar(kNext));
+      }
+    };
+    auto answer = [&] {
+      mbar_wait_bounded(bar(kNext), asked & 1, p.err, kErrWaitFull, flags);
+      ++asked;
+      x = next_cta(next_smem);
+      fence_proxy_async_smem();  // the answer has been read before the next one is written
+      __syncwarp();
+    };
+    while (true) {
+      if (x >= 0) ask();
       // the sequence that holds row block x / Hkv: 32 sequences at a time
       Item it;
-      const int mb = x / p.Hkv;
-      it.kvh = x - mb * p.Hkv;
+      const int mb = x < 0 ? 0x7fffffff : x / p.Hkv;  // (none left: past every sequence)
+      it.kvh = x < 0 ? 0 : x - mb * p.Hkv;
       it.lq = -1;
       it.lk = it.q0 = it.k0 = it.p0 = 0;
+      if (mb < base) base = b0 = 0;
       while (b0 < p.B) {
         const int b = b0 + lane;
         int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
@@ -275,6 +319,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         base += __shfl_sync(0xffffffffu, end, 31);
         b0 += 32;
       }
+      if (x >= 0 && it.lq < 0) {  // the grid has CTAs for the most items there can be
+        answer();
+        if (*(volatile int*)flags) break;
+        continue;
+      }
       const int slot = n % kItems;
       mbar_wait_bounded(bar(kItemEmpty + slot), ((n / kItems) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
       if (lane == 0) {
@@ -300,7 +349,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         }
         load_kv(&p.tm_v, row, it.kvh, valid, true);
       }
+      if (*(volatile int*)flags) break;
+      answer();
+      ++n;
     }
+    if (*(volatile int*)flags)  // given up with an answer on its way
+      mbar_wait_bounded(bar(kNext), asked & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
     // every stage released (all MMAs that read them done, and so every copy) before the CTA may end
     for (int i = kv > kStagesP ? kv - kStagesP : 0; i < kv; ++i)
       mbar_wait_bounded(bar(kKvEmpty + i % kStagesP), (i / kStagesP) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
