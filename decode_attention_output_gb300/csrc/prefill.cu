@@ -178,6 +178,12 @@ __device__ __forceinline__ int next_cta(uint32_t src) {
       : "memory");
   return x;
 }
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // (x, y) * (a, a) + (c, c)
@@ -281,9 +287,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       fence_proxy_async_smem();  // the answer has been read before the next one is written
       __syncwarp();
     };
-    while (true) {
-      if (x >= 0) ask();
-      // the sequence that holds row block x / Hkv: 32 sequences at a time
+    // Item x: the sequence that holds row block x / Hkv, looked for 32 sequences at a time.
+    // lq < 0: none (x < 0, or past the last: the grid has CTAs for the most there can be).
+    auto find = [&] {
       Item it;
       const int mb = x < 0 ? 0x7fffffff : x / p.Hkv;  // (none left: past every sequence)
       it.kvh = x < 0 ? 0 : x - mb * p.Hkv;
@@ -319,10 +325,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         base += __shfl_sync(0xffffffffu, end, 31);
         b0 += 32;
       }
-      if (x >= 0 && it.lq < 0) {  // the grid has CTAs for the most items there can be
+      return it;
+    };
+    Item it = find();
+    while (true) {
+      while (x >= 0 && it.lq < 0 && !*(volatile int*)flags) {
+        ask();
         answer();
-        if (*(volatile int*)flags) break;
-        continue;
+        it = find();
       }
       const int slot = n % kItems;
       mbar_wait_bounded(bar(kItemEmpty + slot), ((n / kItems) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
@@ -331,10 +341,17 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         mbar_arrive(bar(kItemFull + slot));
       }
       if (it.lq < 0 || *(volatile int*)flags) break;
-      const int nt[2] = {kv_tiles(it, 0, npos), kv_tiles(it, 1, npos)};
-      for (int j = 0; j < max(nt[0], nt[1]) && !*(volatile int*)flags; ++j) {
+      ++n;
+      // The queries of both tiles, which come into shared memory when the item before has had
+      // its last S computed, are on their way into L2 until then.
+      if (lane < 4) tma_prefetch_4d(&p.tm_q, 0, it.kvh * G, it.q0 + it.p0 + (lane >> 1) * npos, lane & 1);
+      const int nt[2] = {kv_tiles(it, 0, npos), kv_tiles(it, 1, npos)}, top = max(nt[0], nt[1]);
+      if (top == 0) ask();
+      for (int j = 0; j < top && !*(volatile int*)flags; ++j) {
+        if (j == max(0, top - 3)) ask();  // late, so that no item waits behind a long one
         const int row = it.k0 + j * kN, valid = it.lk - j * kN;
         load_kv(&p.tm_k, row, it.kvh, valid, false);
+        load_kv(&p.tm_v, row, it.kvh, valid, true);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (j > 0 || nt[w] == 0) continue;
@@ -347,11 +364,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
                           it.q0 + it.p0 + w * npos, c);
           }
         }
-        load_kv(&p.tm_v, row, it.kvh, valid, true);
       }
       if (*(volatile int*)flags) break;
       answer();
-      ++n;
+      it = find();
     }
     if (*(volatile int*)flags)  // given up with an answer on its way
       mbar_wait_bounded(bar(kNext), asked & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
