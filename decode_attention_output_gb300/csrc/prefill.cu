@@ -61,8 +61,8 @@ enum Bar {
   kPFull = kSFull + 2,             // per tile: its P is in TMEM, O is corrected
   kPvDone = kPFull + 2,            // per tile: its PV has completed
   kSFree = kPvDone + 2,            // the S columns have been read
-  kVFix,                           // a V tile that needs clearing has landed
-  kNext,                           // the next item's index has been answered
+  kSIssued,                        // per tile: the MMAs of its S are on their way
+  kNext = kSIssued + 2,                           // the next item's index has been answered
   kItemFull, kItemEmpty = kItemFull + kItems,
   kKvFull = kItemEmpty + kItems, kKvEmpty = kKvFull + kStagesP,
   kBars = kKvEmpty + kStagesP
@@ -194,6 +194,16 @@ __device__ __forceinline__ float2 fma2(float2 x, float a, float c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(xx), "l"(aa), "l"(cc));
   return *reinterpret_cast<float2*>(&r);
 }
+// Lanes with bit D of t give `lo` and lanes without it `hi`; each takes the other's.
+template <int D>
+__device__ __forceinline__ void exchange(uint32_t (&lo)[4], uint32_t (&hi)[4], int t) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, t & D ? lo[k] : hi[k], D);
+    lo[k] = t & D ? got : lo[k];
+    hi[k] = t & D ? hi[k] : got;
+  }
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -246,30 +256,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     // ------------------------------------------------------------ producer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     int base = 0, b0 = 0;  // items of the sequences before b0 (a multiple of 32) and b0
-    int kv = 0, fixes = 0, qn[2] = {0, 0};
-    auto load_kv = [&](const CUtensorMap* map, int row, int kvh, int valid, bool is_v) {  // valid: the sequence's tokens from row on
+    int kv = 0, qn[2] = {0, 0};
+    auto load_kv = [&](const CUtensorMap* map, int row, int kvh) {
       const int s = kv % kStagesP;
       mbar_wait_bounded(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
       ++kv;
-      // A V tile that ends inside another sequence's rows: their weights are 0, but 0 times a
-      // NaN or infinity there is not, so those rows are cleared before the MMA sees them.
-      const bool fix = is_v && valid < kN && row + valid < p.Tk;
-      const int full = fix ? kVFix : kKvFull + s;
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar(full), kTileP);
-        tma_load_4d(ring + s * kTileP, map, bar(full), 0, row, 0, kvh);
-      }
-      if (fix) {
-        mbar_wait_bounded(bar(kVFix), fixes & 1, p.err, kErrWaitFull, flags);
-        ++fixes;
-        uint4* tile = reinterpret_cast<uint4*>(smem + kOffRing + s * kTileP);
-        for (int i = valid * 8 + lane; i < kN * 8; i += 32) {
-          tile[i] = make_uint4(0, 0, 0, 0);
-          tile[i + kHalf / 16] = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kKvFull + s));
+        mbar_arrive_expect_tx(bar(kKvFull + s), kTileP);
+        tma_load_4d(ring + s * kTileP, map, bar(kKvFull + s), 0, row, 0, kvh);
       }
     };
     const uint32_t next_smem = smem_u32(smem + kOffNext);
@@ -349,9 +343,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       if (top == 0) ask();
       for (int j = 0; j < top && !*(volatile int*)flags; ++j) {
         if (j == max(0, top - 3)) ask();  // late, so that no item waits behind a long one
-        const int row = it.k0 + j * kN, valid = it.lk - j * kN;
-        load_kv(&p.tm_k, row, it.kvh, valid, false);
-        load_kv(&p.tm_v, row, it.kvh, valid, true);
+        load_kv(&p.tm_k, it.k0 + j * kN, it.kvh);
+        load_kv(&p.tm_v, it.k0 + j * kN, it.kvh);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (j > 0 || nt[w] == 0) continue;
@@ -388,7 +381,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     const uint64_t kv_desc = pv ? umma_smem_desc(ring, kHalf, 1024) : umma_smem_desc(ring, 16, 1024);
     int ks = pv ? 1 : 0, kph = 0;  // ring position of the next V or K tile (they alternate)
     int tn = 0;                    // bit w: the parity that tile w's P (or Q) completes next
-    int sn = 0;
+    int sn = 0, pn0 = 0, pn1 = 0;
     for (int n = 0;; ++n) {
       const int slot = n % kItems;
       wait(kItemFull + slot, (n / kItems) & 1, kErrWaitFull);
@@ -398,6 +391,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       __syncwarp();
       if (uniform(it.lq < 0 || *(volatile int*)flags)) break;
       const int nt0 = uniform(kv_tiles(it, 0, npos)), nt1 = uniform(kv_tiles(it, 1, npos));
+      // A V tile that ends inside another sequence's rows: their weights are 0, but 0 times a
+      // NaN or infinity there is not, so those rows are cleared before the MMAs see them.
+      const int clear_at = uniform(pv && it.lk % kN != 0 && it.k0 + it.lk < p.Tk ? it.lk / kN : -1);
       for (int j = 0; j < max(nt0, nt1); ++j) {
         const int stage = ks;
         wait(kKvFull + stage, kph, kErrWaitFull);
@@ -407,6 +403,15 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
           kph ^= 1;
         }
         const uint64_t b = kv_desc + (uint64_t)(stage * (kTileP >> 4));
+        if (j == clear_at) {
+          uint4* tile = reinterpret_cast<uint4*>(smem + kOffRing + stage * kTileP);
+          for (int i = it.lk % kN * 8 + lane; i < kN * 8; i += 32) {
+            tile[i] = make_uint4(0, 0, 0, 0);
+            tile[i + kHalf / 16] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
           const int nt = w ? nt1 : nt0;
@@ -414,6 +419,16 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
           if (pv) {  // O_w += P_w V
             wait(kPFull + w, tn >> w & 1, kErrWaitMma);
             tn ^= 1 << w;
+            // Behind the tile's next S, which the softmax waits for, rather than mixed with it
+            // (8192 tokens x 64 heads in a short run: 575 us, 640 without this); after some polls
+            // regardless, as that S may itself be waiting, for its K tile or for the softmax.
+            ++(w ? pn1 : pn0);
+            if (j + 1 < nt) {
+#pragma unroll 1
+              for (int i = 0; i < 16 && !mbar_try_wait(bar(kSIssued + w), (w ? pn1 : pn0) & 1); ++i) {
+              }
+            }
+            __syncwarp();
             tc_fence_after_sync();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
@@ -435,6 +450,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
               warp_umma_ss(tmem, a + off, b + off, kIdescS, kk != 0);
             }
             warp_umma_commit(bar(kSFull + w));
+            if (lane == 0) mbar_arrive(bar(kSIssued + w));
+            __syncwarp();
             if (j == nt - 1) warp_umma_commit(bar(kQEmpty + w));
           }
         }
@@ -460,22 +477,34 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       tc_fence_after_sync();
     };
     auto store = [&](__nv_bfloat16* to, float sum) {
-      const float inv = 1.f / sum;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const bool none = sum == 0.f;  // a row without a key: zeros, whatever its O columns hold
+      // Four lanes exchange their rows' 16-byte pieces, so that they write 64 bytes of one row
+      // at a time: a store of 16 bytes to each of 32 rows takes the load-store unit 32 cycles.
+      const int t = lane & 3;
+      __nv_bfloat16* rows[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        rows[i] = reinterpret_cast<__nv_bfloat16*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), (lane & ~3) + i));
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         float o[32];
         tmem_ld_x32(o_tmem + c * 32, o);
         tmem_ld_wait_x32(o);
-        if (to) {
+        uint32_t y[4][4];  // 16-byte pieces of this row, then piece t of the four rows
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t y[4];
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              y[k] = sum == 0.f ? 0u : pack_bf16x2(o[i * 8 + 2 * k] * inv, o[i * 8 + 2 * k + 1] * inv);
-            *reinterpret_cast<uint4*>(to + c * 32 + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        }
+          for (int k = 0; k < 4; ++k) y[i][k] = none ? 0u : pack_bf16x2(o[i * 8 + 2 * k] * inv, o[i * 8 + 2 * k + 1] * inv);
+        exchange<1>(y[0], y[1], t);
+        exchange<1>(y[2], y[3], t);
+        exchange<2>(y[0], y[2], t);
+        exchange<2>(y[1], y[3], t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (rows[i])
+            *reinterpret_cast<uint4*>(rows[i] + c * 32 + t * 8) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
       }
     };
     for (int n = 0;; ++n) {
@@ -511,7 +540,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
           const float none = neg ? -kNegInfP : kNegInfP;
           const int left = lim - j * kN;
 #pragma unroll
-          for (int c = 0; c < kN; ++c) s[c] = c < left ? s[c] : none;
+          for (int h = 0; h < 4; ++h) {  // a bit per key (tests of single bits share an instruction)
+            const int n32 = min(max(left - 32 * h, 0), 32);
+            const uint32_t keep = n32 == 32 ? ~0u : (1u << n32) - 1u;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[32 * h + c] = keep >> c & 1u ? s[32 * h + c] : none;
+          }
         }
         float mx[4];
 #pragma unroll
