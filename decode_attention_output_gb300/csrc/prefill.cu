@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       for (int i = 0; i < 4; ++i)
         rows[i] = reinterpret_cast<__nv_bfloat16*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), (lane & ~3) + i));
-#pragma unroll
+#pragma unroll 1  // (run once an item: the time goes into fetching the instructions)
       for (int c = 0; c < 4; ++c) {
         float o[32];
         tmem_ld_x32(o_tmem + c * 32, o);
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
           if (step > 0) store(out, l_old);
           out = to;
         } else if (any) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float o[32];
             tmem_ld_x32(o_tmem + c * 32, o);
