@@ -474,8 +474,13 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
       bad |= (unsigned)bk == nblk;
       // one copy per tensor: box s = all D/64 dim boxes of its rows ([box][dim box][rows])
       const uint32_t off = (uint32_t)(s * kTokenBytes) << lsub;
-      tma_load_5d_hint(kdst + off, &p.tm_k, fb, 0, row, 0, c.kvh, bk, kv_policy);
-      tma_load_5d_hint(kdst + kKTileBytes + off, &p.tm_v, fb, 0, row, 0, c.kvh, bk, kv_policy);
+      if (KV8) {  // box s: its rows of both tensors, in one copy where one map spans the pools
+        tma_load_5d_hint(kdst + 2 * off, &p.tm_k, fb, 0, row, 0, c.kvh, bk, kv_policy);
+        if (!p.kv_pair) tma_load_5d_hint(kdst + 2 * off + sub_bytes, &p.tm_v, fb, 0, row, 0, c.kvh, bk, kv_policy);
+      } else {
+        tma_load_5d_hint(kdst + off, &p.tm_k, fb, 0, row, 0, c.kvh, bk, kv_policy);
+        tma_load_5d_hint(kdst + kKTileBytes + off, &p.tm_v, fb, 0, row, 0, c.kvh, bk, kv_policy);
+      }
       if (KV8)  // box s: its K scales, then its V scales
         tma_load_4d_hint(scales + stage * AttnSmem::kScaleStageBytes + ((uint32_t)s << (lsub + 3)), &p.tm_scales, fb, row, 0,
                          c.kvh, bk, kv_policy);
@@ -875,6 +880,23 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
     };
     const uint32_t qk_row = row_off(tb + (lane & 7) + ((lane >> 3) & 1) * 8);  // ldmatrix rows of S^T
     const uint32_t pv_row = row_off(tb + (lane & 7) + ((lane >> 4) & 1) * 8);  // ldmatrix.trans rows of V
+    // fp8 caches: byte offset in the stage of this lane's row of each 16-row half, in K and in
+    // V. Paged: [box][K rows, V rows] (or V first); contiguous: the K tile, then the V tile.
+    uint32_t k8_at[2] = {0, 0}, v8_at[2] = {0, 0};
+    if constexpr (KV8) {
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = tb + 16 * hh + (lane & 7) + ((lane >> 3) & 1) * 8;
+        if (kScaled) {
+          const uint32_t at = ((uint32_t)(r >> lbox) << (lbox + 8)) + ((uint32_t)(r & ((1 << lbox) - 1)) << 7);
+          k8_at[hh] = at + (p.kv_pair == 2 ? 128u << lbox : 0u);
+          v8_at[hh] = at + (p.kv_pair == 2 ? 0u : 128u << lbox);
+        } else {
+          k8_at[hh] = r * 128;
+          v8_at[hh] = kKB + r * 128;
+        }
+      }
+    }
     const float sl2 = p.scale_log2;
     // q fragments of a segment's (batch row, KV head): head h's row at rows + h * stride bytes
     // (in shared memory for the segments that start inside the range, whose first tiles carry
@@ -948,12 +970,11 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) se[nb][i] = so[nb][i] = 0.f;
-              const int row = tb + 16 * hh + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
               for (int kk = 0; kk < kKs / 2; ++kk) {
                 const int chunk = 2 * kk + (lane >> 4);
                 uint32_t m[4];
-                ldsm_x4(kbase + row * 128 + ((chunk ^ (lane & 7)) << 4), m[0], m[1], m[2], m[3]);
+                ldsm_x4(kbase + k8_at[hh] + ((chunk ^ (lane & 7)) << 4), m[0], m[1], m[2], m[3]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   uint32_t a[4];
@@ -1063,7 +1084,6 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
             // a lane tokens 2t, 2t+1 of dims 2g, 2g+1 (a byte each); a byte permute makes
             // (dim 2g: two tokens) and (dim 2g+1: two tokens), widened to f16 exactly, so the
             // MMA's rows g and g+8 of m-tile mb are dims 16mb + 2g and 16mb + 2g + 1.
-            const uint32_t vbase = kbase + kKB;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               // valid tokens of this half: a half past the length is masked whole (its weights
@@ -1073,12 +1093,11 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
               // the permute itself puts zeros in place of tokens past the sequence (which may hold
               // anything; P is 0 there): byte 4 is the first of its zero operand
               const uint32_t sel_lo = pair_select(2 * t, vwh), sel_hi = pair_select(2 * t + 8, vwh);
-              const int row = tb + 16 * hh + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
               for (int mp = 0; mp < 4; ++mp) {
                 const int chunk = 2 * mp + (lane >> 4);
                 uint32_t m[4];
-                ldsm_x4_trans(vbase + row * 128 + ((chunk ^ (lane & 7)) << 4), m[0], m[1], m[2], m[3]);
+                ldsm_x4_trans(kbase + v8_at[hh] + ((chunk ^ (lane & 7)) << 4), m[0], m[1], m[2], m[3]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   uint32_t a[4];  // from tokens 2t, 2t+1 and 2t+8, 2t+9

@@ -172,6 +172,9 @@ struct AttnParams {
   // paged fp8 caches: a scale per token and KV head instead, [num_blocks][Hkv][2][block_size]
   // fp32 (K's, then V's), box min(block size, 128) tokens x 2
   CUtensorMap tm_scales;
+  // paged fp8 caches: 1, 2: tm_k maps both pools, the third coordinate choosing K (1) or V (2)
+  // first, and one copy brings a box of both; 0: a copy from each of tm_k and tm_v
+  int kv_pair;
   // Cluster mode (> 1): the grid is launched in clusters of `cluster` consecutive CTAs; the
   // tiles are split over the CTAs as always, and a sequence whose parts all lie in one
   // cluster merges them in distributed shared memory (the others through L2).

@@ -127,6 +127,28 @@ def test_token_major_pool_views_and_padded_table():
     assert torch.equal(out, out2)
 
 
+@pytest.mark.parametrize("bs", [16, 64, 256])
+def test_where_the_pools_lie(bs):
+    """K before V in memory, V before K, one interleaved allocation, different layouts of the two, one pool as both."""
+    x = case(3, 8, 2, [250, 100, 1], bs, seed=13)
+    out, _ = check(x, "plain")
+    q, k, v, scales, table, lens = on(x)
+    n = k.numel()
+    both = torch.empty(2 * n, dtype=torch.uint8, device=DEV)
+    wide = torch.empty((*k.shape[:2], 2, *k.shape[2:]), dtype=torch.uint8, device=DEV)
+    flat = [both[i * n:(i + 1) * n].view(k.shape).view(torch.float8_e4m3fn) for i in range(2)]
+    mixed = k.transpose(1, 2).contiguous().transpose(1, 2)
+    for k2, v2 in (flat, flat[::-1], [wide[:, :, i].view(torch.float8_e4m3fn) for i in range(2)], (mixed, v)):
+        k2.view(torch.uint8).copy_(k.view(torch.uint8))
+        v2.view(torch.uint8).copy_(v.view(torch.uint8))
+        out2 = torch.empty_like(out)
+        da.decode_attn_only_paged_fp8(q, k2, v2, scales, table, lens, out2, SCALE)
+        torch.cuda.synchronize()
+        assert torch.equal(out, out2)
+    check((x[0], x[1], x[1], *x[3:]), "one pool")
+    assert da.decode_attn_last_device_error() == 0
+
+
 def test_block_outside_the_pool_reads_as_zeros():
     x = case(2, 8, 2, [64, 64], 16, seed=8)
     x[4][1, 2] = x[1].shape[0] + 7
