@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
   if (warp == kSoftWarps) {
     // ------------------------------------------------------------ producer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    int base = 0, b0 = 0;  // items of the sequences before b0 (a multiple of 32) and b0
+    int base = 0, b0 = 0;  // row blocks of the sequences before b0 (a multiple of 32) and b0
+    int total = 0x7fffffff;  // row blocks in all, once known
     int kv = 0, qn[2] = {0, 0};
     auto load_kv = [&](const CUtensorMap* map, int row, int kvh) {
       const int s = kv % kStagesP;
@@ -285,10 +286,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     // lq < 0: none (x < 0, or past the last: the grid has CTAs for the most there can be).
     auto find = [&] {
       Item it;
-      const int mb = x < 0 ? 0x7fffffff : x / p.Hkv;  // (none left: past every sequence)
+      const int mb = x < 0 ? total : x / p.Hkv;
       it.kvh = x < 0 ? 0 : x - mb * p.Hkv;
       it.lq = -1;
       it.lk = it.q0 = it.k0 = it.p0 = 0;
+      if (mb >= total) return it;
       if (mb < base) base = b0 = 0;
       while (b0 < p.B) {
         const int b = b0 + lane;
@@ -319,6 +321,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         base += __shfl_sync(0xffffffffu, end, 31);
         b0 += 32;
       }
+      if (it.lq < 0) total = base;
       return it;
     };
     Item it = find();

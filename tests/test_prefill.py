@@ -159,6 +159,16 @@ def test_other_sequences_do_not_reach_a_row(bad):
     assert torch.equal(out.cpu()[cq[1]:cq[2]], clean[cq[1]:cq[2]])
 
 
+def test_many_short_sequences():
+    """1000 sequences, most of them empty: far fewer work items than there could be."""
+    lq = [0] * 1000
+    for i in range(0, 1000, 37):
+        lq[i] = 1 + i % 5
+    lk = [n + (i % 3) * 7 if n else 0 for i, n in enumerate(lq)]
+    check(*inputs(lq, lk, 8, 8, seed=16), SCALE, "short sequences")
+    check(*inputs([1] * 1024, [1] * 1024, 2, 1, seed=17), SCALE, "1024 single tokens")
+
+
 def test_offsets_are_clamped():
     """Offsets past the tokens end there; a sequence whose end lies before its start is empty."""
     q, k, v, _, _ = inputs([100], [100], 4, 2, seed=11)
