@@ -1285,9 +1285,16 @@ int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_ten
     DA_TRY(encode_packed_map(&p.tm_k, k, 128, 0));
     DA_TRY(encode_packed_map(&p.tm_v, v, 128, 0));
   }
+  // Fewer items than half the SMs: parts of about four K/V tiles or more (by the average
+  // length), as many as there are SMs for.
+  const int64_t sms = std::max(1, sm_count()), tiles = (Tk / B + 127) / 128;
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({sms / items, tiles / 4, (int64_t)kMaxPrefillParts}));
+  const size_t rows = p.parts > 1 ? (size_t)p.parts * Tq * Hq : 0, ml_bytes = align_up(rows * 2 * 4, 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = nullptr;
-  DA_TRY(workspace_get(0, st, &ws));
+  DA_TRY(workspace_get(ml_bytes + rows * 128 * 4, st, &ws));
+  p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
+  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
   p.err = reinterpret_cast<int*>(ws + kErrOff);
   p.out = static_cast<__nv_bfloat16*>(out->data);
   p.o_st = out->stride[0];
@@ -1301,7 +1308,7 @@ int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_ten
   // the kernel masks with infinities: a scale of 0 becomes one that leaves every weight 1
   p.scale_log2 = scale * 1.4426950408889634f;
   if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;
-  return launch_prefill(p, (int)items, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return launch_prefill(p, (int)items * p.parts, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 int decode_attn_cache_write(const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cu_seqlens,

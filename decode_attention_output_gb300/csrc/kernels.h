@@ -227,6 +227,7 @@ cudaError_t launch_attention_paged_fp8(const AttnParams& p, int grid, int nb, cu
 int attn_max_active_clusters(int cluster);
 
 // ------------------------------------------------------------ prompt attention
+constexpr int kMaxPrefillParts = 32;
 struct PrefillParams {
   CUtensorMap tm_q;  // q [Tq][Hq][128] bf16: box 64 dims x G heads x npos tokens, 128B swizzle
   CUtensorMap tm_k;  // k, v [Tk][Hkv][128]: box 64 dims x 128 tokens x both halves of the dims
@@ -238,6 +239,9 @@ struct PrefillParams {
   int B, Hkv, G, Tq, Tk;
   int npos;            // query positions per tile, floor(128 / G)
   float scale_log2;    // scale * log2(e), never 0
+  int parts;           // an item's K/V tiles are cut into at most so many parts (1: none is cut)
+  float* part_o;       // [parts][Tq][Hq][128] unnormalised outputs of the parts
+  float* part_ml;      // [parts][Tq][Hq][2] their maxima (log2 units) and sums
 };
 // grid = as many CTAs as there can be work items; those that run take over the others.
 cudaError_t launch_prefill(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream);

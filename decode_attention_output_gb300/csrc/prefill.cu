@@ -27,9 +27,13 @@
 //    step has its weights.
 //  * The running maximum lags as in the decode kernel: O in TMEM is only rescaled when a row's
 //    maximum grows by more than 2^8, by the thread that owns the row.
+//  * With few rows over many keys (a few new tokens of long sequences) there are fewer items
+//    than SMs: each is then cut into parts of its K/V tiles, which leave fp32 (O, m, l) in the
+//    workspace, and a second kernel joins them in order.
 //  * One producer warp streams K and V tiles (32 KB) by TMA through a ring of five stages, in
 //    the order of their use; it also finds the items (a scan of the offsets) and passes them on.
 #include "kernels.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 namespace da {
@@ -50,6 +54,9 @@ constexpr float kNegInfP = -__builtin_huge_valf();
 
 struct Item {  // in shared memory, as ints
   int lq, lk, q0, k0, p0, kvh;  // lq < 0: no more items
+  int j0, end0, end1;           // K/V tiles from j0 on, to the end of each tile of rows
+  int clear;                    // the V tile whose end is another sequence's (-1: none)
+  int part;                     // of the item (-1: the item is whole)
 };
 constexpr size_t kOffRing = 2 * kTileP;
 constexpr size_t kOffBars = kOffRing + (size_t)kStagesP * kTileP;
@@ -74,13 +81,15 @@ constexpr size_t kOffFlags = kOffNext + 16;
 constexpr size_t kSmemP = 1024 + kOffFlags + 16;
 static_assert(kSmemP <= kMaxDynSmem, "prefill kernel exceeds 227 KB of shared memory");
 
-// K/V tiles that tile w of an item needs: those up to its last row's last key.
-__device__ __forceinline__ int kv_tiles(const Item& it, int w, int npos) {
-  const int first = it.p0 + w * npos;
-  if (first >= it.lq) return 0;
-  const int last = min(first + npos, it.lq) - 1;
-  return max(0, last + it.lk - it.lq + kN) / kN;
+// K/V tiles that npos query positions from `first` on need, of Lq and Lk tokens: those up to
+// the last position's last key.
+__device__ __forceinline__ int kv_tiles(int first, int npos, int lq, int lk) {
+  const int last = min(first + npos, lq) - 1;
+  return first < lq ? max(0, last + lk - lq + kN) / kN : 0;
 }
+// Parts that an item of `top` tiles is cut into, and the first tile of one.
+__device__ __forceinline__ int item_parts(int top, int parts) { return max(1, min(top, parts)); }
+__device__ __forceinline__ int part_begin(int part, int top, int n) { return (int)((long long)part * top / n); }
 
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, float* r) {
   uint32_t* u = reinterpret_cast<uint32_t*>(r);
@@ -286,10 +295,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     // lq < 0: none (x < 0, or past the last: the grid has CTAs for the most there can be).
     auto find = [&] {
       Item it;
-      const int mb = x < 0 ? total : x / p.Hkv;
-      it.kvh = x < 0 ? 0 : x - mb * p.Hkv;
+      const int xi = x < 0 ? 0 : x / p.parts, part = x - xi * p.parts;
+      const int mb = x < 0 ? total : xi / p.Hkv;
+      it.kvh = x < 0 ? 0 : xi - mb * p.Hkv;
       it.lq = -1;
-      it.lk = it.q0 = it.k0 = it.p0 = 0;
+      it.lk = it.q0 = it.k0 = it.p0 = it.j0 = it.end0 = it.end1 = 0;
+      it.clear = it.part = -1;
       if (mb >= total) return it;
       if (mb < base) base = b0 = 0;
       while (b0 < p.B) {
@@ -321,7 +332,23 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         base += __shfl_sync(0xffffffffu, end, 31);
         b0 += 32;
       }
-      if (it.lq < 0) total = base;
+      if (it.lq < 0) {
+        total = base;
+        return it;
+      }
+      it.end0 = kv_tiles(it.p0, npos, it.lq, it.lk);
+      it.end1 = kv_tiles(it.p0 + npos, npos, it.lq, it.lk);
+      it.clear = it.lk % kN != 0 && it.k0 + it.lk < p.Tk ? it.lk / kN : -1;
+      if (p.parts > 1) {
+        const int top = max(it.end0, it.end1), n = item_parts(top, p.parts);
+        if (part >= n) it.lq = -1;  // fewer tiles than parts: not this one
+        if (n > 1) {
+          it.part = part;
+          it.j0 = part_begin(part, top, n);
+          it.end0 = min(it.end0, part_begin(part + 1, top, n));
+          it.end1 = min(it.end1, part_begin(part + 1, top, n));
+        }
+      }
       return it;
     };
     Item it = find();
@@ -342,15 +369,15 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       // The queries of both tiles, which come into shared memory when the item before has had
       // its last S computed, are on their way into L2 until then.
       if (lane < 4) tma_prefetch_4d(&p.tm_q, 0, it.kvh * G, it.q0 + it.p0 + (lane >> 1) * npos, lane & 1);
-      const int nt[2] = {kv_tiles(it, 0, npos), kv_tiles(it, 1, npos)}, top = max(nt[0], nt[1]);
-      if (top == 0) ask();
-      for (int j = 0; j < top && !*(volatile int*)flags; ++j) {
-        if (j == max(0, top - 3)) ask();  // late, so that no item waits behind a long one
+      const int top = max(it.end0, it.end1);
+      if (top <= it.j0) ask();
+      for (int j = it.j0; j < top && !*(volatile int*)flags; ++j) {
+        if (j == max(it.j0, top - 3)) ask();  // late, so that no item waits behind a long one
         load_kv(&p.tm_k, it.k0 + j * kN, it.kvh);
         load_kv(&p.tm_v, it.k0 + j * kN, it.kvh);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          if (j > 0 || nt[w] == 0) continue;
+          if (j > it.j0 || (w ? it.end1 : it.end0) <= it.j0) continue;
           mbar_wait_bounded(bar(kQEmpty + w), (qn[w] & 1) ^ 1, p.err, kErrWaitEmpty, flags);
           ++qn[w];
           if (lane == 0) {
@@ -388,16 +415,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     for (int n = 0;; ++n) {
       const int slot = n % kItems;
       wait(kItemFull + slot, (n / kItems) & 1, kErrWaitFull);
-      const Item it = items[slot];
+      const int j0 = uniform(items[slot].j0), end0 = uniform(items[slot].end0), end1 = uniform(items[slot].end1);
+      const int lk = items[slot].lk, clear_at = pv ? items[slot].clear : -1;
+      const bool none = items[slot].lq < 0 || *(volatile int*)flags;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kItemEmpty + slot));
       __syncwarp();
-      if (uniform(it.lq < 0 || *(volatile int*)flags)) break;
-      const int nt0 = uniform(kv_tiles(it, 0, npos)), nt1 = uniform(kv_tiles(it, 1, npos));
-      // A V tile that ends inside another sequence's rows: their weights are 0, but 0 times a
-      // NaN or infinity there is not, so those rows are cleared before the MMAs see them.
-      const int clear_at = uniform(pv && it.lk % kN != 0 && it.k0 + it.lk < p.Tk ? it.lk / kN : -1);
-      for (int j = 0; j < max(nt0, nt1); ++j) {
+      if (none) break;
+      for (int j = j0; j < max(end0, end1); ++j) {
         const int stage = ks;
         wait(kKvFull + stage, kph, kErrWaitFull);
         ks += 2;
@@ -406,9 +431,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
           kph ^= 1;
         }
         const uint64_t b = kv_desc + (uint64_t)(stage * (kTileP >> 4));
+        // A V tile that ends inside another sequence's rows: their weights are 0, but 0 times a
+        // NaN or infinity there is not, so those rows are cleared before the MMAs see them.
         if (j == clear_at) {
           uint4* tile = reinterpret_cast<uint4*>(smem + kOffRing + stage * kTileP);
-          for (int i = it.lk % kN * 8 + lane; i < kN * 8; i += 32) {
+          for (int i = lk % kN * 8 + lane; i < kN * 8; i += 32) {
             tile[i] = make_uint4(0, 0, 0, 0);
             tile[i + kHalf / 16] = make_uint4(0, 0, 0, 0);
           }
@@ -417,8 +444,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         }
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
-          const int nt = w ? nt1 : nt0;
-          if (j >= nt) continue;
+          const int end = w ? end1 : end0;
+          if (j >= end) continue;
           if (pv) {  // O_w += P_w V
             wait(kPFull + w, tn >> w & 1, kErrWaitMma);
             tn ^= 1 << w;
@@ -426,7 +453,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
             // (8192 tokens x 64 heads in a short run: 575 us, 640 without this); after some polls
             // regardless, as that S may itself be waiting, for its K tile or for the softmax.
             ++(w ? pn1 : pn0);
-            if (j + 1 < nt) {
+            if (j + 1 < end) {
 #pragma unroll 1
               for (int i = 0; i < 16 && !mbar_try_wait(bar(kSIssued + w), (w ? pn1 : pn0) & 1); ++i) {
               }
@@ -436,10 +463,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               warp_umma_ts(tmem + kTmemO + w * 128, tmem + kTmemP + w * 64 + kk * 8, b + ((kk * 16 * 128) >> 4), kIdescO,
-                           kk > 0 || j > 0);
+                           kk > 0 || j > j0);
             warp_umma_commit(bar(kPvDone + w));
           } else {  // S = Q_w K^T
-            if (j == 0) {
+            if (j == j0) {
               wait(kQFull + w, tn >> w & 1, kErrWaitFull);
               tn ^= 1 << w;
             }
@@ -455,7 +482,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
             warp_umma_commit(bar(kSFull + w));
             if (lane == 0) mbar_arrive(bar(kSIssued + w));
             __syncwarp();
-            if (j == nt - 1) warp_umma_commit(bar(kQEmpty + w));
+            if (j == end - 1) warp_umma_commit(bar(kQEmpty + w));
           }
         }
         warp_umma_commit(bar(kKvEmpty + stage));
@@ -474,6 +501,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     int step = 0;
     float m = kNegInfP, l = 0.f;
     __nv_bfloat16* out = nullptr;  // this row of the item in work (null: no such row)
+    long long slot_out = -1;       // its row in the workspace (-1: a whole item; -2: a part, no such row)
     // The O of the tile's last item, complete with PV of its last step (waited for here)
     auto pv_done = [&] {
       if (step > 0) wait_bar(bar(kPvDone + w), (step - 1) & 1, p.err, kErrWaitMma, flags);
@@ -510,6 +538,30 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
             *reinterpret_cast<uint4*>(rows[i] + c * 32 + t * 8) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
       }
     };
+    // A part's row: O as it is, the sum and the reference maximum.
+    auto store_part = [&](float sum, float ref) {
+      if (slot_out >= 0) {
+        p.part_ml[slot_out * 2] = ref;
+        p.part_ml[slot_out * 2 + 1] = sum;
+      }
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(o_tmem + c * 16, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[i]));
+        if (slot_out >= 0)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(p.part_o + slot_out * 128 + c * 16 + i * 4) =
+                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      }
+    };
+    auto finish = [&](float sum, float ref) {
+      if (slot_out == -1) store(out, sum);
+      else store_part(sum, ref);
+    };
     for (int n = 0;; ++n) {
       const int slot = n % kItems;
       wait_bar(bar(kItemFull + slot), (n / kItems) & 1, p.err, kErrWaitFull, flags);
@@ -522,13 +574,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       const bool row_ok = off < npos && pos < it.lq;
       const int lim = min(it.lk, pos + it.lk - it.lq + 1);            // keys of this row
       const int lim0 = min(it.lk, first + off0 + it.lk - it.lq + 1);  // the least of the warp's rows
-      const int nt = kv_tiles(it, w, npos);
+      const int end = w ? it.end1 : it.end0;
       __nv_bfloat16* to = row_ok ? p.out + (long long)(it.q0 + pos) * p.o_st + (long long)(it.kvh * G + g) * p.o_sh : nullptr;
-      if (nt == 0 && to) {  // no key at all
+      if (it.part < 0 && end == 0 && to) {  // no key at all
 #pragma unroll
         for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(to + i * 8) = make_uint4(0, 0, 0, 0);
       }
-      for (int j = 0; j < nt; ++j, ++step) {
+      for (int j = it.j0; j < end; ++j, ++step) {
         wait_bar(bar(kSFull + w), step & 1, p.err, kErrWaitMma, flags);
         tc_fence_after_sync();
         float s[kN];
@@ -563,8 +615,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
           mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
         }
         const float xm = mx[0] * sl2;
-        const float l_old = l;
-        if (j == 0) {
+        const float l_old = l, m_old = m;
+        if (j == it.j0) {
           m = kNegInfP;
           l = 0.f;
         }
@@ -586,9 +638,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         pv_done();
-        if (j == 0) {
-          if (step > 0) store(out, l_old);
+        if (j == it.j0) {
+          if (step > 0) finish(l_old, m_old);
           out = to;
+          slot_out = it.part < 0 ? -1
+                                 : row_ok ? ((long long)it.part * p.Tq + it.q0 + pos) * (p.G * p.Hkv) + it.kvh * G + g : -2;
         } else if (any) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -609,7 +663,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       }
     }
     pv_done();
-    if (step > 0) store(out, l);
+    if (step > 0) finish(l, m);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
   }
@@ -619,6 +673,43 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the parts of the items that were cut: a warp per (token, head), four dims a lane.
+__global__ void __launch_bounds__(128) prefill_join_kernel(const __grid_constant__ PrefillParams p) {
+  const int lane = threadIdx.x & 31, Hq = p.G * p.Hkv;
+  pdl_wait_primary();
+  const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int t = (int)(unit / Hq), h = (int)(unit - (long long)t * Hq);
+  if (t >= p.Tq) return;
+  const int b = find_sequence(p.cu_q, p.B, t, lane);
+  const int q0 = min(max(__ldg(p.cu_q + b), 0), p.Tq), q1 = min(max(__ldg(p.cu_q + b + 1), q0), p.Tq);
+  const int k0 = min(max(__ldg(p.cu_k + b), 0), p.Tk), k1 = min(max(__ldg(p.cu_k + b + 1), k0), p.Tk);
+  if (t < q0 || t >= q1) return;  // a row of no sequence
+  const int lq = q1 - q0, lk = k1 - k0, p0 = (t - q0) / (2 * p.npos) * 2 * p.npos;
+  const int end0 = kv_tiles(p0, p.npos, lq, lk), end1 = kv_tiles(p0 + p.npos, p.npos, lq, lk);
+  const int top = max(end0, end1), n = item_parts(top, p.parts), end = t - q0 - p0 < p.npos ? end0 : end1;
+  if (n == 1) return;  // whole: it has been written
+  float m = kNegInfP, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < n && part_begin(i, top, n) < end; ++i) {  // (parts past the row's last key hold nothing)
+    const long long slot = ((long long)i * p.Tq + t) * Hq + h;
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot * 2);
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot * 128 + lane * 4);
+    if (ml.x == kNegInfP && ml.y == 0.f) continue;  // the part's keys all lie past the row
+    const float mn = fmaxf(m, ml.x), a = m == kNegInfP ? 0.f : fast_exp2(m - mn);
+    const float c = ml.x == kNegInfP ? 1.f : fast_exp2(ml.x - mn);  // (no maximum: NaN scores)
+    l = l * a + ml.y * c;
+    o.x = o.x * a + v.x * c;
+    o.y = o.y * a + v.y * c;
+    o.z = o.z * a + v.z * c;
+    o.w = o.w * a + v.w * c;
+    m = mn;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint2 y = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (l == 0.f) y = make_uint2(0u, 0u);
+  *reinterpret_cast<uint2*>(p.out + (long long)t * p.o_st + (long long)h * p.o_sh + lane * 4) = y;
 }
 
 }  // namespace
@@ -644,7 +735,12 @@ cudaError_t launch_prefill(const PrefillParams& p, int grid, bool pdl, cudaStrea
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, prefill_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, prefill_kernel, p);
+  if (e != cudaSuccess || p.parts == 1) return e;
+  cfg.gridDim = dim3((unsigned)(((long long)p.Tq * p.G * p.Hkv + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, prefill_join_kernel, p);
 }
 
 }  // namespace da

@@ -159,6 +159,60 @@ def test_other_sequences_do_not_reach_a_row(bad):
     assert torch.equal(out.cpu()[cq[1]:cq[2]], clean[cq[1]:cq[2]])
 
 
+FEW_ROWS = [  # few query rows over many keys: the items are cut into parts and joined
+    ([1], [5000], 8, 2),
+    ([64], [4096], 4, 1),
+    ([100], [2500], 16, 4),                   # the second item's rows end in different tiles
+    ([5, 1, 33], [3001, 40, 2049], 8, 2),      # one of them too short to cut
+    ([700], [640], 2, 1),                      # rows without a key beside rows with five tiles of them
+    ([3, 0, 2], [6000, 0, 0], 12, 1),
+    ([130], [1500], 3, 1),
+]
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hkv", FEW_ROWS, ids=[str(i) for i in range(len(FEW_ROWS))])
+def test_few_rows_over_many_keys(lq, lk, Hq, Hkv):
+    q, k, v, cq, ck = inputs(lq, lk, Hq, Hkv, seed=18, first=1, spare=140)
+    out = check(q, k, v, cq, ck, SCALE, "few rows")
+    check(q, (k.float() * torch.linspace(0, 6, len(k))[:, None, None]).to(torch.bfloat16), v, cq, ck, SCALE, "growing keys")
+    check(q, k, v, cq, ck, -0.3, "negative scale")
+    for t, c in ((q, cq), (k, ck), (v, ck)):  # what lies around the sequences does not matter
+        t[:1] = float("nan")
+        t[c[-1]:] = float("inf")
+    again = canaries(q.shape)
+    da.decode_attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), offsets(cq), offsets(ck), again, SCALE)
+    torch.cuda.synchronize()
+    assert torch.equal(again.cpu()[cq[0]:cq[-1]], out[cq[0]:cq[-1]])
+
+
+def test_few_rows_nan_in_the_sequence_reaches_its_rows():
+    q, k, v, cq, ck = inputs([4, 4], [3000, 3000], 4, 1, seed=19)
+    k[100] = float("nan")
+    out = canaries(q.shape)
+    da.decode_attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), offsets(cq), offsets(ck), out, SCALE)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[:4]).all() and torch.isfinite(out[4:]).all()
+
+
+def test_few_rows_captured_with_other_lengths():
+    """The cut follows the lengths on the device: a captured call serves other ones."""
+    q, k, v, cq, ck = inputs([6, 6], [2000, 2000], 8, 2, seed=20)
+    dq, dk, dv, oq, ok = q.to(DEV), k.to(DEV), v.to(DEV), offsets(cq), offsets(ck)
+    out = canaries(q.shape)
+    da.decode_attn_prefill(dq, dk, dv, oq, ok, out, SCALE)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        da.decode_attn_prefill(dq, dk, dv, oq, ok, out, SCALE)
+    for cq, ck in (([0, 1, 12], [0, 3900, 4000]), ([0, 12, 12], [0, 100, 4000]), ([0, 6, 12], [0, 2000, 4000])):
+        oq.copy_(offsets(cq))
+        ok.copy_(offsets(ck))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, tol, _ = prefill_ref(q, k, v, cq, ck, SCALE)
+        assert_within(out.cpu(), ref, tol, f"{cq} {ck}")
+
+
 def test_many_short_sequences():
     """1000 sequences, most of them empty: far fewer work items than there could be."""
     lq = [0] * 1000
