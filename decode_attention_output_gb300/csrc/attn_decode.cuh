@@ -62,6 +62,9 @@
 //    codes, and w 2^-e enters the sum. A token's weight in P.V is then never small because
 //    some other token's V is large, the exponents cost no instruction (two multiplies become
 //    fused multiply-adds), and partial states merge as they do elsewhere, r in m's place.
+//    Four producer lanes share its smaller copies. Measured: batch 64 x 16k 318 us (7.0 TB/s),
+//    ragged batch of 32 in blocks of 16 186 us (6.0 TB/s; two producers and a copy per tensor:
+//    253 us).
 #pragma once
 #include <type_traits>
 

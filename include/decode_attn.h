@@ -17,7 +17,8 @@
  * head, K = kv_len, N = 128; output_proj: M = batch, K = heads * 128,
  * N = hidden). Head dim 256 is the page's other GQA decode (section "仓库源码
  * 佐证": QK^T contracts D = 256 in two halves of 128, attn.V has N = D = 256);
- * every entry point takes D = 128 or D = 256, read from q's last extent.
+ * every entry point takes D = 128 or D = 256, read from q's last extent (those over an
+ * fp8 cache and decode_attn_prefill: D = 128).
  *
  * Conventions shared by every entry point
  *  - Every tensor argument is a da_tensor_t descriptor. Its data pointer is a
@@ -261,6 +262,8 @@ int decode_attn_only_paged_fp8(const da_tensor_t* q, const da_tensor_t* k_pages,
  * Requires Hq % Hkv == 0, Hq / Hkv <= 16, B <= 1024, D = 128 (256 returns DA_ERR_UNSUPPORTED);
  * out 16-byte aligned with strides multiples of 8 elements, like the inputs.
  * The softmax weights enter P.V as bf16, unnormalised; sums and the accumulation are fp32.
+ * With few queries over many keys the keys are cut into parts that meet in the workspace
+ * (by Tq, Tk, B and the head counts, not by the lengths); results do not depend on timing.
  */
 int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v,
                         const da_tensor_t* cu_seqlens_q, const da_tensor_t* cu_seqlens_k, const da_tensor_t* out,
