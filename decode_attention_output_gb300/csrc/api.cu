@@ -1266,7 +1266,7 @@ int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_ten
   if (B < 0 || ck->shape[0] != B + 1) return DA_ERR_SHAPE;
   if (D != kHeadDim || Hq / Hkv > kMaxGroup || B > DA_MAX_BATCH) return DA_ERR_UNSUPPORTED;
   if (Tq > (1 << 30) || Tk > (1 << 30) || Hq > (1 << 20)) return DA_ERR_UNSUPPORTED;
-  if (!std::isfinite(scale)) return DA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale * 1.4426950408889634f)) return DA_ERR_UNSUPPORTED;
   for (const da_tensor_t* t : {cq, ck}) {
     if (!t->data) return DA_ERR_NULL;
     if (B > 0 && t->stride[0] != 1) return DA_ERR_STRIDE;

@@ -251,12 +251,13 @@ int decode_attn_only_paged_fp8(const da_tensor_t* q, const da_tensor_t* k_pages,
  *     cu_seqlens_q[b] .. cu_seqlens_q[b + 1] of q and out, and rows cu_seqlens_k[b] ..
  *     cu_seqlens_k[b + 1] of k and v: Lq queries, which are the LAST Lq of its Lk tokens
  *     (Lq < Lk: a prompt whose beginning is cached already, see decode_attn_cache_read)
- *   scale  softmax scale, any finite float
+ *   scale  softmax scale, any float (its product with log2 e finite)
  *
  * Query i of a sequence (0 <= i < Lq) attends keys j <= i + Lk - Lq; query head h attends with
  * KV head h / (Hq / Hkv). A query without a key (Lk < Lq: the first Lq - Lk ones) gives a row
- * of zeros. Rows of q that belong to no sequence are left as they were in out. Offsets are
- * clamped to [0, Tq] and [0, Tk]; a sequence whose end is not after its start is empty.
+ * of zeros. Rows of q that belong to no sequence are left as they were in out. Offsets must
+ * not decrease; they are clamped to [0, Tq] and [0, Tk], and whatever they hold nothing but
+ * rows of out is written (where they do decrease, which rows is unspecified).
  * Other sequences' rows never reach a sequence's output, whatever they hold; a NaN or infinity
  * in a sequence's own k or v can make any output row of that sequence and KV head non-finite.
  * Requires Hq % Hkv == 0, Hq / Hkv <= 16, B <= 1024, D = 128 (256 returns DA_ERR_UNSUPPORTED);

@@ -63,6 +63,7 @@ def test_prefill_rejects(lib, name, over, code):  # noqa: F811
 def test_prefill_scale_and_empty(lib):  # noqa: F811
     assert call_prefill(lib, prefill_args(), scale=float("inf")) == UNSUP
     assert call_prefill(lib, prefill_args(), scale=float("nan")) == UNSUP
+    assert call_prefill(lib, prefill_args(), scale=3e38) == UNSUP  # times log2 e: no float
     a = prefill_args(Tq=0, Tk=0)
     for n in ("q", "k", "v", "out"):
         a[n].data = None

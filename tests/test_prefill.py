@@ -194,6 +194,17 @@ def test_few_rows_nan_in_the_sequence_reaches_its_rows():
     assert torch.isnan(out[:4]).all() and torch.isfinite(out[4:]).all()
 
 
+def test_few_rows_with_offsets_of_any_kind_stay_inside():
+    q, k, v, _, _ = inputs([30], [3000], 4, 1, seed=21)
+    before = canaries((32, 4, 128))
+    for cq, ck in (([20, 5, 30], [0, 3000, 10]), ([2 ** 31 - 1, -2 ** 31, 7], [-9, 1 << 30, 3]), ([0, 30, 0], [3000, 0, 3000])):
+        out = before.clone()
+        da.decode_attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), offsets(cq), offsets(ck), out[1:31], SCALE)
+        torch.cuda.synchronize()
+        assert da.decode_attn_last_device_error() == 0
+        assert torch.equal(out[[0, 31]].view(torch.int16), before[[0, 31]].view(torch.int16))
+
+
 def test_few_rows_captured_with_other_lengths():
     """The cut follows the lengths on the device: a captured call serves other ones."""
     q, k, v, cq, ck = inputs([6, 6], [2000, 2000], 8, 2, seed=20)
