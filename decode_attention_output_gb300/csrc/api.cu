@@ -541,14 +541,21 @@ int max_active_clusters(int cs) {
   return cache[dev][cs];
 }
 
+// `per_seq` (paged fp8 caches): the four-tiles rule is about long sequences' merges, while several
+// short sequences on one CTA pay for the end of each (47 of one token: 23 us on 12 CTAs, 8 on 47).
+// So, where there are SMs, at least a CTA per (batch, KV head) sequence, and with ragged lengths
+// two (or a tile each): an even split over one per sequence cuts most of them, and a CTA then
+// has two ends (48 of one or two tiles: 20 us on 48 CTAs, 13 on 72).
 AttnPlan plan_attention(const AttnShape& s, const Options& o, int tile_tok = 0, bool fused = false,
-                        ClusterUse clustered = ClusterUse::kNever) {
+                        ClusterUse clustered = ClusterUse::kNever, bool per_seq = false) {
   AttnPlan pl;
   const int sms = std::max(1, sm_count());
   if (tile_tok <= 0) tile_tok = tile_tokens(s.D);
   const long long seqs = (long long)s.B * s.Hkv, tiles_seq = (s.Lcap + tile_tok - 1) / tile_tok;
   const long long tiles = seqs * tiles_seq;
-  const int auto_grid = fused ? sms : (int)std::max<long long>(1, std::min<long long>(sms, (tiles + 3) / 4));
+  const long long least = !per_seq ? 0 : (s.B == 1 ? seqs : std::min(tiles, 2 * seqs));
+  const int auto_grid =
+      fused ? sms : (int)std::max<long long>(1, std::min<long long>(sms, std::max((tiles + 3) / 4, least)));
   // at most kMaxAttnCtas workers: a sequence then has at most that many parts, whose merge
   // weights fit the kernel's merge scratch
   pl.grid = std::min(o.attn_ctas > 0 ? (int)o.attn_ctas : auto_grid, kMaxAttnCtas);
@@ -942,7 +949,7 @@ int only_checked(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* 
   if (s.B == 0) return DA_OK;
   const Options o = options_snapshot();
   const bool fp8 = kv8 || (paged && paged->scales);
-  const AttnPlan pl = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_only(o));
+  const AttnPlan pl = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_only(o), paged && paged->scales);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = nullptr;
   DA_TRY(workspace_get(pl.bytes, st, &ws));
@@ -966,7 +973,7 @@ int fwd_checked(const da_tensor_t* q, const da_tensor_t* k_cache, const da_tenso
   if (s.B == 0) return DA_OK;
   const Options o = options_snapshot();
   const bool fp8 = kv8 || (paged && paged->scales);
-  const AttnPlan ap = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_fwd(o));
+  const AttnPlan ap = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_fwd(o), paged && paged->scales);
   const size_t attn_bytes = align_up((size_t)s.B * K * 2, 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const AttnPlan fap = plan_attention(s, o, 0, true);

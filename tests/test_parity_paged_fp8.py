@@ -112,6 +112,18 @@ def test_split_counts(ctas):
         da.decode_attn_set_option("attn_ctas", old)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(16, 1), (12, 1), (8, 1), (3, 1), (2, 2)])
+@pytest.mark.parametrize("ctas", [0, 30, 500])
+def test_sequences_in_many_parts(Hq, Hkv, ctas):
+    """Ragged lengths on the flat grid: a long sequence's parts meet through L2, up to 70 and 500 of them."""
+    old = da.decode_attn_get_option("attn_ctas")
+    da.decode_attn_set_option("attn_ctas", ctas)
+    try:
+        check(case(3, Hq, Hkv, [9000, 5, 1300], 64, seed=14), f"{Hq} heads")
+    finally:
+        da.decode_attn_set_option("attn_ctas", old)
+
+
 def test_token_major_pool_views_and_padded_table():
     x = case(2, 8, 2, [250, 100], 32, seed=7)
     out, _ = check(x, "plain")
