@@ -1292,10 +1292,13 @@ int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_ten
     DA_TRY(encode_packed_map(&p.tm_k, k, 128, 0));
     DA_TRY(encode_packed_map(&p.tm_v, v, 128, 0));
   }
-  // Fewer items than half the SMs: parts of about four K/V tiles or more (by the average
-  // length), as many as there are SMs for.
-  const int64_t sms = std::max(1, sm_count()), tiles = (Tk / B + 127) / 128;
-  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({sms / items, tiles / 4, (int64_t)kMaxPrefillParts}));
+  // Fewer items than half the SMs, and sequences long enough to gain (a ragged one may be
+  // twice the average): as many parts as there are SMs for; the kernel cuts an item into fewer
+  // where it has few K/V tiles.
+  const int64_t sms = std::max(1, sm_count()), tiles = std::min<int64_t>((Tk + 127) / 128, 2 * ((Tk / B + 127) / 128));
+  p.parts = tiles < kPrefillCutTiles
+                ? 1
+                : (int)std::max<int64_t>(1, std::min<int64_t>({sms / items, tiles / kPrefillPartTiles, (int64_t)kMaxPrefillParts}));
   const size_t rows = p.parts > 1 ? (size_t)p.parts * Tq * Hq : 0, ml_bytes = align_up(rows * 2 * 4, 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = nullptr;

@@ -227,7 +227,7 @@ cudaError_t launch_attention_paged_fp8(const AttnParams& p, int grid, int nb, cu
 int attn_max_active_clusters(int cluster);
 
 // ------------------------------------------------------------ prompt attention
-constexpr int kMaxPrefillParts = 32;
+constexpr int kMaxPrefillParts = 32, kPrefillPartTiles = 4, kPrefillCutTiles = 12;
 struct PrefillParams {
   CUtensorMap tm_q;  // q [Tq][Hq][128] bf16: box 64 dims x G heads x npos tokens, 128B swizzle
   CUtensorMap tm_k;  // k, v [Tk][Hkv][128]: box 64 dims x 128 tokens x both halves of the dims

@@ -264,7 +264,7 @@ int decode_attn_only_paged_fp8(const da_tensor_t* q, const da_tensor_t* k_pages,
  * out 16-byte aligned with strides multiples of 8 elements, like the inputs.
  * The softmax weights enter P.V as bf16, unnormalised; sums and the accumulation are fp32.
  * With few queries over many keys the keys are cut into parts that meet in the workspace
- * (by Tq, Tk, B and the head counts, not by the lengths); results do not depend on timing.
+ * (by Tq, Tk, B, the head counts and the sequence's own lengths); results do not depend on timing.
  */
 int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v,
                         const da_tensor_t* cu_seqlens_q, const da_tensor_t* cu_seqlens_k, const da_tensor_t* out,

@@ -185,6 +185,21 @@ def test_few_rows_over_many_keys(lq, lk, Hq, Hkv):
     assert torch.equal(again.cpu()[cq[0]:cq[-1]], out[cq[0]:cq[-1]])
 
 
+MIXED_CUT = [  # items of one call on both sides of the length from which they are cut (twelve tiles)
+    ([1700], [1700], 4, 1),                    # a prompt: its first rows' items whole, the last ones cut
+    ([2000], [1900], 2, 1),                    # and its first hundred rows without a key
+    ([3, 3, 3, 3], [1408, 1409, 1536, 1537], 8, 2),
+    ([1, 700, 1], [2900, 700, 1411], 4, 2),
+]
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hkv", MIXED_CUT, ids=[str(i) for i in range(len(MIXED_CUT))])
+def test_whole_and_cut_items_in_one_call(lq, lk, Hq, Hkv):
+    q, k, v, cq, ck = inputs(lq, lk, Hq, Hkv, seed=22, first=1, spare=3)
+    check(q, k, v, cq, ck, SCALE, "whole and cut")
+    check(q, (k.float() * torch.linspace(0, 6, len(k))[:, None, None]).to(torch.bfloat16), v, cq, ck, SCALE, "growing keys")
+
+
 def test_few_rows_nan_in_the_sequence_reaches_its_rows():
     q, k, v, cq, ck = inputs([4, 4], [3000, 3000], 4, 1, seed=19)
     k[100] = float("nan")
