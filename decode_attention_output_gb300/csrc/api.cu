@@ -501,6 +501,9 @@ struct AttnPlan {
   long long slots;  // split-KV partial slots in the scratch
   int cluster;    // > 1: CTAs per sequence in cluster mode
   int flat_grid;  // the grid without cluster mode (the fall-back if a cluster launch is refused)
+  bool even;            // paged fp8, automatic grid: equal lengths get as many CTAs each
+  int chip_tiles;       // ... and cluster mode only up to this length
+  int seq_least;        // ... and, where there are tiles, at least so many CTAs each
   size_t part_o_off, part_ml_off, bytes;
 };
 
@@ -542,18 +545,19 @@ int max_active_clusters(int cs) {
 }
 
 // `per_seq` (paged fp8 caches): the four-tiles rule is about long sequences' merges, while several
-// short sequences on one CTA pay for the end of each (47 of one token: 23 us on 12 CTAs, 8 on 47).
-// So, where there are SMs, at least a CTA per (batch, KV head) sequence, and with ragged lengths
-// two (or a tile each): an even split over one per sequence cuts most of them, and a CTA then
-// has two ends (48 of one or two tiles: 20 us on 48 CTAs, 13 on 72).
+// short sequences on one CTA pay for the end of each (47 of one token: 23 us on 12 CTAs, 8 on 47),
+// and cut ones as much (ragged: 38 of two to three tiles 15.2 us on 76 CTAs, 9.8 on 114; 12 of
+// three to six 10.5 on 24, 7.8 on 72). So up to 16 tiles of capacity a CTA per tile where there are
+// SMs; above (4 of 24 to 48 tiles: 9.9 us on 48 CTAs, 13.0 on 152) two per sequence at least.
+// Sequences of equal length then take a number of CTAs each that the kernel chooses by length.
 AttnPlan plan_attention(const AttnShape& s, const Options& o, int tile_tok = 0, bool fused = false,
-                        ClusterUse clustered = ClusterUse::kNever, bool per_seq = false) {
+                        ClusterUse clustered = ClusterUse::kNever, bool per_seq = false, bool step = false) {
   AttnPlan pl;
   const int sms = std::max(1, sm_count());
   if (tile_tok <= 0) tile_tok = tile_tokens(s.D);
   const long long seqs = (long long)s.B * s.Hkv, tiles_seq = (s.Lcap + tile_tok - 1) / tile_tok;
   const long long tiles = seqs * tiles_seq;
-  const long long least = !per_seq ? 0 : (s.B == 1 ? seqs : std::min(tiles, 2 * seqs));
+  const long long least = !per_seq ? 0 : (tiles_seq <= 16 ? tiles : std::min(tiles, 2 * seqs));
   const int auto_grid =
       fused ? sms : (int)std::max<long long>(1, std::min<long long>(sms, std::max((tiles + 3) / 4, least)));
   // at most kMaxAttnCtas workers: a sequence then has at most that many parts, whose merge
@@ -569,17 +573,42 @@ AttnPlan plan_attention(const AttnShape& s, const Options& o, int tile_tok = 0, 
   // sequences whose parts fall in one cluster merge on chip.
   pl.cluster = 0;
   pl.flat_grid = pl.grid;
+  pl.even = per_seq && o.attn_ctas == 0;
+  pl.chip_tiles = 0;
+  // Before a batch's projection, 64 CTAs or more where there are tiles for them: its W_o loads
+  // start beside the attention, and fewer CTAs with several tiles each wait behind them (16
+  // sequences of 512 tokens: 19.9 us a step on 16 CTAs, 20.4 on 32, 14.7 on 64; 32: 19.8 on 32, 15.9
+  // on 64; 64: 15.9 on 64, 17.4 on 128).
+  pl.seq_least = 1;
+  while (step && s.B > 1 && seqs * pl.seq_least < 64) pl.seq_least *= 2;
   const bool small = tiles <= 4ll * sms;
   const bool cluster_ok = (clustered == ClusterUse::kAny || (clustered == ClusterUse::kLarge && !small)) &&
                           attn_smem_bytes(s.B, s.G <= 8 ? 1 : 2, 4, s.D, kStageBytes, true) <= kMaxDynSmem;
   if (!fused && cluster_ok && o.attn_ctas == 0 && 2 * seqs <= sms) {
-    const long long cs = std::min<long long>({(long long)kMaxAttnCluster, sms / seqs, (tiles_seq + 1) / 2});
+    long long cs = std::min<long long>({(long long)kMaxAttnCluster, sms / seqs, (tiles_seq + 1) / 2});
+    if (pl.even) {
+      // Few long sequences leave most SMs idle in clusters of eight (one of 32768 tokens 28.2 us,
+      // 15.8 on 32 CTAs). Where a CTA would hold four tiles more than outside cluster mode, and
+      // where so many clusters are not resident at once, clusters of four or fewer, which fill
+      // the SMs: short sequences then still merge on chip, and the kernel takes the flat split
+      // for long ones.
+      const int k = seq_parts((int)tiles_seq, (int)std::max<long long>(1, pl.grid / seqs), pl.seq_least);
+      if (cs > 4 && (tiles_seq + cs - 1) / cs - (tiles_seq + k - 1) / k >= 4) cs = 4;
+      while (cs > 1 && max_active_clusters((int)cs) < seqs) cs = cs > 4 ? 4 : cs - 1;
+    }
     if (cs >= 2) {
       const long long want = std::max<long long>(seqs, (pl.grid + cs - 1) / cs);  // clusters
       const long long n = std::min<long long>(want, max_active_clusters((int)cs));
       if (n >= seqs) {
         pl.cluster = (int)cs;
         pl.grid = (int)(n * cs);
+        // cluster mode while a CTA holds fewer than four tiles more than outside it with k CTAs
+        // per sequence, and at most eight more than with the tiles split over all CTAs
+        const long long k = std::min<long long>(pl.grid / seqs, 64), used = seqs * cs;
+        long long most = 1ll << 30;
+        if (k > cs) most = (4 * cs * k - 1) / (k - cs);
+        if (pl.grid > used) most = std::min(most, 8 * cs * pl.grid / (pl.grid - used));
+        pl.chip_tiles = (int)most;
       }
     }
   }
@@ -919,6 +948,20 @@ int run_attention(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t*
     const int flat = std::min(grid, p.attn_workers);
     set_split_divisor(p, 0, flat);
     set_split_divisor(p, 1, p.cluster > 1 ? (int)std::min<long long>(flat, (long long)s.B * s.Hkv * p.cluster) : flat);
+    if (pl.even) {
+      const long long seqs = (long long)s.B * s.Hkv;
+      p.seq_ctas = (int)(flat / seqs);
+      p.chip_row_tiles = (int)std::min<long long>((long long)pl.chip_tiles * s.Hkv, 1 << 30);
+      p.seq_least = pl.seq_least;
+      // A whole number of CTAs per sequence spares many CTAs the ends of two sequences (3 to 4 us),
+      // and wins while a CTA then holds at most eight tiles more than with all CTAs at work (96
+      // sequences of 1024 tokens, one CTA each: 12.1 us against 16.5; of 2048 17.3 and 19.5; of
+      // 4096 27.9 and 26.5).
+      const long long used = seqs * p.seq_ctas;
+      p.even_tiles = flat > used ? (int)std::min(8ll * p.seq_ctas * flat / (flat - used), 1ll << 30) : 1 << 30;
+      if (p.cluster <= 1 && p.seq_ctas > 0)
+        set_split_divisor(p, 1, (int)(seqs * seq_parts((int)((s.Lcap + tile_tok - 1) / tile_tok), p.seq_ctas, p.seq_least)));
+    }
     return paged8  ? launch_attention_paged_fp8(p, grid, pl.nb, stream)
            : kv8   ? launch_attention_fp8(p, grid, pl.nb, stream)
            : paged ? launch_attention_paged(p, grid, pl.nb, s.D, stream)
@@ -973,7 +1016,7 @@ int fwd_checked(const da_tensor_t* q, const da_tensor_t* k_cache, const da_tenso
   if (s.B == 0) return DA_OK;
   const Options o = options_snapshot();
   const bool fp8 = kv8 || (paged && paged->scales);
-  const AttnPlan ap = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_fwd(o), paged && paged->scales);
+  const AttnPlan ap = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_fwd(o), paged && paged->scales, true);
   const size_t attn_bytes = align_up((size_t)s.B * K * 2, 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const AttnPlan fap = plan_attention(s, o, 0, true);

@@ -179,17 +179,37 @@ struct AttnParams {
   // tiles are split over the CTAs as always, and a sequence whose parts all lie in one
   // cluster merges them in distributed shared memory (the others through L2).
   int cluster;
+  // Paged fp8 caches, sequences of equal length: cluster mode while a batch row has at most
+  // chip_row_tiles tiles (of all its KV heads); otherwise seq_parts(tiles, seq_ctas, seq_least) CTAs
+  // each (seq_ctas = workers / sequences; 0: the tiles split over all workers), unless that is
+  // seq_ctas and a sequence has more than even_tiles tiles.
+  int chip_row_tiles, seq_ctas, seq_least, even_tiles;
   int pdl;  // 1: launched with programmatic dependent launch (waits before any global access)
   // > 0: each CTA lets the next kernel launch when it reaches the tile this many before the
   // end of its range; 0: right after set-up
   int trigger_at;
   // floor(n / d) = (n * split_mul) >> split_shift, exact for 0 <= n < 2^31, for the two worker
   // counts d that split the tiles over the CTAs: [0] min(grid, attn_workers), [1] (cluster
-  // mode) min(that, B * Hkv * cluster). A worker count that differs is divided the plain way.
+  // mode) min(that, B * Hkv * cluster), or (paged fp8 outside it) the CTAs of full sequences by
+  // seq_parts. A worker count that differs is divided the plain way.
   unsigned long long split_mul[2];
   int split_div[2], split_shift[2];
 };
 constexpr int kMaxAttnCluster = 8;  // portable cluster size
+
+// CTAs for each of several sequences of `tiles` 128-token tiles, `most` at hand for each: one up
+// to four tiles (a tile per group of warps); then parts of two tiles, of four from eight parts on,
+// and more than 64 parts only once they hold 16 tiles, as the one CTA that joins a sequence's
+// parts pays for each (one sequence of 8192 tokens: 10.6 us in 16 parts, 11.0 in 32, 13.8 in 64;
+// of 131072: 24.8 in 64, 28.5 in 152). At least `least` where there are tiles for them.
+__host__ __device__ inline int seq_parts(int tiles, int most, int least) {
+  const int small = tiles / 2 < 8 ? tiles / 2 : 8, mid = tiles / 4 < 64 ? tiles / 4 : 64, large = tiles / 16;
+  int k = tiles <= 4 ? 1 : (small > mid ? small : mid);
+  k = k > large ? k : large;
+  const int low = least < tiles ? least : tiles;
+  k = k > low ? k : low;
+  return k < most ? k : most;
+}
 
 // Paged caches: a power of two from 8 tokens (tiles are cut into blocks, or blocks hold
 // whole tiles; the producer's index arithmetic is shifts and masks).

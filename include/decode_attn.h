@@ -339,7 +339,9 @@ int decode_attn_oproj(const da_tensor_t* attn_flat, const da_tensor_t* o_weight,
  * Tuning options (process-wide; 0 = automatic). Keys:
  *   "attn_ctas"     CTAs of the persistent attention kernel (0: one per SM, fewer for
  *                   small problems: about four tiles each by the cache capacity;
- *                   at most 512)
+ *                   at most 512; paged fp8 caches: a tile each up to 16 tiles of
+ *                   capacity a sequence, and with equal lengths only as many work
+ *                   as give each sequence the same number; a set count is kept)
  *   "oproj_path"    0 auto, 1 CUDA-core GEMV, 2 tcgen05 tensor-core GEMM, 3 (decode_attn_fwd
  *                   at batch 1) o_weight staged in the shared memory and registers of the
  *                   SMs the attention leaves free while the attention runs, then a CUDA-core
@@ -356,6 +358,9 @@ int decode_attn_oproj(const da_tensor_t* attn_flat, const da_tensor_t* o_weight,
  *                   only the sequences whose parts fall in one cluster merge on
  *                   chip (the rest through L2). 2: as 1, and decode_attn_fwd
  *                   takes clusters at every size too. 0: always the flat grid.
+ *                   Paged fp8 caches: clusters of 4 where few sequences have a
+ *                   long capacity, and on chip only while they are short, as 8
+ *                   CTAs a sequence would leave the other SMs idle.
  *                   Results agree within the rounding of the merge order.
  *   "oproj_cluster" 1 (default): the split-K slices of a tcgen05 column tile form a
  *                   thread-block cluster and reduce in distributed shared memory

@@ -124,6 +124,48 @@ def test_sequences_in_many_parts(Hq, Hkv, ctas):
         da.decode_attn_set_option("attn_ctas", old)
 
 
+# (B, Hq, Hkv, length of each, capacity): how many CTAs a sequence gets, and whether its parts meet on chip
+# or through L2, follows the common length and the capacity
+EQUAL = [
+    (1, 4, 1, 9000, 9000), (1, 16, 1, 700, 40000), (1, 2, 1, 2300, 40000), (1, 2, 1, 2305, 40000),  # one long sequence
+    (2, 4, 2, 5000, 20000), (2, 4, 2, 129, 20000), (4, 8, 4, 4096, 4096), (6, 8, 2, 3000, 9000),
+    (9, 6, 2, 3500, 3500), (25, 8, 2, 513, 513), (25, 2, 2, 1500, 1500),  # 18 and 50 sequences: no divisors of the SMs
+    (48, 2, 2, 512, 512), (48, 4, 2, 700, 700), (32, 2, 2, 1, 2048), (5, 8, 8, 256, 256), (100, 2, 2, 200, 200),
+    (3, 4, 2, 0, 2048),
+]
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,n,most", EQUAL, ids=[f"{e[0]}x{e[2]}x{e[3]}" for e in EQUAL])
+def test_equal_lengths(B, Hq, Hkv, n, most):
+    x = case(B, Hq, Hkv, [n] * B, 64, seed=15, max_blocks=-(-most // 64))
+    out, _ = check(x, "equal")
+    again, _ = check(x, "equal again")
+    assert torch.equal(out, again)  # nothing depends on which CTA is last
+    one = list(x[5])
+    one[-1] = max(0, n - 200)  # ragged now: the tiles split over every CTA
+    check((*x[:5], one), "one shorter")
+
+
+def test_captured_call_serves_short_long_equal_and_ragged_lengths():
+    B, most = 4, 12000
+    x = case(B, 8, 2, [most] * B, 64, seed=16)
+    a = on(x)
+    out = torch.empty(x[0].shape, dtype=torch.bfloat16, device=DEV)
+    da.decode_attn_only_paged_fp8(*a, out, SCALE)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        da.decode_attn_only_paged_fp8(*a, out, SCALE)
+    for n in ([most] * 4, [1] * 4, [2048] * 4, [2304] * 4, [2305] * 4, [6000, 1, 0, 3000], [0] * 4, [most, 1, 1, 1], [512] * 4):
+        a[5].copy_(torch.tensor(n, dtype=torch.int32))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert da.decode_attn_last_device_error() == 0
+        ref, tol = token_ref(*x[:5], n, SCALE)
+        assert_within(out.cpu(), ref, tol, f"lengths {n}")
+
+
 def test_token_major_pool_views_and_padded_table():
     x = case(2, 8, 2, [250, 100], 32, seed=7)
     out, _ = check(x, "plain")
@@ -197,6 +239,23 @@ def test_whole_step(B, N):
     ref, tol, w = ref.reshape(B, -1), tol.reshape(B, -1), w.to(F64)
     want = ref @ w
     # the attention's bound through W, K = 2048 products in fp32 (2^-23 of each partial sum), the output's bf16
+    bound = tol @ w.abs() + Hq * 128 * 2.0 ** -23 * (ref.abs() @ w.abs()) + 2.0 ** -8 * want.abs()
+    assert_within(out.cpu(), want, bound * 1.01, "step")
+
+
+@pytest.mark.parametrize("B,n", [(1, 3000), (2, 512), (3, 512), (4, 256), (5, 500), (8, 512), (16, 300), (2, 9000)])
+def test_whole_step_equal_lengths(B, n):
+    Hq, Hkv, N = 16, 8, 264
+    x = case(B, Hq, Hkv, [n] * B, 64, seed=17)
+    ref, tol = token_ref(*x, SCALE)
+    g = torch.Generator().manual_seed(18)
+    w = (torch.randn((Hq * 128, N), generator=g) / math.sqrt(Hq * 128)).to(torch.bfloat16)
+    out = torch.empty((B, N), dtype=torch.bfloat16, device=DEV)
+    da.decode_attn_fwd_paged_fp8(*on(x), w.to(DEV), out, SCALE)
+    torch.cuda.synchronize()
+    assert da.decode_attn_last_device_error() == 0
+    ref, tol, w = ref.reshape(B, -1), tol.reshape(B, -1), w.to(F64)
+    want = ref @ w  # bounds as above
     bound = tol @ w.abs() + Hq * 128 * 2.0 ** -23 * (ref.abs() @ w.abs()) + 2.0 ** -8 * want.abs()
     assert_within(out.cpu(), want, bound * 1.01, "step")
 
