@@ -954,13 +954,13 @@ int run_attention(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t*
       p.chip_row_tiles = (int)std::min<long long>((long long)pl.chip_tiles * s.Hkv, 1 << 30);
       p.seq_least = pl.seq_least;
       // A whole number of CTAs per sequence spares many CTAs the ends of two sequences (3 to 4 us),
-      // and wins while a CTA then holds at most eight tiles more than with all CTAs at work (96
-      // sequences of 1024 tokens, one CTA each: 12.1 us against 16.5; of 2048 17.3 and 19.5; of
-      // 4096 27.9 and 26.5).
-      const long long used = seqs * p.seq_ctas;
-      p.even_tiles = flat > used ? (int)std::min(8ll * p.seq_ctas * flat / (flat - used), 1ll << 30) : 1 << 30;
-      if (p.cluster <= 1 && p.seq_ctas > 0)
-        set_split_divisor(p, 1, (int)(seqs * seq_parts((int)((s.Lcap + tile_tok - 1) / tile_tok), p.seq_ctas, p.seq_least)));
+      // and wins while the longest one's CTAs then hold at most eight tiles more than with all
+      // CTAs at work (96 sequences of 1024 tokens, one CTA each: 12.1 us against 16.5; of 2048 17.3
+      // and 19.5; of 4096 27.9 and 26.5), six with ragged lengths (148 of 147 to 295 tokens 10.4 and
+      // 24.3; 24 of 2533 to 5067 21.6 and 26.7; 64 of 5311 to 7082, 7.6 tiles more, 27.0 and 26.0).
+      p.own_slope = (float)p.seq_ctas / (float)flat;
+      p.own_slack[0] = 8.f * (float)p.seq_ctas;
+      p.own_slack[1] = 6.f * (float)p.seq_ctas;
     }
     return paged8  ? launch_attention_paged_fp8(p, grid, pl.nb, stream)
            : kv8   ? launch_attention_fp8(p, grid, pl.nb, stream)

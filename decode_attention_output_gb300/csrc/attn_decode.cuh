@@ -34,10 +34,10 @@
 //    of one cluster, which merge their partial states through distributed shared memory
 //    after a cluster barrier instead of through L2; with unequal lengths the kernel keeps
 //    the flat split and the L2 merge, and no CTA waits at a cluster barrier.
-//  * Paged fp8 caches: equal lengths outside cluster mode take a whole number of CTAs per
-//    sequence (seq_parts in kernels.h), and few long sequences leave cluster mode, both by
-//    the lengths on the device: one sequence of 131072 tokens 91.9 -> 24.4 us, 96 of 1024
-//    16.4 -> 12.3, 18 of 8192 18.4 -> 15.0 (the set-up takes 0.1 us more).
+//  * Paged fp8 caches: outside cluster mode a whole number of CTAs per sequence (seq_parts in
+//    kernels.h) where the longest one allows it, and few long sequences leave cluster mode,
+//    both by the lengths on the device: one sequence of 131072 tokens 91.9 -> 24.4 us, 96 of
+//    1024 16.4 -> 12.3, 18 of 8192 18.4 -> 15.0 (the set-up takes 0.1 us more).
 //  * Programmatic dependent launch: the kernel waits for the previous kernel in the
 //    stream before its first global access, and lets the next one launch right after its
 //    set-up, or, when the projection follows, a few tiles before the end of its range.
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
   // does before the previous kernel has completed and its writes are visible.
   pdl_wait_primary();
   if (warp == 1) {  // clamped lengths, and tiles per batch row scanned into prefix
-    int carry = 0, v0 = 0;
+    int carry = 0, v0 = 0, longest = 0;  // (longest: tiles of one head's sequence)
     bool unequal = false;  // do the rows differ in tile count?
     for (int base = 0; base < B; base += 32) {
       const int b = base + lane;
@@ -649,6 +649,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
       }
       if (base == 0) v0 = __shfl_sync(0xffffffffu, v, 0);
       unequal |= __any_sync(0xffffffffu, b < B && v != v0);
+      if (kScaled) longest = max(longest, __reduce_max_sync(0xffffffffu, b < B ? (lens[b] + kT - 1) / kT : 0));
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int n = __shfl_up_sync(0xffffffffu, v, off);
@@ -668,24 +669,27 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
     const bool chip = p.cluster > 1 && !unequal && (!kScaled || v0 <= p.chip_row_tiles);
     int workers = min((int)gridDim.x, p.attn_workers);
     if (chip) workers = min(workers, B * Hkv * p.cluster);
-    bool even = false;  // equal lengths outside cluster mode: as many CTAs for each sequence
-    if (kScaled && !chip && !unequal && p.seq_ctas > 0) {
-      const int tiles = (lens[0] + kT - 1) / kT, k = seq_parts(tiles, p.seq_ctas, p.seq_least);
-      even = k < p.seq_ctas || tiles <= p.even_tiles;
-      if (even) workers = min(workers, B * Hkv * k);
+    // > 0: CTAs c * own .. of a launch are sequence c's, a shorter one's the first of them.
+    // Ragged lengths that leave each CTA a tile at most need it only where it spares the merges
+    // (13 x 2 of 106 to 142 tokens, 4 heads each: 5.8 us and 7.8; 16: 8.3 and 13.8), and not where
+    // the projection's loads want many CTAs (a step of 4 x 8 of 100 to 300: 19.6 and 15.7).
+    int own = 0;
+    if (kScaled && !chip && p.seq_ctas > 0 && (!unequal || T > workers || (longest <= 4 && p.seq_least == 1))) {
+      const int k = seq_parts(longest, p.seq_ctas, p.seq_least);
+      if (k < p.seq_ctas || (float)longest <= (float)T * p.own_slope + (unequal ? p.own_slack[1] : p.own_slack[0])) own = k;
     }
     const int P = T > 0 ? min(workers, T) : 1;
     const int cta = blockIdx.x;
     int start = 0, end = 0;
-    if (T > 0 && cta < P) {
+    if (own == 0 && T > 0 && cta < P) {
       if (P == T) {  // one tile each
         start = cta;
         end = cta + 1;
       } else {
         unsigned tq, tr, f0, f1;
-        if (P == (chip || even ? p.split_div[1] : p.split_div[0])) {
-          const unsigned long long m = chip || even ? p.split_mul[1] : p.split_mul[0];
-          const int sh = chip || even ? p.split_shift[1] : p.split_shift[0];
+        if (P == (chip ? p.split_div[1] : p.split_div[0])) {
+          const unsigned long long m = chip ? p.split_mul[1] : p.split_mul[0];
+          const int sh = chip ? p.split_shift[1] : p.split_shift[0];
           tq = div_mul((unsigned)T, m, sh);
           tr = (unsigned)T - tq * (unsigned)P;
           f0 = div_mul((unsigned)cta * tr, m, sh);
@@ -704,7 +708,20 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
     // is non-decreasing: count the rows at or before it, 32 at a time), then the KV head and
     // the tile within the row's share.
     int cb = 0, ckvh = 0, cj = 0, cnt = 1;
-    if (start < end) {
+    if (kScaled && own > 0) {
+      const int seq = div_small(cta, own), part = cta - seq * own, row = div_small(seq, Hkv);
+      if (row < B) {
+        const int nt = (lens[row] + kT - 1) / kT, n = seq_parts(nt, own, p.seq_least);
+        if (part < n && nt > 0) {
+          cb = row;
+          ckvh = seq - row * Hkv;
+          cnt = nt;
+          cj = (int)((unsigned)part * (unsigned)nt / (unsigned)n);
+          start = prefix[row] + ckvh * nt + cj;
+          end = start - cj + (int)((unsigned)(part + 1) * (unsigned)nt / (unsigned)n);
+        }
+      }
+    } else if (start < end) {
       int rows = 0;
       for (int base = 0; base < B; base += 32) {
         const unsigned at = __ballot_sync(0xffffffffu, base + lane < B && prefix[base + lane] <= start);
@@ -741,6 +758,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
       rng[5] = cj;
       rng[6] = cnt;
       rng[7] = chip ? 1 : 0;
+      if (kScaled) flags[4] = own;
     }
   }
   if (kFused) tc_fence_before_sync();
@@ -1315,12 +1333,19 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
         //     two of half d / 128 (warps w0 and w0 + 2, whose partners hold the same softmax
         //     state for the same tokens): thread -> (head, dim)
         const long long F = prefix[b] + (long long)kvh * c.nt;  // first tile of this sequence
-        const int first_cta = cta_of(F, T, P), last_cta = cta_of(F + c.nt - 1, T, P);
-        const int n_parts = last_cta - first_cta + 1;
+        int first_cta, n_parts;
+        const int own = kScaled ? flags[4] : 0;  // (read here: kept, it cost registers)
+        if (kScaled && own > 0) {
+          first_cta = seq * own;
+          n_parts = seq_parts(c.nt, own, p.seq_least);
+        } else {
+          first_cta = cta_of(F, T, P);
+          n_parts = cta_of(F + c.nt - 1, T, P) - first_cta + 1;
+        }
         // Cluster mode: a sequence whose parts all lie in this CTA's cluster leaves its state
         // in shared memory (slot 0 if it is this CTA's first segment, else slot 1) for the
         // on-chip merge after the loop.
-        const bool on_chip = chip && n_parts > 1 && first_cta / cs == last_cta / cs;
+        const bool on_chip = chip && n_parts > 1 && first_cta / cs == (first_cta + n_parts - 1) / cs;
         const int cslot = seg0 == start ? 0 : 1;
         if (on_chip && tid == 0) {  // this CTA merges its share of the sequence's outputs
           int* dt = duty + 4 * cslot;

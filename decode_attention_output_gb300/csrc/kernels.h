@@ -179,19 +179,19 @@ struct AttnParams {
   // tiles are split over the CTAs as always, and a sequence whose parts all lie in one
   // cluster merges them in distributed shared memory (the others through L2).
   int cluster;
-  // Paged fp8 caches, sequences of equal length: cluster mode while a batch row has at most
-  // chip_row_tiles tiles (of all its KV heads); otherwise seq_parts(tiles, seq_ctas, seq_least) CTAs
-  // each (seq_ctas = workers / sequences; 0: the tiles split over all workers), unless that is
-  // seq_ctas and a sequence has more than even_tiles tiles.
-  int chip_row_tiles, seq_ctas, seq_least, even_tiles;
+  // Paged fp8 caches. Sequences of equal length: cluster mode while a batch row has at most
+  // chip_row_tiles tiles (of all its KV heads). Otherwise seq_parts(tiles, seq_ctas, seq_least)
+  // CTAs each (seq_ctas = workers / sequences; 0: the tiles split over all workers), unless the
+  // longest one's would be all seq_ctas and it has more than own_slope * T + own_slack tiles.
+  int chip_row_tiles, seq_ctas, seq_least;
+  float own_slope, own_slack[2];  // (slack: of equal lengths, of ragged ones)
   int pdl;  // 1: launched with programmatic dependent launch (waits before any global access)
   // > 0: each CTA lets the next kernel launch when it reaches the tile this many before the
   // end of its range; 0: right after set-up
   int trigger_at;
   // floor(n / d) = (n * split_mul) >> split_shift, exact for 0 <= n < 2^31, for the two worker
   // counts d that split the tiles over the CTAs: [0] min(grid, attn_workers), [1] (cluster
-  // mode) min(that, B * Hkv * cluster), or (paged fp8 outside it) the CTAs of full sequences by
-  // seq_parts. A worker count that differs is divided the plain way.
+  // mode) min(that, B * Hkv * cluster). A worker count that differs is divided the plain way.
   unsigned long long split_mul[2];
   int split_div[2], split_shift[2];
 };

@@ -340,8 +340,9 @@ int decode_attn_oproj(const da_tensor_t* attn_flat, const da_tensor_t* o_weight,
  *   "attn_ctas"     CTAs of the persistent attention kernel (0: one per SM, fewer for
  *                   small problems: about four tiles each by the cache capacity;
  *                   at most 512; paged fp8 caches: a tile each up to 16 tiles of
- *                   capacity a sequence, and with equal lengths only as many work
- *                   as give each sequence the same number; a set count is kept)
+ *                   capacity a sequence, and where the longest sequence allows it
+ *                   each one gets CTAs of its own; a set count is kept, its tiles
+ *                   split evenly)
  *   "oproj_path"    0 auto, 1 CUDA-core GEMV, 2 tcgen05 tensor-core GEMM, 3 (decode_attn_fwd
  *                   at batch 1) o_weight staged in the shared memory and registers of the
  *                   SMs the attention leaves free while the attention runs, then a CUDA-core

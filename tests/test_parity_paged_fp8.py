@@ -146,6 +146,24 @@ def test_equal_lengths(B, Hq, Hkv, n, most):
     check((*x[:5], one), "one shorter")
 
 
+# (B, Hq, Hkv, lengths, capacity): ragged ones whose sequences keep CTAs of their own, and ones too uneven for it
+RAGGED = [
+    (24, 4, 4, [138 + 6 * b for b in range(24)], 300), (37, 2, 2, [147 + 4 * b for b in range(37)], 300),
+    (13, 32, 8, [254 + 20 * b for b in range(13)], 512), (13, 32, 2, [106 + 3 * b for b in range(13)], 142),
+    (5, 16, 8, [2900, 3000, 0, 2700, 3100], 3200), (24, 4, 1, [800 + 15 * b for b in range(24)], 1200),
+    (24, 4, 1, [1, 0, 5000] * 8, 5000), (3, 16, 1, [9600, 11000, 12000], 12800), (38, 4, 4, [512, 1] * 19, 512),
+    (60, 4, 2, [1 + 9 * b for b in range(60)], 600), (7, 8, 2, [0, 0, 700, 0, 0, 900, 0], 1024), (80, 4, 2, [300] * 79 + [7], 512),
+]
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,lens,most", RAGGED, ids=[str(i) for i in range(len(RAGGED))])
+def test_ragged_lengths(B, Hq, Hkv, lens, most):
+    x = case(B, Hq, Hkv, lens, 32, seed=19, max_blocks=-(-most // 32))
+    out, _ = check(x, "ragged")
+    again, _ = check(x, "ragged again")
+    assert torch.equal(out, again)
+
+
 def test_captured_call_serves_short_long_equal_and_ragged_lengths():
     B, most = 4, 12000
     x = case(B, 8, 2, [most] * B, 64, seed=16)
