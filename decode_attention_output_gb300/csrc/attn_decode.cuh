@@ -61,14 +61,16 @@
 //  * fp8 (e4m3) cache: a warp owns 32 tokens (two 16-row halves, one softmax update);
 //    codes are widened to f16 in registers (exact) for f16 MMAs, q and P in f16.
 //  * Paged fp8 cache: a scale per (token, KV head) for K and one for V, copied with each box
-//    of the tile. With V's scale 2^e m (1 <= m < 2) and x the scaled log2 score, the kernel
-//    takes w = 2^(x + e - r), r the running maximum of x + e: w m (f16) enters P.V with the
-//    codes, and w 2^-e enters the sum. A token's weight in P.V is then never small because
-//    some other token's V is large, the exponents cost no instruction (two multiplies become
-//    fused multiply-adds), and partial states merge as they do elsewhere, r in m's place.
-//    Four producer lanes share its smaller copies. Measured: batch 64 x 16k 318 us (7.0 TB/s),
-//    ragged batch of 32 in blocks of 16 186 us (6.0 TB/s; two producers and a copy per tensor:
-//    253 us).
+//    of the tile. With x the scaled log2 score and vs V's scale, p = 2^(x - m) enters the sum
+//    and p vs 2^(m - r) (f16) enters P.V with the codes, m and r running maxima of x and of
+//    x + log2 vs: P.V's weights keep f16's accuracy whatever V's scales are, and the sum has
+//    every token whose p is at least 2^-126, whatever its V is. At a segment's end O goes over
+//    to m, and partial states merge as they do elsewhere. Four producer lanes share its smaller
+//    copies. Measured: batch 64 x 16k 323 us (6.9 TB/s), ragged batch of 32 in blocks of 16
+//    187 us (6.0 TB/s; two producers and a copy per tensor: 253 us). Up to eight heads a group
+//    the second reference costs no time (against one for both, two fused multiply-adds a
+//    weight: 8 x 8192 29.0 us, 29.6 before; 32 x 1-16384 in blocks of 16 115.9 and 115.0); with
+//    sixteen it does (32 x 8192, 128 / 8 heads: 133.8 us, 130.1 before).
 #pragma once
 #include <type_traits>
 
@@ -85,6 +87,11 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // below 2^kSlack, and most tiles skip the maximum's shuffle reduction and the rescale.
 // Every merge takes a part's reference as its m: the result does not depend on it.
 constexpr float kSlack = 8.f;
+// Paged fp8 caches: a reference that no token has set (finite, so that differences are no NaN).
+constexpr float kNoRef = -3e38f;
+// ... and how far O's reference lies below the largest weight (log2 units): f16 weights then have
+// their full accuracy down to 2^-(14 + kBelow) of it, and 2^(m - r) of the largest V is no subnormal.
+constexpr float kBelow = 5.f;
 
 // Position of the current tile in the flattened tile order.
 struct Cursor {
@@ -134,25 +141,10 @@ __device__ __forceinline__ int cta_of(long long x, long long T, int P) {
 
 __device__ __forceinline__ int clamp_len(int L, int Lcap) { return L < 0 ? 0 : (L > Lcap ? Lcap : L); }
 
-// What the scales (ks, vs) of one token of a paged fp8 cache do to its weight: the scaled
-// log2 score is x = s * k with k = ks * scale * log2 e; with vs = 2^e m the weight in P.V is
-// 2^(x + e - r) m and the share in the sum 2^(x + e - r) * inv with inv = 2^-e. e is kept at
-// -100 at least (below it m shrinks instead), so that inv and a sum of 2^20 tokens stay finite
-// in fp32; a zero scale gives m = 0. Whatever bits stand past a sequence's end, m and inv are
-// finite: their weight 0 stays 0.
-struct TokenScale {
-  float k, e, m, inv;
-};
-__device__ __forceinline__ TokenScale token_scale(float ks, float vs, float sl2) {
-  const uint32_t bits = __float_as_uint(vs);
-  const uint32_t ef = vs == 0.f ? 127u : min(max((bits >> 23) & 0xffu, 27u), 254u);  // e + 127
-  TokenScale t;
-  t.k = ks * sl2;
-  t.e = __uint_as_float(0x4b000000u | ef) - (8388608.f + 127.f);  // 2^23 + ef, exactly
-  t.inv = __uint_as_float((254u - ef) << 23);
-  const float m = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
-  t.m = (bits & 0x7f800000u) >= (27u << 23) ? m : vs * 0x1p100f;
-  return t;
+// floor(log2 |x|) of a finite x (-126 for a subnormal one; kNoRef for 0).
+__device__ __forceinline__ float exponent_of(float x) {
+  const uint32_t ef = max(__float_as_uint(x) >> 23 & 0xffu, 1u);
+  return x == 0.f ? kNoRef : (float)((int)ef - 127);
 }
 
 // Keep the bf16 halves of v whose token index (tok for the low half, tok + 1 for
@@ -888,9 +880,12 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
     uint32_t qf[NB][kKs][2];
     float o[8][NB][4];
     float m_run[NB][2], l_run[NB][2];
+    float r_run[NB][2];  // paged fp8 caches: the reference of O, m_run being the sum's alone
+    constexpr float kNoMax = kScaled ? kNoRef : kNegInf;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      m_run[nb][0] = m_run[nb][1] = kNegInf;
+      m_run[nb][0] = m_run[nb][1] = kNoMax;
+      if (kScaled) r_run[nb][0] = r_run[nb][1] = kNoRef;
       l_run[nb][0] = l_run[nb][1] = 0.f;
 #pragma unroll
       for (int mb = 0; mb < 8; ++mb) o[mb][nb][0] = o[mb][nb][1] = o[mb][nb][2] = o[mb][nb][3] = 0.f;
@@ -1025,91 +1020,145 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
             }
             // ---- online softmax over the 32 tokens (element i of half hh: token
             // 16hh + g + 8(i>>1), head 8nb + 2t + (i&1)); P rounded to f16 for P.V
-            // (paged: the factors of this lane's four tokens; see TokenScale)
-            TokenScale ts[2][2];
+            uint32_t pb[2][NB][2];
             if constexpr (kScaled) {
+              // With x the scaled log2 score (K's scale in it) and vs V's scale, a token's share of
+              // the sum is p = 2^(x - m) and its weight in P.V p vs 2^(m - r), m and r running
+              // maxima of x and of log2 (2^x vs): against one reference for both, a token whose V is
+              // 2^126 times smaller than another's would leave the sum.
               const float* sc = scales + stage * (AttnSmem::kScaleStageBytes / 4);
+              float vs[2][2];
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                  const int tok = tb + 16 * hh + g + 8 * r;
-                  const int at = ((tok >> lbox) << (lbox + 1)) + (tok & ((1 << lbox) - 1));
-                  ts[hh][r] = token_scale(sc[at], sc[at + (1 << lbox)], sl2);
+                  const int tok = 16 * hh + g + 8 * r, at = tb + tok;
+                  const float* one = sc + ((at >> lbox) << (lbox + 1)) + (at & ((1 << lbox) - 1));
+                  const bool have = tok < vw;  // (else the scales may hold anything)
+                  const float k = *one * sl2;
+                  vs[hh][r] = have ? one[1 << lbox] : 0.f;
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) {
+                      float& x = sa[hh][nb][2 * r + cc];
+                      x = have ? x * k : kNegInf;
+                    }
                 }
-            }
-            float xv[NB][2][4];
-            bool grow = false;
+              // (the largest vs with the largest x of the lane's tokens: at least what any has)
+              const float e_top = exponent_of(fmaxf(fmaxf(fabsf(vs[0][0]), fabsf(vs[0][1])), fmaxf(fabsf(vs[1][0]), fabsf(vs[1][1]))));
+              bool grow = false;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+              for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                const bool v0 = 16 * hh + g < vw, v1 = 16 * hh + g + 8 < vw;
-                if constexpr (kScaled) {
-                  xv[nb][hh][0] = v0 ? fmaf(sa[hh][nb][0], ts[hh][0].k, ts[hh][0].e) : kNegInf;
-                  xv[nb][hh][1] = v0 ? fmaf(sa[hh][nb][1], ts[hh][0].k, ts[hh][0].e) : kNegInf;
-                  xv[nb][hh][2] = v1 ? fmaf(sa[hh][nb][2], ts[hh][1].k, ts[hh][1].e) : kNegInf;
-                  xv[nb][hh][3] = v1 ? fmaf(sa[hh][nb][3], ts[hh][1].k, ts[hh][1].e) : kNegInf;
-                } else {
+                for (int cc = 0; cc < 2; ++cc) {
+                  const float top = fmaxf(fmaxf(sa[0][nb][cc], sa[0][nb][cc + 2]), fmaxf(sa[1][nb][cc], sa[1][nb][cc + 2]));
+                  grow |= top > m_run[nb][cc] + kSlack;
+                  grow |= top + e_top > r_run[nb][cc] + (kBelow + kSlack);
+                }
+              if (__any_sync(0xffffffffu, grow)) {  // the references move to the running maxima
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                  for (int cc = 0; cc < 2; ++cc) {
+                    float mx = kNoRef, mr = kNoRef;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const float x = sa[i >> 1][nb][2 * (i & 1) + cc];
+                      mx = fmaxf(mx, x);
+                      mr = fmaxf(mr, x + exponent_of(vs[i >> 1][i & 1]));
+                    }
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) {
+                      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                      mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, off));
+                    }
+                    // whole numbers, so that the factors from one to the next are exact; r stays so
+                    // near m that 2^(m - r) is finite
+                    const float mn = fmaxf(m_run[nb][cc], ceilf(mx));
+                    const float rn = fmaxf(fmaxf(r_run[nb][cc], ceilf(mr) - kBelow), mn - 120.f);
+                    l_run[nb][cc] *= fast_exp2(m_run[nb][cc] - mn);
+                    const float al = fast_exp2(r_run[nb][cc] - rn);
+                    m_run[nb][cc] = mn;
+                    r_run[nb][cc] = rn;
+#pragma unroll
+                    for (int mb = 0; mb < 8; ++mb) {
+                      o[mb][nb][cc] *= al;
+                      o[mb][nb][cc + 2] *= al;
+                    }
+                  }
+              }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const float c0 = fast_exp2(m_run[nb][0] - r_run[nb][0]), c1 = fast_exp2(m_run[nb][1] - r_run[nb][1]);
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r) {
+                    const float p0 = fast_exp2(sa[hh][nb][2 * r] - m_run[nb][0]);
+                    const float p1 = fast_exp2(sa[hh][nb][2 * r + 1] - m_run[nb][1]);
+                    l_run[nb][0] += p0;
+                    l_run[nb][1] += p1;
+                    // (p vs first: with p = 0 it is 0, whatever vs and the factor are)
+                    pb[hh][nb][r] = movmatrix_trans(pack_f16x2(p0 * vs[hh][r] * c0, p1 * vs[hh][r] * c1));  // as below
+                  }
+              }
+            } else {
+              float xv[NB][2][4];
+              bool grow = false;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  const bool v0 = 16 * hh + g < vw, v1 = 16 * hh + g + 8 < vw;
                   xv[nb][hh][0] = v0 ? sa[hh][nb][0] * sl2 : kNegInf;
                   xv[nb][hh][1] = v0 ? sa[hh][nb][1] * sl2 : kNegInf;
                   xv[nb][hh][2] = v1 ? sa[hh][nb][2] * sl2 : kNegInf;
                   xv[nb][hh][3] = v1 ? sa[hh][nb][3] * sl2 : kNegInf;
+                  grow |= fmaxf(xv[nb][hh][0], xv[nb][hh][2]) > m_run[nb][0] + kSlack;
+                  grow |= fmaxf(xv[nb][hh][1], xv[nb][hh][3]) > m_run[nb][1] + kSlack;
                 }
-                grow |= fmaxf(xv[nb][hh][0], xv[nb][hh][2]) > m_run[nb][0] + kSlack;
-                grow |= fmaxf(xv[nb][hh][1], xv[nb][hh][3]) > m_run[nb][1] + kSlack;
+              if (__any_sync(0xffffffffu, grow)) {  // the reference moves to the running maximum
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                  float mx0 = fmaxf(fmaxf(xv[nb][0][0], xv[nb][0][2]), fmaxf(xv[nb][1][0], xv[nb][1][2]));
+                  float mx1 = fmaxf(fmaxf(xv[nb][0][1], xv[nb][0][3]), fmaxf(xv[nb][1][1], xv[nb][1][3]));
+#pragma unroll
+                  for (int off = 4; off < 32; off <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+                  }
+                  const float mn0 = fmaxf(m_run[nb][0], mx0), mn1 = fmaxf(m_run[nb][1], mx1);
+                  const float al0 = fast_exp2(m_run[nb][0] - mn0), al1 = fast_exp2(m_run[nb][1] - mn1);
+                  m_run[nb][0] = mn0;
+                  m_run[nb][1] = mn1;
+                  l_run[nb][0] *= al0;
+                  l_run[nb][1] *= al1;
+#pragma unroll
+                  for (int mb = 0; mb < 8; ++mb) {
+                    o[mb][nb][0] *= al0;
+                    o[mb][nb][1] *= al1;
+                    o[mb][nb][2] *= al0;
+                    o[mb][nb][3] *= al1;
+                  }
+                }
               }
-            if (__any_sync(0xffffffffu, grow)) {  // the reference moves to the running maximum
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                float mx0 = fmaxf(fmaxf(xv[nb][0][0], xv[nb][0][2]), fmaxf(xv[nb][1][0], xv[nb][1][2]));
-                float mx1 = fmaxf(fmaxf(xv[nb][0][1], xv[nb][0][3]), fmaxf(xv[nb][1][1], xv[nb][1][3]));
+                const float m0 = m_run[nb][0], m1 = m_run[nb][1];
+                float ls0 = 0.f, ls1 = 0.f;
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                  mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-                  mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-                }
-                const float mn0 = fmaxf(m_run[nb][0], mx0), mn1 = fmaxf(m_run[nb][1], mx1);
-                const float al0 = fast_exp2(m_run[nb][0] - mn0), al1 = fast_exp2(m_run[nb][1] - mn1);
-                m_run[nb][0] = mn0;
-                m_run[nb][1] = mn1;
-                l_run[nb][0] *= al0;
-                l_run[nb][1] *= al1;
-#pragma unroll
-                for (int mb = 0; mb < 8; ++mb) {
-                  o[mb][nb][0] *= al0;
-                  o[mb][nb][1] *= al1;
-                  o[mb][nb][2] *= al0;
-                  o[mb][nb][3] *= al1;
-                }
-              }
-            }
-            uint32_t pb[2][NB][2];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              const float m0 = m_run[nb][0], m1 = m_run[nb][1];
-              float ls0 = 0.f, ls1 = 0.f;
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                uint32_t r0, r1;
-                if constexpr (kScaled) {
-                  const float w0 = fast_exp2(xv[nb][hh][0] - m0), w1 = fast_exp2(xv[nb][hh][1] - m1);
-                  const float w2 = fast_exp2(xv[nb][hh][2] - m0), w3 = fast_exp2(xv[nb][hh][3] - m1);
-                  ls0 = fmaf(w0, ts[hh][0].inv, fmaf(w2, ts[hh][1].inv, ls0));
-                  ls1 = fmaf(w1, ts[hh][0].inv, fmaf(w3, ts[hh][1].inv, ls1));
-                  r0 = pack_f16x2(w0 * ts[hh][0].m, w1 * ts[hh][0].m);
-                  r1 = pack_f16x2(w2 * ts[hh][1].m, w3 * ts[hh][1].m);
-                } else {
-                  r0 = pack_f16x2(fast_exp2(xv[nb][hh][0] - m0), fast_exp2(xv[nb][hh][1] - m1));
-                  r1 = pack_f16x2(fast_exp2(xv[nb][hh][2] - m0), fast_exp2(xv[nb][hh][3] - m1));
+                for (int hh = 0; hh < 2; ++hh) {
+                  const uint32_t r0 = pack_f16x2(fast_exp2(xv[nb][hh][0] - m0), fast_exp2(xv[nb][hh][1] - m1));
+                  const uint32_t r1 = pack_f16x2(fast_exp2(xv[nb][hh][2] - m0), fast_exp2(xv[nb][hh][3] - m1));
                   ls0 += f16lo_to_f32(r0) + f16lo_to_f32(r1);  // the weights that enter P.V
                   ls1 += f16hi_to_f32(r0) + f16hi_to_f32(r1);
+                  pb[hh][nb][0] = movmatrix_trans(r0);  // P[head g][tokens 16hh + 2t, +1]
+                  pb[hh][nb][1] = movmatrix_trans(r1);  // P[head g][tokens 16hh + 2t + 8, +9]
                 }
-                pb[hh][nb][0] = movmatrix_trans(r0);  // P[head g][tokens 16hh + 2t, +1]
-                pb[hh][nb][1] = movmatrix_trans(r1);  // P[head g][tokens 16hh + 2t + 8, +9]
+                l_run[nb][0] += ls0;
+                l_run[nb][1] += ls1;
               }
-              l_run[nb][0] += ls0;
-              l_run[nb][1] += ls1;
             }
             // ---- O^T += V^T . P^T, one k-step per half. ldmatrix.trans of 16-bit pairs hands
             // a lane tokens 2t, 2t+1 of dims 2g, 2g+1 (a byte each); a byte permute makes
@@ -1264,6 +1313,29 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
           for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) l_run[nb][cc] += __shfl_xor_sync(0xffffffffu, l_run[nb][cc], off);
+        // Paged fp8 caches: O goes over to the sum's reference, which every merge below takes, with
+        // the sum brought to 2^-16 .. 2^-15: O then is 2^-16 to 2^-15 times a mean of V's rows, and
+        // the sum of 2^13 of them is finite whatever V's scales are. In two steps, as V's exponent
+        // alone may be past fp32's.
+        if constexpr (kScaled) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              const float l = l_run[nb][cc];
+              const int up = (int)(__float_as_uint(l) >> 23 & 0xffu) - 127 + 16;
+              const float f = fast_exp2((r_run[nb][cc] - m_run[nb][cc] - (float)up) * 0.5f);
+              if (l > 0.f) {  // (else the warp had no token)
+                m_run[nb][cc] += (float)up;
+                l_run[nb][cc] = l * __uint_as_float((uint32_t)(127 - up) << 23);
+              }
+#pragma unroll
+              for (int mb = 0; mb < 8; ++mb) {
+                o[mb][nb][cc] = o[mb][nb][cc] * f * f;
+                o[mb][nb][cc + 2] = o[mb][nb][cc + 2] * f * f;
+              }
+            }
+        }
         float* mo = merge_o + wg * HP * kMergeRow;
         float* ml = merge_ml + wg * HP * 2;
         if (!(sm_ok(smem_u32(mo), HP * kMergeRow * 4) && sm_ok(smem_u32(ml), HP * 2 * 4))) mo = ml = merge_ml;
@@ -1452,7 +1524,8 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
         // the next segment starts from an empty state
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          m_run[nb][0] = m_run[nb][1] = kNegInf;
+          m_run[nb][0] = m_run[nb][1] = kNoMax;
+          if (kScaled) r_run[nb][0] = r_run[nb][1] = kNoRef;
           l_run[nb][0] = l_run[nb][1] = 0.f;
 #pragma unroll
           for (int mb = 0; mb < 8; ++mb) o[mb][nb][0] = o[mb][nb][1] = o[mb][nb][2] = o[mb][nb][3] = 0.f;

@@ -226,9 +226,10 @@ int decode_attn_only_fp8(const da_tensor_t* q, const da_tensor_t* k_cache, const
  *
  *   k_pages, v_pages [num_blocks, Hkv, block_size, 128] e4m3; strides multiples of 16 elements
  *   kv_scales [num_blocks, Hkv, 2, block_size] fp32 (K's scales, then V's); strides multiples
- *             of 4 elements. Any finite values; V's between 2^-100 and 2^100 in magnitude keep
- *             the accuracy of the other entry points (smaller ones lose it gradually), 0 makes
- *             the row zero.
+ *             of 4 elements. Any finite values, in any mixture; V's of 2^-100 and more in
+ *             magnitude keep the accuracy of the other entry points (smaller ones lose it
+ *             gradually), 0 makes the row zero. A token whose softmax weight is below 2^-126 of
+ *             the largest counts as none.
  *   other arguments as decode_attn_fwd_paged / decode_attn_only_paged
  * block_size: a power of two from 16 to 2^20. Head dim 128 only (D = 256 returns
  * DA_ERR_UNSUPPORTED). q and the softmax weights as in decode_attn_fwd_fp8. A table entry
