@@ -63,14 +63,14 @@
 //  * Paged fp8 cache: a scale per (token, KV head) for K and one for V, copied with each box
 //    of the tile. With x the scaled log2 score and vs V's scale, p = 2^(x - m) enters the sum
 //    and p vs 2^(m - r) (f16) enters P.V with the codes, m and r running maxima of x and of
-//    x + log2 vs: P.V's weights keep f16's accuracy whatever V's scales are, and the sum has
-//    every token whose p is at least 2^-126, whatever its V is. At a segment's end O goes over
-//    to m, and partial states merge as they do elsewhere. Four producer lanes share its smaller
-//    copies. Measured: batch 64 x 16k 323 us (6.9 TB/s), ragged batch of 32 in blocks of 16
-//    187 us (6.0 TB/s; two producers and a copy per tensor: 253 us). Up to eight heads a group
-//    the second reference costs no time (against one for both, two fused multiply-adds a
-//    weight: 8 x 8192 29.0 us, 29.6 before; 32 x 1-16384 in blocks of 16 115.9 and 115.0); with
-//    sixteen it does (32 x 8192, 128 / 8 heads: 133.8 us, 130.1 before).
+//    x + log2 vs (over rows of V that hold anything but zeros): P.V's weights keep f16's
+//    accuracy whatever V's scales are, and the sum has every token whose p is at least 2^-126,
+//    whatever its V is. At a segment's end O goes over to m, and partial states merge as they do
+//    elsewhere. Four producer lanes share its smaller copies. Measured: batch 64 x 16k 323 us
+//    (6.9 TB/s), ragged batch of 32 in blocks of 16 189 us (5.9 TB/s; two producers and a copy
+//    per tensor: 253 us). Against one reference for both and no look at V's rows (two fused
+//    multiply-adds a weight): 8 x 8192 29.3 us and 29.6, 32 x 1-16384 in blocks of 16 117.8 and
+//    115.0, with sixteen heads a group 32 x 8192 133.7 and 130.1.
 #pragma once
 #include <type_traits>
 
@@ -1057,6 +1057,21 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
                   grow |= top + e_top > r_run[nb][cc] + (kBelow + kSlack);
                 }
               if (__any_sync(0xffffffffu, grow)) {  // the references move to the running maxima
+                // A row of V that holds zeros (the writer gives it scale 1, beside ordinary rows of
+                // 2^-7 and less) must not set r, or the others' f16 weights lose their bits: its scale
+                // counts as 0. A lane looks at one of the warp's 32 rows, its 16-byte chunks in an
+                // order that spreads the lanes over the banks.
+                const int row = tb + lane;
+                const uint32_t row_at = kbase + ((uint32_t)(row >> lbox) << (lbox + 8)) +
+                                        ((uint32_t)(row & ((1 << lbox) - 1)) << 7) + (p.kv_pair == 2 ? 0u : 128u << lbox);
+                uint32_t bits = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bits |= lds_or4(row_at + (((i + lane) & 7) << 4));
+                const uint32_t zeros = __ballot_sync(0xffffffffu, (bits & 0x7f7f7f7fu) == 0);  // (-0 too)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r) vs[hh][r] = zeros >> (16 * hh + g + 8 * r) & 1u ? 0.f : vs[hh][r];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll

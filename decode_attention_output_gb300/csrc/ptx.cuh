@@ -279,6 +279,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_bytes) {
   return r;
 }
 
+// The OR of the four words of 16 bytes of shared memory.
+__device__ __forceinline__ uint32_t lds_or4(uint32_t addr) {
+  uint32_t a, b, c, d;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+  return a | b | c | d;
+}
+
 // Four e4m3 values: the low two to `lo`, the high two to `hi` (f16x2 each).
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import decode_attention_output_gb300 as da
-from test_parity_paged_fp8 import DEV, _library, case, check  # noqa: F401
+from prompt_helpers import F64, assert_within, bound, gather, softmax_rows, token_ref
+from test_parity_paged_fp8 import DEV, SCALE, _library, case, check, on  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +71,99 @@ def test_all_scales_at_an_end_of_the_range(e, n):
     x[2].copy_((x[2].float().nan_to_num(0).clamp(-1.75, 1.75) if e > 100 else x[2].float().nan_to_num(0)).to(x[2].dtype))
     x[3][:, :, 1] = torch.where(x[3][:, :, 1].isnan(), math.nan, 2.0 ** e)
     check(x, f"2^{e}")
+
+
+def strict(x, scale=SCALE):
+    """(reference, bound) as prompt_helpers.token_ref's, but what f16 weights lose at the small end is taken against the
+    largest weight of a row of V that has a code other than 0. With y = log2 (weight) + floor(log2 V's scale), f16 weights
+    are off by 2^-25 of their unit at most, and the unit lies 4 or more below the largest y (or 119 below the largest
+    score, where that is more)."""
+    q, k, v, scales, table, lens = x
+    ref, tol = token_ref(*x, scale)
+    B, Hq, _ = q.shape
+    for b in range(B):
+        L = lens[b]
+        if L == 0:
+            continue
+        sc = gather(scales.transpose(2, 3).contiguous(), table, b, L).to(F64)
+        code = gather(v.float(), table, b, L).to(F64)
+        key, val = gather(k.float(), table, b, L).to(F64) * sc[..., :1], code * sc[..., 1:]
+        for h in range(Hq):
+            j = h // (Hq // k.shape[1])
+            s = key[j] @ q[b, h].to(F64) * scale
+            p = softmax_rows(s[None])[0]
+            X = float((key[j].abs() @ q[b, h].to(F64).abs()).max()) * abs(scale)
+            x2 = s / math.log(2)
+            e = torch.frexp(sc[j, :, 1].abs())[1].to(F64) - 1
+            some = (code[j].abs().sum(-1) > 0) & (sc[j, :, 1] != 0)
+            top = (x2 + e)[some].max() if some.any() else torch.tensor(-math.inf, dtype=F64)
+            unit = torch.maximum(top - 4, x2.max() - 119) - torch.logsumexp(s, 0) / math.log(2)
+            tol[b, h] = bound(ref[b, h], p @ val[j].abs(), X, 2.0 ** -11, 2.0 ** -25 * code[j].abs().sum(0) * 2.0 ** unit)
+    return ref, tol
+
+
+def check_strict(x, what):
+    ref, tol = strict(x)
+    out = torch.full(x[0].shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    da.decode_attn_only_paged_fp8(*on(x), out, SCALE)
+    torch.cuda.synchronize()
+    assert da.decode_attn_last_device_error() == 0
+    assert_within(out.cpu(), ref, tol, what)
+
+
+def zero_rows(x, b, tokens, up, code=0.0, scale=1.0):
+    """Rows of V that hold zeros, with V's scale 1 (as the writer leaves them) and scores about `up` powers of two above
+    the others'."""
+    q, k, v, scales, table, lens = x
+    bs = k.shape[2]
+    for t in tokens:
+        i, r = table[b, t // bs], t % bs
+        size = q.float().abs().sum(-1).mean() * SCALE
+        k[i, :, r] = torch.full((k.shape[1], 128), 16.0).to(k.dtype)
+        scales[i, :, 0, r] = float(up * math.log(2) / size / 16)
+        v.view(torch.uint8)[i, :, r] = 0
+        if code:
+            v[i, :, r] = torch.full((k.shape[1], 128), code).to(v.dtype)
+        scales[i, :, 1, r] = scale
+
+
+def small_values(B, Hq, lens, e, seed=25):
+    x = case(B, Hq, 2, lens, 16, seed=seed)
+    x[0].abs_()
+    x[3][:, :, 1] = torch.where(x[3][:, :, 1].isnan(), math.nan, 2.0 ** e)
+    return x
+
+
+@pytest.mark.parametrize("e", [-7, -13, -20, -60])
+@pytest.mark.parametrize("up", [10, 20, 40])
+@pytest.mark.parametrize("Hq", [8, 32])
+def test_zero_rows_do_not_set_the_reference(e, up, Hq):
+    """A row of zeros with scale 1 and a score far above the others', beside ordinary rows of small scales: first, in the
+    middle of a warp's tokens, alone in its warp, last, several, in every tile."""
+    n = 1024
+    for tokens in ([0], [13], [500], [n - 1], [3, 4, 40, 700], list(range(5, n, 50))):
+        x = small_values(1, Hq, [n], e)
+        zero_rows(x, 0, tokens, up)
+        check_strict(x, f"{len(tokens)} from {tokens[0]}")
+    x = small_values(2, Hq, [32, 2], e)
+    zero_rows(x, 0, [0], up)
+    zero_rows(x, 1, [1], up)
+    check_strict(x, "short")
+
+
+def test_zero_scales_minus_zeros_and_rows_of_nothing_else():
+    x = small_values(3, 8, [700, 129, 20], -13)
+    zero_rows(x, 0, [2, 300], 20, scale=0.0)  # a scale of 0 in place of codes of 0
+    zero_rows(x, 1, list(range(129)), 3)  # no other rows at all: zeros
+    check_strict(x, "zeros")
+    x[2].view(torch.uint8)[x[2].view(torch.uint8) == 0] = 0x80  # -0
+    check_strict(x, "minus zeros")
+
+
+@pytest.mark.parametrize("code", [2.0 ** -9, 0.5, 448.0])
+def test_rows_of_small_codes(code):
+    """Rows whose codes are far below what their scale allows, with a dominating score."""
+    x = small_values(2, 16, [600, 40], -10)
+    zero_rows(x, 0, [1, 77, 411], 12, code=code)
+    zero_rows(x, 1, [39], 12, code=code)
+    check_strict(x, f"codes of {code}")
