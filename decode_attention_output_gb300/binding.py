@@ -4,7 +4,8 @@ Argument marshalling only: each function turns ``torch.Tensor`` arguments into
 ``da_tensor_t`` descriptors (data pointer, dtype, shape, strides in elements),
 passes the current CUDA stream, and raises :class:`DecodeAttnError` on a
 nonzero status. The entry points that take tensors go through ``_da_dispatch``
-(csrc/dispatch.cpp), which reads the tensors in C++; the others through ctypes.
+(csrc/dispatch.cpp), which reads the tensors in C++ and raises ``ValueError`` for
+one that is not on the current CUDA device; the others through ctypes.
 Every step of the computation runs in the library's kernels.
 The library must have been built (``decode_attention_output_gb300.build``);
 there is no fallback of any kind.

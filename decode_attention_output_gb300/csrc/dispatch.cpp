@@ -6,6 +6,7 @@
 // stream. It reads a tensor in some 20 ns; asking for the same fields from Python takes 0.8 us a
 // tensor on the GB300's host, 6 us of a 10 us call that writes one decode step's tokens.
 #include <Python.h>
+#include <c10/core/impl/DeviceGuardImplInterface.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -28,7 +29,22 @@ int dtype_code(at::ScalarType t) {
   }
 }
 
-bool describe(PyObject* o, da_tensor_t* d) {
+// The library launches on the current device and reads every tensor there: an address of the host
+// or of another GPU is refused here (a check that the C ABI, which sees addresses alone, leaves to
+// its caller). `device`: the current one, asked for once a call (-1: not yet).
+bool on_current_device(const at::Tensor& t, int* device) {
+  if (!t.is_cuda()) {
+    PyErr_Format(PyExc_ValueError, "expected a CUDA tensor, got one on %s", t.device().str().c_str());
+    return false;
+  }
+  if (*device < 0) *device = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA)->getDevice().index();
+  if (t.device().index() == *device) return true;
+  PyErr_Format(PyExc_ValueError, "expected a tensor on the current device cuda:%d, got one on %s", *device,
+               t.device().str().c_str());
+  return false;
+}
+
+bool describe(PyObject* o, da_tensor_t* d, int* device) {
   if (!THPVariable_Check(o)) {
     PyErr_Format(PyExc_TypeError, "expected a torch.Tensor, got %.100s", Py_TYPE(o)->tp_name);
     return false;
@@ -39,6 +55,7 @@ bool describe(PyObject* o, da_tensor_t* d) {
     PyErr_Format(PyExc_TypeError, "unsupported dtype %s", c10::toString(t.scalar_type()));
     return false;
   }
+  if (t.numel() && !on_current_device(t, device)) return false;
   const int64_t n = t.dim();
   if (n > 4) {
     PyErr_SetString(PyExc_ValueError, "at most 4 dimensions");
@@ -94,11 +111,12 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   da_tensor_t desc[kMaxTensors];
   const da_tensor_t* d[kMaxTensors];
   float f[kMaxFloats] = {};
+  int device = -1;
   try {
     for (long i = 0; i < n; ++i) {
       d[i] = nullptr;
       if (args[3 + i] == Py_None) continue;
-      if (!describe(args[3 + i], &desc[i])) return nullptr;
+      if (!describe(args[3 + i], &desc[i], &device)) return nullptr;
       d[i] = &desc[i];
     }
   } catch (const std::exception& e) {
