@@ -1,5 +1,6 @@
-"""Builds libdecode_attn.so in-tree for sm_103a with nvcc (no cmake, no torch), and beside it
-``_lib/_da_dispatch.so``, the binding's caller (csrc/dispatch.cpp, g++ with torch's headers).
+"""Builds libdecode_attn.so in-tree for sm_103a with nvcc (no cmake, no torch), and beside it, where
+torch is installed, ``_lib/_da_dispatch.so``, the binding's caller (csrc/dispatch.cpp, g++ with
+torch's headers). ``python decode_attention_output_gb300/build.py`` needs no torch for the library.
 
 Each .cu file compiles in its own nvcc process (in parallel), then one link
 step produces ``_lib/libdecode_attn.so``. A stamp of the sources, headers and
@@ -13,6 +14,7 @@ error word); the tests load it beside the regular library.
 from __future__ import annotations
 
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -58,11 +60,17 @@ def _stamp(extra=()) -> str:
     h = hashlib.sha1()
     for d in (CSRC, INCLUDE):
         for name in sorted(os.listdir(d)):
-            if name.endswith((".cu", ".cuh", ".h", ".cpp")):
+            if name.endswith((".cu", ".cuh", ".h")):
                 with open(os.path.join(d, name), "rb") as f:
                     h.update(name.encode() + f.read())
     h.update(" ".join(ARCH + NVCC_FLAGS + list(extra)).encode())
     return h.hexdigest()
+
+
+def has_torch() -> bool:
+    if "torch" in sys.modules:
+        return sys.modules["torch"] is not None
+    return importlib.util.find_spec("torch") is not None
 
 
 def build_dispatch(force: bool = False) -> str:
@@ -96,7 +104,8 @@ def build_dispatch(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: bool = False) -> str:
-    """Compile and link the library (or its bounds-checked copy); returns its path."""
+    """Compile and link the library (or its bounds-checked copy); returns its path. The binding's
+    caller is built beside it where torch is installed; if that fails, the library is there already."""
     if checked:
         extra_flags = [*CHECKED_FLAGS, *extra_flags]
     out = lib_path(checked)
@@ -108,7 +117,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
     if not force and os.path.exists(out) and os.path.exists(stamp_file):
         with open(stamp_file) as f:
             if f.read().strip() == stamp:
-                build_dispatch()
+                if has_torch():
+                    build_dispatch()
                 return out
     exe = nvcc()
 
@@ -125,9 +135,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        caller = ex.submit(build_dispatch, force)
+        caller = ex.submit(build_dispatch, force) if has_torch() else None
         objs = list(ex.map(compile_one, SOURCES))
-        caller.result()
     tmp = out + f".tmp{os.getpid()}"
     cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -136,6 +145,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
     os.replace(tmp, out)
     with open(stamp_file, "w") as f:
         f.write(stamp)
+    if caller:
+        caller.result()
     return out
 
 
