@@ -162,20 +162,27 @@ __device__ __forceinline__ void warp_umma_commit(uint32_t bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
-// mbar_wait_bounded in few instructions: the issuing warp's code competes with the softmax
-// loop for the instruction cache.
+// mbar_wait_bounded in few instructions, for a whole warp: the issuing warp's code competes with
+// the softmax loop for the instruction cache. Lanes may leave the loop apart, and what follows
+// (TMEM loads and stores, elections, shuffles) needs them together.
 __device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, int* err, int code, int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return;
-  const unsigned long long t0 = globaltimer_ns();
+  if (!mbar_try_wait(bar, parity)) {
+    const unsigned long long t0 = globaltimer_ns();
 #pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (*(volatile int*)abort_flag) return;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      atomicOr(err, code);
-      *(volatile int*)abort_flag = 1;
-      return;
+    while (!mbar_try_wait(bar, parity)) {
+      if (*(volatile int*)abort_flag) break;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        atomicOr(err, code);
+        *(volatile int*)abort_flag = 1;
+        break;
+      }
     }
   }
+  __syncwarp();
+}
+// Has a warp given up? One answer for the whole warp, so that its lanes leave their loops together.
+__device__ __forceinline__ bool given_up(const int* abort_flag) {
+  return __any_sync(0xffffffffu, *(const volatile int*)abort_flag != 0);
 }
 // Asks for a CTA of the grid that has not started, to run it here; the 16-byte answer lands at
 // `dst` and completes on `bar`.
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     int kv = 0, qn[2] = {0, 0};
     auto load_kv = [&](const CUtensorMap* map, int row, int kvh) {
       const int s = kv % kStagesP;
-      mbar_wait_bounded(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+      mbar_wait_warp(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
       ++kv;
       if (lane == 0) {
         mbar_arrive_expect_tx(bar(kKvFull + s), kTileP);
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       }
     };
     auto answer = [&] {
-      mbar_wait_bounded(bar(kNext), asked & 1, p.err, kErrWaitFull, flags);
+      mbar_wait_warp(bar(kNext), asked & 1, p.err, kErrWaitFull, flags);
       ++asked;
       x = next_cta(next_smem);
       fence_proxy_async_smem();  // the answer has been read before the next one is written
@@ -364,32 +371,32 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     };
     Item it = find();
     while (true) {
-      while (x >= 0 && it.lq < 0 && !*(volatile int*)flags) {
+      while (x >= 0 && it.lq < 0 && !given_up(flags)) {
         ask();
         answer();
         it = find();
       }
       const int slot = n % kItems;
-      mbar_wait_bounded(bar(kItemEmpty + slot), ((n / kItems) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+      mbar_wait_warp(bar(kItemEmpty + slot), ((n / kItems) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
       if (lane == 0) {
         items[slot] = it;
         mbar_arrive(bar(kItemFull + slot));
       }
-      if (it.lq < 0 || *(volatile int*)flags) break;
+      if (it.lq < 0 || given_up(flags)) break;
       ++n;
       // The queries of both tiles, which come into shared memory when the item before has had
       // its last S computed, are on their way into L2 until then.
       if (lane < 4) tma_prefetch_4d(&p.tm_q, 0, it.kvh * G, it.q0 + it.p0 + (lane >> 1) * npos, lane & 1);
       const int top = max(it.end0, it.end1);
       if (top <= it.j0) ask();
-      for (int j = it.j0; j < top && !*(volatile int*)flags; ++j) {
+      for (int j = it.j0; j < top && !given_up(flags); ++j) {
         if (j == max(it.j0, top - 3)) ask();  // late, so that no item waits behind a long one
         load_kv(&p.tm_k, it.k0 + j * kN, it.kvh);
         load_kv(&p.tm_v, it.k0 + j * kN, it.kvh);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (j > it.j0 || (w ? it.end1 : it.end0) <= it.j0) continue;
-          mbar_wait_bounded(bar(kQEmpty + w), (qn[w] & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+          mbar_wait_warp(bar(kQEmpty + w), (qn[w] & 1) ^ 1, p.err, kErrWaitEmpty, flags);
           ++qn[w];
           if (lane == 0) {
             mbar_arrive_expect_tx(bar(kQFull + w), (uint32_t)(npos * G) * 256);
@@ -399,11 +406,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
           }
         }
       }
-      if (*(volatile int*)flags) break;
+      if (given_up(flags)) break;
       answer();
       it = find();
     }
-    if (*(volatile int*)flags)  // given up with an answer on its way
+    if (given_up(flags))  // with an answer on its way
       mbar_wait_bounded(bar(kNext), asked & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
     // every stage released (all MMAs that read them done, and so every copy) before the CTA may end
     for (int i = kv > kStagesP ? kv - kStagesP : 0; i < kv; ++i)
@@ -414,10 +421,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     // ------------------------------------------- MMA issuers: S = Q K^T; O += P V
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     const bool pv = warp == kSoftWarps + 2;
-    auto wait = [&](int b, int parity, int code) {
-      wait_bar(bar(b), parity, p.err, code, flags);
-      __syncwarp();
-    };
+    auto wait = [&](int b, int parity, int code) { wait_bar(bar(b), parity, p.err, code, flags); };
     const uint64_t q_desc = umma_smem_desc(q_smem, 16, 1024);
     const uint64_t kv_desc = pv ? umma_smem_desc(ring, kHalf, 1024) : umma_smem_desc(ring, 16, 1024);
     int ks = pv ? 1 : 0, kph = 0;  // ring position of the next V or K tile (they alternate)
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       wait(kItemFull + slot, (n / kItems) & 1, kErrWaitFull);
       const int j0 = uniform(items[slot].j0), end0 = uniform(items[slot].end0), end1 = uniform(items[slot].end1);
       const int lk = items[slot].lk, clear_at = pv ? items[slot].clear : -1;
-      const bool none = items[slot].lq < 0 || *(volatile int*)flags;
+      const bool none = items[slot].lq < 0 || given_up(flags);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kItemEmpty + slot));
       __syncwarp();
@@ -576,11 +580,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     for (int n = 0;; ++n) {
       const int slot = n % kItems;
       wait_bar(bar(kItemFull + slot), (n / kItems) & 1, p.err, kErrWaitFull, flags);
-      __syncwarp();
       const Item it = items[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kItemEmpty + slot));
-      if (it.lq < 0 || *(volatile int*)flags) break;
+      if (it.lq < 0 || given_up(flags)) break;
       const int first = it.p0 + w * npos, pos = first + off;
       const bool row_ok = off < npos && pos < it.lq;
       const int lim = min(it.lk, pos + it.lk - it.lq + 1);            // keys of this row

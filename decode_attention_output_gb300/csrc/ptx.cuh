@@ -128,6 +128,14 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// ... of a whole warp, whose lanes may leave the wait apart and are brought together again: what
+// follows (matrix and TMEM loads, shuffles, votes) needs them so.
+__device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, int* err, int code,
+                                               volatile int* abort_flag) {
+  mbar_wait_bounded(bar, parity, err, code, abort_flag);
+  __syncwarp();
+}
+
 // --------------------------------------------------------------------- TMA
 // 4-D tiled tensor load into this CTA's shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
