@@ -68,6 +68,10 @@ constexpr int kMaxDevices = 64;
 struct Workspace {
   char* base = nullptr;
   size_t bytes = 0;
+  // smaller ones before it: captured graphs may hold their addresses (each at least twice the
+  // one before, from 32 MiB on: 16 would be 2 TiB)
+  char* outgrown[16] = {};
+  int n_outgrown = 0;
 };
 Workspace g_ws[kMaxDevices];
 
@@ -75,9 +79,10 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Returns the workspace of the current device with at least `scratch` bytes after
 // the header, growing it if needed. Growth is stream-ordered on `stream` (no device-wide
-// synchronisation): the old block is released with cudaFreeAsync behind the work already
-// queued on `stream`, the new one comes from cudaMallocAsync and its header is zeroed by
-// cudaMemsetAsync, all on `stream`.
+// synchronisation): the new block comes from cudaMallocAsync and its header is zeroed by
+// cudaMemsetAsync on `stream`. It is twice the old one at least, which is kept until
+// decode_attn_release: a captured graph, or a call under way on another thread, may use it
+// still. While `stream` is captured nothing is allocated: the block would be the graph's.
 int workspace_get(size_t scratch, cudaStream_t stream, char** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DA_ERR_CUDA;
@@ -85,12 +90,13 @@ int workspace_get(size_t scratch, cudaStream_t stream, char** out) {
   Workspace& ws = g_ws[dev];
   const size_t need = kHeaderBytes + align_up(scratch, 256);
   if (need > ws.bytes) {
-    if (ws.base) {
-      if (cudaFreeAsync(ws.base, stream) != cudaSuccess) return DA_ERR_CUDA;
-      ws.base = nullptr;
-      ws.bytes = 0;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) {
+      cudaGetLastError();
+      return DA_ERR_NOMEM;
     }
-    const size_t bytes = std::max(need, (size_t)32 << 20);
+    if (ws.n_outgrown == 16) return DA_ERR_NOMEM;
+    const size_t bytes = std::max(std::max(need, 2 * ws.bytes), (size_t)32 << 20);
     void* p = nullptr;
     if (cudaMallocAsync(&p, bytes, stream) != cudaSuccess) {
       cudaGetLastError();
@@ -100,6 +106,7 @@ int workspace_get(size_t scratch, cudaStream_t stream, char** out) {
       cudaFreeAsync(p, stream);
       return DA_ERR_CUDA;
     }
+    if (ws.base) ws.outgrown[ws.n_outgrown++] = ws.base;
     ws.base = static_cast<char*>(p);
     ws.bytes = bytes;
   }
@@ -1387,18 +1394,18 @@ int decode_attn_last_device_error(void* stream, int32_t* host_code) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return DA_ERR_CUDA;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DA_ERR_CUDA;
-  char* base = nullptr;
+  char* headers[16 + 2] = {};  // outgrown workspaces (a graph's replay may have written them) too
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    base = g_ws[dev].base;
+    for (int i = 0; i < g_ws[dev].n_outgrown; ++i) headers[i] = g_ws[dev].outgrown[i];
+    headers[16] = g_ws[dev].base;
   }
-  char* fixed = nullptr;  // the no-allocation scratch, once a call has looked it up here
   {
-    std::lock_guard<std::mutex> lk(g_noalloc_mu);
-    fixed = static_cast<char*>(g_noalloc_addr[dev]);
+    std::lock_guard<std::mutex> lk(g_noalloc_mu);  // the no-allocation scratch, once a call has looked it up here
+    headers[17] = static_cast<char*>(g_noalloc_addr[dev]);
   }
   int32_t code = 0;
-  for (char* b : {base, fixed}) {
+  for (char* b : headers) {
     if (!b) continue;
     int32_t c = 0;
     if (cudaMemcpy(&c, b + kErrOff, sizeof(c), cudaMemcpyDeviceToHost) != cudaSuccess) return DA_ERR_CUDA;
@@ -1424,10 +1431,10 @@ void decode_attn_release(void) {
     if (!g_ws[d].base) continue;
     if (cudaSetDevice(d) == cudaSuccess) {
       cudaDeviceSynchronize();
+      for (int i = 0; i < g_ws[d].n_outgrown; ++i) cudaFree(g_ws[d].outgrown[i]);
       cudaFree(g_ws[d].base);
     }
-    g_ws[d].base = nullptr;
-    g_ws[d].bytes = 0;
+    g_ws[d] = Workspace();
   }
   cudaSetDevice(cur);
 }

@@ -36,11 +36,13 @@
  *  - The library owns one workspace per device (partial results of the split
  *    KV pass and of the split-K projection, completion counters, the bf16
  *    attention intermediate). When a call needs more, it is grown in stream
- *    order on that call's stream (cudaFreeAsync of the old block, cudaMallocAsync
- *    of the new one, cudaMemsetAsync of its header; no device-wide
- *    synchronisation), so the first call with the largest shapes should precede
- *    any CUDA graph capture. Calls on different streams of the same device share
- *    it: the caller must order them (their work must not overlap on the GPU).
+ *    order on that call's stream (cudaMallocAsync of a new block, twice the old one
+ *    at least, cudaMemsetAsync of its header; no device-wide synchronisation). The
+ *    old block is kept until decode_attn_release, so a graph captured before can be
+ *    replayed. A call that would have to grow it while its stream is being captured
+ *    returns DA_ERR_NOMEM: the first call with the largest shapes must precede the
+ *    capture. Calls on different streams of the same device share it, graph replays
+ *    among them: the caller must order them (their work must not overlap on the GPU).
  *  - seq_lens lives on the device. Each length is clamped to [0, Lcap] on the
  *    device; a length of 0 gives an all-zero attention row.
  *  - Bounded device waits: every wait inside a kernel gives up after about
@@ -427,7 +429,8 @@ int decode_attn_last_device_error(void* stream, int32_t* host_code);
 /* The same call under its earlier name. */
 int decode_attn_device_error(void* stream, int32_t* host_code);
 
-/* Frees the workspace of every device (synchronises those devices). */
+/* Frees the workspace of every device (synchronises those devices). Graphs captured before
+ * must not be replayed afterwards. */
 void decode_attn_release(void);
 
 /* A static, human-readable name for a da_status_t. */
