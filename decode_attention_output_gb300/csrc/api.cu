@@ -313,6 +313,16 @@ int check_tensor(const da_tensor_t* t, int dtype, int ndim, Use use) {
     if (_rc != DA_OK) return _rc; \
   } while (0)
 
+// Elements from a tensor's first to one past its last.
+long long span_of(const da_tensor_t* t) {
+  long long last = 0;
+  for (int i = 0; i < t->ndim; ++i) {
+    if (t->shape[i] == 0) return 0;
+    last += (t->shape[i] - 1) * t->stride[i];
+  }
+  return last + 1;
+}
+
 struct AttnShape {
   int B, Hq, Hkv, G, Lcap, D;
 };
@@ -499,6 +509,12 @@ int check_cache(const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* c
   p->max_blocks = (int)MB;
   p->num_blocks = (int)NB;
   while ((1 << p->block_shift) < BS) ++p->block_shift;
+  p->k_span = span_of(k);
+  p->v_span = span_of(v);
+  p->kp_span = span_of(kp);
+  p->vp_span = span_of(vp);
+  p->sc_span = kv8 ? span_of(scales) : 0;
+  p->table_span = B > 0 ? (B - 1) * p->bt_stride + MB : 0;
   return DA_OK;
 }
 
@@ -1359,6 +1375,8 @@ int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_ten
   p.out = static_cast<__nv_bfloat16*>(out->data);
   p.o_st = out->stride[0];
   p.o_sh = out->stride[1];
+  p.out_span = span_of(out);
+  p.part_rows = (long long)rows;
   p.cu_q = static_cast<const int*>(cq->data);
   p.cu_k = static_cast<const int*>(ck->data);
   p.B = (int)B;

@@ -386,7 +386,7 @@ __device__ void fused_epilogue(const AttnParams& p, uint64_t* bars, uint32_t tme
 // not loaded (the consumers mask those tokens). A block id outside [0, num_blocks) is
 // recorded in the error word and read past the pool's end, which TMA fills with zeros.
 template <int S, int DIM, bool KV8>
-__device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t ring, uint32_t scales, uint8_t* q_slots,
+__device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t smem_lo, uint32_t ring, uint32_t scales, uint8_t* q_slots,
                                                size_t q_slot, uint64_t* bars, int* flags, const int* prefix, const int* lens,
                                                int* ids, long long start, long long end, const Cursor& c_start,
                                                int role) {
@@ -463,6 +463,12 @@ __device__ __forceinline__ void paged_producer(const AttnParams& p, uint32_t rin
     for (int s = 0; s < kMaxSub; ++s) blk[s] = idr[s];  // within the row; checked where used
     const uint32_t fb = full_bar(stage);
     const uint32_t kdst = ring + stage * kStageBytes;
+    // checked build, as for contiguous caches: recorded and clamped, every wait still ends
+    if (!(smem_in_bounds(smem_lo, kdst, kStageBytes, p.err) && smem_in_bounds(smem_lo, smem_u32(idr), kMaxSub * 4, p.err) &&
+          smem_in_bounds(smem_lo, smem_u32(q_slots + stage * q_slot), G * kQRow, p.err) &&
+          (!KV8 || smem_in_bounds(smem_lo, scales + stage * AttnSmem::kScaleStageBytes, AttnSmem::kScaleStageBytes, p.err)) &&
+          in_bounds(n_load >= 1 && row >= 0 && row + (1 << lsub) <= 1 << lbs, p.err)))
+      c.b = c.kvh = 0;
     bool bad = false;  // an id outside the pool
     mbar_wait_bounded(empty_bar(stage), ((it / S) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
     mbar_arrive_expect_tx(fb, n_load * (2 * sub_bytes + (KV8 ? 8u << lsub : 0u)) + (with_q ? G * DIM * 2 : 0));
@@ -789,7 +795,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
     // ------------------------------------------------------------ producer(s)
     if constexpr (PAGED) {
       if (lane == 0)
-        paged_producer<S, DIM, KV8>(p, ring, smem_u32(scales), q_slots, kFixed.q_slot(), bars, flags, prefix, lens,
+        paged_producer<S, DIM, KV8>(p, smem_lo, ring, smem_u32(scales), q_slots, kFixed.q_slot(), bars, flags, prefix, lens,
                                reinterpret_cast<int*>(smem + lay.off_ids()), start, end, c_start,
                                warp - kGroups * kGroupWarps);
     } else if (lane == 0) {
@@ -1034,6 +1040,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
                 for (int r = 0; r < 2; ++r) {
                   const int tok = 16 * hh + g + 8 * r, at = tb + tok;
                   const float* one = sc + ((at >> lbox) << (lbox + 1)) + (at & ((1 << lbox) - 1));
+                  if (!sm_ok(smem_u32(one), 4 + (4u << lbox))) one = sc;
                   const bool have = tok < vw;  // (else the scales may hold anything)
                   const float k = *one * sl2;
                   vs[hh][r] = have ? one[1 << lbox] : 0.f;
@@ -1062,8 +1069,9 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
                 // counts as 0. A lane looks at one of the warp's 32 rows, its 16-byte chunks in an
                 // order that spreads the lanes over the banks.
                 const int row = tb + lane;
-                const uint32_t row_at = kbase + ((uint32_t)(row >> lbox) << (lbox + 8)) +
-                                        ((uint32_t)(row & ((1 << lbox) - 1)) << 7) + (p.kv_pair == 2 ? 0u : 128u << lbox);
+                uint32_t row_at = kbase + ((uint32_t)(row >> lbox) << (lbox + 8)) +
+                                  ((uint32_t)(row & ((1 << lbox) - 1)) << 7) + (p.kv_pair == 2 ? 0u : 128u << lbox);
+                if (!(sm_ok(row_at, 128) && ok(row_at >= kbase && row_at + 128 <= kbase + kSB))) row_at = kbase;
                 uint32_t bits = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) bits |= lds_or4(row_at + (((i + lane) & 7) << 4));

@@ -259,9 +259,11 @@ struct PrefillParams {
   int B, Hkv, G, Tq, Tk;
   int npos;            // query positions per tile, floor(128 / G)
   float scale_log2;    // scale * log2(e), never 0
+  long long out_span;      // elements of out from its first to one past its last (bounds-checked build)
   int parts;           // an item's K/V tiles are cut into at most so many parts (1: none is cut)
   float* part_o;       // [parts][Tq][Hq][128] unnormalised outputs of the parts
   float* part_ml;      // [parts][Tq][Hq][2] their maxima (log2 units) and sums
+  long long part_rows;  // rows of both (0: no item is cut)
 };
 // grid = as many CTAs as there can be work items; those that run take over the others.
 cudaError_t launch_prefill(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream);
@@ -281,6 +283,8 @@ struct CacheParams {
   int* err;
   int B, Hkv, T, max_blocks, block_shift, num_blocks;
   int head_groups;             // set by the launcher
+  // elements from the first to one past the last (bounds-checked build)
+  long long k_span, v_span, kp_span, vp_span, sc_span, table_span;
 };
 cudaError_t launch_cache(CacheParams& p, int dim, bool kv8, bool write, bool pdl, cudaStream_t stream);
 

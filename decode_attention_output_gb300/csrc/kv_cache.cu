@@ -46,7 +46,8 @@ __device__ __forceinline__ bool locate(const CacheParams& p, int t, int lane, in
   if (pos < 0) return false;  // older than the sequence's first token
   const long long at = pos >> p.block_shift;
   int blk = -1;
-  if (at < p.max_blocks) blk = __ldg(p.table + b * p.bt_stride + at);
+  if (at < p.max_blocks && in_bounds(b >= 0 && b < p.B && b * p.bt_stride + at < p.table_span, p.err))
+    blk = __ldg(p.table + b * p.bt_stride + at);
   *row = (int)(pos & ((1ll << p.block_shift) - 1));
   *block = blk;
   if ((unsigned)blk < (unsigned)p.num_blocks) return true;
@@ -103,6 +104,19 @@ __global__ void __launch_bounds__(kCacheWarps * 32) kv_cache_kernel(const CacheP
   };
   auto page_step = [&](int q) { return is_v[q] ? p.vp_sh : p.kp_sh; };
   auto pool = [&](int q) { return is_v[q] ? p.v_pages : p.k_pages; };
+  // checked build: this lane's HG shares of rows lie inside the tokens, the pool and the scales
+  auto tokens_ok = [&](int q) {
+    const long long at = token_row(q) - (is_v[q] ? p.v : p.k);
+    return in_bounds(h0 + HG <= p.Hkv && at >= 0 && at + (HG - 1) * token_step(q) + 8 <= (is_v[q] ? p.v_span : p.k_span), p.err);
+  };
+  auto page_ok = [&](int q) {
+    const long long at = page_row(q);
+    return in_bounds(row < 1 << p.block_shift && at >= 0 && at + (HG - 1) * page_step(q) + 8 <= (is_v[q] ? p.vp_span : p.kp_span), p.err);
+  };
+  auto scale_ok = [&] {
+    const long long at = block * p.sc_sb + h0 * p.sc_sh + (is_v[0] ? p.sc_st : 0) + row;
+    return in_bounds(at >= 0 && at + (HG - 1) * p.sc_sh < p.sc_span, p.err);
+  };
   if (WRITE) {
     uint4 x[kPer][HG];
 #pragma unroll
@@ -110,12 +124,13 @@ __global__ void __launch_bounds__(kCacheWarps * 32) kv_cache_kernel(const CacheP
       const __nv_bfloat16* from = token_row(q);
       const long long step = token_step(q);
 #pragma unroll
-      for (int h = 0; h < HG; ++h, from += step) x[q][h] = ldg_stream_v4(from);
+      for (int h = 0; h < HG; ++h, from += step) x[q][h] = tokens_ok(q) ? ldg_stream_v4(from) : make_uint4(0, 0, 0, 0);
     }
     if (!locate<true>(p, t, lane, &block, &row)) return;
     if constexpr (KV8) {
       uint8_t* to = static_cast<uint8_t*>(pool(0)) + page_row(0);
       const long long step = page_step(0);
+      const bool in = page_ok(0) && scale_ok();
       float* scale = p.scales + block * p.sc_sb + h0 * p.sc_sh + (is_v[0] ? p.sc_st : 0) + row;
 #pragma unroll
       for (int h = 0; h < HG; ++h, to += step, scale += p.sc_sh) {
@@ -139,14 +154,15 @@ __global__ void __launch_bounds__(kCacheWarps * 32) kv_cache_kernel(const CacheP
               if (mag > 0x77u && mag < 0x7fu) c[i] -= (mag - 0x77u) << b;
             }
         }
-        *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
-        if (col == 0) *scale = __int_as_float((127 + e) << 23);
+        if (in) *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+        if (col == 0 && in) *scale = __int_as_float((127 + e) << 23);
       }
     } else {
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
         __nv_bfloat16* to = static_cast<__nv_bfloat16*>(pool(q)) + page_row(q);
         const long long step = page_step(q);
+        if (!page_ok(q)) continue;
 #pragma unroll
         for (int h = 0; h < HG; ++h, to += step) *reinterpret_cast<uint4*>(to) = x[q][h];
       }
@@ -159,6 +175,8 @@ __global__ void __launch_bounds__(kCacheWarps * 32) kv_cache_kernel(const CacheP
       const uint8_t* from = static_cast<const uint8_t*>(pool(0)) + page_row(0);
       const long long step = page_step(0);
       const float* scale = p.scales + block * p.sc_sb + h0 * p.sc_sh + (is_v[0] ? p.sc_st : 0) + row;
+      if (block >= 0 && !(page_ok(0) && scale_ok())) block = -1;
+      if (!tokens_ok(0)) return;
 #pragma unroll
       for (int h = 0; h < HG; ++h, from += step, scale += p.sc_sh) {
         x[h] = block >= 0 ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0, 0);
@@ -181,6 +199,8 @@ __global__ void __launch_bounds__(kCacheWarps * 32) kv_cache_kernel(const CacheP
         uint4 x[HG];
         const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(pool(q)) + page_row(q);
         const long long step = page_step(q);
+        if (block >= 0 && !page_ok(q)) block = -1;
+        if (!tokens_ok(q)) continue;
 #pragma unroll
         for (int h = 0; h < HG; ++h, from += step)
           x[h] = block >= 0 ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);

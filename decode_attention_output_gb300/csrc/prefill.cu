@@ -254,6 +254,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
   int* flags = reinterpret_cast<int*>(smem + kOffFlags);  // [0] abort, [1] TMEM address
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](int i) { return smem_u32(bars + i); };
+  // Guards of the bounds-checked build (constant true otherwise): shared memory that copies and
+  // plain stores write, rows of the output and of the workspace.
+  auto sm_ok = [&](uint32_t addr, uint32_t bytes) { return smem_in_bounds(smem_u32(smem_raw), addr, bytes, p.err); };
+  auto out_ok = [&](const __nv_bfloat16* at, int n) { return in_bounds(at >= p.out && at + n <= p.out + p.out_span, p.err); };
+  auto part_ok = [&](long long slot) { return in_bounds(slot >= 0 && slot < p.part_rows, p.err); };
   const uint32_t q_smem = smem_u32(smem), ring = q_smem + kOffRing;
   const int G = p.G, npos = p.npos;
 
@@ -286,7 +291,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     int total = 0x7fffffff;  // row blocks in all, once known
     int kv = 0, qn[2] = {0, 0};
     auto load_kv = [&](const CUtensorMap* map, int row, int kvh) {
-      const int s = kv % kStagesP;
+      int s = kv % kStagesP;
+      if (!sm_ok(ring + s * kTileP, kTileP)) s = 0;
       mbar_wait_warp(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
       ++kv;
       if (lane == 0) {
@@ -378,7 +384,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       }
       const int slot = n % kItems;
       mbar_wait_warp(bar(kItemEmpty + slot), ((n / kItems) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
-      if (lane == 0) {
+      if (lane == 0 && sm_ok(smem_u32(items + slot), sizeof(Item))) {
         items[slot] = it;
         mbar_arrive(bar(kItemFull + slot));
       }
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
           if (j > it.j0 || (w ? it.end1 : it.end0) <= it.j0) continue;
           mbar_wait_warp(bar(kQEmpty + w), (qn[w] & 1) ^ 1, p.err, kErrWaitEmpty, flags);
           ++qn[w];
-          if (lane == 0) {
+          if (lane == 0 && sm_ok(q_smem + w * kTileP, kHalf + (uint32_t)(npos * G) * 128) && in_bounds(npos * G <= 128, p.err)) {
             mbar_arrive_expect_tx(bar(kQFull + w), (uint32_t)(npos * G) * 256);
             for (int c = 0; c < 2; ++c)
               tma_load_4d(q_smem + w * kTileP + c * kHalf, &p.tm_q, bar(kQFull + w), 0, it.kvh * G,
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         // NaN or infinity there is not, so those rows are cleared before the MMAs see them.
         if (j == clear_at) {
           uint4* tile = reinterpret_cast<uint4*>(smem + kOffRing + stage * kTileP);
-          for (int i = lk % kN * 8 + lane; i < kN * 8; i += 32) {
+          for (int i = lk % kN * 8 + lane; i < kN * 8 && sm_ok(smem_u32(tile + i), kHalf + 16); i += 32) {
             tile[i] = make_uint4(0, 0, 0, 0);
             tile[i + kHalf / 16] = make_uint4(0, 0, 0, 0);
           }
@@ -549,13 +555,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         exchange<2>(y[1], y[3], t);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (rows[i])
+          if (rows[i] && out_ok(rows[i] + c * 32 + t * 8, 8))
             *reinterpret_cast<uint4*>(rows[i] + c * 32 + t * 8) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
       }
     };
     // A part's row: O as it is, the sum and the reference maximum.
     auto store_part = [&](float sum, float ref) {
-      if (slot_out >= 0) {
+      if (slot_out >= 0 && part_ok(slot_out)) {
         p.part_ml[slot_out * 2] = ref;
         p.part_ml[slot_out * 2 + 1] = sum;
       }
@@ -566,7 +572,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(o[i]));
-        if (slot_out >= 0)
+        if (slot_out >= 0 && part_ok(slot_out))
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<uint4*>(p.part_o + slot_out * 128 + c * 16 + i * 4) =
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       const int lim0 = min(it.lk, first + off0 + it.lk - it.lq + 1);  // the least of the warp's rows
       const int end = w ? it.end1 : it.end0;
       __nv_bfloat16* to = row_ok ? p.out + (long long)(it.q0 + pos) * p.o_st + (long long)(it.kvh * G + g) * p.o_sh : nullptr;
-      if (it.part < 0 && end == 0 && to) {  // no key at all
+      if (it.part < 0 && end == 0 && to && out_ok(to, 128)) {  // no key at all
 #pragma unroll
         for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(to + i * 8) = make_uint4(0, 0, 0, 0);
       }
@@ -708,6 +714,7 @@ __global__ void __launch_bounds__(128) prefill_join_kernel(const __grid_constant
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i < n && part_begin(i, top, n) < end; ++i) {  // (parts past the row's last key hold nothing)
     const long long slot = ((long long)i * p.Tq + t) * Hq + h;
+    if (!in_bounds(slot < p.part_rows, p.err)) continue;
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot * 2);
     const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot * 128 + lane * 4);
     if (ml.x == kNegInfP && ml.y == 0.f) continue;  // the part's keys all lie past the row
@@ -723,7 +730,8 @@ __global__ void __launch_bounds__(128) prefill_join_kernel(const __grid_constant
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2 y = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   if (l == 0.f) y = make_uint2(0u, 0u);
-  *reinterpret_cast<uint2*>(p.out + (long long)t * p.o_st + (long long)h * p.o_sh + lane * 4) = y;
+  __nv_bfloat16* to = p.out + (long long)t * p.o_st + (long long)h * p.o_sh + lane * 4;
+  if (in_bounds(to + 4 <= p.out + p.out_span, p.err)) *reinterpret_cast<uint2*>(to) = y;
 }
 
 }  // namespace
