@@ -207,8 +207,9 @@ int decode_attn_only_paged(const da_tensor_t* q, const da_tensor_t* k_pages, con
  *   other arguments as decode_attn_fwd / decode_attn_only
  * Head dim 128 only (D = 256 returns DA_ERR_UNSUPPORTED); the fused option does not apply.
  * The kernels widen the codes to f16 (exact) and multiply them with q rounded to f16,
- * which is exact for |q| <= 65504; larger |q| is clamped to 65504. The softmax weights
- * enter P.V as f16 (bf16 on the bf16 path).
+ * which is exact for 2^-17 <= |q| <= 65504 (and 0); smaller |q| goes to the nearest
+ * multiple of 2^-24, larger |q| is clamped to 65504. The softmax weights enter P.V as
+ * f16 (bf16 on the bf16 path).
  */
 int decode_attn_fwd_fp8(const da_tensor_t* q, const da_tensor_t* k_cache, const da_tensor_t* v_cache,
                         const da_tensor_t* seq_lens, const da_tensor_t* o_weight, const da_tensor_t* out, float scale,

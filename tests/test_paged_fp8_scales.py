@@ -167,3 +167,27 @@ def test_rows_of_small_codes(code):
     zero_rows(x, 0, [1, 77, 411], 12, code=code)
     zero_rows(x, 1, [39], 12, code=code)
     check_strict(x, f"codes of {code}")
+
+
+@pytest.mark.parametrize("small", [-10, -17, -21])
+def test_small_queries_with_large_key_scales(small):
+    """q enters the product as f16: exact from 2^-17 on, below it within 2^-25 of each element, so a score within
+    2^-25 * scale * sum |k|, its weight by as large a factor, and the output by twice that of its mean magnitude."""
+    x = case(2, 8, 2, [300, 77], 16, seed=26)
+    q, k, v, scales, table, lens = x
+    g = torch.Generator().manual_seed(27)
+    size = 2.0 ** small * (1 + torch.rand(q.shape, generator=g))
+    q.copy_((size * torch.sign(torch.randn(q.shape, generator=g))).to(torch.bfloat16))
+    scales[:, :, 0] *= 2.0 ** -small
+    ref, tol = token_ref(*x, SCALE)
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device=DEV)
+    da.decode_attn_only_paged_fp8(*on(x), out, SCALE)
+    torch.cuda.synchronize()
+    for b, L in enumerate(lens):
+        sc = gather(scales.transpose(2, 3).contiguous(), table, b, L).to(F64)
+        key, val = gather(k.float(), table, b, L).to(F64) * sc[..., :1], gather(v.float(), table, b, L).to(F64) * sc[..., 1:]
+        for h in range(8):
+            off = 0.0 if small >= -17 else 2.0 ** -25 * SCALE * key[h // 4].abs().sum(-1).max().item()
+            p = softmax_rows((key[h // 4] @ q[b, h].to(F64) * SCALE)[None])[0]
+            tol[b, h] += 2 * math.expm1(off) * (p @ val[h // 4].abs())
+    assert_within(out.cpu(), ref, tol, f"q of 2^{small}")
