@@ -521,6 +521,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
     const bool neg = sl2 < 0.f;
     int step = 0;
     float m = kNegInfP, l = 0.f;
+    bool big = false;  // a row of the warp has a maximum past 2^24
     __nv_bfloat16* out = nullptr;  // this row of the item in work (null: no such row)
     long long slot_out = -1;       // its row in the workspace (-1: a whole item; -2: a part, no such row)
     // The O of the tile's last item, complete with PV of its last step (waited for here)
@@ -645,12 +646,21 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         const float al = grow ? fast_exp2(m - xm) : 1.f;
         m = grow ? xm : m;
         l *= al;
+        // The weights' exponent is one fused s * sl2 - m, and m a rounded product: past 2^24 they part
+        // by whole powers of two, past 2^32 by more than fp32 holds. There the products are rounded
+        // first, as the maximum's is.
+        if (any) big = __any_sync(0xffffffffu, (__float_as_uint(m) & 0x7fffffffu) - 0x4b800000u < 0x34000000u);
+        if (big) {
+#pragma unroll
+          for (int c = 0; c < kN; ++c) s[c] *= sl2;
+        }
+        const float mul = big ? 1.f : sl2;
         const float mr = m == kNegInfP ? 0.f : -m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t pk[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-          float2 x = fma2(make_float2(s[2 * i], s[2 * i + 1]), sl2, mr);
+          float2 x = fma2(make_float2(s[2 * i], s[2 * i + 1]), mul, mr);
           x.x = fast_exp2(x.x);
           x.y = fast_exp2(x.y);
           sum[i & 1] = add2(sum[i & 1], x);
