@@ -1383,9 +1383,10 @@ int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_ten
   p.Hkv = (int)Hkv;
   p.Tq = (int)Tq;
   p.Tk = (int)Tk;
-  // the kernel masks with infinities: a scale of 0 becomes one that leaves every weight 1
+  // the kernel masks with infinities: a scale of 0 becomes the smallest number, which leaves every
+  // weight within 2^-21 of 1 whatever the products are
   p.scale_log2 = scale * 1.4426950408889634f;
-  if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;
+  if (p.scale_log2 == 0.f) p.scale_log2 = 0x1p-149f;
   return launch_prefill(p, (int)items * p.parts, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 

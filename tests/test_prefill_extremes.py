@@ -1,4 +1,5 @@
-"""The prompt attention where scores are far larger than any model's: the largest one's V row comes out."""
+"""The prompt attention where scores are far larger than any model's: the largest one's V row comes out, and a scale
+of 0 gives the mean whatever the products are."""
 import math
 
 import pytest
@@ -46,3 +47,17 @@ def test_scores_past_24_bits(size, scale, lq, lk):
                 ref, size_of = rows.mean(0), rows.abs().mean(0)
                 d = (out[i, h].double() - ref).abs()
                 assert bool((d <= 2.0 ** -8 * size_of + 2.0 ** -8 * ref.abs()).all()), (b, i, h, d.max())
+
+
+@pytest.mark.parametrize("power", [0, 10, 59])
+def test_scale_of_zero_and_large_products(power):
+    """Products up to 2^(2 * power + 7), times a scale of 0: the mean of the keys' V rows. (Weights 1 are exact in bf16;
+    the sum of up to 300 of them and their V rows is fp32.)"""
+    g = torch.Generator().manual_seed(52)
+    q, k = (torch.randn((300, 2, 128), generator=g).sign() * 2.0 ** power * torch.randint(1, 3, (300, 2, 1), generator=g) for _ in range(2))
+    v = torch.randn((300, 2, 128), generator=g).to(torch.bfloat16)
+    out = run(q.to(torch.bfloat16), k.to(torch.bfloat16), v, [0, 300], [0, 300], 0.0)
+    n = torch.arange(1, 301).double()[:, None, None]
+    ref = v.double().cumsum(0) / n
+    size = v.double().abs().cumsum(0) / n
+    assert bool(((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -14 * size).all())
