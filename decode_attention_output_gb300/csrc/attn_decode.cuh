@@ -1066,20 +1066,23 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
               if (__any_sync(0xffffffffu, grow)) {  // the references move to the running maxima
                 // A row of V that holds zeros (the writer gives it scale 1, beside ordinary rows of
                 // 2^-7 and less) must not set r, or the others' f16 weights lose their bits: its scale
-                // counts as 0. A lane looks at one of the warp's 32 rows, its 16-byte chunks in an
-                // order that spreads the lanes over the banks.
+                // counts as 0. A lane looks at one of the warp's 32 rows: at 16 bytes of it (each lane
+                // of eight at others, which spreads them over the banks), and at the rest where some
+                // row's are zeros.
                 const int row = tb + lane;
                 uint32_t row_at = kbase + ((uint32_t)(row >> lbox) << (lbox + 8)) +
                                   ((uint32_t)(row & ((1 << lbox) - 1)) << 7) + (p.kv_pair == 2 ? 0u : 128u << lbox);
                 if (!(sm_ok(row_at, 128) && ok(row_at >= kbase && row_at + 128 <= kbase + kSB))) row_at = kbase;
-                uint32_t bits = 0;
+                uint32_t bits = lds_or4(row_at + ((lane & 7) << 4)) & 0x7f7f7f7fu;  // (-0 too)
+                if (__any_sync(0xffffffffu, lane < vw && bits == 0)) {
+#pragma unroll 1
+                  for (int i = 1; i < 8; ++i) bits |= lds_or4(row_at + (((i + lane) & 7) << 4)) & 0x7f7f7f7fu;
+                  const uint32_t zeros = __ballot_sync(0xffffffffu, bits == 0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) bits |= lds_or4(row_at + (((i + lane) & 7) << 4));
-                const uint32_t zeros = __ballot_sync(0xffffffffu, (bits & 0x7f7f7f7fu) == 0);  // (-0 too)
+                  for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                  for (int r = 0; r < 2; ++r) vs[hh][r] = zeros >> (16 * hh + g + 8 * r) & 1u ? 0.f : vs[hh][r];
+                    for (int r = 0; r < 2; ++r) vs[hh][r] = zeros >> (16 * hh + g + 8 * r) & 1u ? 0.f : vs[hh][r];
+                }
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1347,15 +1350,24 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
             for (int cc = 0; cc < 2; ++cc) {
               const float l = l_run[nb][cc];
               const int up = (int)(__float_as_uint(l) >> 23 & 0xffu) - 127 + 16;
-              const float f = fast_exp2((r_run[nb][cc] - m_run[nb][cc] - (float)up) * 0.5f);
+              const float d = r_run[nb][cc] - m_run[nb][cc] - (float)up;
+              const float f = fast_exp2(fminf(fmaxf(d, -120.f), 120.f));
               if (l > 0.f) {  // (else the warp had no token)
                 m_run[nb][cc] += (float)up;
                 l_run[nb][cc] = l * __uint_as_float((uint32_t)(127 - up) << 23);
               }
 #pragma unroll
               for (int mb = 0; mb < 8; ++mb) {
-                o[mb][nb][cc] = o[mb][nb][cc] * f * f;
-                o[mb][nb][cc + 2] = o[mb][nb][cc + 2] * f * f;
+                o[mb][nb][cc] *= f;
+                o[mb][nb][cc + 2] *= f;
+              }
+              if (fabsf(d) > 120.f) {
+                const float rest = fast_exp2(d > 0.f ? d - 120.f : d + 120.f);
+#pragma unroll
+                for (int mb = 0; mb < 8; ++mb) {
+                  o[mb][nb][cc] *= rest;
+                  o[mb][nb][cc + 2] *= rest;
+                }
               }
             }
         }
