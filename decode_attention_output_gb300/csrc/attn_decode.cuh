@@ -886,12 +886,14 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
     uint32_t qf[NB][kKs][2];
     float o[8][NB][4];
     float m_run[NB][2], l_run[NB][2];
-    float r_run[NB][2];  // paged fp8 caches: the reference of O, m_run being the sum's alone
+    // paged fp8 caches: m_run is the sum's reference, m_run + d_run that of O (kept apart: past 2^24
+    // their sum would lose the difference)
+    float d_run[NB][2];
     constexpr float kNoMax = kScaled ? kNoRef : kNegInf;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       m_run[nb][0] = m_run[nb][1] = kNoMax;
-      if (kScaled) r_run[nb][0] = r_run[nb][1] = kNoRef;
+      if (kScaled) d_run[nb][0] = d_run[nb][1] = 0.f;
       l_run[nb][0] = l_run[nb][1] = 0.f;
 #pragma unroll
       for (int mb = 0; mb < 8; ++mb) o[mb][nb][0] = o[mb][nb][1] = o[mb][nb][2] = o[mb][nb][3] = 0.f;
@@ -1029,7 +1031,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
             uint32_t pb[2][NB][2];
             if constexpr (kScaled) {
               // With x the scaled log2 score (K's scale in it) and vs V's scale, a token's share of
-              // the sum is p = 2^(x - m) and its weight in P.V p vs 2^(m - r), m and r running
+              // the sum is p = 2^(x - m) and its weight in P.V p vs 2^(m - r), m and r = m + d running
               // maxima of x and of log2 (2^x vs): against one reference for both, a token whose V is
               // 2^126 times smaller than another's would leave the sum.
               const float* sc = scales + stage * (AttnSmem::kScaleStageBytes / 4);
@@ -1060,8 +1062,9 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
 #pragma unroll
                 for (int cc = 0; cc < 2; ++cc) {
                   const float top = fmaxf(fmaxf(sa[0][nb][cc], sa[0][nb][cc + 2]), fmaxf(sa[1][nb][cc], sa[1][nb][cc + 2]));
-                  grow |= top > m_run[nb][cc] + kSlack;
-                  grow |= top + e_top > r_run[nb][cc] + (kBelow + kSlack);
+                  const float over = top - m_run[nb][cc];
+                  grow |= over > kSlack;
+                  grow |= over + e_top > d_run[nb][cc] + (kBelow + kSlack);
                 }
               if (__any_sync(0xffffffffu, grow)) {  // the references move to the running maxima
                 // A row of V that holds zeros (the writer gives it scale 1, beside ordinary rows of
@@ -1087,26 +1090,24 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                   for (int cc = 0; cc < 2; ++cc) {
-                    float mx = kNoRef, mr = kNoRef;
+                    float mx = kNoRef, md = kNoRef;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      const float x = sa[i >> 1][nb][2 * (i & 1) + cc];
-                      mx = fmaxf(mx, x);
-                      mr = fmaxf(mr, x + exponent_of(vs[i >> 1][i & 1]));
-                    }
+                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sa[i >> 1][nb][2 * (i & 1) + cc]);
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) {
-                      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                      mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, off));
-                    }
+                    for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                     // whole numbers, so that the factors from one to the next are exact; r stays so
                     // near m that 2^(m - r) is finite
-                    const float mn = fmaxf(m_run[nb][cc], ceilf(mx));
-                    const float rn = fmaxf(fmaxf(r_run[nb][cc], ceilf(mr) - kBelow), mn - 120.f);
-                    l_run[nb][cc] *= fast_exp2(m_run[nb][cc] - mn);
-                    const float al = fast_exp2(r_run[nb][cc] - rn);
+                    const float mn = fmaxf(m_run[nb][cc], ceilf(mx)), up = mn - m_run[nb][cc];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                      md = fmaxf(md, sa[i >> 1][nb][2 * (i & 1) + cc] - mn + exponent_of(vs[i >> 1][i & 1]));
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) md = fmaxf(md, __shfl_xor_sync(0xffffffffu, md, off));
+                    const float d_old = d_run[nb][cc] - up, dn = fmaxf(fmaxf(d_old, ceilf(md) - kBelow), -120.f);
+                    l_run[nb][cc] *= fast_exp2(-up);
+                    const float al = fast_exp2(d_old - dn);
                     m_run[nb][cc] = mn;
-                    r_run[nb][cc] = rn;
+                    d_run[nb][cc] = dn;
 #pragma unroll
                     for (int mb = 0; mb < 8; ++mb) {
                       o[mb][nb][cc] *= al;
@@ -1116,7 +1117,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
               }
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                const float c0 = fast_exp2(m_run[nb][0] - r_run[nb][0]), c1 = fast_exp2(m_run[nb][1] - r_run[nb][1]);
+                const float c0 = fast_exp2(-d_run[nb][0]), c1 = fast_exp2(-d_run[nb][1]);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -1339,30 +1340,23 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
           for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) l_run[nb][cc] += __shfl_xor_sync(0xffffffffu, l_run[nb][cc], off);
-        // Paged fp8 caches: O goes over to the sum's reference, which every merge below takes, with
-        // the sum brought to 2^-16 .. 2^-15: O then is 2^-16 to 2^-15 times a mean of V's rows, and
-        // the sum of 2^13 of them is finite whatever V's scales are. In two steps, as V's exponent
-        // alone may be past fp32's.
+        // Paged fp8 caches: O goes over to the sum's reference, which every merge below takes, and both
+        // become 2^-32 of themselves: the sums of 2^24 tokens' V rows (of weights up to 2^kSlack) are
+        // finite whatever V's scales are.
         if constexpr (kScaled) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
-              const float l = l_run[nb][cc];
-              const int up = (int)(__float_as_uint(l) >> 23 & 0xffu) - 127 + 16;
-              const float d = r_run[nb][cc] - m_run[nb][cc] - (float)up;
-              const float f = fast_exp2(fminf(fmaxf(d, -120.f), 120.f));
-              if (l > 0.f) {  // (else the warp had no token)
-                m_run[nb][cc] += (float)up;
-                l_run[nb][cc] = l * __uint_as_float((uint32_t)(127 - up) << 23);
-              }
+              const float d = d_run[nb][cc], f = fast_exp2(fmaxf(d, -90.f) - 32.f);
+              l_run[nb][cc] *= 0x1p-32f;
 #pragma unroll
               for (int mb = 0; mb < 8; ++mb) {
                 o[mb][nb][cc] *= f;
                 o[mb][nb][cc + 2] *= f;
               }
-              if (fabsf(d) > 120.f) {
-                const float rest = fast_exp2(d > 0.f ? d - 120.f : d + 120.f);
+              if (d < -90.f) {
+                const float rest = fast_exp2(d + 90.f);
 #pragma unroll
                 for (int mb = 0; mb < 8; ++mb) {
                   o[mb][nb][cc] *= rest;
@@ -1560,7 +1554,7 @@ __global__ void __launch_bounds__(attn_threads(attn_producers(PAGED, NPAD > 0, S
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           m_run[nb][0] = m_run[nb][1] = kNoMax;
-          if (kScaled) r_run[nb][0] = r_run[nb][1] = kNoRef;
+          if (kScaled) d_run[nb][0] = d_run[nb][1] = 0.f;
           l_run[nb][0] = l_run[nb][1] = 0.f;
 #pragma unroll
           for (int mb = 0; mb < 8; ++mb) o[mb][nb][0] = o[mb][nb][1] = o[mb][nb][2] = o[mb][nb][3] = 0.f;

@@ -191,3 +191,38 @@ def test_small_queries_with_large_key_scales(small):
             p = softmax_rows((key[h // 4] @ q[b, h].to(F64) * SCALE)[None])[0]
             tol[b, h] += 2 * math.expm1(off) * (p @ val[h // 4].abs())
     assert_within(out.cpu(), ref, tol, f"q of 2^{small}")
+
+
+@pytest.mark.parametrize("size", [10, 20, 26, 29, 31, 40, 60, 110])
+@pytest.mark.parametrize("e", [-60, -13, 0, 40, 100])
+def test_scores_past_24_bits(size, e):
+    """Scores scale * 2^size * c_j, the c_j whole numbers up to 255, so the keys with the largest one share the row: their
+    V rows' mean, in warps, tiles and CTAs of their own. Their weights are powers of two; the sums are fp32."""
+    for lens, Hq, ctas in (([300, 1, 40], 8, 0), ([4000, 129], 24, 0), ([2000] * 2, 8, 7)):
+        x = case(len(lens), Hq, 2, lens, 16, seed=28)
+        q, k, v, scales, table, _ = x
+        g = torch.Generator().manual_seed(29)
+        sign = torch.where(torch.rand((len(lens), Hq, 1), generator=g) < 0.5, -1.0, 1.0)
+        q.copy_(sign.expand(-1, -1, 128))
+        k.copy_(torch.ones(k.shape).to(k.dtype))
+        c = torch.randint(1, 256, scales[:, :, 0].shape, generator=g).float()
+        scales[:, :, 0] = c * 2.0 ** (size - 7)
+        scales[:, :, 1] = 2.0 ** e
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=DEV)
+        old = da.decode_attn_get_option("attn_ctas")
+        da.decode_attn_set_option("attn_ctas", ctas)
+        try:
+            da.decode_attn_only_paged_fp8(*on(x), out, SCALE)
+        finally:
+            da.decode_attn_set_option("attn_ctas", old)
+        torch.cuda.synchronize()
+        got = out.cpu().to(F64)
+        for b, L in enumerate(lens):
+            cs, code = gather(c[..., None], table, b, L)[..., 0], gather(v.float(), table, b, L).to(F64)
+            for h in range(Hq):
+                j = h // (Hq // 2)
+                top = cs[j].max() if sign[b, h, 0] > 0 else cs[j].min()
+                rows = code[j][cs[j] == top] * 2.0 ** e
+                ref, size_of = rows.mean(0), rows.abs().mean(0)
+                # (at size 10 the next whole number has 2^-130 of the weight)
+                assert bool(((got[b, h] - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -18 * size_of).all()), (lens, b, h)
