@@ -568,10 +568,10 @@ int max_active_clusters(int cs) {
 }
 
 // `per_seq` (paged fp8 caches): the four-tiles rule is about long sequences' merges, while several
-// short sequences on one CTA pay for the end of each (47 of one token: 23 us on 12 CTAs, 8 on 47),
-// and cut ones as much (ragged: 38 of two to three tiles 15.2 us on 76 CTAs, 9.8 on 114; 12 of
-// three to six 10.5 on 24, 7.8 on 72). So up to 16 tiles of capacity a CTA per tile where there are
-// SMs; above (4 of 24 to 48 tiles: 9.9 us on 48 CTAs, 13.0 on 152) two per sequence at least.
+// short sequences on one CTA pay for the end of each (47 of one token: 14.5 us on 12 CTAs, 6.0 on
+// 47), and cut ones as much (ragged: 38 of two to three tiles 12.9 us on 76 CTAs, 8.6 on 114; 12 of
+// three to six 11.9 on 24, 8.2 on 72). So up to 16 tiles of capacity a CTA per tile where there are
+// SMs; above (4 of 24 to 48 tiles: 10.5 us on 48 CTAs, 12.9 on 152) two per sequence at least.
 // Sequences of equal length then take a number of CTAs each that the kernel chooses by length.
 AttnPlan plan_attention(const AttnShape& s, const Options& o, int tile_tok = 0, bool fused = false,
                         ClusterUse clustered = ClusterUse::kNever, bool per_seq = false, bool step = false) {
@@ -600,8 +600,8 @@ AttnPlan plan_attention(const AttnShape& s, const Options& o, int tile_tok = 0, 
   pl.chip_tiles = 0;
   // Before a batch's projection, 64 CTAs or more where there are tiles for them: its W_o loads
   // start beside the attention, and fewer CTAs with several tiles each wait behind them (16
-  // sequences of 512 tokens: 19.9 us a step on 16 CTAs, 20.4 on 32, 14.7 on 64; 32: 19.8 on 32, 15.9
-  // on 64; 64: 15.9 on 64, 17.4 on 128).
+  // sequences of 512 tokens: 19.9 us a step on 16 CTAs, 20.8 on 32, 15.3 on 64; 32: 20.1 on 32, 16.0
+  // on 64; 64: 15.9 on 64, 17.6 on 128).
   pl.seq_least = 1;
   while (step && s.B > 1 && seqs * pl.seq_least < 64) pl.seq_least *= 2;
   const bool small = tiles <= 4ll * sms;
@@ -610,8 +610,8 @@ AttnPlan plan_attention(const AttnShape& s, const Options& o, int tile_tok = 0, 
   if (!fused && cluster_ok && o.attn_ctas == 0 && 2 * seqs <= sms) {
     long long cs = std::min<long long>({(long long)kMaxAttnCluster, sms / seqs, (tiles_seq + 1) / 2});
     if (pl.even) {
-      // Few long sequences leave most SMs idle in clusters of eight (one of 32768 tokens 28.2 us,
-      // 15.8 on 32 CTAs). Where a CTA would hold four tiles more than outside cluster mode, and
+      // Few long sequences leave most SMs idle in clusters of eight (one of 32768 tokens 28.0 us,
+      // 15.6 on 32 CTAs). Where a CTA would hold four tiles more than outside cluster mode, and
       // where so many clusters are not resident at once, clusters of four or fewer, which fill
       // the SMs: short sequences then still merge on chip, and the kernel takes the flat split
       // for long ones.
@@ -917,7 +917,7 @@ int run_attention(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t*
   const int tile_tok = kv8 || paged8 ? kTileFp8 : tile_tokens(s.D);
   const int box_tokens = paged ? std::min(paged->block_size, tile_tok) : (kv8 ? kTileFp8 : 0);
   // Blocks below 64 tokens: the copies' number sets the pace (a ragged batch of 32: in blocks of
-  // 16 195 us with a copy per tensor, 186 with one for both; of 32 182 and 178; from 64 on
+  // 16 199 us with a copy per tensor, 188 with one for both; of 32 182 and 181; from 64 on
   // within 1% either way).
   if (paged8 && box_tokens < 64) p.kv_pair = encode_kv_pair_map(&p.tm_k, k, v, box_tokens);
   if (!p.kv_pair) DA_TRY(encode_kv_map(&p.tm_k, k, box_tokens));
@@ -978,9 +978,9 @@ int run_attention(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t*
       p.seq_least = pl.seq_least;
       // A whole number of CTAs per sequence spares many CTAs the ends of two sequences (3 to 4 us),
       // and wins while the longest one's CTAs then hold at most eight tiles more than with all
-      // CTAs at work (96 sequences of 1024 tokens, one CTA each: 12.1 us against 16.5; of 2048 17.3
-      // and 19.5; of 4096 27.9 and 26.5), six with ragged lengths (148 of 147 to 295 tokens 10.4 and
-      // 24.3; 24 of 2533 to 5067 21.6 and 26.7; 64 of 5311 to 7082, 7.6 tiles more, 27.0 and 26.0).
+      // CTAs at work (96 sequences of 1024 tokens, one CTA each: 12.3 us against 17.0; of 2048 17.4
+      // and 20.4; of 4096 27.9 and 27.1), six with ragged lengths (148 of 147 to 295 tokens 8.5 and
+      // 14.1; 24 of 2533 to 5067 14.5 and 17.1; 64 of 5311 to 7082, 7.6 tiles more, 29.3 and 27.5).
       p.own_slope = (float)p.seq_ctas / (float)flat;
       p.own_slack[0] = 8.f * (float)p.seq_ctas;
       p.own_slack[1] = 6.f * (float)p.seq_ctas;

@@ -36,7 +36,7 @@
 //    the flat split and the L2 merge, and no CTA waits at a cluster barrier.
 //  * Paged fp8 caches: outside cluster mode a whole number of CTAs per sequence (seq_parts in
 //    kernels.h) where the longest one allows it, and few long sequences leave cluster mode,
-//    both by the lengths on the device: one sequence of 131072 tokens 91.9 -> 24.4 us, 96 of
+//    both by the lengths on the device: one sequence of 131072 tokens 91.9 -> 23.9 us, 96 of
 //    1024 16.4 -> 12.3, 18 of 8192 18.4 -> 15.0 (the set-up takes 0.1 us more).
 //  * Programmatic dependent launch: the kernel waits for the previous kernel in the
 //    stream before its first global access, and lets the next one launch right after its
@@ -67,10 +67,10 @@
 //    accuracy whatever V's scales are, and the sum has every token whose p is at least 2^-126,
 //    whatever its V is. At a segment's end O goes over to m, and partial states merge as they do
 //    elsewhere. Four producer lanes share its smaller copies. Measured: batch 64 x 16k 323 us
-//    (6.9 TB/s), ragged batch of 32 in blocks of 16 189 us (5.9 TB/s; two producers and a copy
+//    (6.9 TB/s), ragged batch of 32 in blocks of 16 188 us (5.9 TB/s; two producers and a copy
 //    per tensor: 253 us). Against one reference for both and no look at V's rows (two fused
-//    multiply-adds a weight): 8 x 8192 29.3 us and 29.6, 32 x 1-16384 in blocks of 16 117.8 and
-//    115.0, with sixteen heads a group 32 x 8192 133.7 and 130.1.
+//    multiply-adds a weight): 8 x 8192 30.0 us and 30.3, 8 x 2048 8.6 and 8.4, ragged batch of 32
+//    188 and 186, with sixteen heads a group 3 x 8401 19.6 and 19.5, 4 x 488-977 13.1 and 12.8.
 #pragma once
 #include <type_traits>
 

@@ -200,8 +200,8 @@ constexpr int kMaxAttnCluster = 8;  // portable cluster size
 // CTAs for each of several sequences of `tiles` 128-token tiles, `most` at hand for each: one up
 // to four tiles (a tile per group of warps); then parts of two tiles, of four from eight parts on,
 // and more than 64 parts only once they hold 16 tiles, as the one CTA that joins a sequence's
-// parts pays for each (one sequence of 8192 tokens: 10.6 us in 16 parts, 11.0 in 32, 13.8 in 64;
-// of 131072: 24.8 in 64, 28.5 in 152). At least `least` where there are tiles for them.
+// parts pays for each (one sequence of 8192 tokens: 10.7 us in 16 parts, 11.1 in 32, 14.3 in 64;
+// of 131072: 24.8 in 64, 29.2 in 152). At least `least` where there are tiles for them.
 __host__ __device__ inline int seq_parts(int tiles, int most, int least) {
   const int small = tiles / 2 < 8 ? tiles / 2 : 8, mid = tiles / 4 < 64 ? tiles / 4 : 64, large = tiles / 16;
   int k = tiles <= 4 ? 1 : (small > mid ? small : mid);

@@ -33,9 +33,9 @@
 //    workspace, and a second kernel joins them in order.
 //  * One producer warp streams K and V tiles (32 KB) by TMA through a ring of five stages, in
 //    the order of their use; it also finds the items (a scan of the offsets) and passes them on.
-// Measured: 8192 tokens, 64 / 8 heads 657 us (1.67 PFLOP/s; a short run, before the power limit
-// lowers the clock, 572 us); four chunks of 512 over 7.7k 176 us (1.51); 16 ragged prompts of up
-// to 2048 109 us (1.12): a step costs 1.2 us, an item 2.8 us more (its output, the diagonal's
+// Measured: 8192 tokens, 64 / 8 heads 667 us (1.65 PFLOP/s; a short run, before the power limit
+// lowers the clock, 581 us); four chunks of 512 over 7.7k 180 us (1.48); 16 ragged prompts of up
+// to 2048 112 us (1.09): a step costs 1.2 us, an item 2.8 us more (its output, the diagonal's
 // masks, the hand-over), of which 16 ragged prompts have 11 on each SM.
 #include "kernels.h"
 #include "packed.cuh"
