@@ -11,6 +11,7 @@
 
 #include <cstring>
 #include <exception>
+#include <string>
 #include <utility>
 
 #include "decode_attn.h"
@@ -29,22 +30,20 @@ int dtype_code(at::ScalarType t) {
   }
 }
 
-// The library launches on the current device and reads every tensor there: an address of the host
-// or of another GPU is refused here (a check that the C ABI, which sees addresses alone, leaves to
-// its caller). `device`: the current one, asked for once a call (-1: not yet).
-bool on_current_device(const at::Tensor& t, int* device) {
-  if (!t.is_cuda()) {
-    PyErr_Format(PyExc_ValueError, "expected a CUDA tensor, got one on %s", t.device().str().c_str());
-    return false;
-  }
-  if (*device < 0) *device = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA)->getDevice().index();
-  if (t.device().index() == *device) return true;
-  PyErr_Format(PyExc_ValueError, "expected a tensor on the current device cuda:%d, got one on %s", *device,
-               t.device().str().c_str());
-  return false;
+// The library launches on the current device and reads every tensor there, but sees addresses
+// alone. A tensor on the host or on another GPU goes to it with a null address, which every entry
+// point refuses (a wrong type of that tensor before it); the caller is then told where it lies.
+struct Devices {
+  int current = -1;              // asked for once a call
+  const at::Tensor* off = nullptr;  // the first tensor that is not there
+};
+bool on_current_device(const at::Tensor& t, Devices* dev) {
+  if (!t.is_cuda()) return false;
+  if (dev->current < 0) dev->current = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA)->getDevice().index();
+  return t.device().index() == dev->current;
 }
 
-bool describe(PyObject* o, da_tensor_t* d, int* device) {
+bool describe(PyObject* o, da_tensor_t* d, Devices* dev) {
   if (!THPVariable_Check(o)) {
     PyErr_Format(PyExc_TypeError, "expected a torch.Tensor, got %.100s", Py_TYPE(o)->tp_name);
     return false;
@@ -55,14 +54,17 @@ bool describe(PyObject* o, da_tensor_t* d, int* device) {
     PyErr_Format(PyExc_TypeError, "unsupported dtype %s", c10::toString(t.scalar_type()));
     return false;
   }
-  if (t.numel() && !on_current_device(t, device)) return false;
   const int64_t n = t.dim();
   if (n > 4) {
     PyErr_SetString(PyExc_ValueError, "at most 4 dimensions");
     return false;
   }
   d->ndim = (int32_t)n;
-  d->data = t.numel() ? t.data_ptr() : nullptr;
+  d->data = nullptr;
+  if (t.numel()) {
+    if (on_current_device(t, dev)) d->data = t.data_ptr();
+    else if (!dev->off) dev->off = &t;
+  }
   const at::IntArrayRef shape = t.sizes(), stride = t.strides();
   for (int64_t i = 0; i < 4; ++i) {
     d->shape[i] = i < n ? shape[i] : 0;
@@ -111,12 +113,12 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   da_tensor_t desc[kMaxTensors];
   const da_tensor_t* d[kMaxTensors];
   float f[kMaxFloats] = {};
-  int device = -1;
+  Devices dev;
   try {
     for (long i = 0; i < n; ++i) {
       d[i] = nullptr;
       if (args[3 + i] == Py_None) continue;
-      if (!describe(args[3 + i], &desc[i], &device)) return nullptr;
+      if (!describe(args[3 + i], &desc[i], &dev)) return nullptr;
       d[i] = &desc[i];
     }
   } catch (const std::exception& e) {
@@ -138,6 +140,14 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     default: status = invoke_floats<8>(fn, d, f, (int)floats, stream); break;
   }
   Py_END_ALLOW_THREADS;
+  if (dev.off && (status == DA_ERR_NULL || status == DA_OK)) {
+    const std::string where = dev.off->device().str();
+    if (dev.off->is_cuda())
+      PyErr_Format(PyExc_ValueError, "expected a tensor on the current device cuda:%d, got one on %s", dev.current, where.c_str());
+    else
+      PyErr_Format(PyExc_ValueError, "expected a CUDA tensor, got one on %s", where.c_str());
+    return nullptr;
+  }
   return PyLong_FromLong(status);
 }
 

@@ -1,5 +1,7 @@
 """The entry points refuse tensors that are not on the current CUDA device before the library sees their addresses:
 lengths, offsets and block tables are easily left on the host."""
+import ctypes
+
 import pytest
 import torch
 
@@ -83,3 +85,30 @@ def test_tensors_without_elements_may_lie_anywhere():
     q = torch.empty((0, 8, 128), dtype=torch.bfloat16)
     k = torch.empty((0, 2, 32, 128), dtype=torch.bfloat16)
     da.decode_attn_only(q, k, k, torch.empty((0,), dtype=torch.int32), q.clone(), 0.1)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: without a GPU only")
+@pytest.mark.parametrize("name", NAMES)
+def test_the_library_refuses_a_null_address_of_every_tensor(name):
+    """What the binding relies on: each tensor with elements but no address is DA_ERR_NULL, whatever the others are."""
+    full = {"fwd": "decode_attn_fwd", "only": "decode_attn_only", "only_noalloc": "decode_attn_only_noalloc"}
+    lib = binding.load()
+    fn = getattr(lib, full.get(name, "decode_attn_" + name))
+    _, _, tensors, rest = calls("cpu")[NAMES.index(name)]
+    for at in tensors:
+        descs = []
+        for n, t in tensors.items():
+            d = binding.describe(t)
+            d.data = None if n == at else 0x10000000
+            descs.append(d)
+        assert fn(*(ctypes.byref(d) for d in descs), *rest, None) == -1, at
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host tensors' addresses: without a GPU only")
+def test_a_wrong_type_is_told_first():
+    """The library looks at a tensor's type before its address."""
+    _, fn, tensors, rest = calls("cpu")[NAMES.index("prefill")]
+    tensors["q"] = tensors["q"].float()
+    with pytest.raises(da.DecodeAttnError) as e:
+        fn(*tensors.values(), *rest, stream=0)
+    assert e.value.code == -2
