@@ -22,7 +22,7 @@
 //    softmax thread holds one row (no shuffles; the row's maximum, sum and O correction are
 //    one thread's), takes its S into registers and frees it at once. An item's O is stored
 //    when its tile's next step has its weights.
-//  * A step's MMAs compute for 2048 cycles and keep the tensor pipe busy for 88% of it (2300
+//  * A step's MMAs compute for 2048 cycles and keep the tensor pipe busy for 86% of it (2400
 //    cycles). One issuing warp, with P over its S (PV(r), then S(r + 1)), took 2860: each side
 //    waited for the other in turn, and every wait costs an issuing warp some 200 cycles in which
 //    nothing else is issued. Issued by one lane in a branch, an MMA took 100 cycles.
