@@ -30,7 +30,7 @@ _DTYPES = {torch.bfloat16: DA_DTYPE_BF16, torch.float32: DA_DTYPE_F32, torch.int
 # every symbol declared in include/decode_attn.h
 EXPORTS = ("decode_attn_fwd", "decode_attn_only", "decode_attn_only_noalloc", "decode_attn_fwd_paged",
            "decode_attn_only_paged", "decode_attn_fwd_fp8", "decode_attn_only_fp8", "decode_attn_fwd_paged_fp8", "decode_attn_only_paged_fp8",
-           "decode_attn_prefill", "decode_attn_cache_write", "decode_attn_cache_read", "decode_attn_scores", "decode_attn_oproj", "decode_attn_set_option", "decode_attn_get_option", "decode_attn_last_device_error", "decode_attn_device_error",
+           "decode_attn_prefill", "decode_attn_cache_write", "decode_attn_cache_read", "decode_attn_rope", "decode_attn_rope_cache_write", "decode_attn_scores", "decode_attn_oproj", "decode_attn_set_option", "decode_attn_get_option", "decode_attn_last_device_error", "decode_attn_device_error",
            "decode_attn_release", "decode_attn_status_str")
 
 
@@ -47,6 +47,7 @@ class DecodeAttnError(RuntimeError):
 
 _lib = None
 _call = None  # _da_dispatch.call(address, stream, n, tensors ..., floats ...) -> status
+_call_ints = None  # _da_dispatch.call_ints(address, stream, n, tensors ..., float, ints ...) -> status
 _lock = threading.Lock()
 
 
@@ -70,6 +71,9 @@ def load_library(path: str) -> ctypes.CDLL:
     lib.decode_attn_prefill.argtypes = [P, P, P, P, P, P, f32, vp]
     lib.decode_attn_cache_write.argtypes = [P, P, P, P, P, P, P, P, vp]
     lib.decode_attn_cache_read.argtypes = [P, P, P, P, P, P, P, vp]
+    i32 = ctypes.c_int32
+    lib.decode_attn_rope.argtypes = [P] * 9 + [f32, i32, vp]
+    lib.decode_attn_rope_cache_write.argtypes = [P] * 15 + [f32, i32, vp]
     lib.decode_attn_scores.argtypes = [P, P, P, P, vp]
     lib.decode_attn_oproj.argtypes = [P, P, P, vp]
     lib.decode_attn_set_option.argtypes = [ctypes.c_char_p, i64]
@@ -89,32 +93,33 @@ def load_library(path: str) -> ctypes.CDLL:
 
 def load(path: str | None = None) -> ctypes.CDLL:
     """Loads the library (once). Fails loudly if it has not been built."""
-    global _lib, _call
+    global _lib
     with _lock:
         if _lib is None:
-            if _call is None:
-                _call = _load_dispatch()
+            _load_dispatch()
             _lib = load_library(path or _build.lib_path())
     return _lib
 
 
 def _load_dispatch():
+    global _call, _call_ints
+    if _call is not None:
+        return
     path = _build.dispatch_path()
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: run decode_attention_output_gb300.build.build() first")
     loader = importlib.machinery.ExtensionFileLoader("_da_dispatch", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_da_dispatch", loader))
     loader.exec_module(module)
-    return module.call
+    _call_ints, _call = module.call_ints, module.call
 
 
 def use_library(lib: ctypes.CDLL | None) -> ctypes.CDLL | None:
     """Makes ``lib`` (from :func:`load_library`) the library every entry point below calls
     and returns the previous one; the tests use it to run the bounds-checked build."""
-    global _lib, _call
+    global _lib
     with _lock:
-        if _call is None:
-            _call = _load_dispatch()
+        _load_dispatch()
         prev, _lib = _lib, lib
     return prev
 
@@ -290,6 +295,32 @@ def decode_attn_cache_read(k_pages, v_pages, kv_scales, block_table, cu_seqlens,
            _call(lib.addr["decode_attn_cache_read"], _stream(stream), 7,
                  k_pages, v_pages, kv_scales, block_table, cu_seqlens, k_out, v_out))
     return k_out, v_out
+
+
+def decode_attn_rope(q, k, cos_sin, positions, q_out, k_out, q_weight=None, k_weight=None, axes=None, eps: float = 1e-6,
+                     interleaved: bool = False, stream=None):
+    """Norms per head (where a weight [D] is given) and the position rotation of q [T, Hq, D] and k [T, Hkv, D] (either may
+    be None, with its output) into q_out and k_out, which may be q and k. cos_sin [P, R] fp32: the cosines of R / 2 pairs,
+    then their sines, at each position; positions [T] int32, or [A, T] with axes [R / 2] int32, the axis of each pair; pairs
+    of dims (i, i + R / 2), or with ``interleaved`` (2 i, 2 i + 1). Returns ``(q_out, k_out)``."""
+    lib = _lib or load()  # the lock only until the library is loaded
+    _check("decode_attn_rope",
+           _call_ints(lib.addr["decode_attn_rope"], _stream(stream), 9,
+                      q, k, cos_sin, positions, q_out, k_out, q_weight, k_weight, axes, eps, bool(interleaved)))
+    return q_out, k_out
+
+
+def decode_attn_rope_cache_write(q, k, v, cos_sin, cu_seqlens, block_table, seq_lens, q_out, k_pages, v_pages, kv_scales=None,
+                                 positions=None, q_weight=None, k_weight=None, axes=None, eps: float = 1e-6,
+                                 interleaved: bool = False, stream=None):
+    """decode_attn_rope of the new tokens' q (into q_out; both may be None) and k, with k and v going straight into the pages
+    as decode_attn_cache_write puts them there. positions None: each token's place in its sequence. Returns ``q_out``."""
+    lib = _lib or load()  # the lock only until the library is loaded
+    _check("decode_attn_rope_cache_write",
+           _call_ints(lib.addr["decode_attn_rope_cache_write"], _stream(stream), 15,
+                      q, k, v, cos_sin, cu_seqlens, block_table, seq_lens, q_out, k_pages, v_pages, kv_scales, positions,
+                      q_weight, k_weight, axes, eps, bool(interleaved)))
+    return q_out
 
 
 def decode_attn_scores(q, k_cache, seq_lens, scores, stream=None) -> torch.Tensor:

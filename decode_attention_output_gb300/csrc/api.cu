@@ -1083,6 +1083,95 @@ int run_cache(CacheParams& p, int dim, bool kv8, bool write, void* stream) {
   return launch_cache(p, dim, kv8, write, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
+// The table of cosines and sines, positions, axes, weights and queries of the rotating entry points; T tokens, head dim D.
+// `places`: positions may be left out (the tokens' places are used).
+int check_rope(const da_tensor_t* q, const da_tensor_t* q_out, const da_tensor_t* cos_sin, const da_tensor_t* positions,
+               const da_tensor_t* q_weight, const da_tensor_t* k_weight, const da_tensor_t* axes, float eps, int64_t T, int64_t D,
+               bool places, RopeParams* p) {
+  if (!q != !q_out) return DA_ERR_NULL;
+  if (D != kHeadDim && D != kHeadDimWide) return DA_ERR_SHAPE;
+  if (q) {
+    DA_TRY(check_tensor(q, DA_DTYPE_BF16, 3, kInput16));
+    DA_TRY(check_tensor(q_out, DA_DTYPE_BF16, 3, kInput16));
+    if (q->shape[0] != T || q->shape[1] <= 0 || q->shape[2] != D) return DA_ERR_SHAPE;
+    for (int i = 0; i < 3; ++i)
+      if (q_out->shape[i] != q->shape[i]) return DA_ERR_SHAPE;
+    if (q->shape[1] > (1 << 20)) return DA_ERR_UNSUPPORTED;
+    p->q = static_cast<const __nv_bfloat16*>(q->data);
+    p->q_out = static_cast<__nv_bfloat16*>(q_out->data);
+    p->q_st = q->stride[0];
+    p->q_sh = q->stride[1];
+    p->qo_st = q_out->stride[0];
+    p->qo_sh = q_out->stride[1];
+    p->q_span = span_of(q);
+    p->qo_span = span_of(q_out);
+    p->Hq = (int)q->shape[1];
+  }
+  for (const da_tensor_t* w : {q_weight, k_weight}) {
+    if (!w) continue;
+    if (w->dtype != DA_DTYPE_F32) DA_TRY(check_tensor(w, DA_DTYPE_BF16, 1, kInput16));
+    else DA_TRY(check_tensor(w, DA_DTYPE_F32, 1, kInput16));
+    if (w->shape[0] != D) return DA_ERR_SHAPE;
+  }
+  if (q_weight) {
+    p->q_weight = q_weight->data;
+    p->q_weight_f32 = q_weight->dtype == DA_DTYPE_F32;
+  }
+  if (k_weight) {
+    p->k_weight = k_weight->data;
+    p->k_weight_f32 = k_weight->dtype == DA_DTYPE_F32;
+  }
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return DA_ERR_UNSUPPORTED;
+  p->eps = eps;
+  DA_TRY(check_tensor(cos_sin, DA_DTYPE_F32, 2, kInput16));
+  const int64_t P = cos_sin->shape[0], R = cos_sin->shape[1];
+  if (P <= 0 || R <= 0 || R > D) return DA_ERR_SHAPE;
+  if (R % 8 || P >= ((int64_t)1 << 31)) return DA_ERR_UNSUPPORTED;
+  p->table = static_cast<const float*>(cos_sin->data);
+  p->table_st = P > 1 ? cos_sin->stride[0] : R;
+  if (P > 1 && p->table_st < R) return DA_ERR_STRIDE;
+  p->P = (int)P;
+  p->R = (int)R;
+  p->A = 1;
+  if (!positions) {
+    if (!places) return DA_ERR_NULL;
+    if (axes) return DA_ERR_SHAPE;  // one axis: the tokens' places
+  } else {
+    if (positions->dtype != DA_DTYPE_I32) return DA_ERR_DTYPE;
+    if (positions->ndim != 1 && positions->ndim != 2) return DA_ERR_SHAPE;
+    const int last = positions->ndim - 1;
+    const int64_t A = last ? positions->shape[0] : 1;
+    if (positions->shape[last] != T || A < 1) return DA_ERR_SHAPE;
+    if (A > 4) return DA_ERR_UNSUPPORTED;
+    if (A > 1 && !axes) return DA_ERR_NULL;
+    if (T > 0 && !positions->data) return DA_ERR_NULL;
+    if (T > 1 && positions->stride[last] != 1) return DA_ERR_STRIDE;
+    if (A > 1 && T > 0 && positions->stride[0] <= 0) return DA_ERR_STRIDE;
+    if (reinterpret_cast<uintptr_t>(positions->data) % 4) return DA_ERR_ALIGN;
+    p->pos = static_cast<const int*>(positions->data);
+    p->pos_sa = A > 1 ? positions->stride[0] : 0;
+    p->A = (int)A;
+  }
+  if (axes) {
+    if (axes->dtype != DA_DTYPE_I32) return DA_ERR_DTYPE;
+    if (axes->ndim != 1 || axes->shape[0] != R / 2) return DA_ERR_SHAPE;
+    if (!axes->data) return DA_ERR_NULL;
+    if (axes->stride[0] != 1) return DA_ERR_STRIDE;
+    if (reinterpret_cast<uintptr_t>(axes->data) % 4) return DA_ERR_ALIGN;
+    p->axes = static_cast<const int*>(axes->data);
+  }
+  p->T = (int)T;
+  return DA_OK;
+}
+
+int run_rope(RopeParams& p, int64_t D, bool interleaved, bool pages, bool kv8, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = nullptr;
+  DA_TRY(workspace_get(0, st, &ws));
+  p.err = p.cache.err = reinterpret_cast<int*>(ws + kErrOff);
+  return launch_rope(p, (int)D, !interleaved, pages, kv8, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
 }  // namespace
 
 // ======================================================================= C ABI
@@ -1404,6 +1493,55 @@ int decode_attn_cache_read(const da_tensor_t* k_pages, const da_tensor_t* v_page
   CacheParams p;
   DA_TRY(check_cache(k_out, v_out, cu_seqlens, block_table, nullptr, false, k_pages, v_pages, kv_scales, &p));
   return run_cache(p, (int)k_out->shape[2], k_pages->dtype == DA_DTYPE_E4M3, false, stream);
+}
+
+int decode_attn_rope(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* cos_sin, const da_tensor_t* positions,
+                     const da_tensor_t* q_out, const da_tensor_t* k_out, const da_tensor_t* q_weight, const da_tensor_t* k_weight,
+                     const da_tensor_t* axes, float eps, int32_t interleaved, void* stream) {
+  if (!q && !k) return DA_ERR_NULL;
+  if (!k != !k_out) return DA_ERR_NULL;
+  RopeParams p;
+  memset(&p, 0, sizeof(p));
+  const da_tensor_t* first = q ? q : k;
+  if (first->ndim != 3) return DA_ERR_SHAPE;
+  const int64_t T = first->shape[0], D = first->shape[2];
+  if (T < 0) return DA_ERR_SHAPE;
+  if (T >= ((int64_t)1 << 31)) return DA_ERR_UNSUPPORTED;
+  if (k) {
+    DA_TRY(check_tensor(k, DA_DTYPE_BF16, 3, kInput16));
+    DA_TRY(check_tensor(k_out, DA_DTYPE_BF16, 3, kInput16));
+    if (k->shape[0] != T || k->shape[1] <= 0 || k->shape[2] != D) return DA_ERR_SHAPE;
+    for (int i = 0; i < 3; ++i)
+      if (k_out->shape[i] != k->shape[i]) return DA_ERR_SHAPE;
+    if (k->shape[1] > (1 << 20)) return DA_ERR_UNSUPPORTED;
+    p.cache.k = static_cast<const __nv_bfloat16*>(k->data);
+    p.cache.k_st = k->stride[0];
+    p.cache.k_sh = k->stride[1];
+    p.cache.k_span = span_of(k);
+    p.cache.Hkv = (int)k->shape[1];
+    p.k_out = static_cast<__nv_bfloat16*>(k_out->data);
+    p.ko_st = k_out->stride[0];
+    p.ko_sh = k_out->stride[1];
+    p.ko_span = span_of(k_out);
+  }
+  DA_TRY(check_rope(q, q_out, cos_sin, positions, q_weight, k_weight, axes, eps, T, D, false, &p));
+  if (interleaved != 0 && interleaved != 1) return DA_ERR_UNSUPPORTED;
+  if (T == 0) return DA_OK;
+  return run_rope(p, D, interleaved != 0, false, false, stream);
+}
+
+int decode_attn_rope_cache_write(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cos_sin,
+                                 const da_tensor_t* cu_seqlens, const da_tensor_t* block_table, const da_tensor_t* seq_lens,
+                                 const da_tensor_t* q_out, const da_tensor_t* k_pages, const da_tensor_t* v_pages,
+                                 const da_tensor_t* kv_scales, const da_tensor_t* positions, const da_tensor_t* q_weight,
+                                 const da_tensor_t* k_weight, const da_tensor_t* axes, float eps, int32_t interleaved, void* stream) {
+  RopeParams p;
+  memset(&p, 0, sizeof(p));
+  DA_TRY(check_cache(k, v, cu_seqlens, block_table, seq_lens, true, k_pages, v_pages, kv_scales, &p.cache));
+  DA_TRY(check_rope(q, q_out, cos_sin, positions, q_weight, k_weight, axes, eps, k->shape[0], k->shape[2], true, &p));
+  if (interleaved != 0 && interleaved != 1) return DA_ERR_UNSUPPORTED;
+  if (p.T == 0 || p.cache.B == 0) return DA_OK;
+  return run_rope(p, k->shape[2], interleaved != 0, true, k_pages->dtype == DA_DTYPE_E4M3, stream);
 }
 
 int decode_attn_last_device_error(void* stream, int32_t* host_code) {

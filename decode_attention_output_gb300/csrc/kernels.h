@@ -288,6 +288,29 @@ struct CacheParams {
 };
 cudaError_t launch_cache(CacheParams& p, int dim, bool kv8, bool write, bool pdl, cudaStream_t stream);
 
+// --------------------- norms per head and the position rotation, apart or into a paged cache
+struct RopeParams {
+  CacheParams cache;          // keys (and for pages values and the pools); keys to packed rows: k, k_st, k_sh, Hkv, k_span alone
+  const __nv_bfloat16* q;     // [T][Hq][D]
+  __nv_bfloat16 *q_out, *k_out;
+  long long q_st, q_sh, qo_st, qo_sh, ko_st, ko_sh;
+  const void *q_weight, *k_weight;  // [D] bf16 or fp32, null: no norm
+  int q_weight_f32, k_weight_f32;
+  float eps;
+  const float* table;         // [P][R] fp32: cosines, then sines
+  long long table_st;
+  int P, R;
+  const int* pos;             // [A][T] positions (null: the tokens' places in their sequences)
+  long long pos_sa;
+  int A;
+  const int* axes;            // [R / 2] the axis of each pair (null: one axis)
+  int* err;
+  int T, Hq;                  // heads of q: 0 where there is none
+  int groups, q_groups, k_groups;  // set by the launcher: warps of a token, of its queries, of its keys
+  long long q_span, qo_span, ko_span;  // elements from the first to one past the last (bounds-checked build)
+};
+cudaError_t launch_rope(RopeParams& p, int dim, bool halves, bool pages, bool kv8, bool pdl, cudaStream_t stream);
+
 // ------------------------------------------------------- projection: GEMV path
 constexpr int kGemvThreads = 256;
 constexpr int kGemvCols = 256;  // 32 lanes x 8 columns

@@ -34,28 +34,6 @@ namespace {
 
 constexpr int kCacheWarps = 4;
 
-// Where token t lives: flat row index parts (block, row in the block), or false where the
-// token has no place. Whole warps call it; `lane` 0's error report counts once.
-template <bool WRITE>
-__device__ __forceinline__ bool locate(const CacheParams& p, int t, int lane, int* block, int* row) {
-  const int b = find_sequence(p.cu, p.B, t, lane);
-  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
-  if (t < c0 || t >= c1) return false;  // a row of no sequence
-  long long pos = t - c0;
-  if (WRITE) pos += (long long)__ldg(p.seq_lens + b) - ((long long)c1 - c0);
-  if (pos < 0) return false;  // older than the sequence's first token
-  const long long at = pos >> p.block_shift;
-  int blk = -1;
-  if (at < p.max_blocks && in_bounds(b >= 0 && b < p.B && b * p.bt_stride + at < p.table_span, p.err))
-    blk = __ldg(p.table + b * p.bt_stride + at);
-  *row = (int)(pos & ((1ll << p.block_shift) - 1));
-  *block = blk;
-  if ((unsigned)blk < (unsigned)p.num_blocks) return true;
-  if (lane == 0) atomicOr(p.err, kErrBlockTable);  // past the table, or a block outside the pool
-  *block = -1;
-  return !WRITE;  // such a token is not written, and reads as zeros
-}
-
 // Largest magnitudes of a lane's eight bf16 values, as two packed bf16 bit patterns (their
 // order is the magnitudes' order). Infinities and NaN, 0x7f80 and more, only with ALL.
 template <bool ALL>
@@ -72,13 +50,6 @@ __device__ __forceinline__ unsigned row_max(unsigned m) {
 #pragma unroll
   for (int off = LANES / 2; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
   return max(m & 0xffffu, m >> 16);
-}
-
-// Two floats to e4m3 codes (lo in the low byte), round to nearest even, saturating.
-__device__ __forceinline__ unsigned e4m3x2(float lo, float hi) {
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 template <int DIM, bool KV8, bool WRITE, int HG>

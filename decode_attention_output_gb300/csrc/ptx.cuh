@@ -21,6 +21,7 @@ enum : int {
   kErrTmem = 16,         // TMEM allocation failed
   kErrGridSync = 32,     // the fused step's grid barrier did not complete
   kErrBlockTable = 64,   // a paged cache's block table named a block outside the pool
+  kErrPosition = 128,    // a position outside the table of cosines and sines
   kErrBounds = 256,      // bounds-checked build: an index fell outside its buffer (access skipped)
 };
 

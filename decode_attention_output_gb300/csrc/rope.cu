@@ -1,0 +1,283 @@
+// rope.cu -- norms per head and the position rotation of queries and keys, and the same on the way into a paged cache.
+//
+// Per (token, head) row x of D dims, in fp32 and rounded once at the end:
+//   y = x * r * w,  r = (sum x^2 / D + eps)^-1/2                      (with a weight; y = x without)
+//   z_a = y_a c - y_b s,  z_b = y_b c + y_a s    for the R / 2 pairs (a, b) of dims, the others as they are
+// c, s = table[p][i], table[p][R / 2 + i]: pair i's angle at the token's position p on that pair's axis. Pairs are (i, i + R / 2), or
+// neighbours (2 i, 2 i + 1). Products and their difference are rounded one by one (no fused multiply-add): the largest
+// value of a row decides its scale in an e4m3 cache, and this way it is what the written formula gives.
+//
+// Into the cache: a key's z is rounded once, to bf16 or to e4m3 codes over 2^e with the least e that holds the row, as
+// kv_cache.cu does for values; the values are its rows unchanged. Queries go to packed rows.
+//
+// Bound by bytes: a row is read and written once, 4 D bytes (a key into an e4m3 cache 3 D + 4); its ~60 instructions a half
+// warp come near that only for the normed rows. A lane holds dims 4 l .. 4 l + 3 and their partners, so that neither pairing
+// needs a shuffle and a call may work in place; the norm's sum is four shuffles. A warp takes one token and eight rows of its
+// heads (two where tokens are few), so that the token's place, its position and its eight cosines and sines are found once,
+// while the rows are already on their way.
+#include "kernels.h"
+#include "packed.cuh"
+#include "ptx.cuh"
+
+namespace da {
+namespace {
+
+constexpr int kRopeWarps = 4;
+
+// Four weights of dims `at` .. `at` + 3.
+__device__ __forceinline__ float4 four_weights(const void* w, bool f32, int at) {
+  if (f32) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + at));
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + at));
+  return make_float4(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y));
+}
+
+__device__ __forceinline__ uint2 ldg_stream_v2(const void* p) {
+  uint2 r;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+
+// The least e with max <= 448 * 2^e for a row's largest magnitude (its fp32 bits), in [-124, 120]; 0 for a row of zeros.
+__device__ __forceinline__ int e4m3_exponent(unsigned m) {
+  // m = (1 + f / 2^23) 2^(E - 127); it fits 448 2^e = 1.75 2^(8 + e) with e = E - 135 when f <= 0.75 * 2^23, else with
+  // one more: adding 0x1fffff carries into E exactly when f is past that
+  return m == 0 ? 0 : min(max((int)((m + 0x1fffffu) >> 23) - 135, -124), 120);
+}
+
+enum Dest { kPacked, kPages16, kPages8 };  // where keys go
+
+// ROWS: rows of a warp, per lane group that holds one.
+template <int DIM, bool HALVES, int DEST, int ROWS>
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams p) {
+  constexpr int kLanes = DIM / 8, kAt = 32 / kLanes;  // lanes of a row; rows at a time
+  constexpr int kRows = ROWS * kAt;
+  const CacheParams& cp = p.cache;
+  const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
+  pdl_wait_primary();
+  const long long unit = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const int t = (int)(unit / p.groups), g = (int)(unit - (long long)t * p.groups);
+  if (t >= p.T) return;
+  const bool is_q = g < p.q_groups, is_k = !is_q && g < p.q_groups + p.k_groups;
+  const int heads = is_q ? p.Hq : cp.Hkv;
+  const int h0 = (is_q ? g : is_k ? g - p.q_groups : g - p.q_groups - p.k_groups) * kRows + sub;
+
+  // This lane's two runs of four dims. Pairs of halves: dims 4 l and the same of the other half, and
+  // behind the R rotated ones two runs that stay. Neighbours: any two runs.
+  const int eighth = p.R / 8;
+  int d0 = 4 * l, d1 = 4 * l + DIM / 2;
+  bool turn0 = d0 < p.R, turn1 = d1 < p.R;
+  if (HALVES) {
+    turn0 = turn1 = l < eighth;
+    d0 = turn0 ? 4 * l : 4 * (l + eighth);
+    d1 = turn0 ? 4 * (l + eighth) : 4 * l + DIM / 2;
+  }
+
+  const __nv_bfloat16* from = is_q ? p.q + t * p.q_st : is_k ? cp.k + t * cp.k_st : cp.v + t * cp.v_st;
+  const long long from_sh = is_q ? p.q_sh : is_k ? cp.k_sh : cp.v_sh;
+  const __nv_bfloat16* from_end = is_q ? p.q + p.q_span : is_k ? cp.k + cp.k_span : cp.v + cp.v_span;
+  uint2 x[ROWS][2];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const __nv_bfloat16* at = from + (h0 + i * kAt) * from_sh;
+    const bool ok = h0 + i * kAt < heads && in_bounds(at + DIM <= from_end, p.err);
+    x[i][0] = ok ? ldg_stream_v2(at + d0) : make_uint2(0, 0);
+    x[i][1] = ok ? ldg_stream_v2(at + d1) : make_uint2(0, 0);
+  }
+
+  // The token's place, and with it its position unless the caller gives one
+  int seq = 0, block = 0, row = 0;
+  long long place = 0;
+  if (DEST != kPacked) {
+    if (!token_place<true>(cp, t, lane, &seq, &place)) return;
+    if (!is_q && !place_block<true>(cp, seq, place, lane, &block, &row)) return;
+  }
+
+  float c[4], s[4];  // halves: of this lane's four pairs; neighbours: two of each run
+  if (DEST == kPacked || is_q || is_k) {
+    bool far = false;  // a position that the table does not hold: an angle of 0
+    if (p.axes == nullptr) {
+      const long long pos = p.pos ? (long long)__ldg(p.pos + t) : place;
+      far = pos < 0 || pos >= p.P;
+      const float* tr = p.table + (far ? 0 : pos) * p.table_st;
+      const float *c0 = tr + (HALVES ? 4 * l : 2 * l), *c1 = tr + (HALVES ? 4 * l + 2 : 2 * l + DIM / 4);
+      const bool t0 = turn0 && !far && in_bounds((HALVES ? 4 * l + 4 : 2 * l + 2) <= p.R / 2, p.err);
+      const bool t1 = turn1 && !far && in_bounds((HALVES ? 4 * l + 4 : 2 * l + DIM / 4 + 2) <= p.R / 2, p.err);
+      const float2 one = make_float2(1.f, 1.f), zero = make_float2(0.f, 0.f);
+      const float2 ca = t0 ? __ldg(reinterpret_cast<const float2*>(c0)) : one, cb = t1 ? __ldg(reinterpret_cast<const float2*>(c1)) : one;
+      const float2 sa = t0 ? __ldg(reinterpret_cast<const float2*>(c0 + p.R / 2)) : zero,
+                   sb = t1 ? __ldg(reinterpret_cast<const float2*>(c1 + p.R / 2)) : zero;
+      c[0] = ca.x, c[1] = ca.y, c[2] = cb.x, c[3] = cb.y;
+      s[0] = sa.x, s[1] = sa.y, s[2] = sb.x, s[3] = sb.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int pair = HALVES ? 4 * l + i : i < 2 ? 2 * l + i : 2 * l + DIM / 4 + i - 2;
+        const bool turn = i < 2 ? turn0 : turn1;
+        const int axis = turn ? __ldg(p.axes + pair) : 0;
+        const bool known = (unsigned)axis < (unsigned)p.A;
+        const int pos = turn && known ? __ldg(p.pos + axis * p.pos_sa + t) : 0;
+        const bool off = !known || (unsigned)pos >= (unsigned)p.P;
+        const float* at = p.table + (long long)pos * p.table_st + pair;
+        far |= turn && off;
+        c[i] = turn && !off ? __ldg(at) : 1.f;
+        s[i] = turn && !off ? __ldg(at + p.R / 2) : 0.f;
+      }
+    }
+    if (__any_sync(0xffffffffu, far) && lane == 0) atomicOr(p.err, kErrPosition);
+  } else {
+    turn0 = turn1 = false;
+  }
+  const void* weight = is_q ? p.q_weight : is_k ? p.k_weight : nullptr;
+  const bool w32 = is_q ? p.q_weight_f32 : p.k_weight_f32;
+  float4 w0 = make_float4(1.f, 1.f, 1.f, 1.f), w1 = w0;
+  if (weight) {
+    w0 = four_weights(weight, w32, d0);
+    w1 = four_weights(weight, w32, d1);
+  }
+
+  // Where the rows go
+  const bool packed = is_q || DEST == kPacked;
+  __nv_bfloat16* to = is_q ? p.q_out + t * p.qo_st : p.k_out + t * p.ko_st;
+  long long to_sh = is_q ? p.qo_sh : p.ko_sh;
+  const __nv_bfloat16* to_end = is_q ? p.q_out + p.qo_span : p.k_out + p.ko_span;
+  if (!packed) {
+    const long long at = is_k ? block * cp.kp_sb + row * cp.kp_sr : block * cp.vp_sb + row * cp.vp_sr;
+    to_sh = is_k ? cp.kp_sh : cp.vp_sh;
+    void* pool = is_k ? cp.k_pages : cp.v_pages;
+    if (DEST == kPages8) {
+      to = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(pool) + at);
+      to_end = reinterpret_cast<const __nv_bfloat16*>(static_cast<uint8_t*>(pool) + (is_k ? cp.kp_span : cp.vp_span));
+    } else {
+      to = static_cast<__nv_bfloat16*>(pool) + at;
+      to_end = static_cast<const __nv_bfloat16*>(pool) + (is_k ? cp.kp_span : cp.vp_span);
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int h = h0 + i * kAt;
+    if (i > 0 && __all_sync(0xffffffffu, h >= heads)) break;
+    float y[8] = {bf16lo_to_f32(x[i][0].x), bf16hi_to_f32(x[i][0].x), bf16lo_to_f32(x[i][0].y), bf16hi_to_f32(x[i][0].y),
+                  bf16lo_to_f32(x[i][1].x), bf16hi_to_f32(x[i][1].x), bf16lo_to_f32(x[i][1].y), bf16hi_to_f32(x[i][1].y)};
+    if (weight) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = fmaf(y[k], y[k], sum);
+#pragma unroll
+      for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      const float r = rsqrtf(sum * (1.f / DIM) + p.eps);
+      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = y[k] * r * w[k];
+    }
+    if (HALVES) {
+      if (turn0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = y[k], b = y[k + 4];
+          y[k] = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
+          y[k + 4] = __fadd_rn(__fmul_rn(b, c[k]), __fmul_rn(a, s[k]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k < 2 ? turn0 : turn1) {
+          const float a = y[2 * k], b = y[2 * k + 1];
+          y[2 * k] = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
+          y[2 * k + 1] = __fadd_rn(__fmul_rn(b, c[k]), __fmul_rn(a, s[k]));
+        }
+      }
+    }
+    if (DEST == kPages8 && !is_q) {
+      unsigned m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(y[k]) & 0x7fffffffu);
+#pragma unroll
+      for (int off = kLanes / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {  // infinities and NaN do not count
+        m = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const unsigned b = __float_as_uint(y[k]) & 0x7fffffffu;
+          m = max(m, b < 0x7f800000u ? b : 0u);
+        }
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      }
+      const int e = e4m3_exponent(m);
+      const float inv = __int_as_float((127 - e) << 23);
+      unsigned code[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) code[k] = e4m3x2(y[2 * k] * inv, y[2 * k + 1] * inv);
+      if (e == 120) {  // codes 0x78 .. 0x7e (256 .. 448) become 0x77 (240), as 256 * 2^120 is no bf16 value; 0x7f is NaN
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int b = 0; b < 16; b += 8) {
+            const unsigned mag = code[k] >> b & 0x7fu;
+            if (mag > 0x77u && mag < 0x7fu) code[k] -= (mag - 0x77u) << b;
+          }
+      }
+      uint8_t* at = reinterpret_cast<uint8_t*>(to) + h * to_sh;
+      const long long sc = block * cp.sc_sb + h * cp.sc_sh + (is_k ? 0 : cp.sc_st) + row;
+      if (h < heads && in_bounds(at + DIM <= reinterpret_cast<const uint8_t*>(to_end) && sc < cp.sc_span, p.err)) {
+        *reinterpret_cast<unsigned*>(at + d0) = __byte_perm(code[0], code[1], 0x5410);
+        *reinterpret_cast<unsigned*>(at + d1) = __byte_perm(code[2], code[3], 0x5410);
+        if (l == 0) cp.scales[sc] = __int_as_float((127 + e) << 23);
+      }
+    } else {
+      __nv_bfloat16* at = to + h * to_sh;
+      if (h < heads && in_bounds(at + DIM <= to_end, p.err)) {
+        const bool as_is = DEST == kPages16 && !is_q && !is_k;  // values: their bits, of NaN too
+        *reinterpret_cast<uint2*>(at + d0) = as_is ? x[i][0] : make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+        *reinterpret_cast<uint2*>(at + d1) = as_is ? x[i][1] : make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+      }
+    }
+  }
+}
+
+template <int DIM, bool HALVES, int DEST>
+cudaError_t launch_rows(RopeParams& p, bool pdl, cudaStream_t stream) {
+  constexpr int kAt = 32 / (DIM / 8);
+  auto plan = [&](int rows) {
+    const int each = rows * kAt;
+    p.q_groups = (p.Hq + each - 1) / each;
+    p.k_groups = (p.cache.Hkv + each - 1) / each;
+    p.groups = p.q_groups + p.k_groups * (DEST == kPacked ? 1 : 2);
+    return (long long)p.T * p.groups;
+  };
+  // Four rows of each lane group, or one where that would leave SMs without a warp (a decode step's few tokens)
+  const bool many = plan(4) >= 4096;
+  const long long warps = many ? plan(4) : plan(1), blocks = (warps + kRopeWarps - 1) / kRopeWarps;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kRopeWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  const RopeParams& c = p;
+  return many ? cudaLaunchKernelEx(&cfg, rope_kernel<DIM, HALVES, DEST, 4>, c) : cudaLaunchKernelEx(&cfg, rope_kernel<DIM, HALVES, DEST, 1>, c);
+}
+
+template <int DIM, int DEST>
+cudaError_t launch_pairs(RopeParams& p, bool halves, bool pdl, cudaStream_t stream) {
+  return halves ? launch_rows<DIM, true, DEST>(p, pdl, stream) : launch_rows<DIM, false, DEST>(p, pdl, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(RopeParams& p, int dim, bool halves, bool pages, bool kv8, bool pdl, cudaStream_t stream) {
+  if (dim == kHeadDim) {
+    if (!pages) return launch_pairs<kHeadDim, kPacked>(p, halves, pdl, stream);
+    return kv8 ? launch_pairs<kHeadDim, kPages8>(p, halves, pdl, stream) : launch_pairs<kHeadDim, kPages16>(p, halves, pdl, stream);
+  }
+  if (dim != kHeadDimWide || (pages && kv8)) return cudaErrorInvalidValue;
+  return pages ? launch_pairs<kHeadDimWide, kPages16>(p, halves, pdl, stream) : launch_pairs<kHeadDimWide, kPacked>(p, halves, pdl, stream);
+}
+
+}  // namespace da

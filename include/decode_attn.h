@@ -320,6 +320,55 @@ int decode_attn_cache_read(const da_tensor_t* k_pages, const da_tensor_t* v_page
                            const da_tensor_t* v_out, void* stream);
 
 /*
+ * decode_attn_rope -- the norms per head and the position rotation of packed tokens' queries and
+ * keys, in one pass: what stands between their projection and an attention.
+ *
+ *   q [T, Hq, D], k [T, Hkv, D] bf16, D = 128 or 256; q_out and k_out like them, written, apart
+ *              or the same memory as their inputs (in place; no other overlap). q with q_out, or k
+ *              with k_out, may be NULL.
+ *   cos_sin    [P, R] fp32: of the R / 2 pairs of dims that are rotated, the cosines and then the
+ *              sines at each position; R a multiple of 8, at most D
+ *   positions  [T] int32 (device), or [A, T] for positions of A axes (A <= 4: time, height,
+ *              width); the last dimension contiguous
+ *   q_weight, k_weight [D] bf16 or fp32, contiguous and 16-byte aligned: the norm's weights; NULL:
+ *              no norm
+ *   axes       [R / 2] int32 (device), contiguous: the position axis that each pair follows; NULL: axis 0
+ *              (A > 1 needs it)
+ *   eps        finite, >= 0
+ *   interleaved  0: pair i is dims (i, i + R / 2); 1: dims (2 i, 2 i + 1)
+ *
+ * Per row: y = x / sqrt(mean(x^2) + eps) * weight where there is one; then (a, b) becomes
+ * (a c - b s, b c + a s) for each pair; dims from R on keep y. All in fp32 (the mean's sum too),
+ * rounded once to bf16. A position outside [0, P), or an axis outside [0, A), counts as an angle of
+ * 0 and sets bit 128 of the device error word.
+ */
+int decode_attn_rope(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* cos_sin, const da_tensor_t* positions,
+                     const da_tensor_t* q_out, const da_tensor_t* k_out, const da_tensor_t* q_weight, const da_tensor_t* k_weight,
+                     const da_tensor_t* axes, float eps, int32_t interleaved, void* stream);
+
+/*
+ * decode_attn_rope_cache_write -- decode_attn_rope of the new tokens' q and k, with k and v going
+ * straight into a paged cache: decode_attn_rope and decode_attn_cache_write in one launch.
+ *
+ *   q, q_out [T, Hq, D] bf16, or both NULL; k, v [T, Hkv, D] bf16
+ *   cos_sin, q_weight, k_weight, axes, eps, interleaved: as decode_attn_rope
+ *   positions  as decode_attn_rope, or NULL: each token's place in its sequence (one axis)
+ *   cu_seqlens, block_table, seq_lens, k_pages, v_pages, kv_scales: as decode_attn_cache_write
+ *
+ * A bf16 pool holds what decode_attn_rope gives for k, and v unchanged. An e4m3 pool's codes and
+ * scales of k come from the rotated fp32 values directly (one rounding: they can differ by one from
+ * those of the bf16 values), by the rule of decode_attn_cache_write; v's are that function's own.
+ * Tokens that decode_attn_cache_write would not write are not written; q_out is left as it was in
+ * rows that belong to no sequence and in those before a sequence's first token. Bits 64 and 128
+ * of the device error word as in those two functions.
+ */
+int decode_attn_rope_cache_write(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cos_sin,
+                                 const da_tensor_t* cu_seqlens, const da_tensor_t* block_table, const da_tensor_t* seq_lens,
+                                 const da_tensor_t* q_out, const da_tensor_t* k_pages, const da_tensor_t* v_pages,
+                                 const da_tensor_t* kv_scales, const da_tensor_t* positions, const da_tensor_t* q_weight,
+                                 const da_tensor_t* k_weight, const da_tensor_t* axes, float eps, int32_t interleaved, void* stream);
+
+/*
  * decode_attn_scores -- the first contraction alone: the page's `scores_fp32`
  * (q_grouped . k_cache^T, b_trans=True), unscaled, in fp32.
  *   scores [B, Hq, Lcap] fp32: scores[b, h, t] is written for t < seq_lens[b]
@@ -421,7 +470,7 @@ int decode_attn_get_option(const char* key, int64_t* value);
  * 2 a producer gave up waiting for a free stage, 4 copies still in flight at
  * exit, 8 a tensor-core completion never arrived, 32 the fused step's grid
  * barrier did not complete, 64 a paged cache's block table named a block outside
- * the pool. A non-zero word is cleared, and with it the completion counters and
+ * the pool, 128 a position outside the table of cosines and sines. A non-zero word is cleared, and with it the completion counters and
  * grid-barrier words beside it (a CTA that gave up left them short of the count
  * that resets them), so that the next call starts clean. Returns DA_OK, or
  * DA_ERR_CUDA when the synchronisation or a copy failed.
