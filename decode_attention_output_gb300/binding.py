@@ -30,7 +30,7 @@ _DTYPES = {torch.bfloat16: DA_DTYPE_BF16, torch.float32: DA_DTYPE_F32, torch.int
 # every symbol declared in include/decode_attn.h
 EXPORTS = ("decode_attn_fwd", "decode_attn_only", "decode_attn_only_noalloc", "decode_attn_fwd_paged",
            "decode_attn_only_paged", "decode_attn_fwd_fp8", "decode_attn_only_fp8", "decode_attn_fwd_paged_fp8", "decode_attn_only_paged_fp8",
-           "decode_attn_prefill", "decode_attn_cache_write", "decode_attn_cache_read", "decode_attn_rope", "decode_attn_rope_cache_write", "decode_attn_scores", "decode_attn_oproj", "decode_attn_set_option", "decode_attn_get_option", "decode_attn_last_device_error", "decode_attn_device_error",
+           "decode_attn_prefill", "decode_attn_prefill_window", "decode_attn_chunk", "decode_attn_cache_write", "decode_attn_cache_read", "decode_attn_rope", "decode_attn_rope_cache_write", "decode_attn_scores", "decode_attn_oproj", "decode_attn_set_option", "decode_attn_get_option", "decode_attn_last_device_error", "decode_attn_device_error",
            "decode_attn_release", "decode_attn_status_str")
 
 
@@ -72,6 +72,8 @@ def load_library(path: str) -> ctypes.CDLL:
     lib.decode_attn_cache_write.argtypes = [P, P, P, P, P, P, P, P, vp]
     lib.decode_attn_cache_read.argtypes = [P, P, P, P, P, P, P, vp]
     i32 = ctypes.c_int32
+    lib.decode_attn_prefill_window.argtypes = [P] * 6 + [f32, i32, i32, vp]
+    lib.decode_attn_chunk.argtypes = [P] * 8 + [f32, i32, i32, vp]
     lib.decode_attn_rope.argtypes = [P] * 9 + [f32, i32, vp]
     lib.decode_attn_rope_cache_write.argtypes = [P] * 15 + [f32, i32, vp]
     lib.decode_attn_scores.argtypes = [P, P, P, P, vp]
@@ -273,6 +275,30 @@ def decode_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, out, scale: float, 
     lib = _lib or load()  # the lock only until the library is loaded
     _check("decode_attn_prefill",
            _call(lib.addr["decode_attn_prefill"], _stream(stream), 6, q, k, v, cu_seqlens_q, cu_seqlens_k, out, scale))
+    return out
+
+
+def decode_attn_prefill_window(q, k, v, cu_seqlens_q, cu_seqlens_k, out, scale: float, window: int, sinks: int = 0,
+                               stream=None) -> torch.Tensor:
+    """decode_attn_prefill in which the query at position i sees keys i - window + 1 .. i and the first ``sinks`` ones
+    (window 0: all, as decode_attn_prefill). Returns ``out``."""
+    lib = _lib or load()  # the lock only until the library is loaded
+    _check("decode_attn_prefill_window",
+           _call_ints(lib.addr["decode_attn_prefill_window"], _stream(stream), 6,
+                      q, k, v, cu_seqlens_q, cu_seqlens_k, out, scale, window, sinks))
+    return out
+
+
+def decode_attn_chunk(q, k_pages, v_pages, kv_scales, block_table, cu_seqlens, seq_lens, out, scale: float, window: int = 0,
+                      sinks: int = 0, stream=None) -> torch.Tensor:
+    """Attention of a chunk of new tokens over a paged cache that holds them already: q and out [T, Hq, 128], rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] the last tokens of the seq_lens[b] of sequence b (one each: a decode step). Pools
+    as decode_attn_cache_write fills them (kv_scales None: bf16). With a window the query at position i sees keys
+    i - window + 1 .. i and the first ``sinks`` ones; 0: all up to i. Returns ``out``."""
+    lib = _lib or load()  # the lock only until the library is loaded
+    _check("decode_attn_chunk",
+           _call_ints(lib.addr["decode_attn_chunk"], _stream(stream), 8,
+                      q, k_pages, v_pages, kv_scales, block_table, cu_seqlens, seq_lens, out, scale, window, sinks))
     return out
 
 

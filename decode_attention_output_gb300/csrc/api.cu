@@ -153,7 +153,8 @@ EncodeTiledFn encode_fn() {
 // rows, 128-byte swizzle): one copy per tile and tensor (box_tokens 0: tile_tokens(D)).
 // An fp8 (e4m3) cache is mapped the same way with 128-dim boxes (128-byte rows): at
 // D = 128 a tile is one box of 64 tokens x 128 bytes.
-int encode_kv_map(CUtensorMap* map, const da_tensor_t* t, int box_tokens = 0) {
+// box_dims > 0: so many of the D/64 dim boxes a copy instead of all.
+int encode_kv_map(CUtensorMap* map, const da_tensor_t* t, int box_tokens = 0, int box_dims = 0) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return DA_ERR_CUDA;
   const int64_t B = t->shape[0], H = t->shape[1], L = t->shape[2], D = t->shape[3];
@@ -165,7 +166,7 @@ int encode_kv_map(CUtensorMap* map, const da_tensor_t* t, int box_tokens = 0) {
   cuuint64_t dims[5] = {(cuuint64_t)inner, (cuuint64_t)L, (cuuint64_t)(D / inner), (cuuint64_t)H, (cuuint64_t)B};
   cuuint64_t strides[4] = {(cuuint64_t)(st * es), 128, (cuuint64_t)(sh * es), (cuuint64_t)(sb * es)};
   cuuint32_t box[5] = {(cuuint32_t)inner, (cuuint32_t)(box_tokens > 0 ? box_tokens : tile_tokens((int)D)),
-                       (cuuint32_t)(D / inner), 1, 1};
+                       (cuuint32_t)(box_dims > 0 ? box_dims : D / inner), 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUtensorMapDataType type = es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUresult r = enc(map, type, 5, t->data, dims, strides, box, estr,
@@ -1073,6 +1074,101 @@ int fwd_checked(const da_tensor_t* q, const da_tensor_t* k_cache, const da_tenso
                         o.pdl != 0, st);
 }
 
+int check_window(float scale, int window, int sinks) {
+  if (!std::isfinite(scale * 1.4426950408889634f)) return DA_ERR_UNSUPPORTED;
+  return window < 0 || sinks < 0 ? DA_ERR_UNSUPPORTED : DA_OK;
+}
+
+enum PrefillOver { kPrompt, kPromptWindow, kChunk16, kChunk8 };
+
+// The attention of packed queries after its checks: p holds the keys (cu_q, cu_k, Tk, maps, pages); `longest`: keys of
+// a sequence at most, as far as the host knows.
+int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const da_tensor_t* out, int64_t B, int64_t Hkv,
+                int64_t longest, float scale, int window, int sinks, void* stream) {
+  const int64_t Tq = q->shape[0], Hq = q->shape[1];
+  p.G = (int)(Hq / Hkv);
+  p.npos = 128 / p.G;
+  // items: 2 * npos positions of one sequence and KV head, at most one ragged per sequence
+  const int64_t items = ((Tq + 2 * p.npos - 1) / (2 * p.npos) + B - 1) * Hkv;
+  if (items >= ((int64_t)1 << 31) - 4096) return DA_ERR_UNSUPPORTED;
+  DA_TRY(encode_packed_map(&p.tm_q, q, p.npos, p.G));
+  p.window = window ? std::min(window, 1 << 30) : 1 << 30;
+  p.sinks = window ? std::min(sinks, 1 << 30) : 0;
+  // Fewer items than half the SMs, and sequences long enough to gain: as many parts as there are SMs for; the kernel cuts
+  // an item into fewer where it has few K/V tiles.
+  int64_t tiles = (longest + 127) / 128;
+  if (window) tiles = std::min<int64_t>(tiles, ((int64_t)p.window + 2 * p.npos + 127) / 128 + 1 + ((int64_t)p.sinks + 127) / 128);
+  const int64_t sms = std::max(1, sm_count());
+  p.parts = tiles < kPrefillCutTiles
+                ? 1
+                : (int)std::max<int64_t>(1, std::min<int64_t>({sms / items, tiles / kPrefillPartTiles, (int64_t)kMaxPrefillParts}));
+  const size_t rows = p.parts > 1 ? (size_t)p.parts * Tq * Hq : 0, ml_bytes = align_up(rows * 2 * 4, 256);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = nullptr;
+  DA_TRY(workspace_get(ml_bytes + rows * 128 * 4, st, &ws));
+  p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
+  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
+  p.err = reinterpret_cast<int*>(ws + kErrOff);
+  p.out = static_cast<__nv_bfloat16*>(out->data);
+  p.o_st = out->stride[0];
+  p.o_sh = out->stride[1];
+  p.out_span = span_of(out);
+  p.part_rows = (long long)rows;
+  p.B = (int)B;
+  p.Hkv = (int)Hkv;
+  p.Tq = (int)Tq;
+  // the kernel masks with infinities: a scale of 0 becomes the smallest number, which leaves every
+  // weight within 2^-21 of 1 whatever the products are
+  p.scale_log2 = scale * 1.4426950408889634f;
+  if (p.scale_log2 == 0.f) p.scale_log2 = 0x1p-149f;
+  const int grid = (int)items * p.parts;
+  const bool pdl = options_snapshot().attn_pdl != 0;
+  const cudaError_t e = over == kPrompt         ? launch_prefill(p, grid, pdl, st)
+                        : over == kPromptWindow ? launch_prefill_window(p, grid, pdl, st)
+                                                : launch_prefill_paged(p, grid, over == kChunk8, pdl, st);
+  return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+// decode_attn_prefill and, with a window, decode_attn_prefill_window.
+int prefill_checked(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cq, const da_tensor_t* ck,
+                    const da_tensor_t* out, float scale, int window, int sinks, void* stream) {
+  DA_TRY(check_tensor(q, DA_DTYPE_BF16, 3, kInput16));
+  DA_TRY(check_tensor(k, DA_DTYPE_BF16, 3, kInput16));
+  DA_TRY(check_tensor(v, DA_DTYPE_BF16, 3, kInput16));
+  DA_TRY(check_tensor(out, DA_DTYPE_BF16, 3, kInput16));  // rows leave in 16-byte stores
+  if (!cq || !ck) return DA_ERR_NULL;
+  if (cq->dtype != DA_DTYPE_I32 || ck->dtype != DA_DTYPE_I32) return DA_ERR_DTYPE;
+  if (cq->ndim != 1 || ck->ndim != 1) return DA_ERR_SHAPE;
+  const int64_t Tq = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
+  if (D != kHeadDim && D != kHeadDimWide) return DA_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i)
+    if (out->shape[i] != q->shape[i] || v->shape[i] != k->shape[i]) return DA_ERR_SHAPE;
+  if (k->shape[2] != D || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return DA_ERR_SHAPE;
+  const int64_t B = cq->shape[0] - 1;
+  if (B < 0 || ck->shape[0] != B + 1) return DA_ERR_SHAPE;
+  if (D != kHeadDim || Hq / Hkv > kMaxGroup || B > DA_MAX_BATCH) return DA_ERR_UNSUPPORTED;
+  if (Tq > (1 << 30) || Tk > (1 << 30) || Hq > (1 << 20)) return DA_ERR_UNSUPPORTED;
+  DA_TRY(check_window(scale, window, sinks));
+  for (const da_tensor_t* t : {cq, ck}) {
+    if (!t->data) return DA_ERR_NULL;
+    if (B > 0 && t->stride[0] != 1) return DA_ERR_STRIDE;
+    if (reinterpret_cast<uintptr_t>(t->data) % 4) return DA_ERR_ALIGN;
+  }
+  if (B == 0 || Tq == 0) return DA_OK;
+  PrefillParams p;
+  memset(&p, 0, sizeof(p));
+  if (Tk > 0) {
+    DA_TRY(encode_packed_map(&p.tm_k, k, 128, 0));
+    DA_TRY(encode_packed_map(&p.tm_v, v, 128, 0));
+  }
+  p.cu_q = static_cast<const int*>(cq->data);
+  p.cu_k = static_cast<const int*>(ck->data);
+  p.Tk = (int)Tk;
+  // (a ragged sequence may be twice the average: of whole tiles, in keys)
+  const int64_t longest = std::min<int64_t>(Tk, 256 * ((Tk / B + 127) / 128));
+  return run_prefill(p, window ? kPromptWindow : kPrompt, q, out, B, Hkv, longest, scale, window, sinks, stream);
+}
+
 // decode_attn_cache_write / _read after their checks: one launch.
 int run_cache(CacheParams& p, int dim, bool kv8, bool write, void* stream) {
   if (p.T == 0 || p.B == 0) return DA_OK;
@@ -1411,72 +1507,70 @@ int decode_attn_fwd_paged_fp8(const da_tensor_t* q, const da_tensor_t* k_pages, 
 int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v,
                         const da_tensor_t* cu_seqlens_q, const da_tensor_t* cu_seqlens_k, const da_tensor_t* out,
                         float scale, void* stream) {
+  return prefill_checked(q, k, v, cu_seqlens_q, cu_seqlens_k, out, scale, 0, 0, stream);
+}
+
+int decode_attn_prefill_window(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v,
+                               const da_tensor_t* cu_seqlens_q, const da_tensor_t* cu_seqlens_k, const da_tensor_t* out,
+                               float scale, int32_t window, int32_t sinks, void* stream) {
+  return prefill_checked(q, k, v, cu_seqlens_q, cu_seqlens_k, out, scale, window, sinks, stream);
+}
+
+int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages, const da_tensor_t* kv_scales,
+                      const da_tensor_t* block_table, const da_tensor_t* cu_seqlens, const da_tensor_t* seq_lens,
+                      const da_tensor_t* out, float scale, int32_t window, int32_t sinks, void* stream) {
   DA_TRY(check_tensor(q, DA_DTYPE_BF16, 3, kInput16));
-  DA_TRY(check_tensor(k, DA_DTYPE_BF16, 3, kInput16));
-  DA_TRY(check_tensor(v, DA_DTYPE_BF16, 3, kInput16));
   DA_TRY(check_tensor(out, DA_DTYPE_BF16, 3, kInput16));  // rows leave in 16-byte stores
-  const da_tensor_t *cq = cu_seqlens_q, *ck = cu_seqlens_k;
-  if (!cq || !ck) return DA_ERR_NULL;
-  if (cq->dtype != DA_DTYPE_I32 || ck->dtype != DA_DTYPE_I32) return DA_ERR_DTYPE;
-  if (cq->ndim != 1 || ck->ndim != 1) return DA_ERR_SHAPE;
-  const int64_t Tq = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
+  const da_tensor_t *kp = k_pages, *vp = v_pages, *table = block_table, *cu = cu_seqlens, *lens = seq_lens;
+  if (!kp || !vp || !table || !cu || !lens) return DA_ERR_NULL;
+  if (kp->dtype != DA_DTYPE_BF16 && kp->dtype != DA_DTYPE_E4M3) return DA_ERR_DTYPE;
+  const bool kv8 = kp->dtype == DA_DTYPE_E4M3;
+  DA_TRY(check_tensor(kp, kp->dtype, 4, kInput16));
+  DA_TRY(check_tensor(vp, kp->dtype, 4, kInput16));
+  if (kv8) DA_TRY(check_scales(kv_scales, kp));
+  else if (kv_scales) return DA_ERR_DTYPE;  // a bf16 pool has no scales
+  if (table->dtype != DA_DTYPE_I32 || cu->dtype != DA_DTYPE_I32 || lens->dtype != DA_DTYPE_I32) return DA_ERR_DTYPE;
+  if (table->ndim != 2 || cu->ndim != 1 || lens->ndim != 1) return DA_ERR_SHAPE;
+  const int64_t Tq = q->shape[0], Hq = q->shape[1], D = q->shape[2];
+  const int64_t NB = kp->shape[0], Hkv = kp->shape[1], BS = kp->shape[2], B = table->shape[0], MB = table->shape[1];
   if (D != kHeadDim && D != kHeadDimWide) return DA_ERR_SHAPE;
   for (int i = 0; i < 3; ++i)
-    if (out->shape[i] != q->shape[i] || v->shape[i] != k->shape[i]) return DA_ERR_SHAPE;
-  if (k->shape[2] != D || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return DA_ERR_SHAPE;
-  const int64_t B = cq->shape[0] - 1;
-  if (B < 0 || ck->shape[0] != B + 1) return DA_ERR_SHAPE;
+    if (out->shape[i] != q->shape[i]) return DA_ERR_SHAPE;
+  for (int i = 0; i < 4; ++i)
+    if (vp->shape[i] != kp->shape[i]) return DA_ERR_SHAPE;
+  if (kp->shape[3] != D || Hq <= 0 || Hkv <= 0 || Hq % Hkv || NB <= 0 || BS <= 0 || MB <= 0) return DA_ERR_SHAPE;
+  if (cu->shape[0] != B + 1 || lens->shape[0] != B) return DA_ERR_SHAPE;
   if (D != kHeadDim || Hq / Hkv > kMaxGroup || B > DA_MAX_BATCH) return DA_ERR_UNSUPPORTED;
-  if (Tq > (1 << 30) || Tk > (1 << 30) || Hq > (1 << 20)) return DA_ERR_UNSUPPORTED;
-  if (!std::isfinite(scale * 1.4426950408889634f)) return DA_ERR_UNSUPPORTED;
-  for (const da_tensor_t* t : {cq, ck}) {
-    if (!t->data) return DA_ERR_NULL;
-    if (B > 0 && t->stride[0] != 1) return DA_ERR_STRIDE;
-    if (reinterpret_cast<uintptr_t>(t->data) % 4) return DA_ERR_ALIGN;
+  if (!paged_block_ok((int)std::min<int64_t>(BS, 1 << 30), (int)D, kv8)) return DA_ERR_UNSUPPORTED;
+  if (Tq > (1 << 30) || Hq > (1 << 20) || NB >= ((int64_t)1 << 31) || MB > ((int64_t)1 << 30) || MB * BS > ((int64_t)1 << 30))
+    return DA_ERR_UNSUPPORTED;
+  DA_TRY(check_window(scale, window, sinks));
+  if (!cu->data) return DA_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(cu->data) % 4) return DA_ERR_ALIGN;
+  if (B > 0) {
+    if (!table->data || !lens->data) return DA_ERR_NULL;
+    if (cu->stride[0] != 1 || (B > 1 && lens->stride[0] != 1)) return DA_ERR_STRIDE;
+    if (MB > 1 && table->stride[1] != 1) return DA_ERR_STRIDE;
+    if (B > 1 && table->stride[0] < MB) return DA_ERR_STRIDE;
+    if (reinterpret_cast<uintptr_t>(table->data) % 4 || reinterpret_cast<uintptr_t>(lens->data) % 4) return DA_ERR_ALIGN;
   }
   if (B == 0 || Tq == 0) return DA_OK;
   PrefillParams p;
   memset(&p, 0, sizeof(p));
-  p.G = (int)(Hq / Hkv);
-  p.npos = 128 / p.G;
-  // items: 2 * npos positions of one sequence and KV head, at most one ragged per sequence
-  const int64_t items = ((Tq + 2 * p.npos - 1) / (2 * p.npos) + B - 1) * Hkv;
-  if (items >= ((int64_t)1 << 31) - 4096) return DA_ERR_UNSUPPORTED;
-  DA_TRY(encode_packed_map(&p.tm_q, q, p.npos, p.G));
-  if (Tk > 0) {
-    DA_TRY(encode_packed_map(&p.tm_k, k, 128, 0));
-    DA_TRY(encode_packed_map(&p.tm_v, v, 128, 0));
-  }
-  // Fewer items than half the SMs, and sequences long enough to gain (a ragged one may be
-  // twice the average): as many parts as there are SMs for; the kernel cuts an item into fewer
-  // where it has few K/V tiles.
-  const int64_t sms = std::max(1, sm_count()), tiles = std::min<int64_t>((Tk + 127) / 128, 2 * ((Tk / B + 127) / 128));
-  p.parts = tiles < kPrefillCutTiles
-                ? 1
-                : (int)std::max<int64_t>(1, std::min<int64_t>({sms / items, tiles / kPrefillPartTiles, (int64_t)kMaxPrefillParts}));
-  const size_t rows = p.parts > 1 ? (size_t)p.parts * Tq * Hq : 0, ml_bytes = align_up(rows * 2 * 4, 256);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  char* ws = nullptr;
-  DA_TRY(workspace_get(ml_bytes + rows * 128 * 4, st, &ws));
-  p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
-  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
-  p.err = reinterpret_cast<int*>(ws + kErrOff);
-  p.out = static_cast<__nv_bfloat16*>(out->data);
-  p.o_st = out->stride[0];
-  p.o_sh = out->stride[1];
-  p.out_span = span_of(out);
-  p.part_rows = (long long)rows;
-  p.cu_q = static_cast<const int*>(cq->data);
-  p.cu_k = static_cast<const int*>(ck->data);
-  p.B = (int)B;
-  p.Hkv = (int)Hkv;
-  p.Tq = (int)Tq;
-  p.Tk = (int)Tk;
-  // the kernel masks with infinities: a scale of 0 becomes the smallest number, which leaves every
-  // weight within 2^-21 of 1 whatever the products are
-  p.scale_log2 = scale * 1.4426950408889634f;
-  if (p.scale_log2 == 0.f) p.scale_log2 = 0x1p-149f;
-  return launch_prefill(p, (int)items * p.parts, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  p.cu_q = static_cast<const int*>(cu->data);
+  p.cu_k = static_cast<const int*>(lens->data);
+  p.Tk = (int)(MB * BS);
+  p.table = static_cast<const int*>(table->data);
+  p.bt_stride = B > 1 ? table->stride[0] : MB;
+  p.table_span = (B - 1) * p.bt_stride + MB;
+  p.num_blocks = (int)NB;
+  while ((1 << p.block_shift) < BS) ++p.block_shift;
+  p.box_shift = std::min(p.block_shift, 7);
+  const int box = 1 << p.box_shift, halves = kv8 || box == 128 ? 0 : 1;
+  DA_TRY(encode_kv_map(&p.tm_k, kp, box, halves));
+  DA_TRY(encode_kv_map(&p.tm_v, vp, box, halves));
+  if (kv8) DA_TRY(encode_scales_map(&p.tm_scales, kv_scales, box));
+  return run_prefill(p, kv8 ? kChunk8 : kChunk16, q, out, B, Hkv, MB * BS, scale, window, sinks, stream);
 }
 
 int decode_attn_cache_write(const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cu_seqlens,

@@ -254,7 +254,7 @@ struct PrefillParams {
   CUtensorMap tm_v;
   __nv_bfloat16* out;  // [Tq][Hq][128]
   long long o_st, o_sh;
-  const int *cu_q, *cu_k;  // [B + 1]
+  const int *cu_q, *cu_k;  // [B + 1]; over pages cu_k is [B], the sequences' lengths, and Tk their capacity
   int* err;
   int B, Hkv, G, Tq, Tk;
   int npos;            // query positions per tile, floor(128 / G)
@@ -264,9 +264,20 @@ struct PrefillParams {
   float* part_o;       // [parts][Tq][Hq][128] unnormalised outputs of the parts
   float* part_ml;      // [parts][Tq][Hq][2] their maxima (log2 units) and sums
   long long part_rows;  // rows of both (0: no item is cut)
+  // A query at position i sees keys i - window + 1 .. i and those below `sinks` (no window: 2^30)
+  int window, sinks;
+  // Pages: tm_k and tm_v map [num_blocks][Hkv][block_size][128], a box of 2^box_shift = min(block size, 128) tokens
+  const int* table;
+  long long bt_stride, table_span;
+  int num_blocks, block_shift, box_shift;
+  CUtensorMap tm_scales;  // e4m3: [num_blocks][Hkv][2][block_size]
 };
 // grid = as many CTAs as there can be work items; those that run take over the others.
 cudaError_t launch_prefill(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream);
+// ... with a window
+cudaError_t launch_prefill_window(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream);
+// ... over a paged cache, bf16 or e4m3
+cudaError_t launch_prefill_paged(const PrefillParams& p, int grid, bool kv8, bool pdl, cudaStream_t stream);
 
 // ------------------------------------------------ paged cache: writing and reading
 struct CacheParams {

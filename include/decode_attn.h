@@ -275,6 +275,45 @@ int decode_attn_prefill(const da_tensor_t* q, const da_tensor_t* k, const da_ten
                         float scale, void* stream);
 
 /*
+ * decode_attn_prefill_window -- decode_attn_prefill in which the query at position i of its sequence
+ * sees keys i - window + 1 .. i and those below `sinks` (the first tokens, which stay visible):
+ *   window  0: no window (sinks is not looked at), else >= 1;  sinks >= 0
+ * Tiles that no row of a work item sees are not read. Everything else as decode_attn_prefill
+ * (position i of a sequence's query r is r + Lk - Lq). Negative numbers return DA_ERR_UNSUPPORTED.
+ */
+int decode_attn_prefill_window(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v,
+                               const da_tensor_t* cu_seqlens_q, const da_tensor_t* cu_seqlens_k, const da_tensor_t* out,
+                               float scale, int32_t window, int32_t sinks, void* stream);
+
+/*
+ * decode_attn_chunk -- attention of new tokens over a paged cache that holds their keys and values
+ * already: the next chunk of prompts, drafted tokens, or one token a sequence, in any mixture. What
+ * decode_attn_cache_read and decode_attn_prefill give together, without the copy.
+ *
+ *   q, out      [Tq, Hq, 128] bf16; 16-byte aligned, strides multiples of 8 elements
+ *   k_pages, v_pages [num_blocks, Hkv, block_size, 128] bf16 or e4m3, any strides obeying the conventions
+ *   kv_scales   [num_blocks, Hkv, 2, block_size] fp32 for e4m3 pools; NULL for bf16
+ *   block_table [B, max_blocks] int32 (device), rows contiguous
+ *   cu_seqlens  [B + 1] int32 (device): rows cu_seqlens[b] .. cu_seqlens[b + 1] of q are the last tokens
+ *   seq_lens    [B] int32 (device) of the seq_lens[b] tokens of sequence b, clamped to
+ *               [0, max_blocks * block_size]
+ *   scale, window, sinks: as decode_attn_prefill_window
+ *
+ * The query at position i sees keys 0 .. i, or with a window i - window + 1 .. i and those below
+ * `sinks`. A query without a key gives a row of zeros; rows of q that belong to no sequence
+ * are left as they were in out. An e4m3 key or value is bf16(code * scale), as decode_attn_cache_read gives it.
+ * Table entries and tokens that no query of the call sees are not read: blocks that a window has
+ * left behind may belong to others by now, and what rows past seq_lens hold does not matter. An entry outside
+ * the pool that is read sets bit 64 of the device error word and its block reads as zeros. A NaN or infinity in a
+ * key or value that some query of a sequence sees can make any output row of that sequence and KV head non-finite.
+ * block_size: a power of two from 8 (e4m3: 16) to 2^20. Other limits and the rounding of the weights as
+ * decode_attn_prefill; with few queries over many keys the keys are cut into parts that meet in the workspace.
+ */
+int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages, const da_tensor_t* kv_scales,
+                      const da_tensor_t* block_table, const da_tensor_t* cu_seqlens, const da_tensor_t* seq_lens,
+                      const da_tensor_t* out, float scale, int32_t window, int32_t sinks, void* stream);
+
+/*
  * decode_attn_cache_write -- the keys and values of new tokens into a paged cache, as
  * decode_attn_*_paged (bf16 pools: copied) or decode_attn_*_paged_fp8 (e4m3 pools: quantised)
  * read them.

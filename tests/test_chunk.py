@@ -1,0 +1,316 @@
+"""decode_attn_chunk and decode_attn_prefill_window against 64 bits: windows and first tokens of every kind, pools of every
+block size and stride, lengths from none to thousands, what no query sees filled with NaN, and rows that are not theirs left
+as they were."""
+import math
+
+import pytest
+import torch
+
+import decode_attention_output_gb300 as da
+from chunk_helpers import attend_ref
+from prompt_helpers import F64, assert_within, quantise_ref
+from test_cache import DEV, _library, bits, cu, i32  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 1 / math.sqrt(128)
+NAN = float("nan")
+
+
+def packed(g, lq, lk, Hq, Hkv, tail=3):
+    cq, ck = cu(lq), cu(lk)
+    q, k, v = (torch.randn((n + tail, h, 128), generator=g).to(torch.bfloat16) for n, h in ((cq[-1], Hq), (ck[-1], Hkv), (ck[-1], Hkv)))
+    return q, k, v, cq, ck
+
+
+def canvas(q):
+    return torch.full(q.shape, 7.5, dtype=torch.bfloat16, device=DEV)
+
+
+def check(out, ref, tol, have, what):
+    out = out.cpu()
+    assert_within(out[have], ref[have], tol[have], what)
+    assert (out[~have] == 7.5).all(), "a row of no sequence was written"
+    assert da.decode_attn_last_device_error() == 0
+
+
+WINDOWS = [  # Hq, Hkv, queries, keys, window, sinks
+    (8, 2, [70, 0, 1, 300], [70, 5, 1, 300], 50, 0), (4, 4, [400], [400], 1, 0), (4, 4, [400], [400], 1, 1), (6, 2, [300], [300], 130, 4),
+    (32, 2, [200, 33], [200, 150], 64, 129), (8, 1, [10], [5000], 777, 4), (8, 1, [10], [5000], 4900, 300), (16, 1, [1, 1, 1], [900, 1, 130], 128, 1),
+    (8, 8, [5], [0], 3, 3), (7, 7, [43, 100], [30, 260], 20, 2), (12, 1, [1000], [1900], 256, 0), (4, 1, [64, 3], [2600, 1700], 2000, 500),
+    (8, 2, [1], [20000], 8192, 4), (8, 2, [600], [600], 100000, 4), (2, 2, [513], [513], 127, 1000), (1, 1, [1], [1], 1, 0), (10, 2, [777], [777], 2 ** 31 - 1, 2 ** 31 - 1),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,lq,lk,window,sinks", WINDOWS, ids=str)
+def test_prefill_window(Hq, Hkv, lq, lk, window, sinks):
+    g = torch.Generator().manual_seed(71)
+    q, k, v, cq, ck = packed(g, lq, lk, Hq, Hkv)
+    k[ck[-1]:], v[ck[-1]:] = NAN, NAN
+    ref, tol, have = attend_ref(q, [k[a:b] for a, b in zip(ck, ck[1:])], [v[a:b] for a, b in zip(ck, ck[1:])], cq, SCALE, window, sinks)
+    out = canvas(q)
+    assert da.decode_attn_prefill_window(q.to(DEV), k.to(DEV), v.to(DEV), i32(cq), i32(ck), out, SCALE, window, sinks) is out
+    check(out, ref, tol, have, "window")
+    # keys outside every query's window are not looked at
+    for b in range(len(lq)):
+        lo, n = max(0, lk[b] - lq[b] - window + 1), min(sinks, lk[b])
+        k[ck[b] + n:ck[b] + lo], v[ck[b] + n:ck[b] + lo] = NAN, NAN
+    again = canvas(q)
+    da.decode_attn_prefill_window(q.to(DEV), k.to(DEV), v.to(DEV), i32(cq), i32(ck), again, SCALE, window, sinks)
+    assert torch.equal(bits(again), bits(out))
+
+
+@pytest.mark.parametrize("lq,lk", [([300, 1, 0, 64], [300, 900, 4, 64]), ([3], [7000])], ids=str)
+def test_no_window_is_the_plain_call(lq, lk):
+    g = torch.Generator().manual_seed(72)
+    q, k, v, cq, ck = packed(g, lq, lk, 8, 2)
+    args = q.to(DEV), k.to(DEV), v.to(DEV), i32(cq), i32(ck)
+    plain, zero, wide = canvas(q), canvas(q), canvas(q)
+    da.decode_attn_prefill(*args, plain, SCALE)
+    da.decode_attn_prefill_window(*args, zero, SCALE, 0, 5)
+    da.decode_attn_prefill_window(*args, wide, SCALE, max(lk), 5)
+    assert torch.equal(bits(zero), bits(plain)) and torch.equal(bits(wide), bits(plain))
+
+
+class Cache:
+    """Pools of shuffled blocks; whatever holds no token of a sequence is NaN, and so are the scales there."""
+
+    def __init__(self, g, lens, Hkv, bs, kv8=False, spare=4, swapped=False, scales="powers"):
+        self.lens, self.bs, B = lens, bs, len(lens)
+        most = max(1, max(-(-n // bs) for n in lens)) + 1
+        nb = B * most + spare
+        self.table = torch.randperm(nb, generator=g)[: B * most].view(B, most)
+        self.kv8 = kv8
+        self.pools, self.scales, self.tokens = [], torch.full((nb, Hkv, 2, bs), NAN) if kv8 else None, []
+        for at in range(2):
+            pool = torch.full((nb, Hkv, bs, 128), NAN, dtype=torch.bfloat16)
+            pool = torch.full(pool.shape, 0x7F, dtype=torch.uint8) if kv8 else pool
+            held = []
+            for b, n in enumerate(lens):
+                x = (torch.randn((n, Hkv, 128), generator=g) * torch.exp(torch.randn((n, Hkv, 1), generator=g) * (0.3 if at == 0 else 1))).to(torch.bfloat16)
+                if kv8:
+                    codes, s = quantise_ref(x)
+                    if scales == "any":
+                        s = s * (torch.rand(s.shape, generator=g) + 0.5) * torch.where(torch.rand(s.shape, generator=g) < 0.1, 0.0, 1.0)
+                        s = torch.where(torch.rand(s.shape, generator=g) < 0.1, -s, s)
+                    held.append((codes.view(torch.float8_e4m3fn).float() * s[..., None]).to(torch.bfloat16))
+                else:
+                    held.append(x)
+                for i in range(-(-n // bs)):
+                    m, blk = min(bs, n - i * bs), int(self.table[b, i])
+                    rows = slice(i * bs, i * bs + m)
+                    pool[blk, :, :m] = (codes if kv8 else x)[rows].transpose(0, 1)
+                    if kv8:
+                        self.scales[blk, :, at, :m] = s[rows].T
+            self.tokens.append(held)
+            self.pools.append(pool.view(torch.float8_e4m3fn) if kv8 else pool)
+        self.swapped = swapped
+
+    def on(self):
+        got = []
+        for p in self.pools:
+            x = p.to(DEV)
+            got.append(x.transpose(1, 2).contiguous().transpose(1, 2) if self.swapped else x)
+        return (*got, None if self.scales is None else self.scales.to(DEV))
+
+    def forget(self, b, first, last):
+        """Tokens first .. last - 1 of sequence b are gone: whole blocks of them leave the table, the others' rows become NaN."""
+        for i in range(self.table.shape[1]):
+            a, z = max(first, i * self.bs), min(last, (i + 1) * self.bs)
+            if z - a == self.bs:
+                self.table[b, i] = [-1, 1 << 30, int(self.table[b, i])][i % 3]
+                blk = int(self.table[b, i])
+                if not 0 <= blk < len(self.pools[0]):
+                    continue
+            if a < z:
+                blk = int(self.table[b, i])
+                for p in self.pools:
+                    if self.kv8:
+                        p.view(torch.uint8)[blk, :, a - i * self.bs:z - i * self.bs] = 0x7F
+                    else:
+                        p[blk, :, a - i * self.bs:z - i * self.bs] = NAN
+                if self.kv8:
+                    self.scales[blk, :, :, a - i * self.bs:z - i * self.bs] = NAN
+
+
+CHUNKS = [  # Hq, Hkv, queries, keys, block size, window, sinks
+    (8, 2, [70, 0, 1, 300], [70, 5, 1, 300], 16, 0, 0), (32, 8, [1], [1], 64, 0, 0), (32, 8, [1], [2049], 64, 0, 0), (4, 4, [1] * 40, list(range(0, 400, 10)), 16, 0, 0),
+    (8, 1, [4, 1, 7, 33], [500, 3000, 7, 5000], 32, 0, 0), (16, 1, [130], [1000], 8, 0, 0), (6, 2, [43, 100, 7], [30, 260, 3], 128, 0, 0),
+    (12, 4, [512], [1700], 256, 0, 0), (7, 1, [18, 19], [700, 19], 512, 0, 0), (8, 8, [5, 0], [0, 0], 64, 0, 0),
+    (8, 2, [1] * 9, [900, 0, 130, 257, 5000, 64, 128, 1, 2000], 64, 128, 4), (32, 2, [200, 33], [200, 1500], 16, 64, 129), (4, 4, [1], [9000], 32, 4096, 1),
+    (8, 1, [64, 3], [2600, 1700], 128, 500, 0), (16, 1, [1, 1], [4000, 70], 256, 1, 1), (8, 2, [300], [5000], 8, 700, 20), (2, 1, [257], [3000], 64, 2 ** 31 - 1, 9),
+    (8, 2, [3], [12000], 16, 3000, 3001), (5, 5, [1] * 3, [4097, 4096, 4095], 1024, 1024, 2),
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "bf16_swapped", "e4m3", "e4m3_any"])
+@pytest.mark.parametrize("Hq,Hkv,lq,lk,bs,window,sinks", CHUNKS, ids=str)
+def test_chunk(Hq, Hkv, lq, lk, bs, window, sinks, kv):
+    kv8 = kv.startswith("e4m3")
+    if kv8 and bs < 16:
+        pytest.skip("e4m3 pools: blocks of 16 and more")
+    g = torch.Generator().manual_seed(73)
+    cache = Cache(g, lk, Hkv, bs, kv8, swapped=kv == "bf16_swapped", scales="any" if kv == "e4m3_any" else "powers")
+    c = cu(lq, first=1)
+    q = torch.randn((c[-1] + 2, Hq, 128), generator=g).to(torch.bfloat16)
+    ref, tol, have = attend_ref(q, *cache.tokens, c, SCALE, window, sinks)
+
+    def call():
+        wide = torch.full((len(lk), cache.table.shape[1] + 3), 1 << 29, dtype=torch.int32)  # rows further apart
+        wide[:, :-3] = cache.table
+        kp, vp, sc = cache.on()
+        out = canvas(q)
+        assert da.decode_attn_chunk(q.to(DEV), kp, vp, sc, wide.to(DEV)[:, :-3], i32(c), i32(lk), out, SCALE, window, sinks) is out
+        return out
+
+    out = call()
+    check(out, ref, tol, have, kv)
+    if window:  # what no query sees any more has been given to others
+        for b in range(len(lq)):
+            cache.forget(b, min(sinks, lk[b]), max(0, lk[b] - lq[b] - window + 1))
+        again = call()
+        check(again, ref, tol, have, "after the window has moved on")
+        assert torch.equal(bits(again), bits(out))
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_chunk_is_read_then_prompt(kv8):
+    """The same bits as the cache read back and decode_attn_prefill over it, where neither cuts the keys into parts."""
+    g = torch.Generator().manual_seed(74)
+    lq, lk = [300, 129, 512, 64], [300, 1000, 1300, 65]
+    cache = Cache(g, lk, 8, 32, kv8)
+    c, ck = cu(lq), cu(lk)
+    q = torch.randn((c[-1], 32, 128), generator=g).to(torch.bfloat16).to(DEV)
+    pools, t = cache.on(), cache.table.to(torch.int32).to(DEV)
+    k, v = (torch.empty((ck[-1], 8, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    da.decode_attn_cache_read(*pools, t, i32(ck), k, v)
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    da.decode_attn_prefill(q, k, v, i32(c), i32(ck), a, SCALE)
+    da.decode_attn_chunk(q, *pools, t, i32(c), i32(lk), b, SCALE)
+    assert torch.equal(bits(a), bits(b))
+    assert da.decode_attn_last_device_error() == 0
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("bs", [16, 256])
+def test_blocks_outside_the_pool(kv8, bs):
+    """They read as zeros and are reported; so are lengths past the table's capacity, which end there."""
+    g = torch.Generator().manual_seed(75)
+    lk = [3 * bs, 2 * bs + 5]
+    cache = Cache(g, lk, 2, bs, kv8)
+    kp, vp, sc = cache.on()
+    q = torch.randn((2, 8, 128), generator=g).to(torch.bfloat16)
+    table = cache.table.clone()
+    table[0, 1], table[1, 0] = -3, len(cache.pools[0])
+    out = canvas(q)
+    da.decode_attn_chunk(q.to(DEV), kp, vp, sc, table.to(torch.int32).to(DEV), i32([0, 1, 2]), i32(lk), out, SCALE)
+    assert da.decode_attn_last_device_error() == 64
+    for held in cache.tokens:
+        held[0][bs:2 * bs] = 0
+        held[1][:bs] = 0
+    ref, tol, _ = attend_ref(q, *cache.tokens, [0, 1, 2], SCALE)
+    assert_within(out.cpu(), ref, tol, "zeros")
+    # a table of two entries each: sequence 0 ends with its second block
+    for held in cache.tokens:
+        held[0], held[1] = held[0][:2 * bs], held[1][:2 * bs]
+    da.decode_attn_chunk(q.to(DEV), kp, vp, sc, table[:, :2].contiguous().to(torch.int32).to(DEV), i32([0, 1, 2]), i32([2 ** 31 - 1, 3 * bs]), out, SCALE)
+    assert da.decode_attn_last_device_error() == 64
+    ref, tol, _ = attend_ref(q, *cache.tokens, [0, 1, 2], SCALE)
+    assert_within(out.cpu(), ref, tol, "capacity")
+
+
+def test_scores_past_24_bits_and_negative_scales():
+    """Scores that fp32 products part by whole powers of two: the largest keys share the row, in a window too."""
+    g = torch.Generator().manual_seed(76)
+    bs, lk, lq, window, sinks = 16, 900, 70, 300, 5
+    for scale in (SCALE, -0.3):
+        for size in (26, 40):
+            cache = Cache(g, [lk], 1, bs)
+            c = torch.randint(1, 256, (lk, 1, 1), generator=g).float()
+            k = (c * 2.0 ** (size - size // 2 - 7)).expand(-1, -1, 128).to(torch.bfloat16)
+            for i in range(-(-lk // bs)):
+                rows = k[i * bs:(i + 1) * bs]
+                cache.pools[0][int(cache.table[0, i]), :, :len(rows)] = rows.transpose(0, 1)
+            q = torch.full((lq, 4, 128), 2.0 ** (size // 2)).to(torch.bfloat16)
+            kp, vp, _ = cache.on()
+            out = canvas(q)
+            da.decode_attn_chunk(q.to(DEV), kp, vp, None, cache.table.to(torch.int32).to(DEV), i32([0, lq]), i32([lk]), out, scale, window, sinks)
+            for r in (0, 1, 35, 69):
+                i = r + lk - lq
+                seen = torch.tensor([j for j in range(i + 1) if j > i - window or j < sinks])
+                cs = c[seen, 0, 0]
+                rows = cache.tokens[1][0][seen, 0].double()[cs == (cs.max() if scale > 0 else cs.min())]
+                d = (out[r, 1].cpu().double() - rows.mean(0)).abs()
+                assert bool((d <= 2.0 ** -8 * (rows.abs().mean(0) + rows.mean(0).abs())).all()), (scale, size, r)
+
+
+def test_pool_past_32_bits():
+    """Blocks whose elements lie past 2^32, of K, V, codes and scales."""
+    g = torch.Generator().manual_seed(77)
+    bs, Hkv = 128, 8
+    nb = (1 << 32) // (Hkv * bs * 128) + 40
+    for kv8 in (False, True):
+        small = Cache(g, [700], Hkv, bs, kv8)
+        n = len(small.pools[0])
+        big = []
+        for p in small.on():
+            if p is not None:
+                x = torch.empty((nb, *p.shape[1:]), dtype=p.dtype, device=DEV)
+                x[nb - n:] = p
+                big.append(x)
+            else:
+                big.append(None)
+        q = torch.randn((40, 16, 128), generator=g).to(torch.bfloat16)
+        out = canvas(q)
+        da.decode_attn_chunk(q.to(DEV), *big, (small.table + nb - n).to(torch.int32).to(DEV), i32([0, 40]), i32([700]), out, SCALE)
+        ref, tol, have = attend_ref(q, *small.tokens, [0, 40], SCALE)
+        check(out, ref, tol, have, "far blocks")
+        del big, x
+
+
+def test_many_sequences():
+    """1000 sequences of one query, and more queries than a table's row of work items."""
+    g = torch.Generator().manual_seed(78)
+    lk = torch.randint(0, 300, (1000,), generator=g).tolist()
+    for kv8 in (False, True):
+        cache = Cache(g, lk, 1, 16, kv8)
+        c = cu([1] * 1000)
+        q = torch.randn((1000, 4, 128), generator=g).to(torch.bfloat16)
+        kp, vp, sc = cache.on()
+        out = canvas(q)
+        da.decode_attn_chunk(q.to(DEV), kp, vp, sc, cache.table.to(torch.int32).to(DEV), i32(c), i32(lk), out, SCALE)
+        ref, tol, have = attend_ref(q, *cache.tokens, c, SCALE)
+        check(out, ref, tol, have, "many")
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_captured_on_a_stream(kv8):
+    """A step captured once and replayed with other queries and lengths on a stream of its own, an eager call between."""
+    g = torch.Generator().manual_seed(79)
+    lk = [1800, 40, 700]
+    cache = Cache(g, lk, 2, 64, kv8)
+    kp, vp, sc = cache.on()
+    t = cache.table.to(torch.int32).to(DEV)
+    q, lens, c = torch.zeros((6, 8, 128), dtype=torch.bfloat16, device=DEV), i32(lk), i32([0, 2, 4, 6])
+    out = torch.zeros_like(q)
+    run = lambda o: da.decode_attn_chunk(q, kp, vp, sc, t, c, lens, o, SCALE, 900, 3)  # noqa: E731
+    run(out)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        run(out)
+    for step in range(3):
+        n = [max(2, x - 7 * step) for x in lk]
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        host = torch.randn(q.shape, generator=g).to(torch.bfloat16)
+        q.copy_(host)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, tol, have = attend_ref(host, [x[:m] for x, m in zip(cache.tokens[0], n)], [x[:m] for x, m in zip(cache.tokens[1], n)], [0, 2, 4, 6], SCALE, 900, 3)
+        assert_within(out.cpu(), ref, tol, f"replay {step}")
+        other = torch.zeros_like(q)
+        run(other)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(other), bits(out))
+    assert da.decode_attn_last_device_error() == 0
