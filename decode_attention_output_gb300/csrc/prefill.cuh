@@ -82,7 +82,9 @@ enum Bar {
   kSIssued,                        // per tile: the MMAs of its S are on their way
   kNext = kSIssued + 2,                           // the next item's index has been answered
   kItemFull, kItemEmpty = kItemFull + kItems,
-  kKvFull = kItemEmpty + kItems, kKvEmpty = kKvFull + kMaxStagesP,
+  // A stage holds a K tile and a V tile in turn, for an issuer each, who tests only its own tiles: with one barrier for both
+  // the test would also pass while the other's tile before it is still on its way.
+  kKFull = kItemEmpty + kItems, kVFull = kKFull + kMaxStagesP, kKvEmpty = kVFull + kMaxStagesP,
   kRawFull = kKvEmpty + kMaxStagesP, kRawEmpty = kRawFull + kMaxRaw,  // e4m3: codes and scales landed / widened
   kBars = kRawEmpty + kMaxRaw
 };
@@ -357,7 +359,7 @@ __device__ __forceinline__ void widen_tiles(const PrefillParams& p, uint8_t* sme
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(kRawEmpty + r));
-          mbar_arrive(bar(kKvFull + s));
+          mbar_arrive(bar((v ? kVFull : kKFull) + s));
         }
       }
     }
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
     if (kWiden) prefetch_tensormap(&p.tm_scales);
     for (int i = 0; i < kBars; ++i) {
       const bool soft = i == kPFull || i == kPFull + 1 || i == kSFree;  // an arrival per warp of a tile
-      const bool widen = kWiden && ((i >= kKvFull && i < kKvEmpty) || i >= kRawEmpty);  // ... or per widening warp
+      const bool widen = kWiden && ((i >= kKFull && i < kKvEmpty) || i >= kRawEmpty);  // ... or per widening warp
       mbar_init(bar(i), soft ? 4 : widen ? kWidenWarps : (i >= kItemEmpty && i < kItemEmpty + kItems ? kSoftWarps + 2 + (kWiden ? kWidenWarps : 0) : 1));
     }
     flags[0] = 0;
@@ -451,6 +453,7 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
         blk = p.num_blocks;
       }
       const int row = (box << p.box_shift) & ((1 << p.block_shift) - 1);
+      if (!in_bounds((unsigned)blk <= (unsigned)p.num_blocks && (unsigned)it.kvh < (unsigned)p.Hkv && t >= 0, p.err)) blk = p.num_blocks;
       if constexpr (kWiden) {
         const uint32_t raw = smem_u32(smem + Sh::kOffRaw);
         int s = kv % Sh::kRaw;
@@ -466,22 +469,24 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
         int s = kv % kStagesP;
         if (!sm_ok(ring + s * kTileP, kTileP)) s = 0;
         mbar_wait_warp(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+        const uint32_t full = bar((kv & 1 ? kVFull : kKFull) + s);
         ++kv;
-        if (lane == 0) mbar_arrive_expect_tx(bar(kKvFull + s), kTileP);
+        if (lane == 0) mbar_arrive_expect_tx(full, kTileP);
         __syncwarp();
         const int half = nb > 1 ? lane & 1 : 0;
         if (mine)
-          tma_load_5d(ring + s * kTileP + half * kHalf + ((uint32_t)i << p.box_shift) * 128, map, bar(kKvFull + s), 0, row, half, it.kvh, blk);
+          tma_load_5d(ring + s * kTileP + half * kHalf + ((uint32_t)i << p.box_shift) * 128, map, full, 0, row, half, it.kvh, blk);
       }
     };
     auto load_kv = [&](const CUtensorMap* map, int row, int kvh) {
       int s = kv % kStagesP;
       if (!sm_ok(ring + s * kTileP, kTileP)) s = 0;
       mbar_wait_warp(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+      const uint32_t full = bar((kv & 1 ? kVFull : kKFull) + s);
       ++kv;
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar(kKvFull + s), kTileP);
-        tma_load_4d(ring + s * kTileP, map, bar(kKvFull + s), 0, row, 0, kvh);
+        mbar_arrive_expect_tx(full, kTileP);
+        tma_load_4d(ring + s * kTileP, map, full, 0, row, 0, kvh);
       }
     };
     const uint32_t next_smem = smem_u32(smem + kOffNext);
@@ -652,12 +657,10 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
       if (none) break;
       for (int j = j0; j < max(end0, end1); ++j) {
         const int stage = ks;
-        wait(kKvFull + stage, kph, kErrWaitFull);
+        wait((pv ? kVFull : kKFull) + stage, kph, kErrWaitFull);
         ks += 2;
-        if (ks >= kStagesP) {
-          ks -= kStagesP;
-          kph ^= 1;
-        }
+        if (ks >= kStagesP) ks -= kStagesP;
+        if (ks == (pv ? 1 : 0)) kph ^= 1;  // every stage has held one of its tiles
         const uint64_t b = kv_desc + (uint64_t)(stage * (kTileP >> 4));
         // A V tile that ends inside another sequence's rows: their weights are 0, but 0 times a
         // NaN or infinity there is not, so those rows are cleared before the MMAs see them. With a window

@@ -268,6 +268,36 @@ def test_pool_past_32_bits():
         del big, x
 
 
+@pytest.mark.parametrize("paged", [None, False, True])
+def test_long_keys_from_far(paged):
+    """More work items of one query tile than SMs, none cut into parts, keys that no cache holds yet: K and V tiles land late
+    and out of step (None: packed keys)."""
+    g = torch.Generator().manual_seed(80)
+    B, H, lq = 24, 8, 2
+    lk = torch.randint(2500, 4500, (B,), generator=g).tolist()
+    c = cu([lq] * B)
+    q = torch.randn((c[-1], H, 128), generator=g).to(torch.bfloat16)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    if paged is None:
+        ck = cu(lk)
+        k, v = (torch.randn((ck[-1], H, 128), generator=g).to(torch.bfloat16) for _ in range(2))
+        tokens = [[x[a:b] for a, b in zip(ck, ck[1:])] for x in (k, v)]
+        args = q.to(DEV), k.to(DEV), v.to(DEV), i32(c), i32(ck)
+        run = lambda out: da.decode_attn_prefill(*args, out, SCALE)  # noqa: E731
+    else:
+        cache = Cache(g, lk, H, 64, paged)
+        tokens = cache.tokens
+        pools = cache.on()
+        args = (q.to(DEV), *pools, cache.table.to(torch.int32).to(DEV), i32(c), i32(lk))
+        run = lambda out: da.decode_attn_chunk(*args, out, SCALE)  # noqa: E731
+    ref, tol, have = attend_ref(q, *tokens, c, SCALE)
+    for i in range(5):
+        out = canvas(q)
+        flush.fill_(i)
+        run(out)
+        check(out, ref, tol, have, f"pass {i}")
+
+
 def test_many_sequences():
     """1000 sequences of one query, and more queries than a table's row of work items."""
     g = torch.Generator().manual_seed(78)
