@@ -99,8 +99,8 @@ struct Shape {
   // two softmax warpgroups and a third: the producer, the issuers of S and of PV, and a spare warp; a fourth widens codes
   static constexpr int kThreads = (kSoftWarps + 4 + (kWiden ? kWidenWarps : 0)) * 32;
   // registers a thread: 168 at launch; the third warpgroup gives 80 of its own to the softmax,
-  // whose threads hold a row of 128 scores (2 * 208 + 88 = 3 * 168; with a fourth 128 at launch, 2 * 208 + 2 * 48 = 4 * 128)
-  static constexpr int kRegsSoft = 208, kRegsRest = kWiden ? 48 : 88;
+  // whose threads hold a row of 128 scores (2 * 208 + 88 = 3 * 168; with a fourth 128 at launch, 2 * 192 + 2 * 64 = 4 * 128)
+  static constexpr int kRegsSoft = kWiden ? 192 : 208, kRegsRest = kWiden ? 64 : 88;
   static constexpr size_t kOffRing = 2 * kTileP;
   static constexpr size_t kOffRaw = kOffRing + (size_t)kStages * kTileP;
   static constexpr size_t kOffBars = kOffRaw + (size_t)kRaw * kRawBytes;
@@ -307,6 +307,20 @@ __device__ __forceinline__ uint2 widen4(uint32_t codes, float scale) {
   return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
 }
 
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint2 a, uint2 b) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y) : "memory");
+}
+
 // The widening warps' part: K and V tiles in turn, from the ring of codes to the ring of bf16 tiles.
 template <int SRC>
 __device__ __forceinline__ void widen_tiles(const PrefillParams& p, uint8_t* smem, const uint8_t* smem_raw, uint64_t* bars,
@@ -315,7 +329,14 @@ __device__ __forceinline__ void widen_tiles(const PrefillParams& p, uint8_t* sme
   constexpr int kStagesP = Sh::kStages, kRaw = Sh::kRaw > 0 ? Sh::kRaw : 1;
   const int lane = threadIdx.x & 31, at = threadIdx.x - (kSoftWarps + 4) * 32;
   auto bar = [&](int i) { return smem_u32(bars + i); };
-  int kv = 0;
+  // This thread's 16 codes of rows row0, row0 + 16, ... (a row's eight pieces lie swizzled in its 128 bytes, by the row's last
+  // three bits, which its rows share), and their 32 bytes of the bf16 tile: pieces 2 c and 2 c + 1 of the row, of which a half's eight
+  // lie swizzled too. Lanes of the second half write theirs the other way round, so that eight lanes reach every bank at a time.
+  const int row0 = at >> 3, c = at & 7, q = (c & 3) * 2, second = c >> 2;
+  const uint32_t from0 = row0 * 128 + ((c ^ (row0 & 7)) << 4), raw = smem_u32(smem + Sh::kOffRaw) + from0;
+  const uint32_t tile = smem_u32(smem + Sh::kOffRing) + second * kHalf + row0 * 128;
+  const uint32_t piece_a = ((q + second) ^ (row0 & 7)) << 4, piece_b = ((q + 1 - second) ^ (row0 & 7)) << 4;
+  int kv = 0, r = 0, rph = 0, s = 0, sph = 0;
   for (int n = 0;; ++n) {
     const int slot = n % kItems;
     wait_bar(bar(kItemFull + slot), (n / kItems) & 1, p.err, kErrWaitFull, flags);
@@ -328,32 +349,29 @@ __device__ __forceinline__ void widen_tiles(const PrefillParams& p, uint8_t* sme
     if (none) break;
     for (int j = j0; j < top && !given_up(flags); ++j) {
       const int base = (j < ns ? j : j + skip) * kN;
+      const bool whole = base + kN <= lk && (base >= lo || base + kN <= p.sinks);  // every row is seen by some row of the item
 #pragma unroll 1
-      for (int v = 0; v < 2; ++v, ++kv) {
-        const int r = kv % kRaw, s = kv % kStagesP;
-        wait_bar(bar(kRawFull + r), (kv / kRaw) & 1, p.err, kErrWaitFull, flags);
-        wait_bar(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
-        const uint8_t* raw = smem + Sh::kOffRaw + r * kRawBytes;
-        const float* scales = reinterpret_cast<const float*>(raw + kRawCodes);
-        uint8_t* tile = smem + Sh::kOffRing + s * kTileP;
-#pragma unroll 4
+      for (int v = 0; v < 2; ++v) {
+        wait_bar(bar(kRawFull + r), rph, p.err, kErrWaitFull, flags);
+        wait_bar(bar(kKvEmpty + s), sph ^ 1, p.err, kErrWaitEmpty, flags);
+        const uint32_t from = raw + r * kRawBytes, to = tile + s * kTileP;
+        // a box's K scales, then its V scales
+        const uint32_t scales = raw - from0 + r * kRawBytes + kRawCodes + ((v << p.box_shift) + row0) * 4;
+        if (!smem_in_bounds(smem_u32(smem_raw), to, 7 * 2048 + 128, p.err)) break;
+        uint4 x = lds_v4(from);
+#pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int row = i * 16 + (at >> 3), c = at & 7, key = base + row;
-          const uint4 x = *reinterpret_cast<const uint4*>(raw + row * 128 + ((c ^ (row & 7)) << 4));
-          // a box's K scales, then its V scales
-          const float scale = scales[((row >> p.box_shift) << (p.box_shift + 1)) + (v << p.box_shift) + (row & ((1 << p.box_shift) - 1))];
-          const bool seen = key < lk && (key >= lo || key < p.sinks);
-          const uint2 y0 = widen4(x.x, scale), y1 = widen4(x.y, scale), y2 = widen4(x.z, scale), y3 = widen4(x.w, scale);
-          uint4 a = make_uint4(y0.x, y0.y, y1.x, y1.y), b = make_uint4(y2.x, y2.y, y3.x, y3.y);
-          if (!seen) a = b = make_uint4(0, 0, 0, 0);
-          // dims 16 c ..: pieces 2 c and 2 c + 1 of the row, of which a half's eight lie swizzled in its 128 bytes. The
-          // lanes of the second half write theirs the other way round, so that eight lanes reach every bank.
-          uint8_t* to = tile + (c >> 2) * kHalf + row * 128;
-          const int q = (c & 3) * 2, sw = row & 7, first = c >> 2;
-          if (smem_in_bounds(smem_u32(smem_raw), smem_u32(to), 128, p.err)) {
-            *reinterpret_cast<uint4*>(to + (((q + first) ^ sw) << 4)) = first ? b : a;
-            *reinterpret_cast<uint4*>(to + (((q + 1 - first) ^ sw) << 4)) = first ? a : b;
+          const int above = i * 16 >> p.box_shift;  // boxes before this row's (a box is 16 rows at least)
+          const float scale = lds_f32(scales + (i * 16 + (above << p.box_shift)) * 4);
+          const uint4 y = second ? make_uint4(x.z, x.w, x.x, x.y) : x;
+          if (i < 7) x = lds_v4(from + (i + 1) * 2048);
+          uint2 a0 = widen4(y.x, scale), a1 = widen4(y.y, scale), b0 = widen4(y.z, scale), b1 = widen4(y.w, scale);
+          if (!whole) {
+            const int key = base + i * 16 + row0;
+            if (!(key < lk && (key >= lo || key < p.sinks))) a0 = a1 = b0 = b1 = make_uint2(0, 0);
           }
+          sts_v4(to + i * 2048 + piece_a, a0, a1);
+          sts_v4(to + i * 2048 + piece_b, b0, b1);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -361,6 +379,9 @@ __device__ __forceinline__ void widen_tiles(const PrefillParams& p, uint8_t* sme
           mbar_arrive(bar(kRawEmpty + r));
           mbar_arrive(bar((v ? kVFull : kKFull) + s));
         }
+        ++kv;
+        if (++r == kRaw) r = 0, rph ^= 1;
+        if (++s == kStagesP) s = 0, sph ^= 1;
       }
     }
   }
