@@ -1129,6 +1129,68 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
   return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
+// decode_attn_chunk after its checks where a sequence has few rows on average: on no tensor memory, 16 rows at a time.
+int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
+            const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, void* stream) {
+  const bool kv8 = kp->dtype == DA_DTYPE_E4M3;
+  const int64_t es = kv8 ? 1 : 2, B = table->shape[0], MB = table->shape[1];
+  FewParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q->data);
+  p.out = static_cast<__nv_bfloat16*>(out->data);
+  p.q_st = q->stride[0];
+  p.q_sh = q->stride[1];
+  p.o_st = out->stride[0];
+  p.o_sh = out->stride[1];
+  p.k_pages = static_cast<const uint8_t*>(kp->data);
+  p.v_pages = static_cast<const uint8_t*>(vp->data);
+  p.kp_sb = kp->stride[0] * es;
+  p.kp_sh = kp->stride[1] * es;
+  p.kp_sr = kp->stride[2] * es;
+  p.vp_sb = vp->stride[0] * es;
+  p.vp_sh = vp->stride[1] * es;
+  p.vp_sr = vp->stride[2] * es;
+  if (kv8) {
+    p.scales = static_cast<const float*>(scales->data);
+    p.sc_sb = scales->stride[0];
+    p.sc_sh = scales->stride[1];
+    p.sc_st = scales->stride[2];
+    p.sc_span = span_of(scales);
+  }
+  p.cu = static_cast<const int*>(cu->data);
+  p.lens = static_cast<const int*>(lens->data);
+  p.table = static_cast<const int*>(table->data);
+  p.bt_stride = B > 1 ? table->stride[0] : MB;
+  p.B = (int)B;
+  p.Hkv = (int)kp->shape[1];
+  p.G = (int)(q->shape[1] / kp->shape[1]);
+  p.Tq = (int)q->shape[0];
+  p.cap = (int)(MB * kp->shape[2]);
+  p.npos = kFewRows / p.G;
+  p.num_blocks = (int)kp->shape[0];
+  while ((1 << p.block_shift) < kp->shape[2]) ++p.block_shift;
+  p.window = window ? std::min(window, 1 << 30) : 1 << 30;
+  p.sinks = window ? std::min(sinks, 1 << 30) : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.q_span = span_of(q);
+  p.out_span = span_of(out);
+  p.kp_span = span_of(kp) * es;
+  p.vp_span = span_of(vp) * es;
+  p.table_span = (B - 1) * p.bt_stride + MB;
+  const int grid = std::max(1, sm_count());
+  p.slots = 2 * grid;
+  p.least = kv8 ? 8 : 16;  // 256 keys
+  const size_t ml_bytes = align_up((size_t)p.slots * kFewRows * 2 * 4, 256);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = nullptr;
+  DA_TRY(workspace_get(ml_bytes + (size_t)p.slots * kFewRows * 128 * 4, st, &ws));
+  p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
+  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
+  p.counters = reinterpret_cast<int*>(ws + kAttnCntOff);
+  p.err = reinterpret_cast<int*>(ws + kErrOff);
+  return launch_chunk_few(p, grid, kv8, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
 // decode_attn_prefill and, with a window, decode_attn_prefill_window.
 int prefill_checked(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cq, const da_tensor_t* ck,
                     const da_tensor_t* out, float scale, int window, int sinks, void* stream) {
@@ -1555,6 +1617,9 @@ int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da
     if (reinterpret_cast<uintptr_t>(table->data) % 4 || reinterpret_cast<uintptr_t>(lens->data) % 4) return DA_ERR_ALIGN;
   }
   if (B == 0 || Tq == 0) return DA_OK;
+  // 16 rows a sequence and KV head on average: above, K and V would be read several times
+  if (Tq * (Hq / Hkv) <= kFewRows * B && Hkv <= 4096)
+    return run_few(q, kp, vp, kv_scales, table, cu, lens, out, scale, window, sinks, stream);
   PrefillParams p;
   memset(&p, 0, sizeof(p));
   p.cu_q = static_cast<const int*>(cu->data);

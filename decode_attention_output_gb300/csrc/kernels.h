@@ -279,6 +279,32 @@ cudaError_t launch_prefill_window(const PrefillParams& p, int grid, bool pdl, cu
 // ... over a paged cache, bf16 or e4m3
 cudaError_t launch_prefill_paged(const PrefillParams& p, int grid, bool kv8, bool pdl, cudaStream_t stream);
 
+// ---------------------------------- attention of a few new tokens over a paged cache
+struct FewParams {
+  const __nv_bfloat16* q;  // [Tq][Hq][128]
+  __nv_bfloat16* out;
+  long long q_st, q_sh, o_st, o_sh;
+  const uint8_t *k_pages, *v_pages;  // [num_blocks][Hkv][block_size][128] bf16 or e4m3; strides and spans in bytes
+  long long kp_sb, kp_sh, kp_sr, vp_sb, vp_sh, vp_sr;
+  const float* scales;               // [num_blocks][Hkv][2][block_size] (e4m3)
+  long long sc_sb, sc_sh, sc_st;
+  const int *cu, *lens, *table;      // [B + 1], [B], [B][max_blocks]
+  long long bt_stride;
+  int* err;
+  int* counters;                     // a CTA each, zero between calls
+  float *part_o, *part_ml;           // [2 * CTAs][16][128], [2 * CTAs][16][2]: states of items that lie in several CTAs
+  int slots;                         // 2 * CTAs
+  int B, Hkv, G, Tq, cap;
+  int npos;                          // query positions of an item, floor(16 / G)
+  int num_blocks, block_shift, window, sinks;
+  float scale_log2;
+  int least;                         // units that a CTA takes at least
+  // elements (pools: bytes) from the first to one past the last (bounds-checked build)
+  long long q_span, out_span, kp_span, vp_span, sc_span, table_span;
+};
+constexpr int kFewRows = 16;
+cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, bool pdl, cudaStream_t stream);
+
 // ------------------------------------------------ paged cache: writing and reading
 struct CacheParams {
   const __nv_bfloat16 *k, *v;  // [T][Hkv][D] packed tokens (read: the destinations)

@@ -268,14 +268,15 @@ def test_pool_past_32_bits():
         del big, x
 
 
+@pytest.mark.parametrize("more", [0, 600])
 @pytest.mark.parametrize("paged", [None, False, True])
-def test_long_keys_from_far(paged):
+def test_long_keys_from_far(paged, more):
     """More work items of one query tile than SMs, none cut into parts, keys that no cache holds yet: K and V tiles land late
-    and out of step (None: packed keys)."""
+    and out of step (None: packed keys; `more`: queries of one sequence besides the two of each)."""
     g = torch.Generator().manual_seed(80)
-    B, H, lq = 24, 8, 2
+    B, H = 24, 8
     lk = torch.randint(2500, 4500, (B,), generator=g).tolist()
-    c = cu([lq] * B)
+    c = cu([2] * (B - 1) + [2 + more])
     q = torch.randn((c[-1], H, 128), generator=g).to(torch.bfloat16)
     flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
     if paged is None:
