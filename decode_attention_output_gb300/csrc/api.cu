@@ -1133,7 +1133,7 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
 int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
             const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, void* stream) {
   const bool kv8 = kp->dtype == DA_DTYPE_E4M3;
-  const int64_t es = kv8 ? 1 : 2, B = table->shape[0], MB = table->shape[1];
+  const int64_t B = table->shape[0], MB = table->shape[1];
   FewParams p;
   memset(&p, 0, sizeof(p));
   p.q = static_cast<const __nv_bfloat16*>(q->data);
@@ -1142,21 +1142,10 @@ int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, 
   p.q_sh = q->stride[1];
   p.o_st = out->stride[0];
   p.o_sh = out->stride[1];
-  p.k_pages = static_cast<const uint8_t*>(kp->data);
-  p.v_pages = static_cast<const uint8_t*>(vp->data);
-  p.kp_sb = kp->stride[0] * es;
-  p.kp_sh = kp->stride[1] * es;
-  p.kp_sr = kp->stride[2] * es;
-  p.vp_sb = vp->stride[0] * es;
-  p.vp_sh = vp->stride[1] * es;
-  p.vp_sr = vp->stride[2] * es;
-  if (kv8) {
-    p.scales = static_cast<const float*>(scales->data);
-    p.sc_sb = scales->stride[0];
-    p.sc_sh = scales->stride[1];
-    p.sc_st = scales->stride[2];
-    p.sc_span = span_of(scales);
-  }
+  const int box = (int)std::min<int64_t>(kp->shape[2], kv8 ? kFewKeys8 : kFewKeys16);
+  DA_TRY(encode_kv_map(&p.tm_k, kp, box));
+  DA_TRY(encode_kv_map(&p.tm_v, vp, box));
+  if (kv8) DA_TRY(encode_scales_map(&p.tm_scales, scales, box));
   p.cu = static_cast<const int*>(cu->data);
   p.lens = static_cast<const int*>(lens->data);
   p.table = static_cast<const int*>(table->data);
@@ -1174,8 +1163,6 @@ int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, 
   p.scale_log2 = scale * 1.4426950408889634f;
   p.q_span = span_of(q);
   p.out_span = span_of(out);
-  p.kp_span = span_of(kp) * es;
-  p.vp_span = span_of(vp) * es;
   p.table_span = (B - 1) * p.bt_stride + MB;
   const int grid = std::max(1, sm_count());
   p.slots = 2 * grid;

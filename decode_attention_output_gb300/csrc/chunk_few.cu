@@ -10,13 +10,17 @@
 //  * Bound by the bytes of K and V. The 128-row tiles of prefill.cuh would be idle but for 16 rows and take 1.3 us
 //    a tile of 128 keys, the time of one softmax, whatever its bytes; here a warp works on a unit of its own
 //    (mma.sync, 16 rows being one tile's height) and the eight of a CTA meet at the item's end only.
-//  * K and V go from memory to the registers that the matrix instructions take them from. Which of a row's dims meet which
-//    lane and step is free as long as Q's follow: lane t of the four that hold a key takes its 16-byte pieces t, t + 4,
-//    ..., and for V, where an instruction wants two keys' values of one dim in a register, a lane takes one piece of two keys
-//    and exchanges halves of its own registers. A unit's 16 loads are issued as soon as the last one's
-//    registers have been used: 8 KB a warp, 64 KB an SM on their way.
-//  * Softmax as in prefill.cuh: the running maximum lags by up to 2^8, the weights enter P V as bf16, sums are fp32. e4m3:
-//    code * scale, rounded once to bf16 (exact for power-of-two scales).
+//  * A warp copies its units of K and V by TMA (4 KB each, a copy each where a block holds a unit), two units ahead and on
+//    into the next item's: 16 KB a warp, 128 KB an SM on their way. Which of a row's dims meet which lane and step of the
+//    matrix instructions is free as long as Q's follow: of a key, lane t of four takes the 16-byte pieces t, t + 4, ...; for V,
+//    where an instruction wants two keys' values of one dim in a register, a lane takes one piece of two keys and exchanges halves
+//    of its own registers. The copies' 128-byte swizzle lets eight lanes reach all banks in both.
+//  * bf16: softmax as in prefill.cuh: the running maximum lags by up to 2^8, the weights enter P V as bf16, sums are fp32.
+//  * e4m3: codes are widened to f16 (exact, half an instruction each; to bf16 with their scale 2.5, which set the pace: 270 us
+//    for the 32 sequences). K's scale multiplies the score; q's rows become f16 over a power of two that puts the
+//    largest under 2^15 (exact down to 2^-32 of it). V's scale joins the weight, w v f as f16: f, a power of two a row, keeps the
+//    largest w v (of rows of V that are not all zero: those have a scale of 1 whatever the others have) between 1 and 2^8,
+//    so that smaller ones are off by 2^-25 of it at most.
 #include "kernels.h"
 #include "packed.cuh"
 #include "ptx.cuh"
@@ -30,11 +34,19 @@ constexpr int kMostParts = 48;   // of an item
 constexpr float kSlackF = 8.f;   // log2 units the maximum may lag
 constexpr float kNegInfF = -__builtin_huge_valf();
 
-// Shared memory: the sequences' units (prefix sums), then the warps' states.
-constexpr size_t kOffState = ((kMaxBatch + 1) * 8 + 15) & ~(size_t)15;
-constexpr size_t kOffMl = kOffState + (size_t)kWarpsF * 16 * kRowF * 4;
-constexpr size_t kOffLast = kOffMl + kWarpsF * 16 * 2 * 4;
-constexpr size_t kSmemF = kOffLast + 16;
+// Shared memory: two units of each warp (K, V, scales of 32 keys), their barriers, the warps' states, the sequences' units
+// (prefix sums)
+constexpr int kStagesF = 2;
+constexpr uint32_t kHalfUnit = 4096;                // K or V of a unit
+constexpr uint32_t kScalesF = 256, kUnitBytes = 2 * kHalfUnit;
+constexpr size_t kOffScales = (size_t)kWarpsF * kStagesF * kUnitBytes;
+constexpr size_t kOffBarsF = kOffScales + (size_t)kWarpsF * kStagesF * kScalesF;
+constexpr size_t kOffMl = kOffBarsF + kWarpsF * kStagesF * 8;
+constexpr size_t kOffState = (kOffMl + kWarpsF * 16 * 2 * 4 + 15) & ~(size_t)15;
+constexpr size_t kOffLast = kOffState + (size_t)kWarpsF * 16 * kRowF * 4;
+constexpr size_t kOffPrefix = kOffLast + 16;
+constexpr size_t kSmemF = 1024 + kOffPrefix + (kMaxBatch + 1) * 8;
+static_assert(kSmemF <= kMaxDynSmem, "the kernel exceeds 227 KB of shared memory");
 
 // Units that a sequence's queries see: those of the first keys, and from the window's beginning on.
 struct Units {
@@ -51,26 +63,42 @@ __device__ __forceinline__ Units units_of(int lo, int lk, int sinks) {
   return u;
 }
 
-__device__ __forceinline__ uint4 ldg_piece(const uint8_t* p, bool ok) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (ok) v = ldg_stream_v4(p);
+__device__ __forceinline__ uint4 lds_piece(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-// (x.x a.x, x.y a.y) as bf16, of an f16 pair
-__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float2 a) {
-  return pack_bf16x2(f16lo_to_f32(f16x2) * a.x, f16hi_to_f32(f16x2) * a.y);
+__device__ __forceinline__ float2 lds_pair(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
 }
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// 2^e, e clamped to what a float holds
+__device__ __forceinline__ float power_of_2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+// floor(log2 x) of a positive float (subnormal ones: -127)
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 0xffu) - 127; }
 
 template <bool KV8>
 __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_constant__ FewParams p) {
-  constexpr int kKeys = KV8 ? 32 : 16, kNT = kKeys / 8;  // keys of a unit, in tiles of 8
-  extern __shared__ __align__(16) uint8_t smem[];
-  long long* prefix = reinterpret_cast<long long*>(smem);
+  constexpr int kKeys = KV8 ? kFewKeys8 : kFewKeys16, kNT = kKeys / 8;  // keys of a unit, in tiles of 8
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  long long* prefix = reinterpret_cast<long long*>(smem + kOffPrefix);
   float* state = reinterpret_cast<float*>(smem + kOffState);
   float* ml = reinterpret_cast<float*>(smem + kOffMl);
   int* last = reinterpret_cast<int*>(smem + kOffLast);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int G = p.G, npos = p.npos;
+  if (lane == 0) {
+    for (int i = 0; i < kStagesF; ++i) mbar_init(smem_u32(smem + kOffBarsF) + (warp * kStagesF + i) * 8, 1);
+    fence_barrier_init();
+    if (warp == 0) {
+      prefetch_tensormap(&p.tm_k);
+      prefetch_tensormap(&p.tm_v);
+      if (KV8) prefetch_tensormap(&p.tm_scales);
+    }
+  }
   pdl_wait_primary();
 
   // A sequence: its rows of q, its tokens, the first key of its first query's window.
@@ -117,33 +145,134 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
   auto owner = [&](long long f) { return (int)(((f + 1) * ctas - 1) / total); };
   const long long f1 = begin_of(blockIdx.x + 1);
 
-  for (long long f = begin_of(blockIdx.x); f < f1;) {
-    // ------------------------------------------------------------ the segment
-    int b = 0;
+  // ---------------------------------------------------------------- a segment: an item's units in this CTA
+  struct Segment {
+    int b, q0, lk, kvh, u0, u1, pos0, most, shift, end, low;
+    long long item0;  // the item's first unit
+    Units un;
+  };
+  auto segment = [&](long long f) {
+    Segment s;
+    s.b = 0;
     for (int step = 512; step > 0; step >>= 1)  // the last b with prefix[b] <= f: B <= 1024
-      if (b + step < p.B && prefix[b + step] <= f) b += step;
-    const Seq sq = sequence(b);
-    const Units un = units_of<kKeys>(sq.lo, sq.lk, p.sinks);
-    const long long within = f - prefix[b], item = within / un.n;
-    const int rg = (int)(item / p.Hkv), kvh = (int)(item - (long long)rg * p.Hkv);
-    const int u0 = (int)(within - item * un.n), u1 = (int)min((long long)un.n, u0 + (f1 - f));
-    const long long item0 = f - u0;  // the item's first unit
-    const int pos0 = rg * npos, most = min(npos, sq.lq - pos0);  // its first query and how many
-    const int shift = sq.lk - sq.lq;                             // position of the sequence's first query
-    const int end = min(sq.lk, pos0 + most + shift);             // keys that its last query sees
-    const int low = max(0, pos0 + shift - p.window + 1);         // the first of its first query's window
-    f += u1 - u0;
+      if (s.b + step < p.B && prefix[s.b + step] <= f) s.b += step;
+    const Seq sq = sequence(s.b);
+    s.un = units_of<kKeys>(sq.lo, sq.lk, p.sinks);
+    const long long within = f - prefix[s.b], item = within / s.un.n;
+    const int rg = (int)(item / p.Hkv);
+    s.kvh = (int)(item - (long long)rg * p.Hkv);
+    s.u0 = (int)(within - item * s.un.n);
+    s.u1 = (int)min((long long)s.un.n, s.u0 + (f1 - f));
+    s.item0 = f - s.u0;
+    s.q0 = sq.q0;
+    s.lk = sq.lk;
+    s.pos0 = rg * npos;  // its first query, and how many
+    s.most = min(npos, sq.lq - s.pos0);
+    s.shift = sq.lk - sq.lq;  // position of the sequence's first query
+    s.end = min(sq.lk, s.pos0 + s.most + s.shift);       // keys that its last query sees
+    s.low = max(0, s.pos0 + s.shift - p.window + 1);  // the first of its first query's window
+    return s;
+  };
+  const uint32_t units = smem_u32(smem) + warp * kStagesF * kUnitBytes;
+  const uint32_t scales = smem_u32(smem + kOffScales) + warp * kStagesF * kScalesF;
+  const uint32_t bars = smem_u32(smem + kOffBarsF) + warp * kStagesF * 8;
+  auto sm_ok = [&](uint32_t addr, uint32_t bytes) { return smem_in_bounds(smem_u32(smem_raw), addr, bytes, p.err); };
 
-    // Q, in the order of dims that K's pieces give: step s holds dims 4 e of piece (16 bytes of a key) ...
+  // The loads, which run ahead of the products and on into the next segments: the segment, this warp's next unit of it, and the
+  // blocks of both halves of 32 units from ids_at on, a unit a lane.
+  struct {
+    long long next;  // the first unit behind the segment
+    Units un;
+    int b, kvh, u, u1, end, low;
+  } ld;
+  int ids[2] = {-1, -1}, ids_at = 0, loaded = 0;
+  auto begin_loads = [&](long long f) {
+    const Segment s = segment(f);
+    ld.next = f + s.u1 - s.u0;
+    ld.un = s.un;
+    ld.b = s.b;
+    ld.kvh = s.kvh;
+    ld.u = s.u0 + warp;
+    ld.u1 = s.u1;
+    ld.end = s.end;
+    ld.low = s.low;
+    ids_at = -32 * kWarpsF;
+  };
+  auto load_unit = [&] {
+    while (ld.u >= ld.u1 && ld.next < f1) begin_loads(ld.next);
+    if (ld.u >= ld.u1) return;  // nothing is left
+    if (ids_at < 0 || (ld.u - ids_at) / kWarpsF == 32) {
+      ids_at = ld.u;
+      const int u = ids_at + lane * kWarpsF, key = ld.un.at(u) * kKeys;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k0 = key + i * (kKeys / 2), k1 = k0 + kKeys / 2 - 1;
+        const bool need = u < ld.u1 && k0 < ld.end && (k0 < p.sinks || k1 >= ld.low);  // some key of the half is seen
+        const long long at = ld.b * p.bt_stride + (k0 >> p.block_shift);
+        ids[i] = need && in_bounds(at < p.table_span, p.err) ? __ldg(p.table + at) : -1;
+        if (need && (unsigned)ids[i] >= (unsigned)p.num_blocks) atomicOr(p.err, kErrBlockTable);
+        // halves that no row of the item sees, and blocks that are none of the pool's, are past its end: zeros
+        if ((unsigned)ids[i] >= (unsigned)p.num_blocks) ids[i] = p.num_blocks;
+      }
+    }
+    const int src = (ld.u - ids_at) / kWarpsF, key0 = ld.un.at(ld.u) * kKeys, row = key0 & ((1 << p.block_shift) - 1);
+    const int id0 = __shfl_sync(0xffffffffu, ids[0], src), id1 = __shfl_sync(0xffffffffu, ids[1], src);
+    // A copy of the unit, or one of each half where a block holds no more. (Where one half only is seen, the copy of both
+    // brings the block's other rows too; they are masked.)
+    const bool split = (1 << p.block_shift) < kKeys;
+    const int st = loaded & 1;
+    const uint32_t to = units + st * kUnitBytes, bar = bars + st * 8, sc = scales + st * kScalesF;
+    __syncwarp();  // the stage has been read
+    if (lane == 0 && sm_ok(to, kUnitBytes) && sm_ok(sc, kScalesF) && in_bounds(ld.kvh < p.Hkv, p.err)) {
+      mbar_arrive_expect_tx(bar, kUnitBytes + (KV8 ? kScalesF : 0));
+      const int first = split ? id0 : min(id0, id1);
+      tma_load_5d(to, &p.tm_k, bar, 0, row, 0, ld.kvh, first);
+      tma_load_5d(to + kHalfUnit, &p.tm_v, bar, 0, row, 0, ld.kvh, first);
+      if (KV8) tma_load_4d(sc, &p.tm_scales, bar, row, 0, ld.kvh, first);
+      if (split) {
+        const int row1 = (key0 + kKeys / 2) & ((1 << p.block_shift) - 1);
+        tma_load_5d(to + kHalfUnit / 2, &p.tm_k, bar, 0, row1, 0, ld.kvh, id1);
+        tma_load_5d(to + kHalfUnit + kHalfUnit / 2, &p.tm_v, bar, 0, row1, 0, ld.kvh, id1);
+        if (KV8) tma_load_4d(sc + kScalesF / 2, &p.tm_scales, bar, row1, 0, ld.kvh, id1);
+      }
+    }
+    __syncwarp();
+    ++loaded;
+    ld.u += kWarpsF;
+  };
+
+  long long f = begin_of(blockIdx.x);
+  if (f >= f1) return;
+  // Addresses in a stage. K: key g of every eight, pieces t and t + 4 of 128 bytes, in the order that gives two keys' lanes
+  // different banks. V: keys 2 t and 2 t + 1, piece g. Scales: a copy's K scales, then its V scales.
+  const bool split = (1 << p.block_shift) < kKeys, odd = g & 1;
+  const uint32_t eight = !KV8 && split ? 2048 : 1024;   // from eight keys to the next
+  const uint32_t second = split ? 1024 : 2048;          // bf16: from a row's first 64 dims to the others
+  const uint32_t k_at = g * 128 + (((t + 4 * (g & 1)) ^ g) << 4);
+  const uint32_t v_at = 2 * t * 128 + ((g ^ (2 * t)) << 4), v_at1 = (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4);
+  // (byte of the K scales of keys 2 t, 2 t + 1 of the nt-th eight; V's lie `scale_v` behind)
+  const uint32_t scale_v = split ? 64 : 128;
+  auto scale_at = [&](int nt) { return (uint32_t)(split ? (nt >> 1) * 128 + (nt & 1) * 32 : nt * 32) + t * 8; };
+
+  begin_loads(f);
+  load_unit();
+  load_unit();
+  int used = 0;       // units taken
+  bool alive = true;  // no wait has run out
+  while (true) {
+    const Segment sg = segment(f);
+    // Q, in the order of dims that K's pieces give; rows g and g + 8: the keys that they see, before lim and from `from` on
+    // (or before sinks), and the factor that turns products into log2 units
     uint32_t aq[8][4];
-    int lim[2], from[2];  // of rows g and g + 8: keys seen before lim, and from `from` on (or before sinks)
+    int lim[2], from[2];
+    float factor[2] = {p.scale_log2, p.scale_log2};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i, pos = pos0 + r / G;
-      const bool ok = r < most * G;
-      lim[i] = ok ? min(sq.lk, pos + shift + 1) : 0;
-      from[i] = pos + shift - p.window + 1;
-      const __nv_bfloat16* row = p.q + (long long)(sq.q0 + pos) * p.q_st + (long long)(kvh * G + r % G) * p.q_sh;
+      const int r = g + 8 * i, pos = sg.pos0 + r / G;
+      const bool ok = r < sg.most * G;
+      lim[i] = ok ? min(sg.lk, pos + sg.shift + 1) : 0;
+      from[i] = pos + sg.shift - p.window + 1;
+      const __nv_bfloat16* row = p.q + (long long)(sg.q0 + pos) * p.q_st + (long long)(sg.kvh * G + r % G) * p.q_sh;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         const int dim = KV8 ? (t + 4 * (s >> 2)) * 16 + (s & 3) * 4 : (t + 4 * (s >> 1)) * 8 + (s & 1) * 4;
@@ -153,194 +282,209 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
         aq[s][2 + i] = v.y;
       }
     }
-
-    // The blocks of both halves of this warp's next 32 units, a unit a lane.
-    int ids[2], ids_at = u0 + warp;
-    auto seen = [&](int key) { return key < end && (key >= low || key < p.sinks); };
-    auto load_ids = [&] {
-      const int key = un.at(ids_at + lane * kWarpsF) * kKeys;
+    if constexpr (KV8) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int k0 = key + i * (kKeys / 2), k1 = k0 + kKeys / 2 - 1;
-        // some key of the half is seen: its first or last, or the sinks or the end fall inside
-        const bool need = ids_at + lane * kWarpsF < u1 && k0 < end && (k0 < p.sinks || k1 >= low);
-        const long long at = b * p.bt_stride + (k0 >> p.block_shift);
-        ids[i] = need && in_bounds(at < p.table_span, p.err) ? __ldg(p.table + at) : -1;
-        if (need && (unsigned)ids[i] >= (unsigned)p.num_blocks) {
-          atomicOr(p.err, kErrBlockTable);
-          ids[i] = -1;
-        }
+        unsigned top = 0;  // the row's largest magnitude, a bf16 pattern
+#pragma unroll
+        for (int s = 0; s < 8; ++s) top = __vmaxu2(top, __vmaxu2(aq[s][i] & 0x7fff7fffu, aq[s][2 + i] & 0x7fff7fffu));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = max(top & 0xffffu, top >> 16);
+        // (a row of zeros, or one with an infinity or NaN: as it is; twice half the power: 2^-112 and less are no floats)
+        const int e = top == 0 || top >= 0x7f80u ? 0 : 14 - ((int)(top >> 7) - 127), e0 = e / 2, e1 = e - e0;
+        const float a = power_of_2(e0), c = power_of_2(e1);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+          for (int k = 0; k < 4; k += 2)
+            aq[s][k + i] = pack_f16x2(bf16lo_to_f32(aq[s][k + i]) * a * c, bf16hi_to_f32(aq[s][k + i]) * a * c);
+        factor[i] = fminf(fmaxf(p.scale_log2 * power_of_2(-e0) * power_of_2(-e1), -3.4e38f), 3.4e38f);
       }
-    };
-    // The rows' addresses in unit u: pool + block * sb + head * sh + row * sr, as bytes
-    uint4 kx[8], vx[8];
-    float ks[KV8 ? kNT : 1];
-    float2 vs[KV8 ? kNT : 1];
-    auto load_k = [&](int u) {
-      const int key0 = un.at(u) * kKeys, src = (u - ids_at) / kWarpsF;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int id = __shfl_sync(0xffffffffu, ids[i], src);
-        const uint8_t* pool = p.k_pages + id * p.kp_sb + kvh * p.kp_sh;
-#pragma unroll
-        for (int n = 0; n < kNT / 2; ++n) {
-          const int nt = i * (kNT / 2) + n, key = key0 + nt * 8 + g;
-          const int row = key & ((1 << p.block_shift) - 1);
-          const uint8_t* at = pool + row * p.kp_sr + t * 16;
-          const bool ok = id >= 0 && u < u1 && seen(key) && in_bounds(at + (KV8 ? 80 : 208) - p.k_pages <= p.kp_span, p.err);
-#pragma unroll
-          for (int j = 0; j < 8 / kNT; ++j) kx[nt * (8 / kNT) + j] = ldg_piece(at + j * 64, ok);
-          if constexpr (KV8) {
-            const float* sc = p.scales + id * p.sc_sb + kvh * p.sc_sh + row;
-            ks[nt] = ok && in_bounds(sc - p.scales < p.sc_span, p.err) ? __ldg(sc) : 0.f;
-          }
-        }
-      }
-    };
-    auto load_v = [&](int u) {
-      const int key0 = un.at(u) * kKeys, src = (u - ids_at) / kWarpsF;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int id = __shfl_sync(0xffffffffu, ids[i], src);
-        const uint8_t* pool = p.v_pages + id * p.vp_sb + kvh * p.vp_sh;
-#pragma unroll
-        for (int n = 0; n < kNT / 2; ++n) {
-          const int nt = i * (kNT / 2) + n, key = key0 + nt * 8 + 2 * t;
-          const int row = key & ((1 << p.block_shift) - 1);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {  // two keys of every eight
-            const uint8_t* at = pool + (row + k) * p.vp_sr + g * 16;
-            const bool ok = id >= 0 && u < u1 && seen(key + k) && in_bounds(at + (KV8 ? 16 : 144) - p.v_pages <= p.vp_span, p.err);
-#pragma unroll
-            for (int j = 0; j < 4 / kNT; ++j) vx[(nt * 2 + k) * (4 / kNT) + j] = ldg_piece(at + j * 128, ok);
-          }
-          if constexpr (KV8) {
-            const float* sc = p.scales + id * p.sc_sb + kvh * p.sc_sh + p.sc_st + row;
-            const bool any = id >= 0 && u < u1 && in_bounds(sc + 1 - p.scales < p.sc_span, p.err);
-            const float2 s2 = any && (seen(key) || seen(key + 1)) ? __ldg(reinterpret_cast<const float2*>(sc)) : make_float2(0.f, 0.f);
-            vs[nt] = make_float2(seen(key) ? s2.x : 0.f, seen(key + 1) ? s2.y : 0.f);
-          }
-        }
-      }
-    };
-
+    }
     float o[16][4];
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     float m[2] = {kNegInfF, kNegInfF}, l[2] = {0.f, 0.f};
-    // ------------------------------------------------------------ units
-    load_ids();
-    load_k(u0 + warp);
-    load_v(u0 + warp);
-    for (int u = u0 + warp; u < u1; u += kWarpsF) {
-      const bool refill = (u + kWarpsF - ids_at) / kWarpsF == 32;
+    float fv[2] = {1.f, 1.f}, largest[2] = {0.f, 0.f};  // e4m3: V's factor, and the largest weight times V scale so far
+    const int all_before = min(sg.lk, sg.pos0 + sg.shift + 1), all_from = sg.pos0 + sg.most - 1 + sg.shift - p.window + 1;
+    for (int u = sg.u0 + warp; u < sg.u1 && alive; u += kWarpsF) {
+      const int st = used & 1;
+      alive = mbar_wait_bounded(bars + st * 8, used >> 1 & 1, p.err, kErrWaitFull, nullptr);
+      alive = __all_sync(0xffffffffu, alive);
+      ++used;
+      const uint32_t kv = units + st * kUnitBytes, sc = scales + st * kScalesF;
       float x[kNT][4];
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
+        for (int h = 0; h < (KV8 ? 1 : 2); ++h) {
+          const uint32_t at = kv + nt * eight + h * second + k_at;
+          const uint4 a = lds_piece(at), c = lds_piece(at ^ 64);
+          const uint4 k0 = odd ? c : a, k1 = odd ? a : c;  // pieces t and t + 4
           if constexpr (KV8) {
-            const uint4 k = kx[nt * 2 + (s >> 2)];
-            const uint32_t codes = (s & 3) == 0 ? k.x : (s & 3) == 1 ? k.y : (s & 3) == 2 ? k.z : k.w;
-            uint32_t lo, hi;
-            e4m3x4_to_f16x4(codes, lo, hi);
-            const float2 sc = make_float2(ks[nt], ks[nt]);
-            mma_bf16_16816(x[nt], aq[s], scaled_bf16x2(lo, sc), scaled_bf16x2(hi, sc));
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+              uint32_t lo, hi;
+              e4m3x4_to_f16x4(word_of(s < 4 ? k0 : k1, s & 3), lo, hi);
+              mma_f16_16816(x[nt], aq[s], lo, hi);
+            }
           } else {
-            const uint4 k = kx[nt * 4 + (s >> 1)];
-            mma_bf16_16816(x[nt], aq[s], s & 1 ? k.z : k.x, s & 1 ? k.w : k.y);
+            mma_bf16_16816(x[nt], aq[h * 4], k0.x, k0.y);
+            mma_bf16_16816(x[nt], aq[h * 4 + 1], k0.z, k0.w);
+            mma_bf16_16816(x[nt], aq[h * 4 + 2], k1.x, k1.y);
+            mma_bf16_16816(x[nt], aq[h * 4 + 3], k1.z, k1.w);
           }
         }
       }
-      const int key0 = un.at(u) * kKeys;
-      if (refill) {  // (V's loads of the next unit want its blocks too, this one's are under way)
-        ids_at = u + kWarpsF;
-        load_ids();
-      }
-      load_k(u + kWarpsF);
-      // Every key of the unit seen by every row?
-      const bool whole = key0 + kKeys <= min(sq.lk, pos0 + shift + 1) && (key0 >= pos0 + most - 1 + shift - p.window + 1 || key0 + kKeys <= p.sinks);
+      const int key0 = sg.un.at(u) * kKeys;
+      auto seen = [&](int key) { return key < sg.end && (key >= sg.low || key < p.sinks); };  // by some row of the item
+      const bool whole = key0 + kKeys <= all_before && (key0 >= all_from || key0 + kKeys <= p.sinks);  // every key seen by every row
       float top[2] = {kNegInfF, kNegInfF};
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int nt = 0; nt < kNT; ++nt) {
+        const float2 ks = KV8 ? lds_pair(sc + scale_at(nt)) : make_float2(1.f, 1.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[nt][i] *= p.scale_log2;
+          x[nt][i] *= factor[i >> 1];
+          if (KV8) x[nt][i] *= i & 1 ? ks.y : ks.x;
           const int key = key0 + nt * 8 + 2 * t + (i & 1);
           if (!whole && !(key < lim[i >> 1] && (key >= from[i >> 1] || key < p.sinks))) x[nt][i] = kNegInfF;
           top[i >> 1] = fmaxf(top[i >> 1], x[nt][i]);
         }
-      if (__any_sync(0xffffffffu, top[0] > m[0] + kSlackF || top[1] > m[1] + kSlackF)) {
+      }
+      const bool grow = __any_sync(0xffffffffu, top[0] > m[0] + kSlackF || top[1] > m[1] + kSlackF);
+      float a[2] = {1.f, 1.f};  // what the sums and O so far are worth against the new maximum
+      if (grow) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float r = top[i];
           r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 1));
           r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 2));
-          const float mn = fmaxf(m[i], r), a = m[i] == kNegInfF ? 0.f : fast_exp2(m[i] - mn);
+          const float mn = fmaxf(m[i], r);
+          a[i] = m[i] == kNegInfF ? 0.f : fast_exp2(m[i] - mn);
           m[i] = mn;
-          l[i] *= a;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            o[j][2 * i] *= a;
-            o[j][2 * i + 1] *= a;
-          }
+          l[i] *= a[i];
+          largest[i] *= a[i];
         }
       }
-      uint32_t w[kNT][2];  // weights of rows g and g + 8
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float ref = m[i] == kNegInfF ? 0.f : m[i];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          const float a = fast_exp2(x[nt][2 * i] - ref), c = fast_exp2(x[nt][2 * i + 1] - ref);
-          l[i] += a + c;
-          w[nt][i] = pack_bf16x2(a, c);
+          x[nt][2 * i] = fast_exp2(x[nt][2 * i] - ref);
+          x[nt][2 * i + 1] = fast_exp2(x[nt][2 * i + 1] - ref);
+          l[i] += x[nt][2 * i] + x[nt][2 * i + 1];
         }
+      }
+      if constexpr (KV8) {
+        float2 vs[kNT];
+        float big[2] = {0.f, 0.f};  // the largest weight times V scale of this lane's
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          vs[nt] = lds_pair(sc + scale_at(nt) + scale_v);
+          if (!whole) {  // (0 times a scale that belongs to no key is not 0)
+            if (!seen(key0 + nt * 8 + 2 * t)) vs[nt].x = 0.f;
+            if (!seen(key0 + nt * 8 + 2 * t + 1)) vs[nt].y = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) big[i] = fmaxf(big[i], fmaxf(fabsf(x[nt][2 * i] * vs[nt].x), fabsf(x[nt][2 * i + 1] * vs[nt].y)));
+        }
+        const bool first = (largest[0] == 0.f && big[0] > 0.f) || (largest[1] == 0.f && big[1] > 0.f);
+        if (__any_sync(0xffffffffu, grow || first || big[0] * fv[0] > 256.f || big[1] * fv[1] > 256.f)) {
+          unsigned some = 0;  // of this lane's keys: does V's row hold a code that is not 0?
+#pragma unroll
+          for (int k = 0; k < 2 * kNT; ++k) {
+            const uint4 v = lds_piece(kv + kHalfUnit + (k >> 1) * eight + (k & 1 ? v_at1 : v_at));
+            some |= ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) ? 1u << k : 0u;
+          }
+          some |= __shfl_xor_sync(0xffffffffu, some, 4);
+          some |= __shfl_xor_sync(0xffffffffu, some, 8);
+          some |= __shfl_xor_sync(0xffffffffu, some, 16);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            if (!(some >> (2 * nt) & 1u)) vs[nt].x = 0.f;
+            if (!(some >> (2 * nt + 1) & 1u)) vs[nt].y = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float r = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) r = fmaxf(r, fmaxf(fabsf(x[nt][2 * i] * vs[nt].x), fabsf(x[nt][2 * i + 1] * vs[nt].y)));
+            r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 1));
+            r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 2));
+            largest[i] = fmaxf(largest[i], r);
+            float to = fv[i];  // the largest times it stays between 1 and 2^8
+            if (largest[i] > 0.f && !(largest[i] * to >= 1.f && largest[i] * to <= 256.f)) to = power_of_2(-exponent_of(largest[i]));
+            a[i] *= fminf(to / fv[i], 0x1p127f);
+            fv[i] = to;
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          x[nt][0] *= vs[nt].x * fv[0];
+          x[nt][1] *= vs[nt].y * fv[0];
+          x[nt][2] *= vs[nt].x * fv[1];
+          x[nt][3] *= vs[nt].y * fv[1];
+        }
+      }
+      // V: key 2 t + k of the nt-th eight, piece g. What no row sees may hold anything: zeros.
+      auto load_v = [&](int nt, int k, uint32_t off) {
+        uint4 v = lds_piece(kv + kHalfUnit + nt * eight + off + (k ? v_at1 : v_at));
+        if (!whole && !seen(key0 + nt * 8 + 2 * t + k)) v = make_uint4(0, 0, 0, 0);
+        return v;
+      };
+      if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][i] *= a[i >> 1];
       }
 #pragma unroll
       for (int kk = 0; kk < kNT / 2; ++kk) {
-        const uint32_t a[4] = {w[2 * kk][0], w[2 * kk][1], w[2 * kk + 1][0], w[2 * kk + 1][1]};
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = KV8 ? pack_f16x2(x[2 * kk + (i >> 1)][2 * (i & 1)], x[2 * kk + (i >> 1)][2 * (i & 1) + 1])
+                     : pack_bf16x2(x[2 * kk + (i >> 1)][2 * (i & 1)], x[2 * kk + (i >> 1)][2 * (i & 1) + 1]);
         if constexpr (KV8) {
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = load_v(2 * kk + (i >> 1), i & 1, 0);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {  // dims 16 g + 4 q ..
-            uint32_t bb[2][4];
+            uint32_t bb[2][4];           // (first key, second key) of a dim
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint4 r0 = vx[(2 * kk + h) * 2], r1 = vx[(2 * kk + h) * 2 + 1];
-              const uint32_t c0 = q == 0 ? r0.x : q == 1 ? r0.y : q == 2 ? r0.z : r0.w, c1 = q == 0 ? r1.x : q == 1 ? r1.y : q == 2 ? r1.z : r1.w;
-              uint32_t d0, d1, d2, d3;  // (first key, second key) of a dim
-              e4m3x4_to_f16x4(__byte_perm(c0, c1, 0x5140), d0, d1);
-              e4m3x4_to_f16x4(__byte_perm(c0, c1, 0x7362), d2, d3);
-              bb[h][0] = scaled_bf16x2(d0, vs[2 * kk + h]);
-              bb[h][1] = scaled_bf16x2(d1, vs[2 * kk + h]);
-              bb[h][2] = scaled_bf16x2(d2, vs[2 * kk + h]);
-              bb[h][3] = scaled_bf16x2(d3, vs[2 * kk + h]);
+              const uint32_t c0 = word_of(v[2 * h], q), c1 = word_of(v[2 * h + 1], q);
+              e4m3x4_to_f16x4(__byte_perm(c0, c1, 0x5140), bb[h][0], bb[h][1]);
+              e4m3x4_to_f16x4(__byte_perm(c0, c1, 0x7362), bb[h][2], bb[h][3]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma_bf16_16816(o[q * 4 + e], a, bb[0][e], bb[1][e]);
+            for (int e = 0; e < 4; ++e) mma_f16_16816(o[q * 4 + e], w, bb[0][e], bb[1][e]);
           }
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // pieces g and g + 8
+            uint4 v[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              auto word = [&](int i) {
-                const uint4 v = vx[i * 2 + h];
-                return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w;
-              };
+            for (int i = 0; i < 4; ++i) v[i] = load_v(i >> 1, i & 1, h * second);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                mma_bf16_16816(o[h * 8 + q * 2 + e], a, __byte_perm(word(0), word(1), e ? 0x7632 : 0x5410),
-                               __byte_perm(word(2), word(3), e ? 0x7632 : 0x5410));
-            }
+                mma_bf16_16816(o[h * 8 + q * 2 + e], w, __byte_perm(word_of(v[0], q), word_of(v[1], q), e ? 0x7632 : 0x5410),
+                               __byte_perm(word_of(v[2], q), word_of(v[3], q), e ? 0x7632 : 0x5410));
           }
         }
       }
-      load_v(u + kWarpsF);
+      if (alive) load_unit();
     }
 
     // ------------------------------------------------------------ the warps' states meet
+    f += sg.u1 - sg.u0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -350,11 +494,12 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float* row = state + (warp * 16 + g + 8 * i) * kRowF;
+      const float back = KV8 ? 1.f / fv[i] : 1.f;
 #pragma unroll
       for (int j = 0; j < 16; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e)  // column 2 t + e of tile j: the dim that lane g = 2 t + e loaded as its j-th
-          row[KV8 ? (2 * t + e) * 16 + j : (2 * t + e + 8 * (j >> 3)) * 8 + (j & 7)] = o[j][2 * i + e];
+          row[KV8 ? (2 * t + e) * 16 + j : (2 * t + e + 8 * (j >> 3)) * 8 + (j & 7)] = o[j][2 * i + e] * back;
       if (t == 0) {
         ml[(warp * 16 + g + 8 * i) * 2] = m[i];
         ml[(warp * 16 + g + 8 * i) * 2 + 1] = l[i];
@@ -363,25 +508,27 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
     __syncthreads();
     const int r = tid >> 4, d0 = (tid & 15) * 8;  // this thread's row and dims from here on
     float top = kNegInfF, sum = 0.f, y[8] = {};
-    auto add = [&](const float* from_o, float fm, float fl, float ref) {  // ref: the largest maximum
-      const float c = fm == kNegInfF ? (fl == 0.f ? 0.f : 1.f) : fast_exp2(fm - ref);  // (no maximum: no key, or NaN scores)
-      sum += fl * c;
-      const float4 a = *reinterpret_cast<const float4*>(from_o), e = *reinterpret_cast<const float4*>(from_o + 4);
-      if (c != 0.f) {
-        y[0] += a.x * c, y[1] += a.y * c, y[2] += a.z * c, y[3] += a.w * c;
-        y[4] += e.x * c, y[5] += e.y * c, y[6] += e.z * c, y[7] += e.w * c;
+    auto add = [&](const float4& c0, const float4& c1, float pm, float pl) {  // a state's O, maximum and sum; top: the largest maximum
+      const float k = pm == kNegInfF ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - top);  // (no maximum: no key, or NaN scores)
+      sum += pl * k;
+      if (k != 0.f) {
+        y[0] += c0.x * k, y[1] += c0.y * k, y[2] += c0.z * k, y[3] += c0.w * k;
+        y[4] += c1.x * k, y[5] += c1.y * k, y[6] += c1.z * k, y[7] += c1.w * k;
       }
     };
 #pragma unroll
     for (int w = 0; w < kWarpsF; ++w) top = fmaxf(top, ml[(w * 16 + r) * 2]);
 #pragma unroll
-    for (int w = 0; w < kWarpsF; ++w) add(state + (w * 16 + r) * kRowF + d0, ml[(w * 16 + r) * 2], ml[(w * 16 + r) * 2 + 1], top);
+    for (int w = 0; w < kWarpsF; ++w) {
+      const float4* from_o = reinterpret_cast<const float4*>(state + (w * 16 + r) * kRowF + d0);
+      add(from_o[0], from_o[1], ml[(w * 16 + r) * 2], ml[(w * 16 + r) * 2 + 1]);
+    }
     bool write = true;
-    if (u1 - u0 < un.n) {
+    if (sg.u1 - sg.u0 < sg.un.n) {
       // Part of an item: its state to the workspace (a CTA starts at most one item that it does not end, and ends or
       // passes through at most one that it did not start).
-      const int slot = 2 * blockIdx.x + (u0 == 0 ? 1 : 0);
-      const int c0 = owner(item0), c1 = owner(item0 + un.n - 1);
+      const int slot = 2 * blockIdx.x + (sg.u0 == 0 ? 1 : 0);
+      const int c0 = owner(sg.item0), c1 = owner(sg.item0 + sg.un.n - 1);
       if (in_bounds(slot < p.slots && c1 < p.slots / 2, p.err)) {
         float* to = p.part_o + ((long long)slot * 16 + r) * 128 + d0;
         *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
@@ -390,42 +537,40 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
       }
       __syncthreads();
       if (tid == 0) {
-        const int done = atomic_add_acq_rel_gpu(p.counters + c0, 1) == c1 - c0;
-        if (done) p.counters[c0] = 0;  // as the next call finds it
-        *last = done;
+        const int ended = atomic_add_acq_rel_gpu(p.counters + c0, 1) == c1 - c0;
+        if (ended) p.counters[c0] = 0;  // as the next call finds it
+        *last = ended;
       }
       __syncthreads();
       write = *last != 0;
-      if (write) {  // the last of its CTAs: all states, in order
+      if (write && r < sg.most * G) {  // the last of its CTAs: all states, in order
+        auto slot_of = [&](int c) { return (long long)(2 * c + (c == c0 ? 1 : 0)) * 16 + r; };
         top = kNegInfF;
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = 0.f;
-        auto slot_of = [&](int c) { return (long long)(2 * c + (c == c0 ? 1 : 0)) * 16 + r; };
+#pragma unroll 8
         for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(p.part_ml + slot_of(c) * 2));
 #pragma unroll 4
         for (int c = c0; c <= c1; ++c) {
           const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot_of(c) * 2));
-          const float* from_o = p.part_o + slot_of(c) * 128 + d0;
-          const float4 a = __ldcg(reinterpret_cast<const float4*>(from_o)), e = __ldcg(reinterpret_cast<const float4*>(from_o + 4));
-          const float both[8] = {a.x, a.y, a.z, a.w, e.x, e.y, e.z, e.w};
-          const float k = v.x == kNegInfF ? (v.y == 0.f ? 0.f : 1.f) : fast_exp2(v.x - top);
-          sum += v.y * k;
-          if (k != 0.f)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] += both[i] * k;
+          const float4* from_o = reinterpret_cast<const float4*>(p.part_o + slot_of(c) * 128 + d0);
+          add(__ldcg(from_o), __ldcg(from_o + 1), v.x, v.y);
         }
       }
     }
-    if (write && r < most * G) {
+    if (write && r < sg.most * G) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      __nv_bfloat16* to = p.out + (long long)(sq.q0 + pos0 + r / G) * p.o_st + (long long)(kvh * G + r % G) * p.o_sh + d0;
+      __nv_bfloat16* to = p.out + (long long)(sg.q0 + sg.pos0 + r / G) * p.o_st + (long long)(sg.kvh * G + r % G) * p.o_sh + d0;
       uint4 v = make_uint4(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv), pack_bf16x2(y[4] * inv, y[5] * inv),
                            pack_bf16x2(y[6] * inv, y[7] * inv));
       if (sum == 0.f) v = make_uint4(0, 0, 0, 0);
       if (in_bounds(to >= p.out && to + 8 <= p.out + p.out_span, p.err)) *reinterpret_cast<uint4*>(to) = v;
     }
+    if (f >= f1) break;
   }
+  for (; used < loaded; ++used)  // (a wait has run out: what is still on its way must not land behind the CTA's end)
+    mbar_wait_bounded(bars + (used & 1) * 8, used >> 1 & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
 }
 
 template <bool KV8>

@@ -284,10 +284,9 @@ struct FewParams {
   const __nv_bfloat16* q;  // [Tq][Hq][128]
   __nv_bfloat16* out;
   long long q_st, q_sh, o_st, o_sh;
-  const uint8_t *k_pages, *v_pages;  // [num_blocks][Hkv][block_size][128] bf16 or e4m3; strides and spans in bytes
-  long long kp_sb, kp_sh, kp_sr, vp_sb, vp_sh, vp_sr;
-  const float* scales;               // [num_blocks][Hkv][2][block_size] (e4m3)
-  long long sc_sb, sc_sh, sc_st;
+  // [num_blocks][Hkv][block_size][128] bf16 or e4m3, a box of a unit's 16 (e4m3: 32) tokens or of a block's where it has
+  // fewer; e4m3: the scales [num_blocks][Hkv][2][block_size]
+  CUtensorMap tm_k, tm_v, tm_scales;
   const int *cu, *lens, *table;      // [B + 1], [B], [B][max_blocks]
   long long bt_stride;
   int* err;
@@ -299,10 +298,10 @@ struct FewParams {
   int num_blocks, block_shift, window, sinks;
   float scale_log2;
   int least;                         // units that a CTA takes at least
-  // elements (pools: bytes) from the first to one past the last (bounds-checked build)
-  long long q_span, out_span, kp_span, vp_span, sc_span, table_span;
+  // elements from the first to one past the last (bounds-checked build)
+  long long q_span, out_span, table_span;
 };
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 16, kFewKeys16 = 16, kFewKeys8 = 32;
 cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, bool pdl, cudaStream_t stream);
 
 // ------------------------------------------------ paged cache: writing and reading

@@ -301,7 +301,9 @@ int decode_attn_prefill_window(const da_tensor_t* q, const da_tensor_t* k, const
  *
  * The query at position i sees keys 0 .. i, or with a window i - window + 1 .. i and those below
  * `sinks`. A query without a key gives a row of zeros; rows of q that belong to no sequence
- * are left as they were in out. An e4m3 key or value is bf16(code * scale), as decode_attn_cache_read gives it.
+ * are left as they were in out. An e4m3 key or value is code * scale, rounded to bf16 where a call has many
+ * rows (exact for the powers of two that decode_attn_cache_write gives; scales: any finite values, V's from 2^-100 on in
+ * magnitude, or 0).
  * Table entries and tokens that no query of the call sees are not read: blocks that a window has
  * left behind may belong to others by now, and what rows past seq_lens hold does not matter. An entry outside
  * the pool that is read sets bit 64 of the device error word and its block reads as zeros. A NaN or infinity in a

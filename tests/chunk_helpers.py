@@ -16,9 +16,10 @@ def visible(lq, lk, window, sinks):
     return ok & ((j > i - window) | (j < sinks)) if window else ok
 
 
-def attend_ref(q, keys, values, cu, scale, window=0, sinks=0, rows=None):
+def attend_ref(q, keys, values, cu, scale, window=0, sinks=0, rows=None, kv_eps=0.0):
     """(reference, bound, rows of a sequence) for q [Tq, Hq, D]; keys[b] and values[b] [Lk, Hkv, D] (CPU). Keys that no query
-    sees may hold anything. `rows`: only these queries of each sequence (a list of indices)."""
+    sees may hold anything. `rows`: only these queries of each sequence (a list of indices). `kv_eps`: how far a key's or value's
+    elements may be off, relative to them: scores by X kv_eps, numerator and sum by that factor each, values by theirs."""
     Tq, Hq, D = q.shape
     ref, tol = torch.zeros((Tq, Hq, D), dtype=F64), torch.zeros((Tq, Hq, D), dtype=F64)
     have = torch.zeros(Tq, dtype=torch.bool)
@@ -44,5 +45,5 @@ def attend_ref(q, keys, values, cu, scale, window=0, sinks=0, rows=None):
                 o = p @ vd
                 X = (qd.abs() @ kd.abs().T * abs(scale)).masked_fill(~ok, 0.0).amax(-1, keepdim=True)
                 ref[at, h] = o
-                tol[at, h] = bound(o, p @ vd.abs(), X, 2.0 ** -8)
+                tol[at, h] = bound(o, p @ vd.abs(), X, 2.0 ** -8) + (2 * torch.expm1(X * kv_eps) + kv_eps) * (p @ vd.abs()) * 1.01
     return ref, tol, have
