@@ -1129,7 +1129,7 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
   return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
-// decode_attn_chunk after its checks where a sequence has few rows on average: on no tensor memory, 16 rows at a time.
+// decode_attn_chunk after its checks where a sequence has few rows on average: 8 or 16 at a time.
 int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
             const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, void* stream) {
   const bool kv8 = kp->dtype == DA_DTYPE_E4M3;
@@ -1155,7 +1155,8 @@ int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, 
   p.G = (int)(q->shape[1] / kp->shape[1]);
   p.Tq = (int)q->shape[0];
   p.cap = (int)(MB * kp->shape[2]);
-  p.npos = kFewRows / p.G;
+  const int rows = p.G <= 8 && (int64_t)p.Tq * p.G <= 8 * B ? 8 : kFewRows;
+  p.npos = rows / p.G;
   p.num_blocks = (int)kp->shape[0];
   while ((1 << p.block_shift) < kp->shape[2]) ++p.block_shift;
   p.window = window ? std::min(window, 1 << 30) : 1 << 30;
@@ -1175,7 +1176,7 @@ int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, 
   p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
   p.counters = reinterpret_cast<int*>(ws + kAttnCntOff);
   p.err = reinterpret_cast<int*>(ws + kErrOff);
-  return launch_chunk_few(p, grid, kv8, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return launch_chunk_few(p, grid, kv8, rows, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 // decode_attn_prefill and, with a window, decode_attn_prefill_window.

@@ -1,7 +1,8 @@
 // chunk_few.cu -- attention of a few new tokens of each sequence over a paged cache: decode_attn_chunk where sequences have
 // one token, or a few drafted ones.
 //
-// An item is 16 rows of one (sequence, KV head): npos = floor(16 / G) query positions x the G heads that share the KV head.
+// An item is 8 or 16 rows of one (sequence, KV head): npos = floor(rows / G) query positions x the G heads that share the KV
+// head.
 // Its keys go by in units of 16 (e4m3: 32), those of the first `sinks` and from the window's beginning on. The
 // units of all items, laid end to end, are cut into equal parts, one for each CTA (one per SM, fewer where little is
 // left to each), whatever the sequences' lengths: an item that lies in several CTAs leaves a state in the
@@ -9,7 +10,8 @@
 //
 //  * Bound by the bytes of K and V. The 128-row tiles of prefill.cuh would be idle but for 16 rows and take 1.3 us
 //    a tile of 128 keys, the time of one softmax, whatever its bytes; here a warp works on a unit of its own
-//    (mma.sync, 16 rows being one tile's height) and the eight of a CTA meet at the item's end only.
+//    (mma.sync) and the eight of a CTA meet at the item's end only. S^T = K Q^T and O^T = V^T P^T: keys and dims are the
+//    instruction's 16 rows, queries its 8 columns, so that eight of them cost half of sixteen.
 //  * A warp copies its units of K and V by TMA (4 KB each, a copy each where a block holds a unit), two units ahead and on
 //    into the next item's: 16 KB a warp, 128 KB an SM on their way. Which of a row's dims meet which lane and step of the
 //    matrix instructions is free as long as Q's follow: of a key, lane t of four takes the 16-byte pieces t, t + 4, ...; for V,
@@ -68,10 +70,16 @@ __device__ __forceinline__ uint4 lds_piece(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ float2 lds_pair(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
+}
+// The maximum over the eight lanes that hold other keys of the same rows.
+__device__ __forceinline__ float max_of_keys(float r) {
+  r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 4));
+  r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 8));
+  return fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 16));
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 // 2^e, e clamped to what a float holds
@@ -79,9 +87,11 @@ __device__ __forceinline__ float power_of_2(int e) { return __int_as_float((min(
 // floor(log2 x) of a positive float (subnormal ones: -127)
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 0xffu) - 127; }
 
-template <bool KV8>
+// NB: blocks of eight rows of an item
+template <bool KV8, int NB>
 __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_constant__ FewParams p) {
-  constexpr int kKeys = KV8 ? kFewKeys8 : kFewKeys16, kNT = kKeys / 8;  // keys of a unit, in tiles of 8
+  constexpr int kKeys = KV8 ? kFewKeys8 : kFewKeys16, kKT = kKeys / 16;  // keys of a unit, in tiles of 16
+  constexpr int kRows = 8 * NB, kDims = kRows / 2;  // rows of an item; dims of a thread where states are joined (256 threads)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   long long* prefix = reinterpret_cast<long long*>(smem + kOffPrefix);
@@ -250,9 +260,9 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
   const uint32_t second = split ? 1024 : 2048;          // bf16: from a row's first 64 dims to the others
   const uint32_t k_at = g * 128 + (((t + 4 * (g & 1)) ^ g) << 4);
   const uint32_t v_at = 2 * t * 128 + ((g ^ (2 * t)) << 4), v_at1 = (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4);
-  // (byte of the K scales of keys 2 t, 2 t + 1 of the nt-th eight; V's lie `scale_v` behind)
+  // K's scale of key g of the nt-th eight; V's lies `scale_v` behind
   const uint32_t scale_v = split ? 64 : 128;
-  auto scale_at = [&](int nt) { return (uint32_t)(split ? (nt >> 1) * 128 + (nt & 1) * 32 : nt * 32) + t * 8; };
+  auto scale_at = [&](int nt) { return (uint32_t)(split ? (nt >> 1) * 128 + (nt & 1) * 32 : nt * 32) + g * 4; };
 
   begin_loads(f);
   load_unit();
@@ -261,52 +271,71 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
   bool alive = true;  // no wait has run out
   while (true) {
     const Segment sg = segment(f);
-    // Q, in the order of dims that K's pieces give; rows g and g + 8: the keys that they see, before lim and from `from` on
-    // (or before sinks), and the factor that turns products into log2 units
-    uint32_t aq[8][4];
-    int lim[2], from[2];
-    float factor[2] = {p.scale_log2, p.scale_log2};
+    // Q, in the order of dims that K's pieces give: row g of each block of eight. e4m3: f16 over a power of two.
+    uint32_t bq[NB][8][2];
+    int e_row[NB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i, pos = sg.pos0 + r / G;
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = nb * 8 + g, pos = sg.pos0 + r / G;
       const bool ok = r < sg.most * G;
-      lim[i] = ok ? min(sg.lk, pos + sg.shift + 1) : 0;
-      from[i] = pos + sg.shift - p.window + 1;
       const __nv_bfloat16* row = p.q + (long long)(sg.q0 + pos) * p.q_st + (long long)(sg.kvh * G + r % G) * p.q_sh;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         const int dim = KV8 ? (t + 4 * (s >> 2)) * 16 + (s & 3) * 4 : (t + 4 * (s >> 1)) * 8 + (s & 1) * 4;
         uint2 v = make_uint2(0, 0);
         if (ok && in_bounds(row + 128 <= p.q + p.q_span, p.err)) v = __ldg(reinterpret_cast<const uint2*>(row + dim));
-        aq[s][i] = v.x;
-        aq[s][2 + i] = v.y;
+        bq[nb][s][0] = v.x;
+        bq[nb][s][1] = v.y;
       }
-    }
-    if constexpr (KV8) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      e_row[nb] = 0;
+      if constexpr (KV8) {
         unsigned top = 0;  // the row's largest magnitude, a bf16 pattern
 #pragma unroll
-        for (int s = 0; s < 8; ++s) top = __vmaxu2(top, __vmaxu2(aq[s][i] & 0x7fff7fffu, aq[s][2 + i] & 0x7fff7fffu));
+        for (int s = 0; s < 8; ++s) top = __vmaxu2(top, __vmaxu2(bq[nb][s][0] & 0x7fff7fffu, bq[nb][s][1] & 0x7fff7fffu));
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = max(top & 0xffffu, top >> 16);
-        // (a row of zeros, or one with an infinity or NaN: as it is; twice half the power: 2^-112 and less are no floats)
-        const int e = top == 0 || top >= 0x7f80u ? 0 : 14 - ((int)(top >> 7) - 127), e0 = e / 2, e1 = e - e0;
-        const float a = power_of_2(e0), c = power_of_2(e1);
+        // (a row of zeros, or one with an infinity or NaN: as it is; in two halves, as 2^-112 and less are no floats)
+        const int e = top == 0 || top >= 0x7f80u ? 0 : 14 - ((int)(top >> 7) - 127);
+        const float a = power_of_2(e / 2), c = power_of_2(e - e / 2);
 #pragma unroll
         for (int s = 0; s < 8; ++s)
 #pragma unroll
-          for (int k = 0; k < 4; k += 2)
-            aq[s][k + i] = pack_f16x2(bf16lo_to_f32(aq[s][k + i]) * a * c, bf16hi_to_f32(aq[s][k + i]) * a * c);
-        factor[i] = fminf(fmaxf(p.scale_log2 * power_of_2(-e0) * power_of_2(-e1), -3.4e38f), 3.4e38f);
+          for (int k = 0; k < 2; ++k) bq[nb][s][k] = pack_f16x2(bf16lo_to_f32(bq[nb][s][k]) * a * c, bf16hi_to_f32(bq[nb][s][k]) * a * c);
+        e_row[nb] = e;
       }
     }
-    float o[16][4];
+    // This lane's scores: keys g and g + 8 of every sixteen, rows 2 t and 2 t + 1 of every eight. The rows see keys before lim
+    // and from `from` on (or before sinks); factor turns products into log2 units.
+    int lim[NB][2], from[NB][2];
+    float factor[NB][2];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m[2] = {kNegInfF, kNegInfF}, l[2] = {0.f, 0.f};
-    float fv[2] = {1.f, 1.f}, largest[2] = {0.f, 0.f};  // e4m3: V's factor, and the largest weight times V scale so far
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nb * 8 + 2 * t + e, pos = sg.pos0 + r / G;
+        lim[nb][e] = r < sg.most * G ? min(sg.lk, pos + sg.shift + 1) : 0;
+        from[nb][e] = pos + sg.shift - p.window + 1;
+        factor[nb][e] = p.scale_log2;
+        if constexpr (KV8) {
+          const int x = __shfl_sync(0xffffffffu, e_row[nb], (2 * t + e) * 4);
+          factor[nb][e] = fminf(fmaxf(p.scale_log2 * power_of_2(-(x / 2)) * power_of_2(-(x - x / 2)), -3.4e38f), 3.4e38f);
+        }
+      }
+    float o[NB][8][4], m[NB][2], l[NB][2];
+    float fv[NB][2], largest[NB][2];  // e4m3: V's factor, and the largest weight times V scale so far
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[nb][j][0] = o[nb][j][1] = o[nb][j][2] = o[nb][j][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[nb][e] = kNegInfF;
+        l[nb][e] = 0.f;
+        fv[nb][e] = 1.f;
+        largest[nb][e] = 0.f;
+      }
+    }
     const int all_before = min(sg.lk, sg.pos0 + sg.shift + 1), all_from = sg.pos0 + sg.most - 1 + sg.shift - p.window + 1;
     for (int u = sg.u0 + warp; u < sg.u1 && alive; u += kWarpsF) {
       const int st = used & 1;
@@ -314,121 +343,144 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
       alive = __all_sync(0xffffffffu, alive);
       ++used;
       const uint32_t kv = units + st * kUnitBytes, sc = scales + st * kScalesF;
-      float x[kNT][4];
+      float x[kKT][NB][4];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+      for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-        for (int h = 0; h < (KV8 ? 1 : 2); ++h) {
-          const uint32_t at = kv + nt * eight + h * second + k_at;
-          const uint4 a = lds_piece(at), c = lds_piece(at ^ 64);
-          const uint4 k0 = odd ? c : a, k1 = odd ? a : c;  // pieces t and t + 4
-          if constexpr (KV8) {
+        for (int nb = 0; nb < NB; ++nb) x[kt][nb][0] = x[kt][nb][1] = x[kt][nb][2] = x[kt][nb][3] = 0.f;
+      // S^T = K Q^T: sixteen keys by eight rows
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-              uint32_t lo, hi;
-              e4m3x4_to_f16x4(word_of(s < 4 ? k0 : k1, s & 3), lo, hi);
-              mma_f16_16816(x[nt], aq[s], lo, hi);
-            }
-          } else {
-            mma_bf16_16816(x[nt], aq[h * 4], k0.x, k0.y);
-            mma_bf16_16816(x[nt], aq[h * 4 + 1], k0.z, k0.w);
-            mma_bf16_16816(x[nt], aq[h * 4 + 2], k1.x, k1.y);
-            mma_bf16_16816(x[nt], aq[h * 4 + 3], k1.z, k1.w);
+      for (int h = 0; h < (KV8 ? 1 : 2); ++h) {
+        uint4 k[kKT][2][2];  // pieces t and t + 4 of keys g and g + 8
+#pragma unroll
+        for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t at = kv + (2 * kt + i) * eight + h * second + k_at;
+            const uint4 a = lds_piece(at), c = lds_piece(at ^ 64);
+            k[kt][i][0] = odd ? c : a;
+            k[kt][i][1] = odd ? a : c;
           }
-        }
+#pragma unroll
+        for (int s = 0; s < (KV8 ? 8 : 4); ++s)
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt) {
+            uint32_t a[4];
+            if constexpr (KV8) {
+              e4m3x4_to_f16x4(word_of(k[kt][0][s >> 2], s & 3), a[0], a[2]);
+              e4m3x4_to_f16x4(word_of(k[kt][1][s >> 2], s & 3), a[1], a[3]);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_f16_16816(x[kt][nb], a, bq[nb][s][0], bq[nb][s][1]);
+            } else {
+              a[0] = word_of(k[kt][0][s >> 1], 2 * (s & 1));
+              a[1] = word_of(k[kt][1][s >> 1], 2 * (s & 1));
+              a[2] = word_of(k[kt][0][s >> 1], 2 * (s & 1) + 1);
+              a[3] = word_of(k[kt][1][s >> 1], 2 * (s & 1) + 1);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(x[kt][nb], a, bq[nb][h * 4 + s][0], bq[nb][h * 4 + s][1]);
+            }
+          }
       }
       const int key0 = sg.un.at(u) * kKeys;
       auto seen = [&](int key) { return key < sg.end && (key >= sg.low || key < p.sinks); };  // by some row of the item
       const bool whole = key0 + kKeys <= all_before && (key0 >= all_from || key0 + kKeys <= p.sinks);  // every key seen by every row
-      float top[2] = {kNegInfF, kNegInfF};
+      float top[NB][2];
+      bool over = false;
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        const float2 ks = KV8 ? lds_pair(sc + scale_at(nt)) : make_float2(1.f, 1.f);
+      for (int nb = 0; nb < NB; ++nb) {
+        top[nb][0] = top[nb][1] = kNegInfF;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[nt][i] *= factor[i >> 1];
-          if (KV8) x[nt][i] *= i & 1 ? ks.y : ks.x;
-          const int key = key0 + nt * 8 + 2 * t + (i & 1);
-          if (!whole && !(key < lim[i >> 1] && (key >= from[i >> 1] || key < p.sinks))) x[nt][i] = kNegInfF;
-          top[i >> 1] = fmaxf(top[i >> 1], x[nt][i]);
-        }
-      }
-      const bool grow = __any_sync(0xffffffffu, top[0] > m[0] + kSlackF || top[1] > m[1] + kSlackF);
-      float a[2] = {1.f, 1.f};  // what the sums and O so far are worth against the new maximum
-      if (grow) {
+        for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float r = top[i];
-          r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 1));
-          r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 2));
-          const float mn = fmaxf(m[i], r);
-          a[i] = m[i] == kNegInfF ? 0.f : fast_exp2(m[i] - mn);
-          m[i] = mn;
-          l[i] *= a[i];
-          largest[i] *= a[i];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float ref = m[i] == kNegInfF ? 0.f : m[i];
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          x[nt][2 * i] = fast_exp2(x[nt][2 * i] - ref);
-          x[nt][2 * i + 1] = fast_exp2(x[nt][2 * i + 1] - ref);
-          l[i] += x[nt][2 * i] + x[nt][2 * i + 1];
-        }
-      }
-      if constexpr (KV8) {
-        float2 vs[kNT];
-        float big[2] = {0.f, 0.f};  // the largest weight times V scale of this lane's
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          vs[nt] = lds_pair(sc + scale_at(nt) + scale_v);
-          if (!whole) {  // (0 times a scale that belongs to no key is not 0)
-            if (!seen(key0 + nt * 8 + 2 * t)) vs[nt].x = 0.f;
-            if (!seen(key0 + nt * 8 + 2 * t + 1)) vs[nt].y = 0.f;
+          for (int i = 0; i < 4; ++i) {
+            float& v = x[kt][nb][i];
+            v *= factor[nb][i & 1];
+            if (KV8) v *= lds_f32(sc + scale_at(2 * kt + (i >> 1)));
+            const int key = key0 + kt * 16 + 8 * (i >> 1) + g;
+            if (!whole && !(key < lim[nb][i & 1] && (key >= from[nb][i & 1] || key < p.sinks))) v = kNegInfF;
+            top[nb][i & 1] = fmaxf(top[nb][i & 1], v);
           }
+        over = over || top[nb][0] > m[nb][0] + kSlackF || top[nb][1] > m[nb][1] + kSlackF;
+      }
+      const bool grow = __any_sync(0xffffffffu, over);
+      float a[NB][2];  // what the sums and O so far are worth against the new maximum
 #pragma unroll
-          for (int i = 0; i < 2; ++i) big[i] = fmaxf(big[i], fmaxf(fabsf(x[nt][2 * i] * vs[nt].x), fabsf(x[nt][2 * i + 1] * vs[nt].y)));
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          a[nb][e] = 1.f;
+          if (grow) {
+            const float mn = fmaxf(m[nb][e], max_of_keys(top[nb][e]));
+            a[nb][e] = m[nb][e] == kNegInfF ? 0.f : fast_exp2(m[nb][e] - mn);
+            m[nb][e] = mn;
+            l[nb][e] *= a[nb][e];
+            largest[nb][e] *= a[nb][e];
+          }
+          const float ref = m[nb][e] == kNegInfF ? 0.f : m[nb][e];
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+            for (int i = e; i < 4; i += 2) {
+              x[kt][nb][i] = fast_exp2(x[kt][nb][i] - ref);
+              l[nb][e] += x[kt][nb][i];
+            }
         }
-        const bool first = (largest[0] == 0.f && big[0] > 0.f) || (largest[1] == 0.f && big[1] > 0.f);
-        if (__any_sync(0xffffffffu, grow || first || big[0] * fv[0] > 256.f || big[1] * fv[1] > 256.f)) {
-          unsigned some = 0;  // of this lane's keys: does V's row hold a code that is not 0?
+      if constexpr (KV8) {
+        float vs[kKT][2];
+        bool redo = grow;
 #pragma unroll
-          for (int k = 0; k < 2 * kNT; ++k) {
+        for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            vs[kt][i] = lds_f32(sc + scale_at(2 * kt + i) + scale_v);
+            if (!whole && !seen(key0 + kt * 16 + 8 * i + g)) vs[kt][i] = 0.f;  // (0 times a scale that belongs to no key is not 0)
+          }
+        auto big = [&](int nb, int e) {  // the largest weight times V scale of this lane's
+          float r = 0.f;
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt) r = fmaxf(r, fmaxf(fabsf(x[kt][nb][e] * vs[kt][0]), fabsf(x[kt][nb][2 + e] * vs[kt][1])));
+          return r;
+        };
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float r = big(nb, e);
+            redo = redo || (largest[nb][e] == 0.f && r > 0.f) || r * fv[nb][e] > 256.f;
+          }
+        if (__any_sync(0xffffffffu, redo)) {
+          unsigned some = 0;  // keys 2 t and 2 t + 1 of every eight: does V's row hold a code that is not 0?
+#pragma unroll
+          for (int k = 0; k < 4 * kKT; ++k) {
             const uint4 v = lds_piece(kv + kHalfUnit + (k >> 1) * eight + (k & 1 ? v_at1 : v_at));
             some |= ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) ? 1u << k : 0u;
           }
           some |= __shfl_xor_sync(0xffffffffu, some, 4);
           some |= __shfl_xor_sync(0xffffffffu, some, 8);
           some |= __shfl_xor_sync(0xffffffffu, some, 16);
+          some = __shfl_sync(0xffffffffu, some, g >> 1) >> (g & 1);  // key g's of every eight
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            if (!(some >> (2 * nt) & 1u)) vs[nt].x = 0.f;
-            if (!(some >> (2 * nt + 1) & 1u)) vs[nt].y = 0.f;
-          }
+          for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float r = 0.f;
+            for (int i = 0; i < 2; ++i)
+              if (!(some >> (2 * (2 * kt + i)) & 1u)) vs[kt][i] = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) r = fmaxf(r, fmaxf(fabsf(x[nt][2 * i] * vs[nt].x), fabsf(x[nt][2 * i + 1] * vs[nt].y)));
-            r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 1));
-            r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 2));
-            largest[i] = fmaxf(largest[i], r);
-            float to = fv[i];  // the largest times it stays between 1 and 2^8
-            if (largest[i] > 0.f && !(largest[i] * to >= 1.f && largest[i] * to <= 256.f)) to = power_of_2(-exponent_of(largest[i]));
-            a[i] *= fminf(to / fv[i], 0x1p127f);
-            fv[i] = to;
-          }
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              largest[nb][e] = fmaxf(largest[nb][e], max_of_keys(big(nb, e)));
+              float to = fv[nb][e];  // the largest times it stays between 1 and 2^8
+              if (largest[nb][e] > 0.f && !(largest[nb][e] * to >= 1.f && largest[nb][e] * to <= 256.f)) to = power_of_2(-exponent_of(largest[nb][e]));
+              a[nb][e] *= fminf(to / fv[nb][e], 0x1p127f);
+              fv[nb][e] = to;
+            }
         }
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          x[nt][0] *= vs[nt].x * fv[0];
-          x[nt][1] *= vs[nt].y * fv[0];
-          x[nt][2] *= vs[nt].x * fv[1];
-          x[nt][3] *= vs[nt].y * fv[1];
-        }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[kt][nb][i] *= vs[kt][i >> 1] * fv[nb][i & 1];
       }
       // V: key 2 t + k of the nt-th eight, piece g. What no row sees may hold anything: zeros.
       auto load_v = [&](int nt, int k, uint32_t off) {
@@ -436,47 +488,55 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
         if (!whole && !seen(key0 + nt * 8 + 2 * t + k)) v = make_uint4(0, 0, 0, 0);
         return v;
       };
-      if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+      bool scaled = false;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+      for (int nb = 0; nb < NB; ++nb) scaled = scaled || a[nb][0] != 1.f || a[nb][1] != 1.f;
+      if (__any_sync(0xffffffffu, scaled)) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] *= a[i >> 1];
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[nb][j][i] *= a[nb][i & 1];
       }
+      // O^T += V^T P^T: sixteen dims by eight rows. A lane's dims of a tile are neighbours of its piece.
 #pragma unroll
-      for (int kk = 0; kk < kNT / 2; ++kk) {
-        uint32_t w[4];
+      for (int kt = 0; kt < kKT; ++kt) {
+        uint32_t w[NB][2];  // weights of keys 2 t, 2 t + 1 of both eights, row g
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = KV8 ? pack_f16x2(x[2 * kk + (i >> 1)][2 * (i & 1)], x[2 * kk + (i >> 1)][2 * (i & 1) + 1])
-                     : pack_bf16x2(x[2 * kk + (i >> 1)][2 * (i & 1)], x[2 * kk + (i >> 1)][2 * (i & 1) + 1]);
-        if constexpr (KV8) {
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            w[nb][i] = movmatrix_trans(KV8 ? pack_f16x2(x[kt][nb][2 * i], x[kt][nb][2 * i + 1]) : pack_bf16x2(x[kt][nb][2 * i], x[kt][nb][2 * i + 1]));
+#pragma unroll
+        for (int h = 0; h < (KV8 ? 1 : 2); ++h) {  // bf16: pieces g and g + 8
           uint4 v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = load_v(2 * kk + (i >> 1), i & 1, 0);
+          for (int i = 0; i < 4; ++i) v[i] = load_v(2 * kt + (i >> 1), i & 1, h * second);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {  // dims 16 g + 4 q ..
-            uint32_t bb[2][4];           // (first key, second key) of a dim
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (KV8) {
+              uint32_t b[2][4];  // (first key, second key) of dims 16 g + 4 q ..
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t c0 = word_of(v[2 * h], q), c1 = word_of(v[2 * h + 1], q);
-              e4m3x4_to_f16x4(__byte_perm(c0, c1, 0x5140), bb[h][0], bb[h][1]);
-              e4m3x4_to_f16x4(__byte_perm(c0, c1, 0x7362), bb[h][2], bb[h][3]);
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t c0 = word_of(v[2 * i], q), c1 = word_of(v[2 * i + 1], q);
+                e4m3x4_to_f16x4(__byte_perm(c0, c1, 0x5140), b[i][0], b[i][1]);
+                e4m3x4_to_f16x4(__byte_perm(c0, c1, 0x7362), b[i][2], b[i][3]);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const uint32_t d[4] = {b[0][e], b[0][e + 1], b[1][e], b[1][e + 1]};
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma_f16_16816(o[nb][q * 2 + (e >> 1)], d, w[nb][0], w[nb][1]);
+              }
+            } else {
+              uint32_t d[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                d[i] = __byte_perm(word_of(v[i & 2], q), word_of(v[(i & 2) + 1], q), i & 1 ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(o[nb][h * 4 + q], d, w[nb][0], w[nb][1]);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mma_f16_16816(o[q * 4 + e], w, bb[0][e], bb[1][e]);
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // pieces g and g + 8
-            uint4 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = load_v(i >> 1, i & 1, h * second);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                mma_bf16_16816(o[h * 8 + q * 2 + e], w, __byte_perm(word_of(v[0], q), word_of(v[1], q), e ? 0x7632 : 0x5410),
-                               __byte_perm(word_of(v[2], q), word_of(v[3], q), e ? 0x7632 : 0x5410));
           }
         }
       }
@@ -486,42 +546,45 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
     // ------------------------------------------------------------ the warps' states meet
     f += sg.u1 - sg.u0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    }
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], 4);
+        l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], 8);
+        l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], 16);
+      }
     __syncthreads();  // the last segment's have been read
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float* row = state + (warp * 16 + g + 8 * i) * kRowF;
-      const float back = KV8 ? 1.f / fv[i] : 1.f;
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
+      for (int e = 0; e < 2; ++e) {
+        const int r = warp * kRows + nb * 8 + 2 * t + e;
+        const float back = KV8 ? 1.f / fv[nb][e] : 1.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)  // column 2 t + e of tile j: the dim that lane g = 2 t + e loaded as its j-th
-          row[KV8 ? (2 * t + e) * 16 + j : (2 * t + e + 8 * (j >> 3)) * 8 + (j & 7)] = o[j][2 * i + e] * back;
-      if (t == 0) {
-        ml[(warp * 16 + g + 8 * i) * 2] = m[i];
-        ml[(warp * 16 + g + 8 * i) * 2 + 1] = l[i];
+        for (int j = 0; j < 8; ++j)  // (the pair of dims whose words made tile j)
+          *reinterpret_cast<float2*>(state + r * kRowF + (KV8 ? 16 * g + 2 * j : (g + 8 * (j >> 2)) * 8 + 2 * (j & 3))) =
+              make_float2(o[nb][j][e] * back, o[nb][j][2 + e] * back);
+        if (g == 0) *reinterpret_cast<float2*>(ml + r * 2) = make_float2(m[nb][e], l[nb][e]);
       }
-    }
     __syncthreads();
-    const int r = tid >> 4, d0 = (tid & 15) * 8;  // this thread's row and dims from here on
-    float top = kNegInfF, sum = 0.f, y[8] = {};
-    auto add = [&](const float4& c0, const float4& c1, float pm, float pl) {  // a state's O, maximum and sum; top: the largest maximum
+    const int r = tid / (128 / kDims), d0 = tid % (128 / kDims) * kDims;  // this thread's row and dims from here on
+    float top = kNegInfF, sum = 0.f, y[kDims] = {};
+    auto add = [&](const float4* c, float pm, float pl) {  // a state's O, maximum and sum; top: the largest maximum
       const float k = pm == kNegInfF ? (pl == 0.f ? 0.f : 1.f) : fast_exp2(pm - top);  // (no maximum: no key, or NaN scores)
       sum += pl * k;
-      if (k != 0.f) {
-        y[0] += c0.x * k, y[1] += c0.y * k, y[2] += c0.z * k, y[3] += c0.w * k;
-        y[4] += c1.x * k, y[5] += c1.y * k, y[6] += c1.z * k, y[7] += c1.w * k;
-      }
+      if (k != 0.f)
+#pragma unroll
+        for (int i = 0; i < kDims; i += 4) {
+          y[i] += c[i / 4].x * k, y[i + 1] += c[i / 4].y * k;
+          y[i + 2] += c[i / 4].z * k, y[i + 3] += c[i / 4].w * k;
+        }
     };
 #pragma unroll
-    for (int w = 0; w < kWarpsF; ++w) top = fmaxf(top, ml[(w * 16 + r) * 2]);
+    for (int w = 0; w < kWarpsF; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
 #pragma unroll
     for (int w = 0; w < kWarpsF; ++w) {
-      const float4* from_o = reinterpret_cast<const float4*>(state + (w * 16 + r) * kRowF + d0);
-      add(from_o[0], from_o[1], ml[(w * 16 + r) * 2], ml[(w * 16 + r) * 2 + 1]);
+      const float2 s = *reinterpret_cast<const float2*>(ml + (w * kRows + r) * 2);
+      add(reinterpret_cast<const float4*>(state + (w * kRows + r) * kRowF + d0), s.x, s.y);
     }
     bool write = true;
     if (sg.u1 - sg.u0 < sg.un.n) {
@@ -530,10 +593,10 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
       const int slot = 2 * blockIdx.x + (sg.u0 == 0 ? 1 : 0);
       const int c0 = owner(sg.item0), c1 = owner(sg.item0 + sg.un.n - 1);
       if (in_bounds(slot < p.slots && c1 < p.slots / 2, p.err)) {
-        float* to = p.part_o + ((long long)slot * 16 + r) * 128 + d0;
-        *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<float4*>(to + 4) = make_float4(y[4], y[5], y[6], y[7]);
-        if ((tid & 15) == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * 16 + r) * 2) = make_float2(top, sum);
+        float* to = p.part_o + ((long long)slot * kRows + r) * 128 + d0;
+#pragma unroll
+        for (int i = 0; i < kDims; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+        if (d0 == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * kRows + r) * 2) = make_float2(top, sum);
       }
       __syncthreads();
       if (tid == 0) {
@@ -544,28 +607,31 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
       __syncthreads();
       write = *last != 0;
       if (write && r < sg.most * G) {  // the last of its CTAs: all states, in order
-        auto slot_of = [&](int c) { return (long long)(2 * c + (c == c0 ? 1 : 0)) * 16 + r; };
+        auto slot_of = [&](int c) { return (long long)(2 * c + (c == c0 ? 1 : 0)) * kRows + r; };
         top = kNegInfF;
         sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = 0.f;
+        for (int i = 0; i < kDims; ++i) y[i] = 0.f;
 #pragma unroll 8
         for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(p.part_ml + slot_of(c) * 2));
-#pragma unroll 4
+#pragma unroll 8
         for (int c = c0; c <= c1; ++c) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot_of(c) * 2));
-          const float4* from_o = reinterpret_cast<const float4*>(p.part_o + slot_of(c) * 128 + d0);
-          add(__ldcg(from_o), __ldcg(from_o + 1), v.x, v.y);
+          const float2 s = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot_of(c) * 2));
+          float4 part[kDims / 4];
+#pragma unroll
+          for (int i = 0; i < kDims / 4; ++i) part[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot_of(c) * 128 + d0) + i);
+          add(part, s.x, s.y);
         }
       }
     }
     if (write && r < sg.most * G) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       __nv_bfloat16* to = p.out + (long long)(sg.q0 + sg.pos0 + r / G) * p.o_st + (long long)(sg.kvh * G + r % G) * p.o_sh + d0;
-      uint4 v = make_uint4(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv), pack_bf16x2(y[4] * inv, y[5] * inv),
-                           pack_bf16x2(y[6] * inv, y[7] * inv));
-      if (sum == 0.f) v = make_uint4(0, 0, 0, 0);
-      if (in_bounds(to >= p.out && to + 8 <= p.out + p.out_span, p.err)) *reinterpret_cast<uint4*>(to) = v;
+      if (in_bounds(to >= p.out && to + kDims <= p.out + p.out_span, p.err))
+#pragma unroll
+        for (int i = 0; i < kDims; i += 4)
+          *reinterpret_cast<uint2*>(to + i) =
+              sum == 0.f ? make_uint2(0, 0) : make_uint2(pack_bf16x2(y[i] * inv, y[i + 1] * inv), pack_bf16x2(y[i + 2] * inv, y[i + 3] * inv));
     }
     if (f >= f1) break;
   }
@@ -573,7 +639,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
     mbar_wait_bounded(bars + (used & 1) * 8, used >> 1 & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
 }
 
-template <bool KV8>
+template <bool KV8, int NB>
 cudaError_t launch_few(const FewParams& p, int grid, bool pdl, cudaStream_t stream) {
   static int configured[64] = {0};  // the shared-memory opt-in, once per device
   int dev = 0;
@@ -581,7 +647,7 @@ cudaError_t launch_few(const FewParams& p, int grid, bool pdl, cudaStream_t stre
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(chunk_few_kernel<KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemF);
+    e = cudaFuncSetAttribute(chunk_few_kernel<KV8, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemF);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
@@ -595,13 +661,14 @@ cudaError_t launch_few(const FewParams& p, int grid, bool pdl, cudaStream_t stre
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, chunk_few_kernel<KV8>, p);
+  return cudaLaunchKernelEx(&cfg, chunk_few_kernel<KV8, NB>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, bool pdl, cudaStream_t stream) {
-  return kv8 ? launch_few<true>(p, grid, pdl, stream) : launch_few<false>(p, grid, pdl, stream);
+cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, int rows, bool pdl, cudaStream_t stream) {
+  if (rows == 8) return kv8 ? launch_few<true, 1>(p, grid, pdl, stream) : launch_few<false, 1>(p, grid, pdl, stream);
+  return kv8 ? launch_few<true, 2>(p, grid, pdl, stream) : launch_few<false, 2>(p, grid, pdl, stream);
 }
 
 }  // namespace da

@@ -291,10 +291,10 @@ struct FewParams {
   long long bt_stride;
   int* err;
   int* counters;                     // a CTA each, zero between calls
-  float *part_o, *part_ml;           // [2 * CTAs][16][128], [2 * CTAs][16][2]: states of items that lie in several CTAs
+  float *part_o, *part_ml;           // [2 * CTAs][rows][128], [2 * CTAs][rows][2]: states of items that lie in several CTAs
   int slots;                         // 2 * CTAs
   int B, Hkv, G, Tq, cap;
-  int npos;                          // query positions of an item, floor(16 / G)
+  int npos;                          // query positions of an item, floor(rows / G)
   int num_blocks, block_shift, window, sinks;
   float scale_log2;
   int least;                         // units that a CTA takes at least
@@ -302,7 +302,8 @@ struct FewParams {
   long long q_span, out_span, table_span;
 };
 constexpr int kFewRows = 16, kFewKeys16 = 16, kFewKeys8 = 32;
-cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, bool pdl, cudaStream_t stream);
+// rows: of an item, 8 or 16
+cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, int rows, bool pdl, cudaStream_t stream);
 
 // ------------------------------------------------ paged cache: writing and reading
 struct CacheParams {
