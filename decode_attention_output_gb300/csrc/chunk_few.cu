@@ -87,73 +87,37 @@ __device__ __forceinline__ float power_of_2(int e) { return __int_as_float((min(
 // floor(log2 x) of a positive float (subnormal ones: -127)
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 0xffu) - 127; }
 
+// A sequence: its rows of q, its tokens, the first key of its first query's window.
+struct Seq {
+  int q0, lq, lk, lo;
+};
+__device__ __forceinline__ Seq sequence(const FewParams& p, int b) {
+  Seq s;
+  s.q0 = min(max(__ldg(p.cu + b), 0), p.Tq);
+  s.lq = min(max(__ldg(p.cu + b + 1), s.q0), p.Tq) - s.q0;
+  s.lk = min(max(__ldg(p.lens + b), 0), p.cap);
+  s.lo = max(0, s.lk - s.lq - p.window + 1);
+  return s;
+}
+
+// The items, or parts of them, of worker `me` of `workers`. ALONE: a worker is a warp and takes items as a whole; else it is a
+// CTA, whose warps take every eighth unit of an item.
 // NB: blocks of eight rows of an item
-template <bool KV8, int NB>
-__global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_constant__ FewParams p) {
+template <bool KV8, int NB, bool ALONE>
+__device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, const uint8_t* smem_raw, int workers, int me) {
   constexpr int kKeys = KV8 ? kFewKeys8 : kFewKeys16, kKT = kKeys / 16;  // keys of a unit, in tiles of 16
   constexpr int kRows = 8 * NB, kDims = kRows / 2;  // rows of an item; dims of a thread where states are joined (256 threads)
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  long long* prefix = reinterpret_cast<long long*>(smem + kOffPrefix);
+  const long long* prefix = reinterpret_cast<const long long*>(smem + kOffPrefix);
   float* state = reinterpret_cast<float*>(smem + kOffState);
   float* ml = reinterpret_cast<float*>(smem + kOffMl);
   int* last = reinterpret_cast<int*>(smem + kOffLast);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int G = p.G, npos = p.npos;
-  if (lane == 0) {
-    for (int i = 0; i < kStagesF; ++i) mbar_init(smem_u32(smem + kOffBarsF) + (warp * kStagesF + i) * 8, 1);
-    fence_barrier_init();
-    if (warp == 0) {
-      prefetch_tensormap(&p.tm_k);
-      prefetch_tensormap(&p.tm_v);
-      if (KV8) prefetch_tensormap(&p.tm_scales);
-    }
-  }
-  pdl_wait_primary();
-
-  // A sequence: its rows of q, its tokens, the first key of its first query's window.
-  struct Seq {
-    int q0, lq, lk, lo;
-  };
-  auto sequence = [&](int b) {
-    Seq s;
-    s.q0 = min(max(__ldg(p.cu + b), 0), p.Tq);
-    s.lq = min(max(__ldg(p.cu + b + 1), s.q0), p.Tq) - s.q0;
-    s.lk = min(max(__ldg(p.lens + b), 0), p.cap);
-    s.lo = max(0, s.lk - s.lq - p.window + 1);
-    return s;
-  };
-  if (tid == 0) *last = 0;
-  __syncthreads();
-  for (int b = tid; b < p.B; b += kThreadsF) {
-    const Seq s = sequence(b);
-    const int n = units_of<kKeys>(s.lo, s.lk, p.sinks).n;
-    prefix[b + 1] = (long long)((s.lq + npos - 1) / npos) * p.Hkv * n;
-    if (s.lq > 0) atomicMax(last, n);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    long long base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      long long v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += o;
-      }
-      if (b0 + lane < p.B) prefix[b0 + lane + 1] = base + v;
-      base += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) prefix[0] = 0;
-  }
-  __syncthreads();
   const long long total = prefix[p.B];
-  // As many CTAs take part as leave each 256 keys, and the longest item in 48 parts at most: one CTA joins them
-  const int ctas = (int)min((long long)gridDim.x, max(total / max(p.least, *last / kMostParts), 1ll));
-  if ((int)blockIdx.x >= ctas) return;
-  auto begin_of = [&](int c) { return total * c / ctas; };
-  auto owner = [&](long long f) { return (int)(((f + 1) * ctas - 1) / total); };
-  const long long f1 = begin_of(blockIdx.x + 1);
+  const int first = ALONE ? 0 : warp;             // this warp's units of a segment
+  constexpr int step = ALONE ? 1 : kWarpsF;
+  auto begin_of = [&](int c) { return total * c / workers; };
+  auto owner = [&](long long f) { return (int)(((f + 1) * workers - 1) / total); };
 
   // ---------------------------------------------------------------- a segment: an item's units in this CTA
   struct Segment {
@@ -161,18 +125,19 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
     long long item0;  // the item's first unit
     Units un;
   };
+  long long f1 = begin_of(me + 1);
   auto segment = [&](long long f) {
     Segment s;
     s.b = 0;
     for (int step = 512; step > 0; step >>= 1)  // the last b with prefix[b] <= f: B <= 1024
       if (s.b + step < p.B && prefix[s.b + step] <= f) s.b += step;
-    const Seq sq = sequence(s.b);
+    const Seq sq = sequence(p, s.b);
     s.un = units_of<kKeys>(sq.lo, sq.lk, p.sinks);
     const long long within = f - prefix[s.b], item = within / s.un.n;
     const int rg = (int)(item / p.Hkv);
     s.kvh = (int)(item - (long long)rg * p.Hkv);
     s.u0 = (int)(within - item * s.un.n);
-    s.u1 = (int)min((long long)s.un.n, s.u0 + (f1 - f));
+    s.u1 = ALONE ? s.un.n : (int)min((long long)s.un.n, s.u0 + (f1 - f));
     s.item0 = f - s.u0;
     s.q0 = sq.q0;
     s.lk = sq.lk;
@@ -202,18 +167,18 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
     ld.un = s.un;
     ld.b = s.b;
     ld.kvh = s.kvh;
-    ld.u = s.u0 + warp;
+    ld.u = s.u0 + first;
     ld.u1 = s.u1;
     ld.end = s.end;
     ld.low = s.low;
-    ids_at = -32 * kWarpsF;
+    ids_at = -1;
   };
   auto load_unit = [&] {
     while (ld.u >= ld.u1 && ld.next < f1) begin_loads(ld.next);
     if (ld.u >= ld.u1) return;  // nothing is left
-    if (ids_at < 0 || (ld.u - ids_at) / kWarpsF == 32) {
+    if (ids_at < 0 || (ld.u - ids_at) / step == 32) {
       ids_at = ld.u;
-      const int u = ids_at + lane * kWarpsF, key = ld.un.at(u) * kKeys;
+      const int u = ids_at + lane * step, key = ld.un.at(u) * kKeys;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int k0 = key + i * (kKeys / 2), k1 = k0 + kKeys / 2 - 1;
@@ -225,7 +190,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
         if ((unsigned)ids[i] >= (unsigned)p.num_blocks) ids[i] = p.num_blocks;
       }
     }
-    const int src = (ld.u - ids_at) / kWarpsF, key0 = ld.un.at(ld.u) * kKeys, row = key0 & ((1 << p.block_shift) - 1);
+    const int src = (ld.u - ids_at) / step, key0 = ld.un.at(ld.u) * kKeys, row = key0 & ((1 << p.block_shift) - 1);
     const int id0 = __shfl_sync(0xffffffffu, ids[0], src), id1 = __shfl_sync(0xffffffffu, ids[1], src);
     // A copy of the unit, or one of each half where a block holds no more. (Where one half only is seen, the copy of both
     // brings the block's other rows too; they are masked.)
@@ -235,10 +200,10 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
     __syncwarp();  // the stage has been read
     if (lane == 0 && sm_ok(to, kUnitBytes) && sm_ok(sc, kScalesF) && in_bounds(ld.kvh < p.Hkv, p.err)) {
       mbar_arrive_expect_tx(bar, kUnitBytes + (KV8 ? kScalesF : 0));
-      const int first = split ? id0 : min(id0, id1);
-      tma_load_5d(to, &p.tm_k, bar, 0, row, 0, ld.kvh, first);
-      tma_load_5d(to + kHalfUnit, &p.tm_v, bar, 0, row, 0, ld.kvh, first);
-      if (KV8) tma_load_4d(sc, &p.tm_scales, bar, row, 0, ld.kvh, first);
+      const int blk = split ? id0 : min(id0, id1);
+      tma_load_5d(to, &p.tm_k, bar, 0, row, 0, ld.kvh, blk);
+      tma_load_5d(to + kHalfUnit, &p.tm_v, bar, 0, row, 0, ld.kvh, blk);
+      if (KV8) tma_load_4d(sc, &p.tm_scales, bar, row, 0, ld.kvh, blk);
       if (split) {
         const int row1 = (key0 + kKeys / 2) & ((1 << p.block_shift) - 1);
         tma_load_5d(to + kHalfUnit / 2, &p.tm_k, bar, 0, row1, 0, ld.kvh, id1);
@@ -248,10 +213,19 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
     }
     __syncwarp();
     ++loaded;
-    ld.u += kWarpsF;
+    ld.u += step;
   };
 
-  long long f = begin_of(blockIdx.x);
+  long long f = begin_of(me);
+  if (ALONE) {  // items as a whole: those that begin in this warp's share
+    auto next_item = [&](long long x) {
+      if (x >= total) return total;
+      const Segment s = segment(x);
+      return s.u0 == 0 ? x : s.item0 + s.un.n;
+    };
+    f = next_item(f);
+    f1 = next_item(f1);
+  }
   if (f >= f1) return;
   // Addresses in a stage. K: key g of every eight, pieces t and t + 4 of 128 bytes, in the order that gives two keys' lanes
   // different banks. V: keys 2 t and 2 t + 1, piece g. Scales: a copy's K scales, then its V scales.
@@ -337,7 +311,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
       }
     }
     const int all_before = min(sg.lk, sg.pos0 + sg.shift + 1), all_from = sg.pos0 + sg.most - 1 + sg.shift - p.window + 1;
-    for (int u = sg.u0 + warp; u < sg.u1 && alive; u += kWarpsF) {
+    for (int u = sg.u0 + first; u < sg.u1 && alive; u += step) {
       const int st = used & 1;
       alive = mbar_wait_bounded(bars + st * 8, used >> 1 & 1, p.err, kErrWaitFull, nullptr);
       alive = __all_sync(0xffffffffu, alive);
@@ -553,6 +527,28 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
         l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], 8);
         l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], 16);
       }
+    if (ALONE) {  // (the pairs of dims of a piece are neighbours)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = nb * 8 + 2 * t + e;
+          const float inv = l[nb][e] == 0.f ? 0.f : 1.f / l[nb][e], back = KV8 ? 1.f / fv[nb][e] : 1.f;
+          __nv_bfloat16* to = p.out + (long long)(sg.q0 + sg.pos0 + r / G) * p.o_st + (long long)(sg.kvh * G + r % G) * p.o_sh;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = l[nb][e] == 0.f ? 0u : pack_bf16x2(o[nb][h * 4 + q][e] * back * inv, o[nb][h * 4 + q][2 + e] * back * inv);
+            __nv_bfloat16* at = to + (KV8 ? 16 * g + 8 * h : (g + 8 * h) * 8);
+            if (r < sg.most * G && in_bounds(at >= p.out && at + 8 <= p.out + p.out_span, p.err))
+              *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      if (f >= f1) break;
+      continue;
+    }
     __syncthreads();  // the last segment's have been read
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -637,6 +633,65 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
   }
   for (; used < loaded; ++used)  // (a wait has run out: what is still on its way must not land behind the CTA's end)
     mbar_wait_bounded(bars + (used & 1) * 8, used >> 1 & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
+}
+
+template <bool KV8, int NB>
+__global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_constant__ FewParams p) {
+  constexpr int kKeys = KV8 ? kFewKeys8 : kFewKeys16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  long long* prefix = reinterpret_cast<long long*>(smem + kOffPrefix);
+  int* last = reinterpret_cast<int*>(smem + kOffLast);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, npos = p.npos;
+  if (lane == 0) {
+    for (int i = 0; i < kStagesF; ++i) mbar_init(smem_u32(smem + kOffBarsF) + (warp * kStagesF + i) * 8, 1);
+    fence_barrier_init();
+    if (warp == 0) {
+      prefetch_tensormap(&p.tm_k);
+      prefetch_tensormap(&p.tm_v);
+      if (KV8) prefetch_tensormap(&p.tm_scales);
+    }
+  }
+  pdl_wait_primary();
+
+  if (tid == 0) last[0] = last[1] = 0;
+  __syncthreads();
+  for (int b = tid; b < p.B; b += kThreadsF) {
+    const Seq s = sequence(p, b);
+    const int n = units_of<kKeys>(s.lo, s.lk, p.sinks).n;
+    prefix[b + 1] = (long long)((s.lq + npos - 1) / npos) * p.Hkv * n;
+    if (s.lq > 0) {
+      atomicMax(last, n);
+      atomicAdd(last + 1, (s.lq + npos - 1) / npos * p.Hkv);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      long long v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += o;
+      }
+      if (b0 + lane < p.B) prefix[b0 + lane + 1] = base + v;
+      base += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) prefix[0] = 0;
+  }
+  __syncthreads();
+  const long long total = prefix[p.B];
+  const int longest = last[0];
+  // As many CTAs take part as leave each 256 keys, and the longest item in 48 parts at most: one CTA joins them
+  int workers = (int)min((long long)gridDim.x, max(total / max(p.least, longest / kMostParts), 1ll));
+  // Many short items: a warp each, from its first unit to its last, and nothing to join. In units a warp, that takes the
+  // longer of its share and an item, and one more in part; items shared by a CTA's warps cost the time of two units
+  // each on top. (256 sequences of 100 tokens, 8 KV heads: 86 us by CTAs.)
+  const long long share = total / (workers * kWarpsF);
+  const bool alone = max(share, (long long)longest) + longest / 2 < share + 2ll * (last[1] / workers + 1);
+  if (alone) run_items<KV8, NB, true>(p, smem, smem_raw, gridDim.x * kWarpsF, warp * gridDim.x + blockIdx.x);
+  else if ((int)blockIdx.x < workers) run_items<KV8, NB, false>(p, smem, smem_raw, workers, blockIdx.x);
 }
 
 template <bool KV8, int NB>

@@ -316,6 +316,92 @@ def test_many_sequences():
 
 
 @pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("G,lq,window,sinks", [(1, 1, 0, 0), (4, 2, 40, 3), (8, 1, 0, 0), (4, 4, 0, 0), (16, 1, 70, 1), (3, 5, 0, 0)], ids=str)
+def test_many_short_items(G, lq, window, sinks, kv8):
+    """Hundreds of sequences of up to 170 keys with 8 KV heads, none and one among them."""
+    g = torch.Generator().manual_seed(81)
+    lk = torch.randint(0, 171, (260,), generator=g).tolist()
+    n = [min(lq, x) if i % 7 else lq for i, x in enumerate(lk)]  # some with more queries than keys
+    n[5] = 0
+    cache = Cache(g, lk, 8, 16, kv8)
+    c = cu(n, first=2)
+    q = torch.randn((c[-1] + 2, 8 * G, 128), generator=g).to(torch.bfloat16)
+    kp, vp, sc = cache.on()
+    out = canvas(q)
+    da.decode_attn_chunk(q.to(DEV), kp, vp, sc, cache.table.to(torch.int32).to(DEV), i32(c), i32(lk), out, SCALE, window, sinks)
+    ref, tol, have = attend_ref(q, *cache.tokens, c, SCALE, window, sinks)
+    check(out, ref, tol, have, "short")
+
+
+def v_scales_case(kind, bs, lk, Hkv, g):
+    """Codes and scales of a cache whose V scales differ from token to token by far more than f16 holds."""
+    nb = -(-lk // bs) + 2
+    codes = [torch.randint(0, 256, (nb, Hkv, bs, 128), generator=g, dtype=torch.uint8) for _ in range(2)]
+    for x in codes:
+        x[(x & 0x7F) == 0x7F] = 0x38  # no NaN
+    scales = torch.exp2(torch.randint(-9, -3, (nb, Hkv, 2, bs), generator=g).float())
+    if kind == "spread":
+        scales[:, :, 1] = torch.exp2(torch.randint(-60, 40, (nb, Hkv, bs), generator=g).float())
+    elif kind == "zero_rows":  # zeros as decode_attn_cache_write leaves them, with a scale of 1, among small values
+        zero = torch.rand((nb, Hkv, bs), generator=g) < 0.5
+        zero[0] = True
+        scales[:, :, 1] = torch.where(zero, 1.0, torch.exp2(torch.randint(-45, -40, (nb, Hkv, bs), generator=g).float()))
+        codes[1][zero] = 0
+    elif kind == "rising":  # larger and larger
+        at = torch.arange(nb * bs).view(nb, 1, bs).expand(-1, Hkv, -1)
+        scales[:, :, 1] = torch.exp2((at % 100).float() - 50)
+    elif kind == "falling_behind_growing_scores":
+        at = torch.arange(nb * bs).view(nb, 1, bs).expand(-1, Hkv, -1)
+        scales[:, :, 1] = torch.exp2(20 - (at // 8 % 60).float())
+        scales[:, :, 0] = torch.exp2((at * 6 / (nb * bs)).floor() - 8)
+    return codes, scales
+
+
+@pytest.mark.parametrize("kind", ["spread", "zero_rows", "rising", "falling_behind_growing_scores"])
+@pytest.mark.parametrize("lq", [1, 4, 90])
+def test_v_scales_of_every_size(kind, lq):
+    """f16 weights are off by at most 2^-25 of the largest weight times V scale of the row's keys whose V is not all zero (and
+    bf16 ones, where there are many rows, by 2^-8 of themselves)."""
+    g = torch.Generator().manual_seed(82)
+    bs, lk, Hkv, G = 16, 700, 2, 4
+    codes, scales = v_scales_case(kind, bs, lk, Hkv, g)
+    q = torch.randn((lq, Hkv * G, 128), generator=g).to(torch.bfloat16)
+    t = torch.arange(codes[0].shape[0])[None].to(torch.int32)
+    out = canvas(q)
+    pools = [x.to(DEV).view(torch.float8_e4m3fn) for x in codes]
+    da.decode_attn_chunk(q.to(DEV), *pools, scales.to(DEV), t.to(DEV), i32([0, lq]), i32([lk]), out, SCALE)
+    flat = [x.view(torch.float8_e4m3fn).float().transpose(1, 2).reshape(-1, Hkv, 128)[:lk].to(F64) for x in codes]
+    sc = scales.permute(0, 3, 1, 2).reshape(-1, Hkv, 2)[:lk].to(F64)
+    k, v = flat[0] * sc[..., :1], flat[1] * sc[..., 1:]
+    ref, tol, have = attend_ref(q, [k], [v], [0, lq], SCALE)
+    for h in range(Hkv * G):  # the floor of the f16 weights
+        j = h // G
+        x = q[:, h].to(F64) @ k[:, j].T * SCALE
+        x = x.masked_fill(torch.arange(lk)[None] > torch.arange(lq)[:, None] + lk - lq, -math.inf)
+        p = torch.softmax(x, -1)
+        some = (flat[1][:, j] != 0).any(-1)
+        r = (p * torch.where(some, sc[:, j, 1], 0.0)).amax(-1, keepdim=True)
+        tol[:, h] += 2.0 ** -25 * r * flat[1][:, j].abs().sum(0)[None]
+    check(out, ref, tol, have, kind)
+
+
+@pytest.mark.parametrize("power", [-120, -40, 40, 110])
+def test_queries_of_every_size(power):
+    """Rows of q around 2^power (f16 holds 2^-24 to 2^16), the scale making up for it; values in a row far apart."""
+    g = torch.Generator().manual_seed(83)
+    lk, Hkv, G = 300, 2, 4
+    cache = Cache(g, [lk], Hkv, 16, True)
+    q = torch.randn((2, Hkv * G, 128), generator=g) * torch.exp2(torch.randint(-12, 1, (2, Hkv * G, 128), generator=g).float())
+    q = (q.double() * 2.0 ** power).to(torch.bfloat16)
+    scale = SCALE * 2.0 ** -power
+    kp, vp, sc = cache.on()
+    out = canvas(q)
+    da.decode_attn_chunk(q.to(DEV), kp, vp, sc, cache.table.to(torch.int32).to(DEV), i32([0, 2]), i32([lk]), out, scale)
+    ref, tol, have = attend_ref(q, *cache.tokens, [0, 2], scale)
+    check(out, ref, tol, have, "sizes")
+
+
+@pytest.mark.parametrize("kv8", [False, True])
 def test_captured_on_a_stream(kv8):
     """A step captured once and replayed with other queries and lengths on a stream of its own, an eager call between."""
     g = torch.Generator().manual_seed(79)
