@@ -31,7 +31,7 @@ LIB_NAME = "libdecode_attn.so"
 CHECKED_NAME = "libdecode_attn_checked.so"
 CHECKED_FLAGS = ["-DDA_BOUNDS_CHECK"]
 SOURCES = ["api.cu", "attn_decode.cu", "attn_decode_d256.cu", "attn_decode_paged.cu", "attn_decode_fp8.cu",
-           "attn_decode_paged_fp8.cu", "kv_cache.cu", "rope.cu", "prefill.cu", "prefill_paged.cu", "chunk_few.cu",
+           "attn_decode_paged_fp8.cu", "kv_cache.cu", "rope.cu", "prefill.cu", "prefill_paged.cu", "chunk_few.cu", "chunk_gather.cu",
            "oproj_gemv.cu", "oproj_umma.cu", "oproj_onchip.cu"]
 DISPATCH_SOURCE, DISPATCH_NAME = "dispatch.cpp", "_da_dispatch.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

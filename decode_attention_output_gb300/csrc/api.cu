@@ -1079,12 +1079,12 @@ int check_window(float scale, int window, int sinks) {
   return window < 0 || sinks < 0 ? DA_ERR_UNSUPPORTED : DA_OK;
 }
 
-enum PrefillOver { kPrompt, kPromptWindow, kChunk16, kChunk8 };
+enum PrefillOver { kPrompt, kPromptWindow, kChunkPages, kChunkGathered };
 
 // The attention of packed queries after its checks: p holds the keys (cu_q, cu_k, Tk, maps, pages); `longest`: keys of
-// a sequence at most, as far as the host knows.
+// a sequence at most, as far as the host knows. gather: over tokens that it lays out first, in the workspace (kv8: of codes).
 int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const da_tensor_t* out, int64_t B, int64_t Hkv,
-                int64_t longest, float scale, int window, int sinks, void* stream) {
+                int64_t longest, float scale, int window, int sinks, void* stream, GatherParams* gather = nullptr, bool kv8 = false) {
   const int64_t Tq = q->shape[0], Hq = q->shape[1];
   p.G = (int)(Hq / Hkv);
   p.npos = 128 / p.G;
@@ -1105,10 +1105,24 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
   const size_t rows = p.parts > 1 ? (size_t)p.parts * Tq * Hq : 0, ml_bytes = align_up(rows * 2 * 4, 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = nullptr;
-  DA_TRY(workspace_get(ml_bytes + rows * 128 * 4, st, &ws));
+  const size_t part_bytes = align_up(ml_bytes + rows * 128 * 4, 256), laid = gather ? (size_t)B * Hkv * gather->rows * 128 : 0;
+  DA_TRY(workspace_get(part_bytes + 2 * laid * 2, st, &ws));
   p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
   p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
   p.err = reinterpret_cast<int*>(ws + kErrOff);
+  if (gather) {
+    gather->k_out = reinterpret_cast<__nv_bfloat16*>(ws + kHeaderBytes + part_bytes);
+    gather->v_out = gather->k_out + laid;
+    gather->span = (long long)laid;
+    gather->err = p.err;
+    gather->window = p.window;
+    gather->sinks = p.sinks;
+    p.gather_rows = gather->rows;
+    da_tensor_t rows_of = {gather->k_out, DA_DTYPE_BF16, 3, {(int64_t)(laid / 128), 1, 128, 0}, {128, 128, 1, 0}};
+    DA_TRY(encode_packed_map(&p.tm_k, &rows_of, 128, 0));
+    rows_of.data = gather->v_out;
+    DA_TRY(encode_packed_map(&p.tm_v, &rows_of, 128, 0));
+  }
   p.out = static_cast<__nv_bfloat16*>(out->data);
   p.o_st = out->stride[0];
   p.o_sh = out->stride[1];
@@ -1123,10 +1137,88 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
   if (p.scale_log2 == 0.f) p.scale_log2 = 0x1p-149f;
   const int grid = (int)items * p.parts;
   const bool pdl = options_snapshot().attn_pdl != 0;
+  if (gather && launch_gather(*gather, (int)B, kv8, pdl, st) != cudaSuccess) return DA_ERR_CUDA;
   const cudaError_t e = over == kPrompt         ? launch_prefill(p, grid, pdl, st)
                         : over == kPromptWindow ? launch_prefill_window(p, grid, pdl, st)
-                                                : launch_prefill_paged(p, grid, over == kChunk8, pdl, st);
+                                                : launch_prefill_paged(p, grid, over == kChunkGathered, pdl, st);
   return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+// decode_attn_chunk after its checks where a sequence has many rows: over the blocks as they are, or (gathered) over their tokens laid
+// out in the workspace, kGatherBytes at a time at most (of a table's whole capacity, as the lengths are on the device): all
+// heads of some sequences, or some heads of one.
+constexpr int kRowsDirect = 16, kRowsGathered = 48;
+constexpr int64_t kGatherBytes = (int64_t)1 << 30;
+int run_chunk(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
+              const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, bool gathered,
+              void* stream) {
+  const bool kv8 = kp->dtype == DA_DTYPE_E4M3;
+  const int64_t B = table->shape[0], MB = table->shape[1], Hkv = kp->shape[1], cap = MB * kp->shape[2], Tq = q->shape[0];
+  PrefillParams p;
+  memset(&p, 0, sizeof(p));
+  p.Tk = (int)cap;
+  p.bt_stride = B > 1 ? table->stride[0] : MB;
+  p.num_blocks = (int)kp->shape[0];
+  while ((1 << p.block_shift) < kp->shape[2]) ++p.block_shift;
+  if (!gathered) {
+    p.cu_q = static_cast<const int*>(cu->data);
+    p.cu_k = static_cast<const int*>(lens->data);
+    p.table = static_cast<const int*>(table->data);
+    p.table_span = (B - 1) * p.bt_stride + MB;
+    p.box_shift = std::min(p.block_shift, 7);
+    const int box = 1 << p.box_shift, dims = box == 128 ? 0 : 1;
+    DA_TRY(encode_kv_map(&p.tm_k, kp, box, dims));
+    DA_TRY(encode_kv_map(&p.tm_v, vp, box, dims));
+    return run_prefill(p, kChunkPages, q, out, B, Hkv, cap, scale, window, sinks, stream);
+  }
+  // tiles that a sequence's queries see at most
+  int64_t tiles = (cap + 127) / 128;
+  if (window) tiles = std::min(tiles, ((int64_t)window + Tq + 127) / 128 + 1 + ((int64_t)sinks + 127) / 128);
+  const int64_t each = tiles * 128 * 2 * 128 * 2, group = Hkv > 0 ? q->shape[1] / Hkv : 1;
+  const int64_t nb = std::max<int64_t>(1, std::min(B, kGatherBytes / (Hkv * each)));
+  const int64_t nh = std::max<int64_t>(1, std::min<int64_t>({Hkv, kGatherBytes / each, 65535}));
+  const int64_t es = kv8 ? 1 : 2;
+  for (int64_t b0 = 0; b0 < B; b0 += nb)
+    for (int64_t h0 = 0; h0 < Hkv; h0 += nh) {
+      const int64_t bn = std::min(nb, B - b0), hn = std::min(nh, Hkv - h0);
+      GatherParams g;
+      memset(&g, 0, sizeof(g));
+      g.kp_sb = kp->stride[0] * es;
+      g.kp_sh = kp->stride[1] * es;
+      g.kp_sr = kp->stride[2] * es;
+      g.vp_sb = vp->stride[0] * es;
+      g.vp_sh = vp->stride[1] * es;
+      g.vp_sr = vp->stride[2] * es;
+      g.k_pages = static_cast<const uint8_t*>(kp->data) + h0 * g.kp_sh;
+      g.v_pages = static_cast<const uint8_t*>(vp->data) + h0 * g.vp_sh;
+      g.kp_span = span_of(kp) * es - h0 * g.kp_sh;
+      g.vp_span = span_of(vp) * es - h0 * g.vp_sh;
+      if (kv8) {
+        g.sc_sb = scales->stride[0];
+        g.sc_sh = scales->stride[1];
+        g.sc_st = scales->stride[2];
+        g.scales = static_cast<const float*>(scales->data) + h0 * g.sc_sh;
+        g.sc_span = span_of(scales) - h0 * g.sc_sh;
+      }
+      g.cu = p.cu_q = static_cast<const int*>(cu->data) + b0;
+      g.lens = p.cu_k = static_cast<const int*>(lens->data) + b0;
+      g.table = static_cast<const int*>(table->data) + b0 * p.bt_stride;
+      g.bt_stride = p.bt_stride;
+      g.table_span = (bn - 1) * p.bt_stride + MB;
+      g.heads = (int)hn;
+      g.rows = (int)(tiles * 128);
+      g.Tq = (int)Tq;
+      g.cap = (int)cap;
+      g.num_blocks = p.num_blocks;
+      g.block_shift = p.block_shift;
+      da_tensor_t qs = *q, os = *out;
+      for (da_tensor_t* t : {&qs, &os}) {
+        t->data = static_cast<__nv_bfloat16*>(t->data) + h0 * group * t->stride[1];
+        t->shape[1] = hn * group;
+      }
+      DA_TRY(run_prefill(p, kChunkGathered, &qs, &os, bn, hn, cap, scale, window, sinks, stream, &g, kv8));
+    }
+  return DA_OK;
 }
 
 // decode_attn_chunk after its checks where a sequence has few rows on average: 8 or 16 at a time.
@@ -1605,25 +1697,12 @@ int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da
     if (reinterpret_cast<uintptr_t>(table->data) % 4 || reinterpret_cast<uintptr_t>(lens->data) % 4) return DA_ERR_ALIGN;
   }
   if (B == 0 || Tq == 0) return DA_OK;
-  // 16 rows a sequence and KV head on average: above, K and V would be read several times
-  if (Tq * (Hq / Hkv) <= kFewRows * B && Hkv <= 4096)
+  // Few rows: K and V are read for every 16 (kRowsDirect: where the alternative reads them by TMA as they are; kRowsGathered:
+  // where it lays them out first)
+  const bool gathered = kv8 || BS < 64;  // (below 64 tokens a block TMA takes eight copies and more a tile)
+  if (Tq * (Hq / Hkv) <= (gathered ? kRowsGathered : kRowsDirect) * B && Hkv <= 4096)
     return run_few(q, kp, vp, kv_scales, table, cu, lens, out, scale, window, sinks, stream);
-  PrefillParams p;
-  memset(&p, 0, sizeof(p));
-  p.cu_q = static_cast<const int*>(cu->data);
-  p.cu_k = static_cast<const int*>(lens->data);
-  p.Tk = (int)(MB * BS);
-  p.table = static_cast<const int*>(table->data);
-  p.bt_stride = B > 1 ? table->stride[0] : MB;
-  p.table_span = (B - 1) * p.bt_stride + MB;
-  p.num_blocks = (int)NB;
-  while ((1 << p.block_shift) < BS) ++p.block_shift;
-  p.box_shift = std::min(p.block_shift, 7);
-  const int box = 1 << p.box_shift, halves = kv8 || box == 128 ? 0 : 1;
-  DA_TRY(encode_kv_map(&p.tm_k, kp, box, halves));
-  DA_TRY(encode_kv_map(&p.tm_v, vp, box, halves));
-  if (kv8) DA_TRY(encode_scales_map(&p.tm_scales, kv_scales, box));
-  return run_prefill(p, kv8 ? kChunk8 : kChunk16, q, out, B, Hkv, MB * BS, scale, window, sinks, stream);
+  return run_chunk(q, kp, vp, kv_scales, table, cu, lens, out, scale, window, sinks, gathered, stream);
 }
 
 int decode_attn_cache_write(const da_tensor_t* k, const da_tensor_t* v, const da_tensor_t* cu_seqlens,

@@ -134,8 +134,9 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
     const Seq sq = sequence(p, s.b);
     s.un = units_of<kKeys>(sq.lo, sq.lk, p.sinks);
     const long long within = f - prefix[s.b], item = within / s.un.n;
-    const int rg = (int)(item / p.Hkv);
-    s.kvh = (int)(item - (long long)rg * p.Hkv);
+    const int rgs = (sq.lq + npos - 1) / npos;  // of a KV head one behind the other: their keys are in L2
+    s.kvh = (int)(item / rgs);
+    const int rg = (int)(item - (long long)s.kvh * rgs);
     s.u0 = (int)(within - item * s.un.n);
     s.u1 = ALONE ? s.un.n : (int)min((long long)s.un.n, s.u0 + (f1 - f));
     s.item0 = f - s.u0;

@@ -270,14 +270,30 @@ struct PrefillParams {
   const int* table;
   long long bt_stride, table_span;
   int num_blocks, block_shift, box_shift;
-  CUtensorMap tm_scales;  // e4m3: [num_blocks][Hkv][2][block_size]
+  // ... or rows of bf16 that launch_gather has laid out, tm_k and tm_v as of [B * Hkv * gather_rows][1][128] packed tokens
+  int gather_rows;
 };
 // grid = as many CTAs as there can be work items; those that run take over the others.
 cudaError_t launch_prefill(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream);
 // ... with a window
 cudaError_t launch_prefill_window(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream);
-// ... over a paged cache, bf16 or e4m3
-cudaError_t launch_prefill_paged(const PrefillParams& p, int grid, bool kv8, bool pdl, cudaStream_t stream);
+// ... over a paged bf16 cache, or over its gathered tokens
+cudaError_t launch_prefill_paged(const PrefillParams& p, int grid, bool gathered, bool pdl, cudaStream_t stream);
+
+// The tokens of a paged cache that a chunk's queries see, as rows of bf16 [batch][heads][rows][128].
+struct GatherParams {
+  const uint8_t *k_pages, *v_pages;  // [num_blocks][Hkv][block_size][128] bf16 or e4m3; strides and spans in bytes
+  long long kp_sb, kp_sh, kp_sr, vp_sb, vp_sh, vp_sr, kp_span, vp_span;
+  const float* scales;               // [num_blocks][Hkv][2][block_size] (e4m3); strides in floats
+  long long sc_sb, sc_sh, sc_st, sc_span;
+  const int *cu, *lens, *table;      // [batch + 1], [batch], [batch][max_blocks]
+  long long bt_stride, table_span;
+  __nv_bfloat16 *k_out, *v_out;
+  long long span;                    // elements of each
+  int* err;
+  int heads, rows, Tq, cap, num_blocks, block_shift, window, sinks;
+};
+cudaError_t launch_gather(const GatherParams& p, int batch, bool kv8, bool pdl, cudaStream_t stream);
 
 // ---------------------------------- attention of a few new tokens over a paged cache
 struct FewParams {

@@ -49,14 +49,13 @@ namespace {
 enum KeySource {
   kPackedKeys,  // rows of k and v, laid end to end
   kPages16,     // a paged bf16 cache
-  kPages8       // a paged e4m3 cache with a scale per token and head
+  kGathered     // a paged cache's tokens as a kernel before this one has laid them out (chunk_gather.cu)
 };
 
 constexpr int kN = 128;                         // keys per tile
 constexpr uint32_t kHalf = 128 * 128;           // 128 rows x 64 dims bf16
 constexpr uint32_t kTileP = 2 * kHalf;          // 128 rows x 128 dims
 constexpr int kSoftWarps = 8;                   // four per tile
-constexpr int kWidenWarps = 4;                  // e4m3: codes to bf16
 constexpr float kSlackP = 8.f;                  // log2 units the maximum may lag
 constexpr float kNegInfP = -__builtin_huge_valf();
 
@@ -71,7 +70,7 @@ struct Item {  // in shared memory, as ints
   int ns, skip, lo;
 };
 constexpr int kItems = 4;  // items on their way from the producer
-constexpr int kMaxStagesP = 5, kMaxRaw = 3;
+constexpr int kStagesP = 5;  // K / V ring
 enum Bar {
   kQFull,                          // per tile: queries landed / free
   kQEmpty = kQFull + 2,
@@ -84,32 +83,23 @@ enum Bar {
   kItemFull, kItemEmpty = kItemFull + kItems,
   // A stage holds a K tile and a V tile in turn, for an issuer each, who tests only its own tiles: with one barrier for both
   // the test would also pass while the other's tile before it is still on its way.
-  kKFull = kItemEmpty + kItems, kVFull = kKFull + kMaxStagesP, kKvEmpty = kVFull + kMaxStagesP,
-  kRawFull = kKvEmpty + kMaxStagesP, kRawEmpty = kRawFull + kMaxRaw,  // e4m3: codes and scales landed / widened
-  kBars = kRawEmpty + kMaxRaw
+  kKFull = kItemEmpty + kItems, kVFull = kKFull + kStagesP, kKvEmpty = kVFull + kStagesP,
+  kBars = kKvEmpty + kStagesP
 };
 constexpr uint32_t kTmemP = 128, kTmemO = 256;  // columns: S, P0, P1, O0, O1
-constexpr uint32_t kRawCodes = 128 * 128, kRawBytes = kRawCodes + 2 * 128 * 4;  // codes of a tile; its K and V scales
 
-template <int SRC>
-struct Shape {
-  static constexpr bool kWiden = SRC == kPages8;
-  // K / V ring: five stages of bf16 tiles; behind codes three, which are widened from three of 17 KB
-  static constexpr int kStages = kWiden ? 3 : kMaxStagesP, kRaw = kWiden ? kMaxRaw : 0;
-  // two softmax warpgroups and a third: the producer, the issuers of S and of PV, and a spare warp; a fourth widens codes
-  static constexpr int kThreads = (kSoftWarps + 4 + (kWiden ? kWidenWarps : 0)) * 32;
-  // registers a thread: 168 at launch; the third warpgroup gives 80 of its own to the softmax,
-  // whose threads hold a row of 128 scores (2 * 208 + 88 = 3 * 168; with a fourth 128 at launch, 2 * 192 + 2 * 64 = 4 * 128)
-  static constexpr int kRegsSoft = kWiden ? 192 : 208, kRegsRest = kWiden ? 64 : 88;
-  static constexpr size_t kOffRing = 2 * kTileP;
-  static constexpr size_t kOffRaw = kOffRing + (size_t)kStages * kTileP;
-  static constexpr size_t kOffBars = kOffRaw + (size_t)kRaw * kRawBytes;
-  static constexpr size_t kOffItems = kOffBars + kBars * 8;
-  static constexpr size_t kOffNext = (kOffItems + kItems * sizeof(Item) + 15) & ~(size_t)15;  // answer to the request for the next item
-  static constexpr size_t kOffFlags = kOffNext + 16;
-  static constexpr size_t kSmem = 1024 + kOffFlags + 16;
-  static_assert(kSmem <= kMaxDynSmem, "prefill kernel exceeds 227 KB of shared memory");
-};
+// two softmax warpgroups and a third: the producer, the issuers of S and of PV, and a spare warp
+constexpr int kThreadsP = (kSoftWarps + 4) * 32;
+// registers a thread: 168 at launch; the third warpgroup gives 80 of its own to the softmax,
+// whose threads hold a row of 128 scores (2 * 208 + 88 = 3 * 168)
+constexpr int kRegsSoft = 208, kRegsRest = 88;
+constexpr size_t kOffRing = 2 * kTileP;
+constexpr size_t kOffBars = kOffRing + (size_t)kStagesP * kTileP;
+constexpr size_t kOffItems = kOffBars + kBars * 8;
+constexpr size_t kOffNext = (kOffItems + kItems * sizeof(Item) + 15) & ~(size_t)15;  // answer to the request for the next item
+constexpr size_t kOffFlags = kOffNext + 16;
+constexpr size_t kSmemP = 1024 + kOffFlags + 16;
+static_assert(kSmemP <= kMaxDynSmem, "prefill kernel exceeds 227 KB of shared memory");
 
 // K/V tiles that npos query positions from `first` on need, of Lq and Lk tokens: those up to
 // the last position's last key.
@@ -131,7 +121,6 @@ __device__ __forceinline__ int part_begin(int part, int top, int n) { return (in
 struct Seen {
   int ns, skip, lo;
   __device__ __forceinline__ int count(int end) const { return end <= ns ? end : max(ns, end - skip); }  // of the tiles below `end`
-  __device__ __forceinline__ int tile(int j) const { return j < ns ? j : j + skip; }
 };
 __device__ __forceinline__ Seen seen_tiles(int p0, int lq, int lk, int window, int sinks) {
   Seen w;
@@ -286,112 +275,10 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return *reinterpret_cast<float2*>(&r);
 }
 
-// (x, y) * (a, a)
-__device__ __forceinline__ float2 mul2(float2 x, float a) {
-  unsigned long long r, aa;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(aa) : "f"(a));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<unsigned long long*>(&x)), "l"(aa));
-  return *reinterpret_cast<float2*>(&r);
-}
-// Four codes times their row's scale, as bf16.
-__device__ __forceinline__ uint2 widen4(uint32_t codes, float scale) {
-  uint32_t lo, hi;
-  e4m3x4_to_f16x4(codes, lo, hi);
-  const float2 a = mul2(make_float2(f16lo_to_f32(lo), f16hi_to_f32(lo)), scale), b = mul2(make_float2(f16lo_to_f32(hi), f16hi_to_f32(hi)), scale);
-  return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
-}
-
-__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts_v4(uint32_t addr, uint2 a, uint2 b) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y) : "memory");
-}
-
-// The widening warps' part: K and V tiles in turn, from the ring of codes to the ring of bf16 tiles.
-template <int SRC>
-__device__ __forceinline__ void widen_tiles(const PrefillParams& p, uint8_t* smem, const uint8_t* smem_raw, uint64_t* bars,
-                                            const Item* items, int* flags) {
-  using Sh = Shape<SRC>;
-  constexpr int kStagesP = Sh::kStages, kRaw = Sh::kRaw > 0 ? Sh::kRaw : 1;
-  const int lane = threadIdx.x & 31, at = threadIdx.x - (kSoftWarps + 4) * 32;
-  auto bar = [&](int i) { return smem_u32(bars + i); };
-  // This thread's 16 codes of rows row0, row0 + 16, ... (a row's eight pieces lie swizzled in its 128 bytes, by the row's last
-  // three bits, which its rows share), and their 32 bytes of the bf16 tile: pieces 2 c and 2 c + 1 of the row, of which a half's eight
-  // lie swizzled too. Lanes of the second half write theirs the other way round, so that eight lanes reach every bank at a time.
-  const int row0 = at >> 3, c = at & 7, q = (c & 3) * 2, second = c >> 2;
-  const uint32_t from0 = row0 * 128 + ((c ^ (row0 & 7)) << 4), raw = smem_u32(smem + Sh::kOffRaw) + from0;
-  const uint32_t tile = smem_u32(smem + Sh::kOffRing) + second * kHalf + row0 * 128;
-  const uint32_t piece_a = ((q + second) ^ (row0 & 7)) << 4, piece_b = ((q + 1 - second) ^ (row0 & 7)) << 4;
-  int kv = 0, r = 0, rph = 0, s = 0, sph = 0;
-  for (int n = 0;; ++n) {
-    const int slot = n % kItems;
-    wait_bar(bar(kItemFull + slot), (n / kItems) & 1, p.err, kErrWaitFull, flags);
-    const int j0 = items[slot].j0, top = max(items[slot].end0, items[slot].end1), lk = items[slot].lk, lo = items[slot].lo;
-    const int ns = items[slot].ns, skip = items[slot].skip;
-    const bool none = items[slot].lq < 0 || given_up(flags);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(kItemEmpty + slot));
-    __syncwarp();
-    if (none) break;
-    for (int j = j0; j < top && !given_up(flags); ++j) {
-      const int base = (j < ns ? j : j + skip) * kN;
-      const bool whole = base + kN <= lk && (base >= lo || base + kN <= p.sinks);  // every row is seen by some row of the item
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        wait_bar(bar(kRawFull + r), rph, p.err, kErrWaitFull, flags);
-        wait_bar(bar(kKvEmpty + s), sph ^ 1, p.err, kErrWaitEmpty, flags);
-        const uint32_t from = raw + r * kRawBytes, to = tile + s * kTileP;
-        // a box's K scales, then its V scales
-        const uint32_t scales = raw - from0 + r * kRawBytes + kRawCodes + ((v << p.box_shift) + row0) * 4;
-        if (!smem_in_bounds(smem_u32(smem_raw), to, 7 * 2048 + 128, p.err)) break;
-        uint4 x = lds_v4(from);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int above = i * 16 >> p.box_shift;  // boxes before this row's (a box is 16 rows at least)
-          const float scale = lds_f32(scales + (i * 16 + (above << p.box_shift)) * 4);
-          const uint4 y = second ? make_uint4(x.z, x.w, x.x, x.y) : x;
-          if (i < 7) x = lds_v4(from + (i + 1) * 2048);
-          uint2 a0 = widen4(y.x, scale), a1 = widen4(y.y, scale), b0 = widen4(y.z, scale), b1 = widen4(y.w, scale);
-          if (!whole) {
-            const int key = base + i * 16 + row0;
-            if (!(key < lk && (key >= lo || key < p.sinks))) a0 = a1 = b0 = b1 = make_uint2(0, 0);
-          }
-          sts_v4(to + i * 2048 + piece_a, a0, a1);
-          sts_v4(to + i * 2048 + piece_b, b0, b1);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kRawEmpty + r));
-          mbar_arrive(bar((v ? kVFull : kKFull) + s));
-        }
-        ++kv;
-        if (++r == kRaw) r = 0, rph ^= 1;
-        if (++s == kStagesP) s = 0, sph ^= 1;
-      }
-    }
-  }
-  // every tile read by the MMAs before the CTA may end
-  for (int i = kv > kStagesP ? kv - kStagesP : 0; i < kv; ++i)
-    mbar_wait_bounded(bar(kKvEmpty + i % kStagesP), (i / kStagesP) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
-}
-
 template <int SRC, bool WINDOW>
-__global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
-  using Sh = Shape<SRC>;
-  static_assert(SRC == kPackedKeys || WINDOW, "over pages the window is always looked at");
-  constexpr bool kPaged = SRC != kPackedKeys, kWiden = Sh::kWiden;
-  constexpr int kStagesP = Sh::kStages, kRegsSoft = Sh::kRegsSoft, kRegsRest = Sh::kRegsRest;
-  constexpr size_t kOffRing = Sh::kOffRing, kOffBars = Sh::kOffBars, kOffItems = Sh::kOffItems, kOffNext = Sh::kOffNext,
-                   kOffFlags = Sh::kOffFlags;
+__global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
+  static_assert(SRC == kPackedKeys || WINDOW, "over a cache the window is always looked at");
+  constexpr bool kCached = SRC != kPackedKeys;
   constexpr uint32_t kIdescS = umma_idesc_bf16(128, kN, /*A MN-major*/ false, /*B MN-major*/ false);
   constexpr uint32_t kIdescO = umma_idesc_bf16(128, 128, /*A MN-major*/ false, /*B MN-major*/ true);
   extern __shared__ uint8_t smem_raw[];
@@ -414,15 +301,13 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
     tmem_relinquish();
   } else if (tid == kSoftWarps * 32) {
     prefetch_tensormap(&p.tm_q);
-    if (kPaged || p.Tk > 0) {
+    if (kCached || p.Tk > 0) {
       prefetch_tensormap(&p.tm_k);
       prefetch_tensormap(&p.tm_v);
     }
-    if (kWiden) prefetch_tensormap(&p.tm_scales);
     for (int i = 0; i < kBars; ++i) {
       const bool soft = i == kPFull || i == kPFull + 1 || i == kSFree;  // an arrival per warp of a tile
-      const bool widen = kWiden && ((i >= kKFull && i < kKvEmpty) || i >= kRawEmpty);  // ... or per widening warp
-      mbar_init(bar(i), soft ? 4 : widen ? kWidenWarps : (i >= kItemEmpty && i < kItemEmpty + kItems ? kSoftWarps + 2 + (kWiden ? kWidenWarps : 0) : 1));
+      mbar_init(bar(i), soft ? 4 : (i >= kItemEmpty && i < kItemEmpty + kItems ? kSoftWarps + 2 : 1));
     }
     flags[0] = 0;
     fence_barrier_init();
@@ -460,38 +345,23 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
         ids_next = box_ids(it, group + 1);
         ids_at = group;
       }
-      const int i = kWiden ? lane & 15 : nb > 1 ? lane >> 1 : lane, box = t * nb + i;
+      const int i = nb > 1 ? lane >> 1 : lane, box = t * nb + i;
       int blk = __shfl_sync(0xffffffffu, ids, box & 31);
       const bool mine = i < nb;
       if ((unsigned)blk >= (unsigned)p.num_blocks) {
         if (mine && box_seen(it, box)) atomicOr(p.err, kErrBlockTable);
         blk = p.num_blocks;
       }
-      const int row = (box << p.box_shift) & ((1 << p.block_shift) - 1);
+      const int row = (box << p.box_shift) & ((1 << p.block_shift) - 1), half = nb > 1 ? lane & 1 : 0;
       if (!in_bounds((unsigned)blk <= (unsigned)p.num_blocks && (unsigned)it.kvh < (unsigned)p.Hkv && t >= 0, p.err)) blk = p.num_blocks;
-      if constexpr (kWiden) {
-        const uint32_t raw = smem_u32(smem + Sh::kOffRaw);
-        int s = kv % Sh::kRaw;
-        if (!sm_ok(raw + s * kRawBytes, kRawBytes)) s = 0;
-        mbar_wait_warp(bar(kRawEmpty + s), ((kv / Sh::kRaw) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
-        ++kv;
-        if (lane == 0) mbar_arrive_expect_tx(bar(kRawFull + s), kRawBytes);
-        __syncwarp();
-        const uint32_t to = raw + s * kRawBytes;
-        if (mine && lane < 16) tma_load_5d(to + ((uint32_t)i << p.box_shift) * 128, map, bar(kRawFull + s), 0, row, 0, it.kvh, blk);
-        if (mine && lane >= 16) tma_load_4d(to + kRawCodes + ((uint32_t)i << p.box_shift) * 8, &p.tm_scales, bar(kRawFull + s), row, 0, it.kvh, blk);
-      } else {
-        int s = kv % kStagesP;
-        if (!sm_ok(ring + s * kTileP, kTileP)) s = 0;
-        mbar_wait_warp(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
-        const uint32_t full = bar((kv & 1 ? kVFull : kKFull) + s);
-        ++kv;
-        if (lane == 0) mbar_arrive_expect_tx(full, kTileP);
-        __syncwarp();
-        const int half = nb > 1 ? lane & 1 : 0;
-        if (mine)
-          tma_load_5d(ring + s * kTileP + half * kHalf + ((uint32_t)i << p.box_shift) * 128, map, full, 0, row, half, it.kvh, blk);
-      }
+      int s = kv % kStagesP;
+      if (!sm_ok(ring + s * kTileP, kTileP)) s = 0;
+      mbar_wait_warp(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+      const uint32_t full = bar((kv & 1 ? kVFull : kKFull) + s);
+      ++kv;
+      if (lane == 0) mbar_arrive_expect_tx(full, kTileP);
+      __syncwarp();
+      if (mine) tma_load_5d(ring + s * kTileP + half * kHalf + ((uint32_t)i << p.box_shift) * 128, map, full, 0, row, half, it.kvh, blk);
     };
     auto load_kv = [&](const CUtensorMap* map, int row, int kvh) {
       int s = kv % kStagesP;
@@ -538,7 +408,7 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
         if (b < p.B) {
           q0 = min(max(__ldg(p.cu_q + b), 0), p.Tq);
           q1 = min(max(__ldg(p.cu_q + b + 1), q0), p.Tq);
-          if constexpr (kPaged) {
+          if constexpr (kCached) {
             k1 = min(max(__ldg(p.cu_k + b), 0), p.Tk);  // (the sequences' lengths, and the table's capacity)
           } else {
             k0 = min(max(__ldg(p.cu_k + b), 0), p.Tk);
@@ -558,7 +428,7 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
           it.lq = __shfl_sync(0xffffffffu, q1 - q0, src);
           it.lk = __shfl_sync(0xffffffffu, k1 - k0, src);
           it.q0 = __shfl_sync(0xffffffffu, q0, src);
-          it.k0 = kPaged ? b0 + src : __shfl_sync(0xffffffffu, k0, src);
+          it.k0 = kCached ? b0 + src : __shfl_sync(0xffffffffu, k0, src);
           it.p0 = (__shfl_sync(0xffffffffu, base + end, src) - 1 - mb) * 2 * npos;  // last block first
           break;
         }
@@ -614,12 +484,17 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
       if (lane < 4) tma_prefetch_4d(&p.tm_q, 0, it.kvh * G, it.q0 + it.p0 + (lane >> 1) * npos, lane & 1);
       const int top = max(it.end0, it.end1);
       if (top <= it.j0) ask();
+      const Seen laid = seen_tiles(0, it.lq, it.lk, p.window, p.sinks);  // kGathered: the tiles that lie there
       for (int j = it.j0; j < top && !given_up(flags); ++j) {
         if (j == max(it.j0, top - 3)) ask();  // late, so that no item waits behind a long one
         const int t = WINDOW && j >= it.ns ? j + it.skip : j;
-        if constexpr (kPaged) {
+        if constexpr (SRC == kPages16) {
           load_pages(&p.tm_k, it, t);
           load_pages(&p.tm_v, it, t);
+        } else if constexpr (SRC == kGathered) {
+          const int row = (it.k0 * p.Hkv + it.kvh) * p.gather_rows + laid.count(t) * kN;
+          load_kv(&p.tm_k, row, 0);
+          load_kv(&p.tm_v, row, 0);
         } else {
           load_kv(&p.tm_k, it.k0 + t * kN, it.kvh);
           load_kv(&p.tm_v, it.k0 + t * kN, it.kvh);
@@ -644,9 +519,8 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
     if (given_up(flags))  // with an answer on its way
       mbar_wait_bounded(bar(kNext), asked & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
     // every stage released (all MMAs that read them done, and so every copy) before the CTA may end
-    constexpr int kLoaded = kWiden ? Sh::kRaw : kStagesP, kLoadedEmpty = kWiden ? kRawEmpty : kKvEmpty;
-    for (int i = kv > kLoaded ? kv - kLoaded : 0; i < kv; ++i)
-      mbar_wait_bounded(bar(kLoadedEmpty + i % kLoaded), (i / kLoaded) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
+    for (int i = kv > kStagesP ? kv - kStagesP : 0; i < kv; ++i)
+      mbar_wait_bounded(bar(kKvEmpty + i % kStagesP), (i / kStagesP) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
     for (int w = 0; w < 2; ++w)
       if (qn[w]) mbar_wait_bounded(bar(kQEmpty + w), (qn[w] - 1) & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
   } else if (warp == kSoftWarps + 1 || warp == kSoftWarps + 2) {
@@ -679,8 +553,8 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
         const uint64_t b = kv_desc + (uint64_t)(stage * (kTileP >> 4));
         // A V tile that ends inside another sequence's rows: their weights are 0, but 0 times a
         // NaN or infinity there is not, so those rows are cleared before the MMAs see them. With a window
-        // also those before it (their blocks may be another sequence's by now). (Widened: cleared there.)
-        if constexpr (WINDOW && !kWiden) {
+        // also those before it (their blocks may be another sequence's by now).
+        if constexpr (WINDOW) {
           const int base = (j < ns ? j : j + skip) * kN;
           const int a = min(max(p.sinks - base, 0), kN), c = min(max(lo - base, 0), kN), e = min(max(lk - base, 0), kN);
           if (pv && (c > a || e < kN)) {
@@ -940,12 +814,6 @@ __global__ void __launch_bounds__(Shape<SRC>::kThreads, 1) prefill_kernel(const 
     }
     pv_done();
     if (step > 0) finish(l, m);
-  } else if (kWiden && warp >= kSoftWarps + 4) {
-    // ------------------------------------------------- e4m3: codes to bf16
-    // A thread takes 16 codes of a row at a time: code -> f16 (exact) -> f32, times the row's scale, rounded once to
-    // bf16 (what decode_attn_cache_read gives). Rows that no row of the item sees become zeros.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    widen_tiles<SRC>(p, smem, smem_raw, bars, items, flags);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
   }
@@ -1011,14 +879,14 @@ cudaError_t launch_prefill_as(const PrefillParams& p, int grid, bool pdl, cudaSt
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(prefill_kernel<SRC, WINDOW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<SRC>::kSmem);
+    e = cudaFuncSetAttribute(prefill_kernel<SRC, WINDOW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemP);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(Shape<SRC>::kThreads);
-  cfg.dynamicSmemBytes = Shape<SRC>::kSmem;
+  cfg.blockDim = dim3(kThreadsP);
+  cfg.dynamicSmemBytes = kSmemP;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
