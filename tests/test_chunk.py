@@ -315,6 +315,22 @@ def test_many_sequences():
         check(out, ref, tol, have, "many")
 
 
+@pytest.mark.parametrize("capacity,lq,lk", [(40_000, [70, 1, 0, 33, 90, 60, 64, 65], [900, 1, 300, 33, 2000, 777, 64, 1300]), (300_000, [150], [3000])], ids=str)
+def test_tables_of_large_capacity(capacity, lq, lk):
+    """A table whose capacity's tokens do not fit the workspace's part for them: sequences, or heads, a few at a time."""
+    g = torch.Generator().manual_seed(84)
+    cache = Cache(g, lk, 8, 16, True)
+    wide = torch.full((len(lk), capacity // 16), -1, dtype=torch.int32)
+    wide[:, :cache.table.shape[1]] = cache.table
+    c = cu(lq, first=3)
+    q = torch.randn((c[-1] + 2, 16, 128), generator=g).to(torch.bfloat16)
+    kp, vp, sc = cache.on()
+    out = canvas(q)
+    da.decode_attn_chunk(q.to(DEV), kp, vp, sc, wide.to(DEV), i32(c), i32(lk), out, SCALE)
+    ref, tol, have = attend_ref(q, *cache.tokens, c, SCALE)
+    check(out, ref, tol, have, "parts")
+
+
 @pytest.mark.parametrize("kv8", [False, True])
 @pytest.mark.parametrize("G,lq,window,sinks", [(1, 1, 0, 0), (4, 2, 40, 3), (8, 1, 0, 0), (4, 4, 0, 0), (16, 1, 70, 1), (3, 5, 0, 0)], ids=str)
 def test_many_short_items(G, lq, window, sinks, kv8):
