@@ -24,6 +24,27 @@ namespace {
 
 constexpr int kRopeWarps = 4;
 
+// Two products, two sums, two x * x + c: of what stands in the same place of both.
+__device__ __forceinline__ unsigned long long bits2(float2 x) { return *reinterpret_cast<unsigned long long*>(&x); }
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 square_add2(float2 x, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+// Two products that stay apart from the sum behind them (that of mul.f32x2 and add.f32x2 becomes one multiply-add)
+__device__ __forceinline__ float2 each(float2 x, float2 y) { return make_float2(__fmul_rn(x.x, y.x), __fmul_rn(x.y, y.y)); }
+
 // Four weights of dims `at` .. `at` + 3.
 __device__ __forceinline__ float4 four_weights(const void* w, bool f32, int at) {
   if (f32) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + at));
@@ -46,8 +67,8 @@ __device__ __forceinline__ int e4m3_exponent(unsigned m) {
 
 enum Dest { kPacked, kPages16, kPages8 };  // where keys go
 
-// ROWS: rows of a warp, per lane group that holds one.
-template <int DIM, bool HALVES, int DEST, int ROWS>
+// ROWS: rows of a warp, per lane group that holds one. NORM: there is a weight, of q or of k.
+template <int DIM, bool HALVES, int DEST, int ROWS, bool NORM>
 __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams p) {
   constexpr int kLanes = DIM / 8, kAt = 32 / kLanes;  // lanes of a row; rows at a time
   constexpr int kRows = ROWS * kAt;
@@ -127,13 +148,22 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
   } else {
     turn0 = turn1 = false;
   }
-  const void* weight = is_q ? p.q_weight : is_k ? p.k_weight : nullptr;
+  // A lane's dims as firsts and seconds of its four pairs, two by two: (first, first), (second, second)
+  const float2 cc[2] = {make_float2(c[0], c[1]), make_float2(c[2], c[3])}, ss[2] = {make_float2(s[0], s[1]), make_float2(s[2], s[3])};
+  const float2 minus_ss[2] = {make_float2(-s[0], -s[1]), make_float2(-s[2], -s[3])};
+  auto firsts_of = [&](float2 (&first)[2], float2 (&second)[2], const float4& run0, const float4& run1) {
+    if (HALVES) {
+      first[0] = make_float2(run0.x, run0.y), first[1] = make_float2(run0.z, run0.w);
+      second[0] = make_float2(run1.x, run1.y), second[1] = make_float2(run1.z, run1.w);
+    } else {
+      first[0] = make_float2(run0.x, run0.z), second[0] = make_float2(run0.y, run0.w);
+      first[1] = make_float2(run1.x, run1.z), second[1] = make_float2(run1.y, run1.w);
+    }
+  };
+  const void* weight = !NORM ? nullptr : is_q ? p.q_weight : is_k ? p.k_weight : nullptr;
   const bool w32 = is_q ? p.q_weight_f32 : p.k_weight_f32;
-  float4 w0 = make_float4(1.f, 1.f, 1.f, 1.f), w1 = w0;
-  if (weight) {
-    w0 = four_weights(weight, w32, d0);
-    w1 = four_weights(weight, w32, d1);
-  }
+  float2 w_first[2] = {}, w_second[2] = {};
+  if (weight) firsts_of(w_first, w_second, four_weights(weight, w32, d0), four_weights(weight, w32, d1));
 
   // Where the rows go
   const bool packed = is_q || DEST == kPacked;
@@ -153,41 +183,56 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
     }
   }
 
+  // The rows' reciprocal roots, whose shuffles wait for one another only within a row
+  float root[ROWS];
+  if (NORM && weight) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        q = square_add2(make_float2(bf16lo_to_f32(x[i][k].x), bf16hi_to_f32(x[i][k].x)), q);
+        q = square_add2(make_float2(bf16lo_to_f32(x[i][k].y), bf16hi_to_f32(x[i][k].y)), q);
+      }
+      root[i] = q.x + q.y;
+    }
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1)
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) root[i] += __shfl_xor_sync(0xffffffffu, root[i], off);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) root[i] = rsqrtf(root[i] * (1.f / DIM) + p.eps);
+  }
+
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int h = h0 + i * kAt;
-    if (i > 0 && __all_sync(0xffffffffu, h >= heads)) break;
-    float y[8] = {bf16lo_to_f32(x[i][0].x), bf16hi_to_f32(x[i][0].x), bf16lo_to_f32(x[i][0].y), bf16hi_to_f32(x[i][0].y),
-                  bf16lo_to_f32(x[i][1].x), bf16hi_to_f32(x[i][1].x), bf16lo_to_f32(x[i][1].y), bf16hi_to_f32(x[i][1].y)};
-    if (weight) {
-      float sum = 0.f;
+    float2 first[2], second[2];
+    firsts_of(first, second, make_float4(bf16lo_to_f32(x[i][0].x), bf16hi_to_f32(x[i][0].x), bf16lo_to_f32(x[i][0].y), bf16hi_to_f32(x[i][0].y)),
+              make_float4(bf16lo_to_f32(x[i][1].x), bf16hi_to_f32(x[i][1].x), bf16lo_to_f32(x[i][1].y), bf16hi_to_f32(x[i][1].y)));
+    if (NORM && weight) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = fmaf(y[k], y[k], sum);
-#pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      const float r = rsqrtf(sum * (1.f / DIM) + p.eps);
-      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = y[k] * r * w[k];
+      for (int k = 0; k < 2; ++k) {
+        first[k] = mul2(mul2(first[k], make_float2(root[i], root[i])), w_first[k]);
+        second[k] = mul2(mul2(second[k], make_float2(root[i], root[i])), w_second[k]);
+      }
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (HALVES || k == 0 ? turn0 : turn1) {
+        const float2 a = first[k], b = second[k];
+        first[k] = add2(each(a, cc[k]), each(b, minus_ss[k]));
+        second[k] = add2(each(b, cc[k]), each(a, ss[k]));
+      }
+    }
+    // in the order of the dims again: this lane's first run, then its second
+    float y[8];
     if (HALVES) {
-      if (turn0) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float a = y[k], b = y[k + 4];
-          y[k] = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
-          y[k + 4] = __fadd_rn(__fmul_rn(b, c[k]), __fmul_rn(a, s[k]));
-        }
-      }
+      y[0] = first[0].x, y[1] = first[0].y, y[2] = first[1].x, y[3] = first[1].y;
+      y[4] = second[0].x, y[5] = second[0].y, y[6] = second[1].x, y[7] = second[1].y;
     } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k < 2 ? turn0 : turn1) {
-          const float a = y[2 * k], b = y[2 * k + 1];
-          y[2 * k] = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
-          y[2 * k + 1] = __fadd_rn(__fmul_rn(b, c[k]), __fmul_rn(a, s[k]));
-        }
-      }
+      y[0] = first[0].x, y[1] = second[0].x, y[2] = first[0].y, y[3] = second[0].y;
+      y[4] = first[1].x, y[5] = second[1].x, y[6] = first[1].y, y[7] = second[1].y;
     }
     if (DEST == kPages8 && !is_q) {
       unsigned m = 0;
@@ -237,7 +282,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
   }
 }
 
-template <int DIM, bool HALVES, int DEST>
+template <int DIM, bool HALVES, int DEST, bool NORM>
 cudaError_t launch_rows(RopeParams& p, bool pdl, cudaStream_t stream) {
   constexpr int kAt = 32 / (DIM / 8);
   auto plan = [&](int rows) {
@@ -247,7 +292,8 @@ cudaError_t launch_rows(RopeParams& p, bool pdl, cudaStream_t stream) {
     p.groups = p.q_groups + p.k_groups * (DEST == kPacked ? 1 : 2);
     return (long long)p.T * p.groups;
   };
-  // Four rows of each lane group, or one where that would leave SMs without a warp (a decode step's few tokens)
+  // Four rows of each lane group, or one where that would leave SMs without a warp (a decode step's few tokens). Eight took
+  // registers from other warps: 46.6k tokens into an e4m3 cache 264 us, against 230.
   const bool many = plan(4) >= 4096;
   const long long warps = many ? plan(4) : plan(1), blocks = (warps + kRopeWarps - 1) / kRopeWarps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -261,12 +307,14 @@ cudaError_t launch_rows(RopeParams& p, bool pdl, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = pdl ? 1 : 0;
   const RopeParams& c = p;
-  return many ? cudaLaunchKernelEx(&cfg, rope_kernel<DIM, HALVES, DEST, 4>, c) : cudaLaunchKernelEx(&cfg, rope_kernel<DIM, HALVES, DEST, 1>, c);
+  return many ? cudaLaunchKernelEx(&cfg, rope_kernel<DIM, HALVES, DEST, 4, NORM>, c) : cudaLaunchKernelEx(&cfg, rope_kernel<DIM, HALVES, DEST, 1, NORM>, c);
 }
 
 template <int DIM, int DEST>
 cudaError_t launch_pairs(RopeParams& p, bool halves, bool pdl, cudaStream_t stream) {
-  return halves ? launch_rows<DIM, true, DEST>(p, pdl, stream) : launch_rows<DIM, false, DEST>(p, pdl, stream);
+  if (p.q_weight || p.k_weight)
+    return halves ? launch_rows<DIM, true, DEST, true>(p, pdl, stream) : launch_rows<DIM, false, DEST, true>(p, pdl, stream);
+  return halves ? launch_rows<DIM, true, DEST, false>(p, pdl, stream) : launch_rows<DIM, false, DEST, false>(p, pdl, stream);
 }
 
 }  // namespace
