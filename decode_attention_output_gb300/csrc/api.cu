@@ -236,7 +236,7 @@ int encode_scales_map(CUtensorMap* map, const da_tensor_t* t, int box_tokens) {
 
 // 4-D map over packed tokens [T][H][128] bf16, the dims in two halves of 64 (128-byte rows,
 // 128-byte swizzle). K and V: one box = 128 tokens of a head, both halves ({dim, token, half,
-// head}). Queries (heads_box > 0): one half of box_tokens tokens x heads_box heads, a token's
+// head}); fewer tokens: of one half. Queries (heads_box > 0): one half of box_tokens tokens x heads_box heads, a token's
 // heads in consecutive rows ({dim, head, token, half}).
 int encode_packed_map(CUtensorMap* map, const da_tensor_t* t, int box_tokens, int heads_box) {
   EncodeTiledFn enc = encode_fn();
@@ -245,7 +245,7 @@ int encode_packed_map(CUtensorMap* map, const da_tensor_t* t, int box_tokens, in
   // a stride of an extent-1 dimension is never used; give it a harmless legal value
   const cuuint64_t sh = (cuuint64_t)(H == 1 ? 128 : t->stride[1]) * 2, st = T == 1 ? sh * H : (cuuint64_t)t->stride[0] * 2;
   cuuint64_t dims[4] = {64, T, 2, H}, strides[3] = {st, 128, sh};
-  cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, 2, 1}, estr[4] = {1, 1, 1, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, box_tokens == 128 ? 2u : 1u, 1}, estr[4] = {1, 1, 1, 1};
   if (heads_box > 0) {
     dims[1] = H;
     dims[2] = T;
@@ -1120,8 +1120,10 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
     p.gather_rows = gather->rows;
     da_tensor_t rows_of = {gather->k_out, DA_DTYPE_BF16, 3, {(int64_t)(laid / 128), 1, 128, 0}, {128, 128, 1, 0}};
     DA_TRY(encode_packed_map(&p.tm_k, &rows_of, 128, 0));
+    if (p.sinks) DA_TRY(encode_packed_map(&p.tm_k8, &rows_of, 8, 0));
     rows_of.data = gather->v_out;
     DA_TRY(encode_packed_map(&p.tm_v, &rows_of, 128, 0));
+    if (p.sinks) DA_TRY(encode_packed_map(&p.tm_v8, &rows_of, 8, 0));
   }
   p.out = static_cast<__nv_bfloat16*>(out->data);
   p.o_st = out->stride[0];
@@ -1302,6 +1304,10 @@ int prefill_checked(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_
   if (Tk > 0) {
     DA_TRY(encode_packed_map(&p.tm_k, k, 128, 0));
     DA_TRY(encode_packed_map(&p.tm_v, v, 128, 0));
+    if (window && sinks) {
+      DA_TRY(encode_packed_map(&p.tm_k8, k, 8, 0));
+      DA_TRY(encode_packed_map(&p.tm_v8, v, 8, 0));
+    }
   }
   p.cu_q = static_cast<const int*>(cq->data);
   p.cu_k = static_cast<const int*>(ck->data);

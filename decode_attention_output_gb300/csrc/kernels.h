@@ -266,6 +266,7 @@ struct PrefillParams {
   long long part_rows;  // rows of both (0: no item is cut)
   // A query at position i sees keys i - window + 1 .. i and those below `sinks` (no window: 2^30)
   int window, sinks;
+  CUtensorMap tm_k8, tm_v8;  // with first keys: k and v by boxes of 64 dims x 8 tokens (not over pages)
   // Pages: tm_k and tm_v map [num_blocks][Hkv][block_size][128], a box of 2^box_shift = min(block size, 128) tokens
   const int* table;
   long long bt_stride, table_span;

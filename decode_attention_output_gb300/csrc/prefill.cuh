@@ -66,8 +66,8 @@ struct Item {  // in shared memory, as ints
   int part;                     // of the item (-1: the item is whole)
   // With a window, j0, end0 and end1 count the tiles that some row of the item sees: tile j is the one of
   // keys 128 j .. of the sequence while j < ns, and the one of 128 (j + skip) .. from there on. lo: the
-  // least key in the first row's window.
-  int ns, skip, lo;
+  // least key in the first row's window. merged: so many rows of the first tile, which lie before lo, hold the sequence's first keys.
+  int ns, skip, lo, merged;
 };
 constexpr int kItems = 4;  // items on their way from the producer
 constexpr int kStagesP = 5;  // K / V ring
@@ -117,17 +117,26 @@ __device__ __forceinline__ int item_parts(int top, int parts) {
 }
 __device__ __forceinline__ int part_begin(int part, int top, int n) { return (int)((long long)part * top / n); }
 
-// The tiles that a window and the first `sinks` keys leave of an item whose first position is p0 (see Item).
+// The tiles that a window and the first `sinks` keys leave of an item whose first position is p0 (see Item). MERGE: where the
+// window begins far enough inside its first tile, the first keys (eight at a time, as a copy's swizzle has it) take the rows before it
+// instead of a tile of their own.
 struct Seen {
-  int ns, skip, lo;
+  int ns, skip, lo, merged;
   __device__ __forceinline__ int count(int end) const { return end <= ns ? end : max(ns, end - skip); }  // of the tiles below `end`
 };
+template <bool MERGE>
 __device__ __forceinline__ Seen seen_tiles(int p0, int lq, int lk, int window, int sinks) {
   Seen w;
   w.lo = max(0, p0 + lk - lq - window + 1);
-  const int first = w.lo / kN, ns = (sinks + kN - 1) / kN;
+  const int first = w.lo / kN, ns = (sinks + kN - 1) / kN, rows = (sinks + 7) & ~7;
   w.ns = first > ns ? ns : 0;
   w.skip = first > ns ? first - ns : 0;
+  w.merged = 0;
+  if (MERGE && sinks > 0 && first > 0 && rows <= w.lo % kN) {
+    w.ns = 0;
+    w.skip = first;
+    w.merged = rows;
+  }
   return w;
 }
 // Bits below n of a 32-bit word, 0 <= n <= 32.
@@ -275,10 +284,13 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return *reinterpret_cast<float2*>(&r);
 }
 
+// Rows one behind the other can be loaded eight at a time.
+__host__ __device__ constexpr bool merges(int src, bool window) { return window && src != kPages16; }
+
 template <int SRC, bool WINDOW>
 __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
   static_assert(SRC == kPackedKeys || WINDOW, "over a cache the window is always looked at");
-  constexpr bool kCached = SRC != kPackedKeys;
+  constexpr bool kCached = SRC != kPackedKeys, kMerge = merges(SRC, WINDOW);
   constexpr uint32_t kIdescS = umma_idesc_bf16(128, kN, /*A MN-major*/ false, /*B MN-major*/ false);
   constexpr uint32_t kIdescO = umma_idesc_bf16(128, 128, /*A MN-major*/ false, /*B MN-major*/ true);
   extern __shared__ uint8_t smem_raw[];
@@ -374,6 +386,18 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         tma_load_4d(ring + s * kTileP, map, full, 0, row, 0, kvh);
       }
     };
+    // A tile from `row` on, but its first `merged` rows from `row0` on: eight rows of half the dims a lane.
+    auto load_merged = [&](const CUtensorMap* map, int row0, int merged, int row, int kvh) {
+      int s = kv % kStagesP;
+      if (!sm_ok(ring + s * kTileP, kTileP)) s = 0;
+      mbar_wait_warp(bar(kKvEmpty + s), ((kv / kStagesP) & 1) ^ 1, p.err, kErrWaitEmpty, flags);
+      const uint32_t full = bar((kv & 1 ? kVFull : kKFull) + s);
+      ++kv;
+      if (lane == 0) mbar_arrive_expect_tx(full, kTileP);
+      __syncwarp();
+      const int at = (lane >> 1) * 8;
+      tma_load_4d(ring + s * kTileP + (lane & 1) * kHalf + at * 128, map, full, 0, (at < merged ? row0 : row) + at, lane & 1, kvh);
+    };
     const uint32_t next_smem = smem_u32(smem + kOffNext);
     int x = blockIdx.x, n = 0, asked = 0;
     auto ask = [&] {
@@ -398,7 +422,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       it.kvh = x < 0 ? 0 : xi - mb * p.Hkv;
       it.lq = -1;
       it.lk = it.q0 = it.k0 = it.p0 = it.j0 = it.end0 = it.end1 = 0;
-      it.ns = it.skip = it.lo = 0;
+      it.ns = it.skip = it.lo = it.merged = 0;
       it.clear = it.part = -1;
       if (mb >= total) return it;
       if (mb < base) base = b0 = 0;
@@ -442,10 +466,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       it.end0 = kv_tiles(it.p0, npos, it.lq, it.lk);
       it.end1 = kv_tiles(it.p0 + npos, npos, it.lq, it.lk);
       if constexpr (WINDOW) {
-        const Seen w = seen_tiles(it.p0, it.lq, it.lk, p.window, p.sinks);
+        const Seen w = seen_tiles<kMerge>(it.p0, it.lq, it.lk, p.window, p.sinks);
         it.ns = w.ns;
         it.skip = w.skip;
         it.lo = w.lo;
+        it.merged = w.merged;
         it.end0 = w.count(it.end0);
         it.end1 = w.count(it.end1);
       } else {
@@ -484,20 +509,23 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       if (lane < 4) tma_prefetch_4d(&p.tm_q, 0, it.kvh * G, it.q0 + it.p0 + (lane >> 1) * npos, lane & 1);
       const int top = max(it.end0, it.end1);
       if (top <= it.j0) ask();
-      const Seen laid = seen_tiles(0, it.lq, it.lk, p.window, p.sinks);  // kGathered: the tiles that lie there
+      const Seen laid = seen_tiles<false>(0, it.lq, it.lk, p.window, p.sinks);  // kGathered: the tiles that lie there
       for (int j = it.j0; j < top && !given_up(flags); ++j) {
         if (j == max(it.j0, top - 3)) ask();  // late, so that no item waits behind a long one
         const int t = WINDOW && j >= it.ns ? j + it.skip : j;
         if constexpr (SRC == kPages16) {
           load_pages(&p.tm_k, it, t);
           load_pages(&p.tm_v, it, t);
-        } else if constexpr (SRC == kGathered) {
-          const int row = (it.k0 * p.Hkv + it.kvh) * p.gather_rows + laid.count(t) * kN;
-          load_kv(&p.tm_k, row, 0);
-          load_kv(&p.tm_v, row, 0);
         } else {
-          load_kv(&p.tm_k, it.k0 + t * kN, it.kvh);
-          load_kv(&p.tm_v, it.k0 + t * kN, it.kvh);
+          const int row0 = SRC == kGathered ? (it.k0 * p.Hkv + it.kvh) * p.gather_rows : it.k0, head = SRC == kGathered ? 0 : it.kvh;
+          const int row = row0 + (SRC == kGathered ? laid.count(t) : t) * kN;
+          if (kMerge && it.merged > 0 && j == 0) {
+            load_merged(&p.tm_k8, row0, it.merged, row, head);
+            load_merged(&p.tm_v8, row0, it.merged, row, head);
+          } else {
+            load_kv(&p.tm_k, row, head);
+            load_kv(&p.tm_v, row, head);
+          }
         }
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
@@ -539,6 +567,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       const int j0 = uniform(items[slot].j0), end0 = uniform(items[slot].end0), end1 = uniform(items[slot].end1);
       const int lk = items[slot].lk, clear_at = pv ? items[slot].clear : -1;
       const int ns = WINDOW ? items[slot].ns : 0, skip = WINDOW ? items[slot].skip : 0, lo = WINDOW ? items[slot].lo : 0;
+      const int merged = WINDOW ? items[slot].merged : 0;
       const bool none = items[slot].lq < 0 || given_up(flags);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kItemEmpty + slot));
@@ -556,7 +585,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         // also those before it (their blocks may be another sequence's by now).
         if constexpr (WINDOW) {
           const int base = (j < ns ? j : j + skip) * kN;
-          const int a = min(max(p.sinks - base, 0), kN), c = min(max(lo - base, 0), kN), e = min(max(lk - base, 0), kN);
+          const int a = merged > 0 && j == 0 ? p.sinks : min(max(p.sinks - base, 0), kN), c = min(max(lo - base, 0), kN), e = min(max(lk - base, 0), kN);
           if (pv && (c > a || e < kN)) {
             uint4* tile = reinterpret_cast<uint4*>(smem + kOffRing + stage * kTileP);
             for (int i = lane; i < kN * 8; i += 32) {
@@ -733,12 +762,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         // some row of the warp ends inside this tile, or its window begins behind a key of it that is none of the first
         if (base + kN > lim0 || (WINDOW && base < low1 && base + kN > p.sinks)) {
           const float none = neg ? -kNegInfP : kNegInfP;
-          const int left = lim - base;
+          const int left = lim - base, kept = it.merged > 0 && j == 0 ? p.sinks : p.sinks - base;  // columns that are first keys
 #pragma unroll
           for (int h = 0; h < 4; ++h) {  // a bit per key (tests of single bits share an instruction)
             uint32_t keep = low_bits(min(max(left - 32 * h, 0), 32));
             if constexpr (WINDOW)
-              keep &= ~low_bits(min(max(low - base - 32 * h, 0), 32)) | low_bits(min(max(p.sinks - base - 32 * h, 0), 32));
+              keep &= ~low_bits(min(max(low - base - 32 * h, 0), 32)) | low_bits(min(max(kept - 32 * h, 0), 32));
 #pragma unroll
             for (int c = 0; c < 32; ++c) s[32 * h + c] = keep >> c & 1u ? s[32 * h + c] : none;
           }
@@ -841,7 +870,7 @@ __global__ void __launch_bounds__(128) prefill_join_kernel(const __grid_constant
   const int lq = q1 - q0, lk = k1 - k0, p0 = (t - q0) / (2 * p.npos) * 2 * p.npos;
   int end0 = kv_tiles(p0, p.npos, lq, lk), end1 = kv_tiles(p0 + p.npos, p.npos, lq, lk);
   if (WINDOW) {
-    const Seen w = seen_tiles(p0, lq, lk, p.window, p.sinks);
+    const Seen w = seen_tiles<merges(SRC, WINDOW)>(p0, lq, lk, p.window, p.sinks);
     end0 = w.count(end0);
     end1 = w.count(end1);
   }

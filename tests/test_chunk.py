@@ -38,7 +38,8 @@ WINDOWS = [  # Hq, Hkv, queries, keys, window, sinks
     (8, 2, [70, 0, 1, 300], [70, 5, 1, 300], 50, 0), (4, 4, [400], [400], 1, 0), (4, 4, [400], [400], 1, 1), (6, 2, [300], [300], 130, 4),
     (32, 2, [200, 33], [200, 150], 64, 129), (8, 1, [10], [5000], 777, 4), (8, 1, [10], [5000], 4900, 300), (16, 1, [1, 1, 1], [900, 1, 130], 128, 1),
     (8, 8, [5], [0], 3, 3), (7, 7, [43, 100], [30, 260], 20, 2), (12, 1, [1000], [1900], 256, 0), (4, 1, [64, 3], [2600, 1700], 2000, 500),
-    (8, 2, [1], [20000], 8192, 4), (8, 2, [600], [600], 100000, 4), (2, 2, [513], [513], 127, 1000), (1, 1, [1], [1], 1, 0), (10, 2, [777], [777], 2 ** 31 - 1, 2 ** 31 - 1),
+    (8, 2, [1], [20000], 8192, 4), (8, 2, [600], [600], 100000, 4), (8, 2, [900, 700], [900, 2000], 200, 120), (4, 1, [700], [800], 130, 8),
+    (16, 2, [300], [1000], 257, 1), (1, 1, [400, 300], [400, 9000], 129, 121), (2, 2, [513], [513], 127, 1000), (1, 1, [1], [1], 1, 0), (10, 2, [777], [777], 2 ** 31 - 1, 2 ** 31 - 1),
 ]
 
 
@@ -139,7 +140,7 @@ CHUNKS = [  # Hq, Hkv, queries, keys, block size, window, sinks
     (12, 4, [512], [1700], 256, 0, 0), (7, 1, [18, 19], [700, 19], 512, 0, 0), (8, 8, [5, 0], [0, 0], 64, 0, 0),
     (8, 2, [1] * 9, [900, 0, 130, 257, 5000, 64, 128, 1, 2000], 64, 128, 4), (32, 2, [200, 33], [200, 1500], 16, 64, 129), (4, 4, [1], [9000], 32, 4096, 1),
     (8, 1, [64, 3], [2600, 1700], 128, 500, 0), (16, 1, [1, 1], [4000, 70], 256, 1, 1), (8, 2, [300], [5000], 8, 700, 20), (2, 1, [257], [3000], 64, 2 ** 31 - 1, 9),
-    (8, 2, [3], [12000], 16, 3000, 3001), (5, 5, [1] * 3, [4097, 4096, 4095], 1024, 1024, 2),
+    (8, 2, [3], [12000], 16, 3000, 3001), (8, 2, [300, 90], [5000, 200], 32, 1000, 4), (4, 4, [700], [900], 16, 65, 100), (5, 5, [1] * 3, [4097, 4096, 4095], 1024, 1024, 2),
 ]
 
 
