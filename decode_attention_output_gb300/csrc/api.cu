@@ -1150,7 +1150,7 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
 // out in the workspace, kGatherBytes at a time at most (of a table's whole capacity, as the lengths are on the device): all
 // heads of some sequences, or some heads of one.
 constexpr int kRowsDirect = 16, kRowsGathered = 48;
-constexpr int64_t kGatherBytes = (int64_t)1 << 30;
+constexpr int64_t kGatherBytes = (int64_t)4 << 30;
 int run_chunk(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
               const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, bool gathered,
               void* stream) {
@@ -1706,7 +1706,7 @@ int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da
   // Few rows: K and V are read for every 16 (kRowsDirect: where the alternative reads them by TMA as they are; kRowsGathered:
   // where it lays them out first)
   const bool gathered = kv8 || BS < 64;  // (below 64 tokens a block TMA takes eight copies and more a tile)
-  if (Tq * (Hq / Hkv) <= (gathered ? kRowsGathered : kRowsDirect) * B && Hkv <= 4096)
+  if (Tq * (Hq / Hkv) <= (gathered ? kRowsGathered : kRowsDirect) * B && Hkv <= 256)
     return run_few(q, kp, vp, kv_scales, table, cu, lens, out, scale, window, sinks, stream);
   return run_chunk(q, kp, vp, kv_scales, table, cu, lens, out, scale, window, sinks, gathered, stream);
 }

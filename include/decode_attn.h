@@ -308,8 +308,14 @@ int decode_attn_prefill_window(const da_tensor_t* q, const da_tensor_t* k, const
  * left behind may belong to others by now, and what rows past seq_lens hold does not matter. An entry outside
  * the pool that is read sets bit 64 of the device error word and its block reads as zeros. A NaN or infinity in a
  * key or value that some query of a sequence sees can make any output row of that sequence and KV head non-finite.
- * block_size: a power of two from 8 (e4m3: 16) to 2^20. Other limits and the rounding of the weights as
- * decode_attn_prefill; with few queries over many keys the keys are cut into parts that meet in the workspace.
+ * block_size: a power of two from 8 (e4m3: 16) to 2^20. Other limits as decode_attn_prefill. The softmax weights enter
+ * P.V unnormalised as bf16, or (e4m3, few rows) with V's scale as f16, off by 2^-25 of the row's largest product
+ * of weight and scale at most.
+ *
+ * By Tq * G / B (rows of a sequence and KV head on average) and the pool: few rows are taken 8 or 16 at a time over
+ * K and V as they lie, and items that several CTAs share meet in the workspace; many rows 256 at a time, over
+ * bf16 blocks of 64 tokens and more as they lie, and else over a bf16 copy of the tokens that the call sees in
+ * the workspace: up to 4 GiB of the tables' capacity at a time (or one head of one sequence, if that has more), the rest after it.
  */
 int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages, const da_tensor_t* kv_scales,
                       const da_tensor_t* block_table, const da_tensor_t* cu_seqlens, const da_tensor_t* seq_lens,

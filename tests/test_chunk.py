@@ -222,10 +222,10 @@ def test_blocks_outside_the_pool(kv8, bs):
 
 
 def test_scores_past_24_bits_and_negative_scales():
-    """Scores that fp32 products part by whole powers of two: the largest keys share the row, in a window too."""
+    """Scores that fp32 products part by whole powers of two: the largest keys share the row, in a window too; few rows and many."""
     g = torch.Generator().manual_seed(76)
-    bs, lk, lq, window, sinks = 16, 900, 70, 300, 5
-    for scale in (SCALE, -0.3):
+    bs, lk, window, sinks = 16, 900, 300, 5
+    for scale, lq in ((SCALE, 70), (-0.3, 70), (SCALE, 3), (-0.3, 2)):
         for size in (26, 40):
             cache = Cache(g, [lk], 1, bs)
             c = torch.randint(1, 256, (lk, 1, 1), generator=g).float()
@@ -237,7 +237,7 @@ def test_scores_past_24_bits_and_negative_scales():
             kp, vp, _ = cache.on()
             out = canvas(q)
             da.decode_attn_chunk(q.to(DEV), kp, vp, None, cache.table.to(torch.int32).to(DEV), i32([0, lq]), i32([lk]), out, scale, window, sinks)
-            for r in (0, 1, 35, 69):
+            for r in sorted({0, 1, lq // 2, lq - 1}):
                 i = r + lk - lq
                 seen = torch.tensor([j for j in range(i + 1) if j > i - window or j < sinks])
                 cs = c[seen, 0, 0]
@@ -301,6 +301,40 @@ def test_long_keys_from_far(paged, more):
         check(out, ref, tol, have, f"pass {i}")
 
 
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("scale", [0.0, 1e-42, -1.0, 3.0])
+def test_scales_of_every_kind(scale, kv8):
+    """0 gives every key the same weight; few rows and many."""
+    g = torch.Generator().manual_seed(85)
+    cache = Cache(g, [200, 333], 2, 16, kv8)
+    for lq in (1, 120):
+        q = torch.randn((2 * lq, 8, 128), generator=g).to(torch.bfloat16)
+        out = canvas(q)
+        da.decode_attn_chunk(q.to(DEV), *cache.on(), cache.table.to(torch.int32).to(DEV), i32([0, lq, 2 * lq]), i32([200, 333]), out, scale)
+        ref, tol, have = attend_ref(q, *cache.tokens, [0, lq, 2 * lq], scale)
+        check(out, ref, tol, have, "scale")
+
+
+def test_offsets_of_any_kind():
+    """Offsets that decrease or lie outside, negative lengths: nothing but rows of out is written, and well-formed sequences come out right."""
+    g = torch.Generator().manual_seed(86)
+    for kv8 in (False, True):
+        for rows in (1, 40):
+            cache = Cache(g, [300, 90, 200], 2, 16, kv8)
+            T = 3 * rows + 4
+            q = torch.randn((T, 4, 128), generator=g).to(torch.bfloat16)
+            for c in ([-5, 2, 1, 10 ** 6], [3, 3, -1, 2], [2 ** 31 - 1, -2 ** 31, 5, 7], [0, T, 0, T]):
+                big = torch.full((T + 2, 4, 128), 7.5, dtype=torch.bfloat16, device=DEV)
+                da.decode_attn_chunk(q.to(DEV), *cache.on(), cache.table.to(torch.int32).to(DEV), i32(c), i32([300, -9, 200]), big[1:-1], SCALE)
+                assert (big[0] == 7.5).all() and (big[-1] == 7.5).all()
+                assert da.decode_attn_last_device_error() == 0
+            out = canvas(q)
+            c = [1, 1 + rows, 1 + rows, 1 + 2 * rows]
+            da.decode_attn_chunk(q.to(DEV), *cache.on(), cache.table.to(torch.int32).to(DEV), i32(c), i32([300, -9, 200]), out, SCALE)
+            held = [[x[0], x[1][:0], x[2]] for x in cache.tokens]
+            check(out, *attend_ref(q, *held, c, SCALE), "sound")
+
+
 def test_many_sequences():
     """1000 sequences of one query, and more queries than a table's row of work items."""
     g = torch.Generator().manual_seed(78)
@@ -316,7 +350,7 @@ def test_many_sequences():
         check(out, ref, tol, have, "many")
 
 
-@pytest.mark.parametrize("capacity,lq,lk", [(40_000, [70, 1, 0, 33, 90, 60, 64, 65], [900, 1, 300, 33, 2000, 777, 64, 1300]), (300_000, [150], [3000])], ids=str)
+@pytest.mark.parametrize("capacity,lq,lk", [(200_000, [70, 1, 0, 33, 90, 60, 64, 65], [900, 1, 300, 33, 2000, 777, 64, 1300]), (1_600_000, [150], [3000])], ids=str)
 def test_tables_of_large_capacity(capacity, lq, lk):
     """A table whose capacity's tokens do not fit the workspace's part for them: sequences, or heads, a few at a time."""
     g = torch.Generator().manual_seed(84)
@@ -333,7 +367,7 @@ def test_tables_of_large_capacity(capacity, lq, lk):
 
 
 @pytest.mark.parametrize("kv8", [False, True])
-@pytest.mark.parametrize("G,lq,window,sinks", [(1, 1, 0, 0), (4, 2, 40, 3), (8, 1, 0, 0), (4, 4, 0, 0), (16, 1, 70, 1), (3, 5, 0, 0)], ids=str)
+@pytest.mark.parametrize("G,lq,window,sinks", [(1, 1, 0, 0), (4, 2, 40, 3), (8, 1, 0, 0), (4, 4, 0, 0), (16, 1, 70, 1), (3, 5, 0, 0), (11, 2, 0, 0)], ids=str)
 def test_many_short_items(G, lq, window, sinks, kv8):
     """Hundreds of sequences of up to 170 keys with 8 KV heads, none and one among them."""
     g = torch.Generator().manual_seed(81)
