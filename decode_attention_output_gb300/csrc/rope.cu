@@ -4,17 +4,20 @@
 //   y = x * r * w,  r = (sum x^2 / D + eps)^-1/2                      (with a weight; y = x without)
 //   z_a = y_a c - y_b s,  z_b = y_b c + y_a s    for the R / 2 pairs (a, b) of dims, the others as they are
 // c, s = table[p][i], table[p][R / 2 + i]: pair i's angle at the token's position p on that pair's axis. Pairs are (i, i + R / 2), or
-// neighbours (2 i, 2 i + 1). Products and their difference are rounded one by one (no fused multiply-add): the largest
-// value of a row decides its scale in an e4m3 cache, and this way it is what the written formula gives.
+// neighbours (2 i, 2 i + 1). Without a norm products and their sum are rounded one by one (no fused multiply-add): the largest
+// value of a row decides its scale in an e4m3 cache, and this way it is what the written formula gives. With one the weights
+// go into the cosines and sines, a token's for all its heads, and r comes last.
 //
 // Into the cache: a key's z is rounded once, to bf16 or to e4m3 codes over 2^e with the least e that holds the row, as
 // kv_cache.cu does for values; the values are its rows unchanged. Queries go to packed rows.
 //
-// Bound by bytes: a row is read and written once, 4 D bytes (a key into an e4m3 cache 3 D + 4); its ~60 instructions a half
-// warp come near that only for the normed rows. A lane holds dims 4 l .. 4 l + 3 and their partners, so that neither pairing
-// needs a shuffle and a call may work in place; the norm's sum is four shuffles. A warp takes one token and eight rows of its
-// heads (two where tokens are few), so that the token's place, its position and its eight cosines and sines are found once,
-// while the rows are already on their way.
+// A row is read and written once, 4 D bytes (a key into an e4m3 cache 3 D + 4), which bounds rows without a norm; with one, and with
+// positions of several axes, instruction issue does (75% of the slots in a profile). A lane holds dims 4 l .. 4 l + 3 and
+// their partners, so that neither pairing needs a shuffle and a call may work in place; the norm's sum is four shuffles a row, four
+// rows side by side. A warp takes one token and eight rows of its heads (two where tokens are few), so that the token's place,
+// its position and its cosines and sines are found once, while the rows are already on their way.
+// Measured (32 / 8 heads): 8191 tokens without norms 27 us (6.3 TB/s), with them 32, and positions of three axes 35; 46.6k
+// tokens with norms into a bf16 cache 179 (6.1 TB/s), into an e4m3 one 218; one token of each of 64 sequences 3.8.
 #include "kernels.h"
 #include "packed.cuh"
 #include "ptx.cuh"
@@ -24,26 +27,18 @@ namespace {
 
 constexpr int kRopeWarps = 4;
 
-// Two products, two sums, two x * x + c: of what stands in the same place of both.
+// Two products, two x * y + c: of what stands in the same place of each.
 __device__ __forceinline__ unsigned long long bits2(float2 x) { return *reinterpret_cast<unsigned long long*>(&x); }
 __device__ __forceinline__ float2 mul2(float2 x, float2 y) {
   unsigned long long r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
   return *reinterpret_cast<float2*>(&r);
 }
-__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 c) {
   unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)), "l"(bits2(c)));
   return *reinterpret_cast<float2*>(&r);
 }
-__device__ __forceinline__ float2 square_add2(float2 x, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(c)));
-  return *reinterpret_cast<float2*>(&r);
-}
-
-// Two products that stay apart from the sum behind them (that of mul.f32x2 and add.f32x2 becomes one multiply-add)
-__device__ __forceinline__ float2 each(float2 x, float2 y) { return make_float2(__fmul_rn(x.x, y.x), __fmul_rn(x.y, y.y)); }
 
 // Four weights of dims `at` .. `at` + 3.
 __device__ __forceinline__ float4 four_weights(const void* w, bool f32, int at) {
@@ -97,9 +92,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
   const long long from_sh = is_q ? p.q_sh : is_k ? cp.k_sh : cp.v_sh;
   const __nv_bfloat16* from_end = is_q ? p.q + p.q_span : is_k ? cp.k + cp.k_span : cp.v + cp.v_span;
   uint2 x[ROWS][2];
+  const __nv_bfloat16* at_row = from + h0 * from_sh;
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const __nv_bfloat16* at = from + (h0 + i * kAt) * from_sh;
+  for (int i = 0; i < ROWS; ++i, at_row += kAt * from_sh) {
+    const __nv_bfloat16* at = at_row;
     const bool ok = h0 + i * kAt < heads && in_bounds(at + DIM <= from_end, p.err);
     x[i][0] = ok ? ldg_stream_v2(at + d0) : make_uint2(0, 0);
     x[i][1] = ok ? ldg_stream_v2(at + d1) : make_uint2(0, 0);
@@ -149,8 +145,6 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
     turn0 = turn1 = false;
   }
   // A lane's dims as firsts and seconds of its four pairs, two by two: (first, first), (second, second)
-  const float2 cc[2] = {make_float2(c[0], c[1]), make_float2(c[2], c[3])}, ss[2] = {make_float2(s[0], s[1]), make_float2(s[2], s[3])};
-  const float2 minus_ss[2] = {make_float2(-s[0], -s[1]), make_float2(-s[2], -s[3])};
   auto firsts_of = [&](float2 (&first)[2], float2 (&second)[2], const float4& run0, const float4& run1) {
     if (HALVES) {
       first[0] = make_float2(run0.x, run0.y), first[1] = make_float2(run0.z, run0.w);
@@ -160,10 +154,27 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
       first[1] = make_float2(run1.x, run1.z), second[1] = make_float2(run1.y, run1.w);
     }
   };
+  // z_a = (a aa + b ba) r, z_b = (b bb + a ab) r, with the weights in the factors (r = 1 without)
   const void* weight = !NORM ? nullptr : is_q ? p.q_weight : is_k ? p.k_weight : nullptr;
   const bool w32 = is_q ? p.q_weight_f32 : p.k_weight_f32;
-  float2 w_first[2] = {}, w_second[2] = {};
-  if (weight) firsts_of(w_first, w_second, four_weights(weight, w32, d0), four_weights(weight, w32, d1));
+  float2 aa[2], ab[2], ba[2], bb[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    aa[k] = bb[k] = make_float2(c[2 * k], c[2 * k + 1]);
+    ab[k] = make_float2(s[2 * k], s[2 * k + 1]);
+    ba[k] = make_float2(-s[2 * k], -s[2 * k + 1]);
+  }
+  if (NORM && weight) {
+    float2 w_first[2], w_second[2];
+    firsts_of(w_first, w_second, four_weights(weight, w32, d0), four_weights(weight, w32, d1));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      aa[k] = mul2(aa[k], w_first[k]);
+      ab[k] = mul2(ab[k], w_first[k]);
+      ba[k] = mul2(ba[k], w_second[k]);
+      bb[k] = mul2(bb[k], w_second[k]);
+    }
+  }
 
   // Where the rows go
   const bool packed = is_q || DEST == kPacked;
@@ -191,8 +202,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
       float2 q = make_float2(0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        q = square_add2(make_float2(bf16lo_to_f32(x[i][k].x), bf16hi_to_f32(x[i][k].x)), q);
-        q = square_add2(make_float2(bf16lo_to_f32(x[i][k].y), bf16hi_to_f32(x[i][k].y)), q);
+        const float2 u = make_float2(bf16lo_to_f32(x[i][k].x), bf16hi_to_f32(x[i][k].x)), v = make_float2(bf16lo_to_f32(x[i][k].y), bf16hi_to_f32(x[i][k].y));
+        q = fma2(v, v, fma2(u, u, q));
       }
       root[i] = q.x + q.y;
     }
@@ -210,19 +221,22 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
     float2 first[2], second[2];
     firsts_of(first, second, make_float4(bf16lo_to_f32(x[i][0].x), bf16hi_to_f32(x[i][0].x), bf16lo_to_f32(x[i][0].y), bf16hi_to_f32(x[i][0].y)),
               make_float4(bf16lo_to_f32(x[i][1].x), bf16hi_to_f32(x[i][1].x), bf16lo_to_f32(x[i][1].y), bf16hi_to_f32(x[i][1].y)));
-    if (NORM && weight) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        first[k] = mul2(mul2(first[k], make_float2(root[i], root[i])), w_first[k]);
-        second[k] = mul2(mul2(second[k], make_float2(root[i], root[i])), w_second[k]);
-      }
-    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (HALVES || k == 0 ? turn0 : turn1) {
-        const float2 a = first[k], b = second[k];
-        first[k] = add2(each(a, cc[k]), each(b, minus_ss[k]));
-        second[k] = add2(each(b, cc[k]), each(a, ss[k]));
+      const float2 a = first[k], b = second[k];
+      const bool turn = HALVES || k == 0 ? turn0 : turn1;
+      if (NORM && weight) {
+        first[k] = mul2(a, aa[k]);
+        second[k] = mul2(b, bb[k]);
+        if (turn) {
+          first[k] = fma2(b, ba[k], first[k]);
+          second[k] = fma2(a, ab[k], second[k]);
+        }
+        first[k] = mul2(first[k], make_float2(root[i], root[i]));
+        second[k] = mul2(second[k], make_float2(root[i], root[i]));
+      } else if (turn) {  // each product and their sum rounded once
+        first[k] = make_float2(__fadd_rn(__fmul_rn(a.x, aa[k].x), __fmul_rn(b.x, ba[k].x)), __fadd_rn(__fmul_rn(a.y, aa[k].y), __fmul_rn(b.y, ba[k].y)));
+        second[k] = make_float2(__fadd_rn(__fmul_rn(b.x, bb[k].x), __fmul_rn(a.x, ab[k].x)), __fadd_rn(__fmul_rn(b.y, bb[k].y), __fmul_rn(a.y, ab[k].y)));
       }
     }
     // in the order of the dims again: this lane's first run, then its second
