@@ -100,6 +100,45 @@ __device__ __forceinline__ Seq sequence(const FewParams& p, int b) {
   return s;
 }
 
+// A segment: an item's units of one worker, from the flat unit f on and before f1 (ALONE: to the item's end).
+struct Segment {
+  int b, q0, lk, kvh, u0, u1, pos0, most, shift, end, low;
+  long long item0;  // the item's first unit
+  Units un;
+};
+template <int KEYS, bool ALONE>
+__device__ __forceinline__ Segment segment_of(const FewParams& p, const long long* prefix, long long f, long long f1) {
+  Segment s;
+  s.b = 0;
+  for (int step = 512; step > 0; step >>= 1)  // the last b with prefix[b] <= f: B <= 1024
+    if (s.b + step < p.B && prefix[s.b + step] <= f) s.b += step;
+  const Seq sq = sequence(p, s.b);
+  s.un = units_of<KEYS>(sq.lo, sq.lk, p.sinks);
+  const long long within = f - prefix[s.b], item = within / s.un.n;
+  const int rgs = (sq.lq + p.npos - 1) / p.npos;  // of a KV head one behind the other: their keys are in L2
+  s.kvh = (int)(item / rgs);
+  const int rg = (int)(item - (long long)s.kvh * rgs);
+  s.u0 = (int)(within - item * s.un.n);
+  s.u1 = ALONE ? s.un.n : (int)min((long long)s.un.n, s.u0 + (f1 - f));
+  s.item0 = f - s.u0;
+  s.q0 = sq.q0;
+  s.lk = sq.lk;
+  s.pos0 = rg * p.npos;  // its first query, and how many
+  s.most = min(p.npos, sq.lq - s.pos0);
+  s.shift = sq.lk - sq.lq;  // position of the sequence's first query
+  s.end = min(sq.lk, s.pos0 + s.most + s.shift);       // keys that its last query sees
+  s.low = max(0, s.pos0 + s.shift - p.window + 1);  // the first of its first query's window
+  return s;
+}
+
+// Where segments are long the kernel's code stays in the instruction cache by being called, not inlined twice (one
+// token each of eight sequences over 8k, e4m3: 39.7 us inlined, 38.3 called). Where each unit or two is a segment the call costs more than that
+// (one token each of 256 sequences of 100: 39 us inlined, 41 called).
+template <int KEYS>
+__device__ __noinline__ Segment segment_called(const FewParams& p, const long long* prefix, long long f, long long f1) {
+  return segment_of<KEYS, false>(p, prefix, f, f1);
+}
+
 // The items, or parts of them, of worker `me` of `workers`. ALONE: a worker is a warp and takes items as a whole; else it is a
 // CTA, whose warps take every eighth unit of an item.
 // NB: blocks of eight rows of an item
@@ -112,42 +151,17 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
   float* ml = reinterpret_cast<float*>(smem + kOffMl);
   int* last = reinterpret_cast<int*>(smem + kOffLast);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int G = p.G, npos = p.npos;
+  const int G = p.G;
   const long long total = prefix[p.B];
   const int first = ALONE ? 0 : warp;             // this warp's units of a segment
   constexpr int step = ALONE ? 1 : kWarpsF;
   auto begin_of = [&](int c) { return total * c / workers; };
   auto owner = [&](long long f) { return (int)(((f + 1) * workers - 1) / total); };
 
-  // ---------------------------------------------------------------- a segment: an item's units in this CTA
-  struct Segment {
-    int b, q0, lk, kvh, u0, u1, pos0, most, shift, end, low;
-    long long item0;  // the item's first unit
-    Units un;
-  };
   long long f1 = begin_of(me + 1);
   auto segment = [&](long long f) {
-    Segment s;
-    s.b = 0;
-    for (int step = 512; step > 0; step >>= 1)  // the last b with prefix[b] <= f: B <= 1024
-      if (s.b + step < p.B && prefix[s.b + step] <= f) s.b += step;
-    const Seq sq = sequence(p, s.b);
-    s.un = units_of<kKeys>(sq.lo, sq.lk, p.sinks);
-    const long long within = f - prefix[s.b], item = within / s.un.n;
-    const int rgs = (sq.lq + npos - 1) / npos;  // of a KV head one behind the other: their keys are in L2
-    s.kvh = (int)(item / rgs);
-    const int rg = (int)(item - (long long)s.kvh * rgs);
-    s.u0 = (int)(within - item * s.un.n);
-    s.u1 = ALONE ? s.un.n : (int)min((long long)s.un.n, s.u0 + (f1 - f));
-    s.item0 = f - s.u0;
-    s.q0 = sq.q0;
-    s.lk = sq.lk;
-    s.pos0 = rg * npos;  // its first query, and how many
-    s.most = min(npos, sq.lq - s.pos0);
-    s.shift = sq.lk - sq.lq;  // position of the sequence's first query
-    s.end = min(sq.lk, s.pos0 + s.most + s.shift);       // keys that its last query sees
-    s.low = max(0, s.pos0 + s.shift - p.window + 1);  // the first of its first query's window
-    return s;
+    if constexpr (ALONE) return segment_of<kKeys, true>(p, prefix, f, f1);
+    else return segment_called<kKeys>(p, prefix, f, f1);
   };
   const uint32_t units = smem_u32(smem) + warp * kStagesF * kUnitBytes;
   const uint32_t scales = smem_u32(smem + kOffScales) + warp * kStagesF * kScalesF;
@@ -240,8 +254,8 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
   auto scale_at = [&](int nt) { return (uint32_t)(split ? (nt >> 1) * 128 + (nt & 1) * 32 : nt * 32) + g * 4; };
 
   begin_loads(f);
-  load_unit();
-  load_unit();
+#pragma unroll 1
+  for (int i = 0; i < kStagesF; ++i) load_unit();
   int used = 0;       // units taken
   bool alive = true;  // no wait has run out
   while (true) {
