@@ -1146,10 +1146,76 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
   return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
+// Rows (Tq * G) a sequence on average up to which a call goes to the kernel of few rows. Where the alternative reads the blocks as
+// they are (32 sequences of 8k, 32 / 8 heads, few and many): 16 rows 166 us and 171, 20 rows 317 and 170. Where it lays them out
+// first: 48 rows of e4m3 361 and 494, 64 rows 475 and 507; blocks of 16 465 and 530, 619 and 545; 16 sequences of 2000, 64 / 8
+// heads, 32 rows 53 and 68, 40 rows 71 and 69.
+constexpr int kRowsDirect = 16, kRowsGathered = 48;
+// From and up to how many a call that lays tokens out may be a batch of prompts' chunks and single tokens, of which each kernel takes
+// its own. 512 new tokens of one sequence and one each of 31 others over 8k, 32 / 8 heads, e4m3: 508 us by the kernel of many rows alone, 233
+// by both (of 63 others: 712 by that of few rows alone, 385). Sequences all alike pay for the other's launches (100 tokens each of
+// 32: 336 -> 341; 8 each: 248 -> 276). Where all items find an SM at once the long chunk's time hides the others'
+// (512 and 3 others: 130 alone, 144 by both).
+constexpr int kRowsMixedFrom = 24, kRowsMixed = 4096;
+bool mixed_rows(int64_t Tq, int64_t group, int64_t B, int64_t Hkv) {
+  return B * Hkv > sm_count() && Hkv <= 256 && Tq * group > kRowsMixedFrom * B && Tq * group <= kRowsMixed * B;
+}
+// decode_attn_chunk after its checks where a sequence has few rows on average: 8 or 16 at a time. few_lq > 0: of the sequences
+// that have so many queries and fewer (mostly one each, so 8 rows where they hold a token's).
+int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
+            const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, void* stream,
+            int few_lq = 0) {
+  const bool kv8 = kp->dtype == DA_DTYPE_E4M3;
+  const int64_t B = table->shape[0], MB = table->shape[1];
+  FewParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q->data);
+  p.out = static_cast<__nv_bfloat16*>(out->data);
+  p.q_st = q->stride[0];
+  p.q_sh = q->stride[1];
+  p.o_st = out->stride[0];
+  p.o_sh = out->stride[1];
+  const int box = (int)std::min<int64_t>(kp->shape[2], kv8 ? kFewKeys8 : kFewKeys16);
+  DA_TRY(encode_kv_map(&p.tm_k, kp, box));
+  DA_TRY(encode_kv_map(&p.tm_v, vp, box));
+  if (kv8) DA_TRY(encode_scales_map(&p.tm_scales, scales, box));
+  p.cu = static_cast<const int*>(cu->data);
+  p.lens = static_cast<const int*>(lens->data);
+  p.table = static_cast<const int*>(table->data);
+  p.bt_stride = B > 1 ? table->stride[0] : MB;
+  p.B = (int)B;
+  p.Hkv = (int)kp->shape[1];
+  p.G = (int)(q->shape[1] / kp->shape[1]);
+  p.Tq = (int)q->shape[0];
+  p.cap = (int)(MB * kp->shape[2]);
+  p.most_lq = few_lq > 0 ? few_lq : p.Tq;
+  const int rows = p.G <= 8 && (few_lq > 0 ? few_lq * p.G <= kRowsDirect : (int64_t)p.Tq * p.G <= 8 * B) ? 8 : kFewRows;
+  p.npos = rows / p.G;
+  p.num_blocks = (int)kp->shape[0];
+  while ((1 << p.block_shift) < kp->shape[2]) ++p.block_shift;
+  p.window = window ? std::min(window, 1 << 30) : 1 << 30;
+  p.sinks = window ? std::min(sinks, 1 << 30) : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.q_span = span_of(q);
+  p.out_span = span_of(out);
+  p.table_span = (B - 1) * p.bt_stride + MB;
+  const int grid = std::max(1, sm_count());
+  p.slots = 2 * grid;
+  p.least = kv8 ? 8 : 16;  // 256 keys
+  const size_t ml_bytes = align_up((size_t)p.slots * kFewRows * 2 * 4, 256);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = nullptr;
+  DA_TRY(workspace_get(ml_bytes + (size_t)p.slots * kFewRows * 128 * 4, st, &ws));
+  p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
+  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
+  p.counters = reinterpret_cast<int*>(ws + kAttnCntOff);
+  p.err = reinterpret_cast<int*>(ws + kErrOff);
+  return launch_chunk_few(p, grid, kv8, rows, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
 // decode_attn_chunk after its checks where a sequence has many rows: over the blocks as they are, or (gathered) over their tokens laid
 // out in the workspace, kGatherBytes at a time at most (of a table's whole capacity, as the lengths are on the device): all
 // heads of some sequences, or some heads of one.
-constexpr int kRowsDirect = 16, kRowsGathered = 48;
 constexpr int64_t kGatherBytes = (int64_t)4 << 30;
 int run_chunk(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
               const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, bool gathered,
@@ -1180,6 +1246,9 @@ int run_chunk(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp
   const int64_t nb = std::max<int64_t>(1, std::min(B, kGatherBytes / (Hkv * each)));
   const int64_t nh = std::max<int64_t>(1, std::min<int64_t>({Hkv, kGatherBytes / each, 65535}));
   const int64_t es = kv8 ? 1 : 2;
+  // Mixed: sequences of few rows by their own kernel, behind the others'. (Where the average is low they may be drafts of many tokens.)
+  const bool mixed = mixed_rows(Tq, group, B, Hkv);
+  const int few_lq = mixed ? (int)((Tq * group <= kRowsGathered * B ? kRowsGathered : kRowsDirect) / group) : 0;
   for (int64_t b0 = 0; b0 < B; b0 += nb)
     for (int64_t h0 = 0; h0 < Hkv; h0 += nh) {
       const int64_t bn = std::min(nb, B - b0), hn = std::min(nh, Hkv - h0);
@@ -1213,6 +1282,7 @@ int run_chunk(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp
       g.cap = (int)cap;
       g.num_blocks = p.num_blocks;
       g.block_shift = p.block_shift;
+      g.few_lq = p.few_lq = few_lq;
       da_tensor_t qs = *q, os = *out;
       for (da_tensor_t* t : {&qs, &os}) {
         t->data = static_cast<__nv_bfloat16*>(t->data) + h0 * group * t->stride[1];
@@ -1220,57 +1290,7 @@ int run_chunk(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp
       }
       DA_TRY(run_prefill(p, kChunkGathered, &qs, &os, bn, hn, cap, scale, window, sinks, stream, &g, kv8));
     }
-  return DA_OK;
-}
-
-// decode_attn_chunk after its checks where a sequence has few rows on average: 8 or 16 at a time.
-int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
-            const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, void* stream) {
-  const bool kv8 = kp->dtype == DA_DTYPE_E4M3;
-  const int64_t B = table->shape[0], MB = table->shape[1];
-  FewParams p;
-  memset(&p, 0, sizeof(p));
-  p.q = static_cast<const __nv_bfloat16*>(q->data);
-  p.out = static_cast<__nv_bfloat16*>(out->data);
-  p.q_st = q->stride[0];
-  p.q_sh = q->stride[1];
-  p.o_st = out->stride[0];
-  p.o_sh = out->stride[1];
-  const int box = (int)std::min<int64_t>(kp->shape[2], kv8 ? kFewKeys8 : kFewKeys16);
-  DA_TRY(encode_kv_map(&p.tm_k, kp, box));
-  DA_TRY(encode_kv_map(&p.tm_v, vp, box));
-  if (kv8) DA_TRY(encode_scales_map(&p.tm_scales, scales, box));
-  p.cu = static_cast<const int*>(cu->data);
-  p.lens = static_cast<const int*>(lens->data);
-  p.table = static_cast<const int*>(table->data);
-  p.bt_stride = B > 1 ? table->stride[0] : MB;
-  p.B = (int)B;
-  p.Hkv = (int)kp->shape[1];
-  p.G = (int)(q->shape[1] / kp->shape[1]);
-  p.Tq = (int)q->shape[0];
-  p.cap = (int)(MB * kp->shape[2]);
-  const int rows = p.G <= 8 && (int64_t)p.Tq * p.G <= 8 * B ? 8 : kFewRows;
-  p.npos = rows / p.G;
-  p.num_blocks = (int)kp->shape[0];
-  while ((1 << p.block_shift) < kp->shape[2]) ++p.block_shift;
-  p.window = window ? std::min(window, 1 << 30) : 1 << 30;
-  p.sinks = window ? std::min(sinks, 1 << 30) : 0;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.q_span = span_of(q);
-  p.out_span = span_of(out);
-  p.table_span = (B - 1) * p.bt_stride + MB;
-  const int grid = std::max(1, sm_count());
-  p.slots = 2 * grid;
-  p.least = kv8 ? 8 : 16;  // 256 keys
-  const size_t ml_bytes = align_up((size_t)p.slots * kFewRows * 2 * 4, 256);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  char* ws = nullptr;
-  DA_TRY(workspace_get(ml_bytes + (size_t)p.slots * kFewRows * 128 * 4, st, &ws));
-  p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
-  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
-  p.counters = reinterpret_cast<int*>(ws + kAttnCntOff);
-  p.err = reinterpret_cast<int*>(ws + kErrOff);
-  return launch_chunk_few(p, grid, kv8, rows, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return mixed ? run_few(q, kp, vp, scales, table, cu, lens, out, scale, window, sinks, stream, few_lq) : DA_OK;
 }
 
 // decode_attn_prefill and, with a window, decode_attn_prefill_window.
@@ -1703,10 +1723,8 @@ int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da
     if (reinterpret_cast<uintptr_t>(table->data) % 4 || reinterpret_cast<uintptr_t>(lens->data) % 4) return DA_ERR_ALIGN;
   }
   if (B == 0 || Tq == 0) return DA_OK;
-  // Few rows: K and V are read for every 16 (kRowsDirect: where the alternative reads them by TMA as they are; kRowsGathered:
-  // where it lays them out first)
-  const bool gathered = kv8 || BS < 64;  // (below 64 tokens a block TMA takes eight copies and more a tile)
-  if (Tq * (Hq / Hkv) <= (gathered ? kRowsGathered : kRowsDirect) * B && Hkv <= 256)
+  const bool gathered = kv8 || BS < 64;  // (below 64 tokens a block TMA takes four copies and more a tile)
+  if (Tq * (Hq / Hkv) <= (gathered ? kRowsGathered : kRowsDirect) * B && Hkv <= 256 && !(gathered && mixed_rows(Tq, Hq / Hkv, B, Hkv)))
     return run_few(q, kp, vp, kv_scales, table, cu, lens, out, scale, window, sinks, stream);
   return run_chunk(q, kp, vp, kv_scales, table, cu, lens, out, scale, window, sinks, gathered, stream);
 }

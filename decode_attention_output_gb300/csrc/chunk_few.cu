@@ -95,6 +95,7 @@ __device__ __forceinline__ Seq sequence(const FewParams& p, int b) {
   Seq s;
   s.q0 = min(max(__ldg(p.cu + b), 0), p.Tq);
   s.lq = min(max(__ldg(p.cu + b + 1), s.q0), p.Tq) - s.q0;
+  if (s.lq > p.most_lq) s.lq = 0;
   s.lk = min(max(__ldg(p.lens + b), 0), p.cap);
   s.lo = max(0, s.lk - s.lq - p.window + 1);
   return s;
@@ -697,6 +698,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
   }
   __syncthreads();
   const long long total = prefix[p.B];
+  if (total == 0) return;
   const int longest = last[0];
   // As many CTAs take part as leave each 256 keys, and the longest item in 48 parts at most: one CTA joins them
   int workers = (int)min((long long)gridDim.x, max(total / max(p.least, longest / kMostParts), 1ll));

@@ -7,70 +7,89 @@
 //
 // Bound by bytes; read once and written once whatever the number of queries, where widening in the attention is done for every
 // 256 rows of queries (four chunks of 512 tokens over 7.7k, 32 / 8 heads: 328 us widened there, 181 over a bf16 cache). A CTA
-// takes a tile of one head, all its loads before its stores.
+// takes a tile of one head at a time, all its loads before its stores. (CTAs that walk all tiles in equal shares, however many:
+// 100 new tokens each of 32 sequences over 4k, e4m3: 336 -> 346 us in all.)
 #include "kernels.h"
 #include "packed.cuh"
 #include "ptx.cuh"
+
+#include <algorithm>
 
 namespace da {
 namespace {
 
 constexpr int kGatherThreads = 256;
 
+// A sequence's tokens (none: nothing of it is laid out) and its first that a window sees; of its tiles the first ns are
+// those of `sinks`, then `skip` are left out.
+struct Kept {
+  int lk, lo, ns, skip;
+};
+__device__ __forceinline__ Kept kept(const GatherParams& p, int b) {
+  Kept s;
+  const int q0 = min(max(__ldg(p.cu + b), 0), p.Tq), lq = min(max(__ldg(p.cu + b + 1), q0), p.Tq) - q0;
+  s.lk = lq <= p.few_lq ? 0 : min(max(__ldg(p.lens + b), 0), p.cap);
+  s.lo = max(0, s.lk - lq - p.window + 1);
+  const int first = s.lo / 128;
+  s.ns = (p.sinks + 127) / 128;
+  s.skip = max(0, first - s.ns);
+  return s;
+}
+
 template <bool KV8>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherParams p) {
   constexpr int kPieces = KV8 ? 8 : 16, kAt = kGatherThreads / kPieces, kPasses = 128 / kAt;  // 16-byte pieces of a row; rows at a time
+  const int c = threadIdx.x % kPieces, row0 = threadIdx.x / kPieces;
   pdl_wait_primary();
   const int b = blockIdx.y, h = blockIdx.z;
-  const int q0 = min(max(__ldg(p.cu + b), 0), p.Tq), lq = min(max(__ldg(p.cu + b + 1), q0), p.Tq) - q0;
-  const int lk = min(max(__ldg(p.lens + b), 0), p.cap), lo = max(0, lk - lq - p.window + 1);
-  const int first = lo / 128, ns = (p.sinks + 127) / 128, skip = first > ns ? first - ns : 0;
-  const int j = blockIdx.x, t = skip > 0 && j >= ns ? j + skip : j;
-  if (lq == 0 || (long long)t * 128 >= lk) return;
-  const int c = threadIdx.x % kPieces, row0 = threadIdx.x / kPieces;
-  uint4 x[2][kPasses];
-  float f[2][KV8 ? kPasses : 1];
-  bool seen[kPasses];
+  const Kept s = kept(p, b);
+  const int lk = s.lk, lo = s.lo, tiles = lk > 0 ? (lk + 127) / 128 - s.skip : 0;
+  for (int j = blockIdx.x; j < tiles; j += gridDim.x) {
+    const int t = s.skip > 0 && j >= s.ns ? j + s.skip : j;
+    uint4 x[2][kPasses];
+    float f[2][KV8 ? kPasses : 1];
+    bool seen[kPasses];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int key = t * 128 + i * kAt + row0, row = key & ((1 << p.block_shift) - 1);
-    seen[i] = key < lk && (key >= lo || key < p.sinks);
-    const long long entry = b * p.bt_stride + (key >> p.block_shift);
-    const int id = seen[i] && in_bounds(entry < p.table_span, p.err) ? __ldg(p.table + entry) : -1;
-    bool ok = (unsigned)id < (unsigned)p.num_blocks;
-    if (seen[i] && !ok) atomicOr(p.err, kErrBlockTable);  // reads as zeros
-    const long long k_at = id * p.kp_sb + h * p.kp_sh + row * p.kp_sr + c * 16, v_at = id * p.vp_sb + h * p.vp_sh + row * p.vp_sr + c * 16;
-    ok = ok && in_bounds(k_at + 16 <= p.kp_span && v_at + 16 <= p.vp_span, p.err);
-    x[0][i] = ok ? ldg_stream_v4(p.k_pages + k_at) : make_uint4(0, 0, 0, 0);
-    x[1][i] = ok ? ldg_stream_v4(p.v_pages + v_at) : make_uint4(0, 0, 0, 0);
-    if constexpr (KV8) {
-      const long long sc = id * p.sc_sb + h * p.sc_sh + row;
-      ok = ok && in_bounds(sc + p.sc_st < p.sc_span, p.err);
-      f[0][i] = ok ? __ldg(p.scales + sc) : 0.f;
-      f[1][i] = ok ? __ldg(p.scales + sc + p.sc_st) : 0.f;
-    }
-  }
-  const long long to = (((long long)b * p.heads + h) * p.rows + j * 128 + row0) * 128 + c * (KV8 ? 16 : 8);
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    if (!seen[i] || !in_bounds(j * 128 + 128 <= p.rows && to + (i * kAt + 1) * 128 <= p.span + 128, p.err)) continue;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      __nv_bfloat16* at = (v ? p.v_out : p.k_out) + to + (long long)i * kAt * 128;
+    for (int i = 0; i < kPasses; ++i) {
+      const int key = t * 128 + i * kAt + row0, row = key & ((1 << p.block_shift) - 1);
+      seen[i] = key < lk && (key >= lo || key < p.sinks);
+      const long long entry = b * p.bt_stride + (key >> p.block_shift);
+      const int id = seen[i] && in_bounds(entry < p.table_span, p.err) ? __ldg(p.table + entry) : -1;
+      bool ok = (unsigned)id < (unsigned)p.num_blocks;
+      if (seen[i] && !ok) atomicOr(p.err, kErrBlockTable);  // reads as zeros
+      const long long k_at = id * p.kp_sb + h * p.kp_sh + row * p.kp_sr + c * 16, v_at = id * p.vp_sb + h * p.vp_sh + row * p.vp_sr + c * 16;
+      ok = ok && in_bounds(k_at + 16 <= p.kp_span && v_at + 16 <= p.vp_span, p.err);
+      x[0][i] = ok ? ldg_stream_v4(p.k_pages + k_at) : make_uint4(0, 0, 0, 0);
+      x[1][i] = ok ? ldg_stream_v4(p.v_pages + v_at) : make_uint4(0, 0, 0, 0);
       if constexpr (KV8) {
-        const uint32_t w[4] = {x[v][i].x, x[v][i].y, x[v][i].z, x[v][i].w};
-        uint32_t o[8];
+        const long long sc = id * p.sc_sb + h * p.sc_sh + row;
+        ok = ok && in_bounds(sc + p.sc_st < p.sc_span, p.err);
+        f[0][i] = ok ? __ldg(p.scales + sc) : 0.f;
+        f[1][i] = ok ? __ldg(p.scales + sc + p.sc_st) : 0.f;
+      }
+    }
+    const long long to = (((long long)b * p.heads + h) * p.rows + j * 128 + row0) * 128 + c * (KV8 ? 16 : 8);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t lo2, hi2;
-          e4m3x4_to_f16x4(w[k], lo2, hi2);
-          o[2 * k] = pack_bf16x2(f16lo_to_f32(lo2) * f[v][i], f16hi_to_f32(lo2) * f[v][i]);
-          o[2 * k + 1] = pack_bf16x2(f16lo_to_f32(hi2) * f[v][i], f16hi_to_f32(hi2) * f[v][i]);
+    for (int i = 0; i < kPasses; ++i) {
+      if (!seen[i] || !in_bounds(j * 128 + 128 <= p.rows && to + (i * kAt + 1) * 128 <= p.span + 128, p.err)) continue;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        __nv_bfloat16* at = (v ? p.v_out : p.k_out) + to + (long long)i * kAt * 128;
+        if constexpr (KV8) {
+          const uint32_t w[4] = {x[v][i].x, x[v][i].y, x[v][i].z, x[v][i].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t lo2, hi2;
+            e4m3x4_to_f16x4(w[k], lo2, hi2);
+            o[2 * k] = pack_bf16x2(f16lo_to_f32(lo2) * f[v][i], f16hi_to_f32(lo2) * f[v][i]);
+            o[2 * k + 1] = pack_bf16x2(f16lo_to_f32(hi2) * f[v][i], f16hi_to_f32(hi2) * f[v][i]);
+          }
+          *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(at + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+        } else {
+          *reinterpret_cast<uint4*>(at) = x[v][i];
         }
-        *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(at + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-      } else {
-        *reinterpret_cast<uint4*>(at) = x[v][i];
       }
     }
   }
@@ -80,7 +99,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
 
 cudaError_t launch_gather(const GatherParams& p, int batch, bool kv8, bool pdl, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.rows / 128), (unsigned)batch, (unsigned)p.heads);
+  cfg.gridDim = dim3((unsigned)std::min(p.rows / 128, p.few_lq ? kGatherCtas / 2 : kGatherCtas), (unsigned)batch, (unsigned)p.heads);
   cfg.blockDim = dim3(kGatherThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;

@@ -273,6 +273,7 @@ struct PrefillParams {
   int num_blocks, block_shift, box_shift;
   // ... or rows of bf16 that launch_gather has laid out, tm_k and tm_v as of [B * Hkv * gather_rows][1][128] packed tokens
   int gather_rows;
+  int few_lq;  // sequences of so many queries and fewer are another kernel's: their rows are left as they are
 };
 // grid = as many CTAs as there can be work items; those that run take over the others.
 cudaError_t launch_prefill(const PrefillParams& p, int grid, bool pdl, cudaStream_t stream);
@@ -293,7 +294,11 @@ struct GatherParams {
   long long span;                    // elements of each
   int* err;
   int heads, rows, Tq, cap, num_blocks, block_shift, window, sinks;
+  int few_lq;                        // sequences of so many new tokens and fewer are another kernel's: left out
 };
+// CTAs of a (sequence, head) at most, each with every so many-th of its tiles: a table's capacity may be far past the lengths (and in
+// a mixed batch most sequences have none: 32 for those)
+constexpr int kGatherCtas = 64;
 cudaError_t launch_gather(const GatherParams& p, int batch, bool kv8, bool pdl, cudaStream_t stream);
 
 // ---------------------------------- attention of a few new tokens over a paged cache
@@ -312,6 +317,7 @@ struct FewParams {
   int slots;                         // 2 * CTAs
   int B, Hkv, G, Tq, cap;
   int npos;                          // query positions of an item, floor(rows / G)
+  int most_lq;                       // sequences with more rows are another kernel's: theirs are left as they are
   int num_blocks, block_shift, window, sinks;
   float scale_log2;
   int least;                         // units that a CTA takes at least

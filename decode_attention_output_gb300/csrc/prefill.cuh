@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
           q1 = min(max(__ldg(p.cu_q + b + 1), q0), p.Tq);
           if constexpr (kCached) {
             k1 = min(max(__ldg(p.cu_k + b), 0), p.Tk);  // (the sequences' lengths, and the table's capacity)
+            if (SRC == kGathered && q1 - q0 <= p.few_lq) q1 = q0;
           } else {
             k0 = min(max(__ldg(p.cu_k + b), 0), p.Tk);
             k1 = min(max(__ldg(p.cu_k + b + 1), k0), p.Tk);
@@ -867,6 +868,7 @@ __global__ void __launch_bounds__(128) prefill_join_kernel(const __grid_constant
   const int first = min(max(__ldg(p.cu_k + b), 0), p.Tk);
   const int k0 = SRC == kPackedKeys ? first : 0, k1 = SRC == kPackedKeys ? min(max(__ldg(p.cu_k + b + 1), k0), p.Tk) : first;
   if (t < q0 || t >= q1) return;  // a row of no sequence
+  if (SRC == kGathered && q1 - q0 <= p.few_lq) return;
   const int lq = q1 - q0, lk = k1 - k0, p0 = (t - q0) / (2 * p.npos) * 2 * p.npos;
   int end0 = kv_tiles(p0, p.npos, lq, lk), end1 = kv_tiles(p0 + p.npos, p.npos, lq, lk);
   if (WINDOW) {

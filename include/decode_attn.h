@@ -316,6 +316,7 @@ int decode_attn_prefill_window(const da_tensor_t* q, const da_tensor_t* k, const
  * K and V as they lie, and items that several CTAs share meet in the workspace; many rows 256 at a time, over
  * bf16 blocks of 64 tokens and more as they lie, and else over a bf16 copy of the tokens that the call sees in
  * the workspace: up to 4 GiB of the tables' capacity at a time (or one head of one sequence, if that has more), the rest after it.
+ * Of a large batch over such a copy each sequence goes the way of its own rows.
  */
 int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages, const da_tensor_t* kv_scales,
                       const da_tensor_t* block_table, const da_tensor_t* cu_seqlens, const da_tensor_t* seq_lens,
