@@ -5,7 +5,6 @@ import torch
 
 import decode_attention_output_gb300 as da
 from chunk_helpers import attend_ref
-from prompt_helpers import assert_within
 from test_cache import DEV, _library, bits, cu, i32  # noqa: F401
 from test_chunk import SCALE, Cache, canvas, check
 
@@ -48,6 +47,37 @@ def test_mixture_a_few_heads_at_a_time():
     out = canvas(q)
     da.decode_attn_chunk(q.to(DEV), kp, vp, sc, wide.to(DEV), i32(c), i32(lk), out, SCALE)
     check(out, *attend_ref(q, *cache.tokens, c, SCALE), "heads")
+
+
+@pytest.mark.parametrize("kv8,bs", KINDS, ids=str)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (15000, 300)], ids=str)
+def test_long_tokens_laid_out(window, sinks, kv8, bs):
+    """More tiles of a sequence than CTAs that lay them out, by itself and in a mixture; the shorter one's rows end inside a tile."""
+    g = torch.Generator().manual_seed(104)
+    for Hq, lq, lk in ((8, [70, 61], [20011, 9001]), (160, [30] + [1], [9001, 300])):
+        Hkv = Hq // 2 if Hq > 8 else 1
+        cache = Cache(g, lk, Hkv, bs, kv8)
+        c = cu(lq, first=1)
+        q = torch.randn((c[-1] + 2, Hq, 128), generator=g).to(torch.bfloat16)
+        kp, vp, sc = cache.on()
+        out = canvas(q)
+        da.decode_attn_chunk(q.to(DEV), kp, vp, sc, cache.table.to(torch.int32).to(DEV), i32(c), i32(lk), out, SCALE, window, sinks)
+        check(out, *attend_ref(q, *cache.tokens, c, SCALE, window, sinks), f"{Hq} heads")
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_equal_items_on_whole_ctas(kv8):
+    """One sequence, or a few of the same length, over so many CTAs that none has parts of two items; and one unit more or fewer."""
+    g = torch.Generator().manual_seed(105)
+    for B, Hkv, n in ((1, 8, 2049), (1, 8, 2048), (1, 8, 2047), (1, 3, 5000), (2, 5, 777), (4, 8, 1600), (1, 1, 17), (19, 8, 300)):
+        lk = [n] * B
+        cache = Cache(g, lk, Hkv, 64, kv8)
+        c = cu([1] * B)
+        q = torch.randn((B, 4 * Hkv, 128), generator=g).to(torch.bfloat16)
+        kp, vp, sc = cache.on()
+        out = canvas(q)
+        da.decode_attn_chunk(q.to(DEV), kp, vp, sc, cache.table.to(torch.int32).to(DEV), i32(c), i32(lk), out, SCALE)
+        check(out, *attend_ref(q, *cache.tokens, c, SCALE), f"{B} {Hkv} {n}")
 
 
 def test_mixture_captured_with_other_lengths():
