@@ -73,7 +73,7 @@ struct Item {  // in shared memory, as ints
   int clear;                    // the V tile whose end is another sequence's (-1: none)
   int part;                     // of the item (-1: the item is whole)
   // With a window, j0, end0 and end1 count the tiles that some row of the item sees: tile j is the one of
-  // keys 128 j .. of the sequence while j < ns, and the one of 128 (j + skip) .. from there on. lo: the
+  // keys 128 j .. of the sequence while j < ns, and the one of 128 j + skip .. from there on. lo: the
   // least key in the first row's window. merged: so many rows of the first tile, which lie before lo, hold the sequence's first keys.
   int ns, skip, lo, merged;
 };
@@ -125,25 +125,33 @@ __device__ __forceinline__ int item_parts(int top, int parts) {
 }
 __device__ __forceinline__ int part_begin(int part, int top, int n) { return (int)((long long)part * top / n); }
 
-// The tiles that a window and the first `sinks` keys leave of an item whose first position is p0 (see Item). MERGE: where the
-// window begins far enough inside its first tile, the first keys (eight at a time, as a copy's swizzle has it) take the rows before it
-// instead of a tile of their own.
+// Keys that npos query positions from `first` on see without a window.
+__device__ __forceinline__ int kv_keys(int first, int npos, int lq, int lk) {
+  return first < lq ? max(0, min(first + npos, lq) + lk - lq) : 0;
+}
+
+// The tiles that a window and the first `sinks` keys leave of an item whose first position is p0 (see Item). ANY: they may begin at
+// any key, the window's first or, where the first keys fit a tile, those (eight at a time, as a copy's swizzle has it) in rows
+// before it; else at multiples of a tile.
 struct Seen {
   int ns, skip, lo, merged;
-  __device__ __forceinline__ int count(int end) const { return end <= ns ? end : max(ns, end - skip); }  // of the tiles below `end`
+  // of the tiles that hold keys before `keys`
+  __device__ __forceinline__ int count(int keys) const {
+    return keys <= ns * kN ? (keys + kN - 1) / kN : max(ns, (keys - skip + kN - 1) / kN);
+  }
 };
-template <bool MERGE>
+template <bool ANY>
 __device__ __forceinline__ Seen seen_tiles(int p0, int lq, int lk, int window, int sinks) {
   Seen w;
   w.lo = max(0, p0 + lk - lq - window + 1);
-  const int first = w.lo / kN, ns = (sinks + kN - 1) / kN, rows = (sinks + 7) & ~7;
-  w.ns = first > ns ? ns : 0;
-  w.skip = first > ns ? first - ns : 0;
-  w.merged = 0;
-  if (MERGE && sinks > 0 && first > 0 && rows <= w.lo % kN) {
-    w.ns = 0;
-    w.skip = first;
+  const int rows = (sinks + 7) & ~7, ns = (sinks + kN - 1) / kN, from = ANY ? w.lo : w.lo / kN * kN;
+  w.ns = w.skip = w.merged = 0;
+  if (ANY && sinks > 0 && rows <= kN && w.lo > rows) {
+    w.skip = w.lo - rows;
     w.merged = rows;
+  } else if (from > ns * kN) {
+    w.ns = ns;
+    w.skip = from - ns * kN;
   }
   return w;
 }
@@ -472,17 +480,17 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         total = base;
         return it;
       }
-      it.end0 = kv_tiles(it.p0, npos, it.lq, it.lk);
-      it.end1 = kv_tiles(it.p0 + npos, npos, it.lq, it.lk);
       if constexpr (WINDOW) {
         const Seen w = seen_tiles<kMerge>(it.p0, it.lq, it.lk, p.window, p.sinks);
         it.ns = w.ns;
         it.skip = w.skip;
         it.lo = w.lo;
         it.merged = w.merged;
-        it.end0 = w.count(it.end0);
-        it.end1 = w.count(it.end1);
+        it.end0 = w.count(kv_keys(it.p0, npos, it.lq, it.lk));
+        it.end1 = w.count(kv_keys(it.p0 + npos, npos, it.lq, it.lk));
       } else {
+        it.end0 = kv_tiles(it.p0, npos, it.lq, it.lk);
+        it.end1 = kv_tiles(it.p0 + npos, npos, it.lq, it.lk);
         it.clear = it.lk % kN != 0 && it.k0 + it.lk < p.Tk ? it.lk / kN : -1;
       }
       ids_at = -2;
@@ -518,19 +526,20 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
       if (lane < 4) tma_prefetch_4d(&p.tm_q, 0, it.kvh * G, it.q0 + it.p0 + (lane >> 1) * npos, lane & 1);
       const int top = max(it.end0, it.end1);
       if (top <= it.j0) ask();
-      const Seen laid = seen_tiles<false>(0, it.lq, it.lk, p.window, p.sinks);  // kGathered: the tiles that lie there
+      const Seen laid = seen_tiles<false>(0, it.lq, it.lk, p.window, p.sinks);  // kGathered: the keys that lie there
       for (int j = it.j0; j < top && !given_up(flags); ++j) {
         if (j == max(it.j0, top - 3)) ask();  // late, so that no item waits behind a long one
-        const int t = WINDOW && j >= it.ns ? j + it.skip : j;
+        const int key = j * kN + (WINDOW && j >= it.ns ? it.skip : 0);
         if constexpr (SRC == kPages16) {
-          load_pages(&p.tm_k, it, t);
-          load_pages(&p.tm_v, it, t);
+          load_pages(&p.tm_k, it, key / kN);
+          load_pages(&p.tm_v, it, key / kN);
         } else {
           const int row0 = SRC == kGathered ? (it.k0 * p.Hkv + it.kvh) * p.gather_rows : it.k0, head = SRC == kGathered ? 0 : it.kvh;
-          const int row = row0 + (SRC == kGathered ? laid.count(t) : t) * kN;
-          if (kMerge && it.merged > 0 && j == 0) {
-            load_merged(&p.tm_k8, row0, it.merged, row, head);
-            load_merged(&p.tm_v8, row0, it.merged, row, head);
+          const int merged = kMerge && j == 0 ? it.merged : 0;
+          const int row = row0 + key - (SRC == kGathered && key + merged >= laid.ns * kN + laid.skip ? laid.skip : 0);
+          if (merged > 0) {
+            load_merged(&p.tm_k8, row0, merged, row, head);
+            load_merged(&p.tm_v8, row0, merged, row, head);
           } else {
             load_kv(&p.tm_k, row, head);
             load_kv(&p.tm_v, row, head);
@@ -593,7 +602,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         // NaN or infinity there is not, so those rows are cleared before the MMAs see them. With a window
         // also those before it (their blocks may be another sequence's by now).
         if constexpr (WINDOW) {
-          const int base = (j < ns ? j : j + skip) * kN;
+          const int base = j * kN + (j < ns ? 0 : skip);
           const int a = merged > 0 && j == 0 ? p.sinks : min(max(p.sinks - base, 0), kN), c = min(max(lo - base, 0), kN), e = min(max(lk - base, 0), kN);
           if (pv && (c > a || e < kN)) {
             uint4* tile = reinterpret_cast<uint4*>(smem + kOffRing + stage * kTileP);
@@ -767,7 +776,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) prefill_kernel(const __grid_cons
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kSFree));
-        const int base = (WINDOW && j >= it.ns ? j + it.skip : j) * kN;
+        const int base = j * kN + (WINDOW && j >= it.ns ? it.skip : 0);
         // some row of the warp ends inside this tile, or its window begins behind a key of it that is none of the first
         if (base + kN > lim0 || (WINDOW && base < low1 && base + kN > p.sinks)) {
           const float none = neg ? -kNegInfP : kNegInfP;
@@ -878,11 +887,14 @@ __global__ void __launch_bounds__(128) prefill_join_kernel(const __grid_constant
   if (t < q0 || t >= q1) return;  // a row of no sequence
   if (SRC == kGathered && q1 - q0 <= p.few_lq) return;
   const int lq = q1 - q0, lk = k1 - k0, p0 = (t - q0) / (2 * p.npos) * 2 * p.npos;
-  int end0 = kv_tiles(p0, p.npos, lq, lk), end1 = kv_tiles(p0 + p.npos, p.npos, lq, lk);
+  int end0, end1;
   if (WINDOW) {
     const Seen w = seen_tiles<merges(SRC, WINDOW)>(p0, lq, lk, p.window, p.sinks);
-    end0 = w.count(end0);
-    end1 = w.count(end1);
+    end0 = w.count(kv_keys(p0, p.npos, lq, lk));
+    end1 = w.count(kv_keys(p0 + p.npos, p.npos, lq, lk));
+  } else {
+    end0 = kv_tiles(p0, p.npos, lq, lk);
+    end1 = kv_tiles(p0 + p.npos, p.npos, lq, lk);
   }
   const int top = max(end0, end1), n = item_parts(top, p.parts), end = t - q0 - p0 < p.npos ? end0 : end1;
   if (n == 1) return;  // whole: it has been written
