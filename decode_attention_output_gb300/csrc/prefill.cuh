@@ -36,15 +36,16 @@
 //    the order of their use; it also finds the items (a scan of the offsets) and passes them on.
 //    A stage takes K and V tiles in turn and has a "full" barrier for each: a wait for the parity of
 //    one that both shared could pass on the tile before the one that it waits for.
-//  * With a window an item takes the tiles that some row of it sees; the first keys, where they are few,
-//    lie in its first tile in place of keys before every row's window, for which there would else be a
-//    tile more (a window of 1024, 4 first keys: 457 -> 441 us).
+//  * With a window an item takes tiles from its first row's first key on, not from a multiple of 128 (16
+//    ragged prompts, window 777: 175 -> 166 us; pages are taken by whole boxes, from a multiple); the first
+//    keys, where they are few, lie in its first tile before that key, for which there would else be a tile
+//    more (a window of 1024, 4 first keys: 457 -> 441 us).
 // Measured: 8192 tokens, 64 / 8 heads 667 us (1.65 PFLOP/s; a short run, before the power limit
 // lowers the clock, 581 us); four chunks of 512 over 7.7k 180 us (1.48); 16 ragged prompts of up
 // to 2048 112 us (1.09): a step costs 1.2 us, an item 2.8 us more (its output, the diagonal's
 // masks, the hand-over), of which 16 ragged prompts have 11 on each SM. In a window: 16384 tokens, 64 / 8 heads, window 1024,
-// 4 first keys 455 us (414 before the power limit lowers the clock), 16 ragged prompts of up to 2048, 32 / 8 heads,
-// window 777 176: ten and eight steps an item, and the softmax warps, which also store the last item's
+// 4 first keys 447 us under the power limit, 16 ragged prompts of up to 2048, 32 / 8 heads,
+// window 777 166: nine and seven steps an item, and the softmax warps, which also store the last item's
 // output, are busy for nine tenths of them.
 #pragma once
 #include "kernels.h"
