@@ -1152,7 +1152,7 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
 // heads, 32 rows 53 and 68, 40 rows 71 and 69.
 constexpr int kRowsDirect = 16, kRowsGathered = 48;
 // From and up to how many a call that lays tokens out may be a batch of prompts' chunks and single tokens, of which each kernel takes
-// its own. 512 new tokens of one sequence and one each of 31 others over 8k, 32 / 8 heads, e4m3: 508 us by the kernel of many rows alone, 233
+// its own. 512 new tokens of one sequence and one each of 31 others over 8k, 32 / 8 heads, e4m3: 508 us by the kernel of many rows alone, 221
 // by both (of 63 others: 712 by that of few rows alone, 385). Sequences all alike pay for the other's launches (100 tokens each of
 // 32: 336 -> 341; 8 each: 248 -> 276). Where all items find an SM at once the long chunk's time hides the others'
 // (512 and 3 others: 130 alone, 144 by both).
@@ -1199,7 +1199,9 @@ int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, 
   p.q_span = span_of(q);
   p.out_span = span_of(out);
   p.table_span = (B - 1) * p.bt_stride + MB;
-  const int grid = std::max(1, sm_count());
+  // Two CTAs of four warps an SM where items are many (one token each of 64 sequences over 1k, e4m3: 55 -> 43 us, of 32 in a window
+  // of 4096 62 -> 57; of one over 128k 54 -> 58, over 2k 10.4 -> 11.3). Over bf16 the bytes bound it (drafts of 32 over 8k 167 -> 168).
+  const int sms = std::max(1, sm_count()), warps = kv8 && B * kp->shape[1] > sms ? 4 : 8, grid = sms * (8 / warps);
   p.slots = 2 * grid;
   p.least = kv8 ? 8 : 16;  // 256 keys
   const size_t ml_bytes = align_up((size_t)p.slots * kFewRows * 2 * 4, 256);
@@ -1210,7 +1212,7 @@ int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, 
   p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
   p.counters = reinterpret_cast<int*>(ws + kAttnCntOff);
   p.err = reinterpret_cast<int*>(ws + kErrOff);
-  return launch_chunk_few(p, grid, kv8, rows, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return launch_chunk_few(p, grid, kv8, rows, warps, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 // decode_attn_chunk after its checks where a sequence has many rows: over the blocks as they are, or (gathered) over their tokens laid

@@ -3,14 +3,15 @@
 //
 // An item is 8 or 16 rows of one (sequence, KV head): npos = floor(rows / G) query positions x the G heads that share the KV
 // head.
-// Its keys go by in units of 16 (e4m3: 32), those of the first `sinks` and from the window's beginning on. The
-// units of all items, laid end to end, are cut into equal parts, one for each CTA (one per SM, fewer where little is
-// left to each), whatever the sequences' lengths: an item that lies in several CTAs leaves a state in the
-// workspace from each, and the last of them to end joins them in order.
+// Its keys go by in units of 16 (e4m3: 32), those of the first `sinks` and from the window's beginning on. The units of all
+// items, laid end to end, are cut into equal parts, one for each CTA (one an SM, or two half as large where items of e4m3 codes
+// are many: one's products then hide the other's beginnings and ends; fewer where little is left to each), whatever the
+// sequences' lengths: an item that lies in several CTAs leaves a state in the workspace from each, and the last of them
+// to end joins them in order.
 //
 //  * Bound by the bytes of K and V. The 128-row tiles of prefill.cuh would be idle but for 16 rows and take 1.3 us
 //    a tile of 128 keys, the time of one softmax, whatever its bytes; here a warp works on a unit of its own
-//    (mma.sync) and the eight of a CTA meet at the item's end only. S^T = K Q^T and O^T = V^T P^T: keys and dims are the
+//    (mma.sync) and those of a CTA meet at the item's end only. S^T = K Q^T and O^T = V^T P^T: keys and dims are the
 //    instruction's 16 rows, queries its 8 columns, so that eight of them cost half of sixteen.
 //  * A warp copies its units of K and V by TMA (4 KB each, a copy each where a block holds a unit), two units ahead and on
 //    into the next item's: 16 KB a warp, 128 KB an SM on their way. Which of a row's dims meet which lane and step of the
@@ -23,8 +24,8 @@
 //    largest under 2^15 (exact down to 2^-32 of it). V's scale joins the weight, w v f as f16: f, a power of two a row, keeps the
 //    largest w v (of rows of V that are not all zero: those have a scale of 1 whatever the others have) between 1 and 2^8,
 //    so that smaller ones are off by 2^-25 of it at most.
-// Measured (32 / 8 heads): four drafted tokens of each of 32 sequences over 8k, bf16 166 us (6.5 TB/s), e4m3 135; one token each of 64
-// sequences over 16k, 64 / 8 heads, 615 us (7.0 TB/s) and 339; of 256 sequences of 100 tokens 39 and 34; of one over 2k 10 and 11.
+// Measured (32 / 8 heads): four drafted tokens of each of 32 sequences over 8k, bf16 166 us (6.5 TB/s), e4m3 122; one token each of 64
+// sequences over 16k, 64 / 8 heads, 605 us (7.1 TB/s) and 331; of 256 sequences of 100 tokens 39 and 34; of one over 2k 10 and 11.
 #include "kernels.h"
 #include "packed.cuh"
 #include "ptx.cuh"
@@ -32,26 +33,28 @@
 namespace da {
 namespace {
 
-constexpr int kWarpsF = 8, kThreadsF = kWarpsF * 32;
 constexpr int kRowF = 132;       // floats of a row of the merge buffer (128 and padding)
 constexpr int kMostParts = 48;   // of an item
 constexpr int kAlignedMore = 16;  // units
 constexpr float kSlackF = 8.f;   // log2 units the maximum may lag
 constexpr float kNegInfF = -__builtin_huge_valf();
 
-// Shared memory: two units of each warp (K, V, scales of 32 keys), their barriers, the warps' states, the sequences' units
-// (prefix sums)
 constexpr int kStagesF = 2;
 constexpr uint32_t kHalfUnit = 4096;                // K or V of a unit
 constexpr uint32_t kScalesF = 256, kUnitBytes = 2 * kHalfUnit;
-constexpr size_t kOffScales = (size_t)kWarpsF * kStagesF * kUnitBytes;
-constexpr size_t kOffBarsF = kOffScales + (size_t)kWarpsF * kStagesF * kScalesF;
-constexpr size_t kOffMl = kOffBarsF + kWarpsF * kStagesF * 8;
-constexpr size_t kOffState = (kOffMl + kWarpsF * 16 * 2 * 4 + 15) & ~(size_t)15;
-constexpr size_t kOffLast = kOffState + (size_t)kWarpsF * 16 * kRowF * 4;
-constexpr size_t kOffPrefix = kOffLast + 16;
-constexpr size_t kSmemF = 1024 + kOffPrefix + (kMaxBatch + 1) * 8;
-static_assert(kSmemF <= kMaxDynSmem, "the kernel exceeds 227 KB of shared memory");
+// Shared memory of a CTA of WARPS: two units of each warp (K, V, scales of 32 keys), their barriers, the warps' states, the
+// sequences' units (prefix sums)
+template <int WARPS>
+struct FewSmem {
+  static constexpr size_t kScales = (size_t)WARPS * kStagesF * kUnitBytes;
+  static constexpr size_t kBars = kScales + (size_t)WARPS * kStagesF * kScalesF;
+  static constexpr size_t kMl = kBars + WARPS * kStagesF * 8;
+  static constexpr size_t kState = (kMl + WARPS * 16 * 2 * 4 + 15) & ~(size_t)15;
+  static constexpr size_t kLast = kState + (size_t)WARPS * 16 * kRowF * 4;
+  static constexpr size_t kPrefix = kLast + 16;
+  static constexpr size_t kAll = 1024 + kPrefix + (kMaxBatch + 1) * 8;
+};
+static_assert(FewSmem<8>::kAll <= kMaxDynSmem && 2 * (FewSmem<4>::kAll + 1024) <= kMaxDynSmem + 1024, "the kernel exceeds an SM's shared memory");
 
 // Units that a sequence's queries see: those of the first keys, and from the window's beginning on.
 struct Units {
@@ -144,21 +147,21 @@ __device__ __noinline__ Segment segment_called(const FewParams& p, const long lo
 }
 
 // The items, or parts of them, of worker `me` of `workers`. ALONE: a worker is a warp and takes items as a whole; else it is a
-// CTA, whose warps take every eighth unit of an item.
+// CTA, whose warps take an item's units in turn.
 // NB: blocks of eight rows of an item
-template <bool KV8, int NB, bool ALONE>
+template <bool KV8, int NB, int WARPS, bool ALONE>
 __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, const uint8_t* smem_raw, int workers, int me) {
   constexpr int kKeys = KV8 ? kFewKeys8 : kFewKeys16, kKT = kKeys / 16;  // keys of a unit, in tiles of 16
-  constexpr int kRows = 8 * NB, kDims = kRows / 2;  // rows of an item; dims of a thread where states are joined (256 threads)
-  const long long* prefix = reinterpret_cast<const long long*>(smem + kOffPrefix);
-  float* state = reinterpret_cast<float*>(smem + kOffState);
-  float* ml = reinterpret_cast<float*>(smem + kOffMl);
-  int* last = reinterpret_cast<int*>(smem + kOffLast);
+  constexpr int kRows = 8 * NB, kDims = kRows * 4 / WARPS;  // rows of an item; dims of a thread where states are joined
+  const long long* prefix = reinterpret_cast<const long long*>(smem + FewSmem<WARPS>::kPrefix);
+  float* state = reinterpret_cast<float*>(smem + FewSmem<WARPS>::kState);
+  float* ml = reinterpret_cast<float*>(smem + FewSmem<WARPS>::kMl);
+  int* last = reinterpret_cast<int*>(smem + FewSmem<WARPS>::kLast);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int G = p.G;
   const long long total = prefix[p.B];
   const int first = ALONE ? 0 : warp;             // this warp's units of a segment
-  constexpr int step = ALONE ? 1 : kWarpsF;
+  constexpr int step = ALONE ? 1 : WARPS;
   const long long each = total / workers;
   const int rest = (int)(total - each * workers);
   auto begin_of = [&](int c) { return each * c + (int)((unsigned)rest * (unsigned)c / (unsigned)workers); };  // total * c / workers
@@ -170,8 +173,8 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
     else return segment_called<kKeys>(p, prefix, f, f1);
   };
   const uint32_t units = smem_u32(smem) + warp * kStagesF * kUnitBytes;
-  const uint32_t scales = smem_u32(smem + kOffScales) + warp * kStagesF * kScalesF;
-  const uint32_t bars = smem_u32(smem + kOffBarsF) + warp * kStagesF * 8;
+  const uint32_t scales = smem_u32(smem + FewSmem<WARPS>::kScales) + warp * kStagesF * kScalesF;
+  const uint32_t bars = smem_u32(smem + FewSmem<WARPS>::kBars) + warp * kStagesF * 8;
   auto sm_ok = [&](uint32_t addr, uint32_t bytes) { return smem_in_bounds(smem_u32(smem_raw), addr, bytes, p.err); };
 
   // The loads, which run ahead of the products and on into the next segments: the segment, this warp's next unit of it, and the
@@ -597,9 +600,9 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
         }
     };
 #pragma unroll
-    for (int w = 0; w < kWarpsF; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
+    for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
 #pragma unroll
-    for (int w = 0; w < kWarpsF; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const float2 s = *reinterpret_cast<const float2*>(ml + (w * kRows + r) * 2);
       add(reinterpret_cast<const float4*>(state + (w * kRows + r) * kRowF + d0), s.x, s.y);
     }
@@ -657,16 +660,16 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
     mbar_wait_bounded(bars + (used & 1) * 8, used >> 1 & 1, p.err, kErrWaitDrain, nullptr, kWaitLimitNs / 10);
 }
 
-template <bool KV8, int NB>
-__global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_constant__ FewParams p) {
+template <bool KV8, int NB, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) chunk_few_kernel(const __grid_constant__ FewParams p) {
   constexpr int kKeys = KV8 ? kFewKeys8 : kFewKeys16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  long long* prefix = reinterpret_cast<long long*>(smem + kOffPrefix);
-  int* last = reinterpret_cast<int*>(smem + kOffLast);
+  long long* prefix = reinterpret_cast<long long*>(smem + FewSmem<WARPS>::kPrefix);
+  int* last = reinterpret_cast<int*>(smem + FewSmem<WARPS>::kLast);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, npos = p.npos;
   if (lane == 0) {
-    for (int i = 0; i < kStagesF; ++i) mbar_init(smem_u32(smem + kOffBarsF) + (warp * kStagesF + i) * 8, 1);
+    for (int i = 0; i < kStagesF; ++i) mbar_init(smem_u32(smem + FewSmem<WARPS>::kBars) + (warp * kStagesF + i) * 8, 1);
     fence_barrier_init();
     if (warp == 0) {
       prefetch_tensormap(&p.tm_k);
@@ -678,7 +681,7 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
 
   if (tid == 0) last[0] = last[1] = 0;
   __syncthreads();
-  for (int b = tid; b < p.B; b += kThreadsF) {
+  for (int b = tid; b < p.B; b += WARPS * 32) {
     const Seq s = sequence(p, b);
     const int n = units_of<kKeys>(s.lo, s.lk, p.sinks).n;
     prefix[b + 1] = (long long)((s.lq + npos - 1) / npos) * p.Hkv * n;
@@ -715,13 +718,13 @@ __global__ void __launch_bounds__(kThreadsF, 1) chunk_few_kernel(const __grid_co
   // Many short items: a warp each, from its first unit to its last, and nothing to join. In units a warp, that takes the
   // longer of its share and an item, and one more in part; items shared by a CTA's warps cost the time of two units
   // each on top. (256 sequences of 100 tokens, 8 KV heads: 86 us by CTAs.)
-  const long long share = total / (workers * kWarpsF);
+  const long long share = total / (workers * WARPS);
   const bool alone = max(share, (long long)longest) + longest / 2 < share + 2ll * (last[1] / workers + 1);
-  if (alone) run_items<KV8, NB, true>(p, smem, smem_raw, gridDim.x * kWarpsF, warp * gridDim.x + blockIdx.x);
-  else if ((int)blockIdx.x < workers) run_items<KV8, NB, false>(p, smem, smem_raw, workers, blockIdx.x);
+  if (alone) run_items<KV8, NB, WARPS, true>(p, smem, smem_raw, gridDim.x * WARPS, warp * gridDim.x + blockIdx.x);
+  else if ((int)blockIdx.x < workers) run_items<KV8, NB, WARPS, false>(p, smem, smem_raw, workers, blockIdx.x);
 }
 
-template <bool KV8, int NB>
+template <bool KV8, int NB, int WARPS>
 cudaError_t launch_few(const FewParams& p, int grid, bool pdl, cudaStream_t stream) {
   static int configured[64] = {0};  // the shared-memory opt-in, once per device
   int dev = 0;
@@ -729,28 +732,29 @@ cudaError_t launch_few(const FewParams& p, int grid, bool pdl, cudaStream_t stre
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(chunk_few_kernel<KV8, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemF);
+    e = cudaFuncSetAttribute(chunk_few_kernel<KV8, NB, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FewSmem<WARPS>::kAll);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreadsF);
-  cfg.dynamicSmemBytes = kSmemF;
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = FewSmem<WARPS>::kAll;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, chunk_few_kernel<KV8, NB>, p);
+  return cudaLaunchKernelEx(&cfg, chunk_few_kernel<KV8, NB, WARPS>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, int rows, bool pdl, cudaStream_t stream) {
-  if (rows == 8) return kv8 ? launch_few<true, 1>(p, grid, pdl, stream) : launch_few<false, 1>(p, grid, pdl, stream);
-  return kv8 ? launch_few<true, 2>(p, grid, pdl, stream) : launch_few<false, 2>(p, grid, pdl, stream);
+cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, int rows, int warps, bool pdl, cudaStream_t stream) {
+  if (!kv8) return rows == 8 ? launch_few<false, 1, 8>(p, grid, pdl, stream) : launch_few<false, 2, 8>(p, grid, pdl, stream);
+  if (warps == 4) return rows == 8 ? launch_few<true, 1, 4>(p, grid, pdl, stream) : launch_few<true, 2, 4>(p, grid, pdl, stream);
+  return rows == 8 ? launch_few<true, 1, 8>(p, grid, pdl, stream) : launch_few<true, 2, 8>(p, grid, pdl, stream);
 }
 
 }  // namespace da

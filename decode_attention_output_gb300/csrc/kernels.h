@@ -325,8 +325,8 @@ struct FewParams {
   long long q_span, out_span, table_span;
 };
 constexpr int kFewRows = 16, kFewKeys16 = 16, kFewKeys8 = 32;
-// rows: of an item, 8 or 16
-cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, int rows, bool pdl, cudaStream_t stream);
+// rows: of an item, 8 or 16; warps: of a CTA, 8, or (e4m3) 4 with two CTAs an SM
+cudaError_t launch_chunk_few(const FewParams& p, int grid, bool kv8, int rows, int warps, bool pdl, cudaStream_t stream);
 
 // ------------------------------------------------ paged cache: writing and reading
 struct CacheParams {
