@@ -387,7 +387,8 @@ int decode_attn_cache_read(const da_tensor_t* k_pages, const da_tensor_t* v_page
  *
  * Per row: y = x / sqrt(mean(x^2) + eps) * weight where there is one; then (a, b) becomes
  * (a c - b s, b c + a s) for each pair; dims from R on keep y. All in fp32 (the mean's sum too),
- * rounded once to bf16. A position outside [0, P), or an axis outside [0, A), counts as an angle of
+ * rounded once to bf16 (with a weight, a row whose squares' sum leaves fp32's range gives zeros, infinities or NaN).
+ * A position outside [0, P), or an axis outside [0, A), counts as an angle of
  * 0 and sets bit 128 of the device error word.
  */
 int decode_attn_rope(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* cos_sin, const da_tensor_t* positions,
