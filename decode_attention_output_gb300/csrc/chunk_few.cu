@@ -23,7 +23,7 @@
 //    for the 32 sequences). K's scale multiplies the score; q's rows become f16 over a power of two that puts the
 //    largest under 2^15 (exact down to 2^-32 of it). V's scale joins the weight, w v f as f16: f, a power of two a row, keeps the
 //    largest w v (of rows of V that are not all zero: those have a scale of 1 whatever the others have) between 1 and 2^8,
-//    so that smaller ones are off by 2^-25 of it at most.
+//    so that smaller ones are off by 2^-25 of it at most. The products are taken as (w v) f: v f can be infinite where w is 0.
 // Measured (32 / 8 heads): four drafted tokens of each of 32 sequences over 8k, bf16 166 us (6.5 TB/s), e4m3 122; one token each of 64
 // sequences over 16k, 64 / 8 heads, 605 us (7.1 TB/s) and 331; of 256 sequences of 100 tokens 39 and 34; of one over 2k 10 and 11.
 #include "kernels.h"
@@ -37,6 +37,7 @@ constexpr int kRowF = 132;       // floats of a row of the merge buffer (128 and
 constexpr int kMostParts = 48;   // of an item
 constexpr int kAlignedMore = 16;  // units
 constexpr float kSlackF = 8.f;   // log2 units the maximum may lag
+constexpr float kVScaleUnit = 0x1p-8f;  // V's scales are held times this: a weight (up to 2^8) times one stays finite
 constexpr float kNegInfF = -__builtin_huge_valf();
 
 constexpr int kStagesF = 2;
@@ -152,6 +153,7 @@ __device__ __noinline__ Segment segment_called(const FewParams& p, const long lo
 template <bool KV8, int NB, int WARPS, bool ALONE>
 __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, const uint8_t* smem_raw, int workers, int me) {
   constexpr int kKeys = KV8 ? kFewKeys8 : kFewKeys16, kKT = kKeys / 16;  // keys of a unit, in tiles of 16
+  constexpr float kUnitBack = KV8 ? 1.f / kVScaleUnit : 1.f;  // of an item's O
   constexpr int kRows = 8 * NB, kDims = kRows * 4 / WARPS;  // rows of an item; dims of a thread where states are joined
   const long long* prefix = reinterpret_cast<const long long*>(smem + FewSmem<WARPS>::kPrefix);
   float* state = reinterpret_cast<float*>(smem + FewSmem<WARPS>::kState);
@@ -320,7 +322,7 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
         }
       }
     float o[NB][8][4], m[NB][2], l[NB][2];
-    float fv[NB][2], largest[NB][2];  // e4m3: V's factor, and the largest weight times V scale so far
+    float fv[NB][2], largest[NB][2];  // e4m3: V's factor, and the largest weight times V scale (times kVScaleUnit) so far
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -329,7 +331,7 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
       for (int e = 0; e < 2; ++e) {
         m[nb][e] = kNegInfF;
         l[nb][e] = 0.f;
-        fv[nb][e] = 1.f;
+        fv[nb][e] = 1.f / kVScaleUnit;
         largest[nb][e] = 0.f;
       }
     }
@@ -429,13 +431,20 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
         for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            vs[kt][i] = lds_f32(sc + scale_at(2 * kt + i) + scale_v);
+            vs[kt][i] = lds_f32(sc + scale_at(2 * kt + i) + scale_v) * kVScaleUnit;
             if (!whole && !seen(key0 + kt * 16 + 8 * i + g)) vs[kt][i] = 0.f;  // (0 times a scale that belongs to no key is not 0)
           }
+        // The weight first: of a key that a row does not see it is 0, and the scale times the row's factor may be infinite.
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[kt][nb][i] *= vs[kt][i >> 1];
         auto big = [&](int nb, int e) {  // the largest weight times V scale of this lane's
           float r = 0.f;
 #pragma unroll
-          for (int kt = 0; kt < kKT; ++kt) r = fmaxf(r, fmaxf(fabsf(x[kt][nb][e] * vs[kt][0]), fabsf(x[kt][nb][2 + e] * vs[kt][1])));
+          for (int kt = 0; kt < kKT; ++kt) r = fmaxf(r, fmaxf(fabsf(x[kt][nb][e]), fabsf(x[kt][nb][2 + e])));
           return r;
         };
 #pragma unroll
@@ -459,8 +468,10 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
 #pragma unroll
           for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (!(some >> (2 * (2 * kt + i)) & 1u)) vs[kt][i] = 0.f;
+            for (int i = 0; i < 4; ++i)
+              if (!(some >> (2 * (2 * kt + (i >> 1))) & 1u))
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) x[kt][nb][i] = 0.f;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -477,7 +488,7 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
 #pragma unroll
           for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[kt][nb][i] *= vs[kt][i >> 1] * fv[nb][i & 1];
+            for (int i = 0; i < 4; ++i) x[kt][nb][i] *= fv[nb][i & 1];
       }
       // V: key 2 t + k of the nt-th eight, piece g. What no row sees may hold anything: zeros.
       auto load_v = [&](int nt, int k, uint32_t off) {
@@ -556,7 +567,7 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = nb * 8 + 2 * t + e;
-          const float inv = l[nb][e] == 0.f ? 0.f : 1.f / l[nb][e], back = KV8 ? 1.f / fv[nb][e] : 1.f;
+          const float inv = l[nb][e] == 0.f ? 0.f : kUnitBack / l[nb][e], back = KV8 ? 1.f / fv[nb][e] : 1.f;
           __nv_bfloat16* to = p.out + (long long)(sg.q0 + sg.pos0 + r / G) * p.o_st + (long long)(sg.kvh * G + r % G) * p.o_sh;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -645,7 +656,7 @@ __device__ __forceinline__ void run_items(const FewParams& p, uint8_t* smem, con
       }
     }
     if (write && r < sg.most * G) {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float inv = sum == 0.f ? 0.f : kUnitBack / sum;
       __nv_bfloat16* to = p.out + (long long)(sg.q0 + sg.pos0 + r / G) * p.o_st + (long long)(sg.kvh * G + r % G) * p.o_sh + d0;
       if (in_bounds(to >= p.out && to + kDims <= p.out + p.out_span, p.err))
 #pragma unroll
