@@ -68,8 +68,8 @@ constexpr int kMaxDevices = 64;
 struct Workspace {
   char* base = nullptr;
   size_t bytes = 0;
-  // smaller ones before it: captured graphs may hold their addresses (each at least twice the
-  // one before, from 32 MiB on: 16 would be 2 TiB)
+  // smaller ones before it: captured graphs may hold their addresses (each of another power of two, from
+  // 32 MiB on, but where memory is short: 16 would be 2 TiB)
   char* outgrown[16] = {};
   int n_outgrown = 0;
 };
@@ -80,9 +80,11 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // Returns the workspace of the current device with at least `scratch` bytes after
 // the header, growing it if needed. Growth is stream-ordered on `stream` (no device-wide
 // synchronisation): the new block comes from cudaMallocAsync and its header is zeroed by
-// cudaMemsetAsync on `stream`. It is twice the old one at least, which is kept until
+// cudaMemsetAsync on `stream`. Its size is the power of two that holds `scratch`, or where the
+// device has no room for that, what is needed; the old one is kept until
 // decode_attn_release: a captured graph, or a call under way on another thread, may use it
-// still. While `stream` is captured nothing is allocated: the block would be the graph's.
+// still. (So all blocks together are less than twice the largest; twice the old one each time, a call a little past
+// 3.9 GiB left 11.7 held.) While `stream` is captured nothing is allocated: the block would be the graph's.
 int workspace_get(size_t scratch, cudaStream_t stream, char** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DA_ERR_CUDA;
@@ -96,11 +98,16 @@ int workspace_get(size_t scratch, cudaStream_t stream, char** out) {
       return DA_ERR_NOMEM;
     }
     if (ws.n_outgrown == 16) return DA_ERR_NOMEM;
-    const size_t bytes = std::max(std::max(need, 2 * ws.bytes), (size_t)32 << 20);
+    size_t bytes = (size_t)32 << 20;
+    while (bytes < need) bytes *= 2;
     void* p = nullptr;
     if (cudaMallocAsync(&p, bytes, stream) != cudaSuccess) {
       cudaGetLastError();
-      return DA_ERR_NOMEM;
+      bytes = need;
+      if (cudaMallocAsync(&p, bytes, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return DA_ERR_NOMEM;
+      }
     }
     if (cudaMemsetAsync(p, 0, kHeaderBytes, stream) != cudaSuccess) {
       cudaFreeAsync(p, stream);
@@ -1217,8 +1224,9 @@ int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, 
 
 // decode_attn_chunk after its checks where a sequence has many rows: over the blocks as they are, or (gathered) over their tokens laid
 // out in the workspace, kGatherBytes at a time at most (of a table's whole capacity, as the lengths are on the device): all
-// heads of some sequences, or some heads of one.
-constexpr int64_t kGatherBytes = (int64_t)4 << 30;
+// heads of some sequences, or some heads of one. With the header and the parts of cut items (those of one for each SM, 20 MB) a block
+// of 4 GiB holds them.
+constexpr int64_t kGatherBytes = ((int64_t)4 << 30) - ((int64_t)64 << 20);
 int run_chunk(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
               const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, bool gathered,
               void* stream) {

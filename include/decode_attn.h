@@ -36,10 +36,12 @@
  *  - The library owns one workspace per device (partial results of the split
  *    KV pass and of the split-K projection, completion counters, the bf16
  *    attention intermediate). When a call needs more, it is grown in stream
- *    order on that call's stream (cudaMallocAsync of a new block, twice the old one
- *    at least, cudaMemsetAsync of its header; no device-wide synchronisation). The
- *    old block is kept until decode_attn_release, so a graph captured before can be
- *    replayed. A call that would have to grow it while its stream is being captured
+ *    order on that call's stream (cudaMallocAsync of a new block of the power of two
+ *    that holds it, from 32 MiB on, or of what is needed where there is no room for that;
+ *    cudaMemsetAsync of its header; no device-wide synchronisation). The
+ *    old blocks are kept until decode_attn_release, so a graph captured before can be
+ *    replayed; together they are smaller than the new one (but where room was short).
+ *    A call that would have to grow it while its stream is being captured
  *    returns DA_ERR_NOMEM: the first call with the largest shapes must precede the
  *    capture. Calls on different streams of the same device share it, graph replays
  *    among them: the caller must order them (their work must not overlap on the GPU).
@@ -315,7 +317,8 @@ int decode_attn_prefill_window(const da_tensor_t* q, const da_tensor_t* k, const
  * By Tq * G / B (rows of a sequence and KV head on average) and the pool: few rows are taken 8 or 16 at a time over
  * K and V as they lie, and items that several CTAs share meet in the workspace; many rows 256 at a time, over
  * bf16 blocks of 64 tokens and more as they lie, and else over a bf16 copy of the tokens that the call sees in
- * the workspace: up to 4 GiB of the tables' capacity at a time (or one head of one sequence, if that has more), the rest after it.
+ * the workspace: so much of the tables' capacity at a time as a block of 4 GiB holds (or one head of one sequence, if that has more), the
+ * rest after it.
  * Of a large batch over such a copy each sequence goes the way of its own rows.
  */
 int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages, const da_tensor_t* kv_scales,
