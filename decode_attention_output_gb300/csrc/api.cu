@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdint>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -40,6 +41,7 @@ struct Options {
   int64_t attn_trigger = 3;     // decode_attn_fwd: each attention CTA lets the projection launch
                                 // this many tiles before its end (0: at set-up); 3 against 0:
                                 // batch 1 15.9 -> 14.9 us, 131k context 306.2 -> 303.5 us
+  int64_t workspace_mib = 0;    // most MiB of a workspace block (0: what a call needs)
   int64_t grid_wait_us = 0;     // test hook: the fused step's grid-barrier wait limit (0: 2 s)
   int64_t grid_wait_extra = 0;  // test hook: arrivals that barrier waits for beyond the grid
 };
@@ -72,10 +74,23 @@ struct Workspace {
   // 32 MiB on, but where memory is short: 16 would be 2 TiB)
   char* outgrown[16] = {};
   int n_outgrown = 0;
+  size_t refused = 0;  // the least size that the device did not have (0: none)
 };
 Workspace g_ws[kMaxDevices];
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// The largest block that the current device's workspace has or may be asked for.
+size_t workspace_most() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  std::lock_guard<std::mutex> lk(g_mu);
+  const Workspace& ws = g_ws[dev];
+  size_t most = g_opt.workspace_mib ? (size_t)g_opt.workspace_mib << 20 : SIZE_MAX;
+  if (ws.refused) most = std::min(most, ws.refused - 1);
+  return std::max(most, ws.bytes);
+}
+size_t block_bytes(size_t scratch) { return kHeaderBytes + align_up(scratch, 256); }
 
 // Returns the workspace of the current device with at least `scratch` bytes after
 // the header, growing it if needed. Growth is stream-ordered on `stream` (no device-wide
@@ -90,22 +105,25 @@ int workspace_get(size_t scratch, cudaStream_t stream, char** out) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DA_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
   Workspace& ws = g_ws[dev];
-  const size_t need = kHeaderBytes + align_up(scratch, 256);
+  const size_t need = block_bytes(scratch);
   if (need > ws.bytes) {
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) {
       cudaGetLastError();
       return DA_ERR_NOMEM;
     }
-    if (ws.n_outgrown == 16) return DA_ERR_NOMEM;
+    const size_t limit = g_opt.workspace_mib ? (size_t)g_opt.workspace_mib << 20 : SIZE_MAX;
+    if (ws.n_outgrown == 16 || need > limit) return DA_ERR_NOMEM;
     size_t bytes = (size_t)32 << 20;
     while (bytes < need) bytes *= 2;
+    bytes = std::min(bytes, limit);
     void* p = nullptr;
     if (cudaMallocAsync(&p, bytes, stream) != cudaSuccess) {
       cudaGetLastError();
       bytes = need;
       if (cudaMallocAsync(&p, bytes, stream) != cudaSuccess) {
         cudaGetLastError();
+        ws.refused = ws.refused ? std::min(ws.refused, need) : need;
         return DA_ERR_NOMEM;
       }
     }
@@ -116,6 +134,7 @@ int workspace_get(size_t scratch, cudaStream_t stream, char** out) {
     if (ws.base) ws.outgrown[ws.n_outgrown++] = ws.base;
     ws.base = static_cast<char*>(p);
     ws.bytes = bytes;
+    if (bytes >= ws.refused) ws.refused = 0;
   }
   *out = ws.base;
   return DA_OK;
@@ -1088,31 +1107,49 @@ int check_window(float scale, int window, int sinks) {
 
 enum PrefillOver { kPrompt, kPromptWindow, kChunkPages, kChunkGathered };
 
-// The attention of packed queries after its checks: p holds the keys (cu_q, cu_k, Tk, maps, pages); `longest`: keys of
-// a sequence at most, as far as the host knows. gather: over tokens that it lays out first, in the workspace (kv8: of codes).
-int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const da_tensor_t* out, int64_t B, int64_t Hkv,
-                int64_t longest, float scale, int window, int sinks, void* stream, GatherParams* gather = nullptr, bool kv8 = false) {
-  const int64_t Tq = q->shape[0], Hq = q->shape[1];
-  p.G = (int)(Hq / Hkv);
-  p.npos = 128 / p.G;
+// The work items of packed queries, and the scratch for those whose keys are cut into parts. `longest`: keys of a sequence at
+// most, as far as the host knows.
+struct PromptPlan {
+  int64_t items;
+  int npos, parts;
+  size_t rows, ml_bytes, bytes;  // of the parts: rows, their maxima and sums, all of it
+};
+PromptPlan plan_prompt(int64_t Tq, int64_t Hq, int64_t Hkv, int64_t B, int64_t longest, int window, int sinks) {
+  PromptPlan pl;
+  pl.npos = 128 / (int)(Hq / Hkv);
   // items: 2 * npos positions of one sequence and KV head, at most one ragged per sequence
-  const int64_t items = ((Tq + 2 * p.npos - 1) / (2 * p.npos) + B - 1) * Hkv;
-  if (items >= ((int64_t)1 << 31) - 4096) return DA_ERR_UNSUPPORTED;
-  DA_TRY(encode_packed_map(&p.tm_q, q, p.npos, p.G));
-  p.window = window ? std::min(window, 1 << 30) : 1 << 30;
-  p.sinks = window ? std::min(sinks, 1 << 30) : 0;
+  pl.items = ((Tq + 2 * pl.npos - 1) / (2 * pl.npos) + B - 1) * Hkv;
   // Fewer items than half the SMs, and sequences long enough to gain: as many parts as there are SMs for; the kernel cuts
   // an item into fewer where it has few K/V tiles.
   int64_t tiles = (longest + 127) / 128;
-  if (window) tiles = std::min<int64_t>(tiles, ((int64_t)p.window + 2 * p.npos + 127) / 128 + 1 + ((int64_t)p.sinks + 127) / 128);
+  if (window)
+    tiles = std::min<int64_t>(tiles, ((int64_t)std::min(window, 1 << 30) + 2 * pl.npos + 127) / 128 + 1 + ((int64_t)std::min(sinks, 1 << 30) + 127) / 128);
   const int64_t sms = std::max(1, sm_count());
-  p.parts = tiles < kPrefillCutTiles
-                ? 1
-                : (int)std::max<int64_t>(1, std::min<int64_t>({sms / items, tiles / kPrefillPartTiles, (int64_t)kMaxPrefillParts}));
-  const size_t rows = p.parts > 1 ? (size_t)p.parts * Tq * Hq : 0, ml_bytes = align_up(rows * 2 * 4, 256);
+  pl.parts = tiles < kPrefillCutTiles
+                 ? 1
+                 : (int)std::max<int64_t>(1, std::min<int64_t>({sms / pl.items, tiles / kPrefillPartTiles, (int64_t)kMaxPrefillParts}));
+  pl.rows = pl.parts > 1 ? (size_t)pl.parts * Tq * Hq : 0;
+  pl.ml_bytes = align_up(pl.rows * 2 * 4, 256);
+  pl.bytes = align_up(pl.ml_bytes + pl.rows * 128 * 4, 256);
+  return pl;
+}
+
+// The attention of packed queries after its checks: p holds the keys (cu_q, cu_k, Tk, maps, pages). gather: over tokens that it
+// lays out first, in the workspace (kv8: of codes).
+int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const da_tensor_t* out, int64_t B, int64_t Hkv,
+                int64_t longest, float scale, int window, int sinks, void* stream, GatherParams* gather = nullptr, bool kv8 = false) {
+  const int64_t Tq = q->shape[0], Hq = q->shape[1];
+  const PromptPlan pl = plan_prompt(Tq, Hq, Hkv, B, longest, window, sinks);
+  if (pl.items >= ((int64_t)1 << 31) - 4096) return DA_ERR_UNSUPPORTED;
+  p.G = (int)(Hq / Hkv);
+  p.npos = pl.npos;
+  DA_TRY(encode_packed_map(&p.tm_q, q, p.npos, p.G));
+  p.window = window ? std::min(window, 1 << 30) : 1 << 30;
+  p.sinks = window ? std::min(sinks, 1 << 30) : 0;
+  p.parts = pl.parts;
+  const size_t ml_bytes = pl.ml_bytes, part_bytes = pl.bytes, laid = gather ? (size_t)B * Hkv * gather->rows * 128 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = nullptr;
-  const size_t part_bytes = align_up(ml_bytes + rows * 128 * 4, 256), laid = gather ? (size_t)B * Hkv * gather->rows * 128 : 0;
   DA_TRY(workspace_get(part_bytes + 2 * laid * 2, st, &ws));
   p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
   p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
@@ -1136,7 +1173,7 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
   p.o_st = out->stride[0];
   p.o_sh = out->stride[1];
   p.out_span = span_of(out);
-  p.part_rows = (long long)rows;
+  p.part_rows = (long long)pl.rows;
   p.B = (int)B;
   p.Hkv = (int)Hkv;
   p.Tq = (int)Tq;
@@ -1144,7 +1181,7 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
   // weight within 2^-21 of 1 whatever the products are
   p.scale_log2 = scale * 1.4426950408889634f;
   if (p.scale_log2 == 0.f) p.scale_log2 = 0x1p-149f;
-  const int grid = (int)items * p.parts;
+  const int grid = (int)pl.items * p.parts;
   const bool pdl = options_snapshot().attn_pdl != 0;
   if (gather && launch_gather(*gather, (int)B, kv8, pdl, st) != cudaSuccess) return DA_ERR_CUDA;
   const cudaError_t e = over == kPrompt         ? launch_prefill(p, grid, pdl, st)
@@ -1167,6 +1204,10 @@ constexpr int kRowsMixedFrom = 24, kRowsMixed = 4096;
 bool mixed_rows(int64_t Tq, int64_t group, int64_t B, int64_t Hkv) {
   return B * Hkv > sm_count() && Hkv <= 256 && Tq * group > kRowsMixedFrom * B && Tq * group <= kRowsMixed * B;
 }
+// Scratch of the states that the kernel of few rows leaves, two of each CTA (two CTAs an SM at most).
+size_t few_ml_bytes(int slots) { return align_up((size_t)slots * kFewRows * 2 * 4, 256); }
+size_t few_bytes(int slots) { return few_ml_bytes(slots) + (size_t)slots * kFewRows * 128 * 4; }
+
 // decode_attn_chunk after its checks where a sequence has few rows on average: 8 or 16 at a time. few_lq > 0: of the sequences
 // that have so many queries and fewer (mostly one each, so 8 rows where they hold a token's).
 int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
@@ -1211,21 +1252,20 @@ int run_few(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, 
   const int sms = std::max(1, sm_count()), warps = kv8 && B * kp->shape[1] > sms ? 4 : 8, grid = sms * (8 / warps);
   p.slots = 2 * grid;
   p.least = kv8 ? 8 : 16;  // 256 keys
-  const size_t ml_bytes = align_up((size_t)p.slots * kFewRows * 2 * 4, 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = nullptr;
-  DA_TRY(workspace_get(ml_bytes + (size_t)p.slots * kFewRows * 128 * 4, st, &ws));
+  DA_TRY(workspace_get(few_bytes(p.slots), st, &ws));
   p.part_ml = reinterpret_cast<float*>(ws + kHeaderBytes);
-  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + ml_bytes);
+  p.part_o = reinterpret_cast<float*>(ws + kHeaderBytes + few_ml_bytes(p.slots));
   p.counters = reinterpret_cast<int*>(ws + kAttnCntOff);
   p.err = reinterpret_cast<int*>(ws + kErrOff);
   return launch_chunk_few(p, grid, kv8, rows, warps, options_snapshot().attn_pdl != 0, st) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 // decode_attn_chunk after its checks where a sequence has many rows: over the blocks as they are, or (gathered) over their tokens laid
-// out in the workspace, kGatherBytes at a time at most (of a table's whole capacity, as the lengths are on the device): all
-// heads of some sequences, or some heads of one. With the header and the parts of cut items (those of one for each SM, 20 MB) a block
-// of 4 GiB holds them.
+// out in the workspace, kGatherBytes at a time at most (of a table's whole capacity, as the lengths are on the device), or what the
+// workspace may have: all heads of some sequences, or some heads of one. With the header and the parts of cut items (those of one
+// for each SM, 20 MB) a block of 4 GiB holds them.
 constexpr int64_t kGatherBytes = ((int64_t)4 << 30) - ((int64_t)64 << 20);
 int run_chunk(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp, const da_tensor_t* scales, const da_tensor_t* table,
               const da_tensor_t* cu, const da_tensor_t* lens, const da_tensor_t* out, float scale, int window, int sinks, bool gathered,
@@ -1253,11 +1293,27 @@ int run_chunk(const da_tensor_t* q, const da_tensor_t* kp, const da_tensor_t* vp
   int64_t tiles = (cap + 127) / 128;
   if (window) tiles = std::min(tiles, ((int64_t)window + Tq + 127) / 128 + 1 + ((int64_t)sinks + 127) / 128);
   const int64_t each = tiles * 128 * 2 * 128 * 2, group = Hkv > 0 ? q->shape[1] / Hkv : 1;
-  const int64_t nb = std::max<int64_t>(1, std::min(B, kGatherBytes / (Hkv * each)));
-  const int64_t nh = std::max<int64_t>(1, std::min<int64_t>({Hkv, kGatherBytes / each, 65535}));
   const int64_t es = kv8 ? 1 : 2;
   // Mixed: sequences of few rows by their own kernel, behind the others'. (Where the average is low they may be drafts of many tokens.)
   const bool mixed = mixed_rows(Tq, group, B, Hkv);
+  // How much at a time; the workspace for all of it before the first launch. Where there is no room, half as much, and so on.
+  int64_t nb = 1, nh = 1;
+  for (int64_t limit = kGatherBytes;; limit /= 2) {
+    nb = std::max<int64_t>(1, std::min(B, limit / (Hkv * each)));
+    nh = std::max<int64_t>(1, std::min<int64_t>({Hkv, limit / each, 65535}));
+    size_t need = mixed ? few_bytes(4 * std::max(1, sm_count())) : 0;
+    for (int64_t bn : {nb, B % nb})
+      for (int64_t hn : {nh, Hkv % nh})
+        if (bn > 0 && hn > 0)
+          need = std::max(need, plan_prompt(Tq, hn * group, hn, bn, cap, window, sinks).bytes + (size_t)(bn * hn * each));
+    const bool least = nb == 1 && nh == 1;
+    if (!least && block_bytes(need) > workspace_most()) continue;
+    char* ws = nullptr;
+    const int rc = workspace_get(need, static_cast<cudaStream_t>(stream), &ws);
+    if (rc == DA_ERR_NOMEM && !least && block_bytes(need) > workspace_most()) continue;  // (not for a capture's sake)
+    DA_TRY(rc);
+    break;
+  }
   const int few_lq = mixed ? (int)((Tq * group <= kRowsGathered * B ? kRowsGathered : kRowsDirect) / group) : 0;
   for (int64_t b0 = 0; b0 < B; b0 += nb)
     for (int64_t h0 = 0; h0 < Hkv; h0 += nh) {
@@ -1486,6 +1542,7 @@ int decode_attn_set_option(const char* key, int64_t value) {
   else if (!strcmp(key, "attn_cluster") && value >= 0 && value <= 2) g_opt.attn_cluster = value;
   else if (!strcmp(key, "attn_pdl") && (value == 0 || value == 1)) g_opt.attn_pdl = value;
   else if (!strcmp(key, "attn_trigger") && value >= 0 && value <= (1 << 20)) g_opt.attn_trigger = value;
+  else if (!strcmp(key, "workspace_mib") && value >= 0 && value <= (1 << 20)) g_opt.workspace_mib = value;
   else if (!strcmp(key, "grid_wait_us") && value >= 0 && value <= 2000000) g_opt.grid_wait_us = value;
   else if (!strcmp(key, "grid_wait_extra") && (value == 0 || value == 1)) g_opt.grid_wait_extra = value;
   else return DA_ERR_OPTION;
@@ -1509,6 +1566,7 @@ int decode_attn_get_option(const char* key, int64_t* value) {
   else if (!strcmp(key, "attn_cluster")) *value = g_opt.attn_cluster;
   else if (!strcmp(key, "attn_pdl")) *value = g_opt.attn_pdl;
   else if (!strcmp(key, "attn_trigger")) *value = g_opt.attn_trigger;
+  else if (!strcmp(key, "workspace_mib")) *value = g_opt.workspace_mib;
   else if (!strcmp(key, "grid_wait_us")) *value = g_opt.grid_wait_us;
   else if (!strcmp(key, "grid_wait_extra")) *value = g_opt.grid_wait_extra;
   else return DA_ERR_OPTION;

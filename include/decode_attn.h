@@ -318,7 +318,8 @@ int decode_attn_prefill_window(const da_tensor_t* q, const da_tensor_t* k, const
  * K and V as they lie, and items that several CTAs share meet in the workspace; many rows 256 at a time, over
  * bf16 blocks of 64 tokens and more as they lie, and else over a bf16 copy of the tokens that the call sees in
  * the workspace: so much of the tables' capacity at a time as a block of 4 GiB holds (or one head of one sequence, if that has more), the
- * rest after it.
+ * rest after it. Where the device or the option "workspace_mib" has no such block, half as much at a time, and so on; a size that the device
+ * did not have is not asked for again until decode_attn_release or a larger block. DA_ERR_NOMEM where one head of one sequence does not fit.
  * Of a large batch over such a copy each sequence goes the way of its own rows.
  */
 int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages, const da_tensor_t* kv_scales,
@@ -503,6 +504,9 @@ int decode_attn_oproj(const da_tensor_t* attn_flat, const da_tensor_t* o_weight,
  *                   pulls the part of its o_weight slice that its ring does not hold
  *                   into L2 before it waits for the attention kernel (measured no
  *                   faster on GB300)
+ *   "workspace_mib" 0 (default): a block of the workspace is as large as calls need; else at most
+ *                   so many MiB (up to 1048576). A call that needs more returns DA_ERR_NOMEM, but
+ *                   decode_attn_chunk takes its tokens in smaller shares. Blocks that are there stay.
  *   "grid_wait_us"  test hook: the fused step's grid-barrier wait limit in microseconds
  *                   (0, the default: two seconds; at most 2000000)
  *   "grid_wait_extra" test hook, 0 (default) or 1: the fused step's grid barrier waits
