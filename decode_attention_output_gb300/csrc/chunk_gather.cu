@@ -71,10 +71,11 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
     const long long to = (((long long)b * p.heads + h) * p.rows + j * 128 + row0) * 128 + c * (KV8 ? 16 : 8);
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      if (!seen[i] || !in_bounds(j * 128 + 128 <= p.rows && to + (i * kAt + 1) * 128 <= p.span + 128, p.err)) continue;
+      const long long first = to + (long long)i * kAt * 128;  // of this store
+      if (!seen[i] || !in_bounds(j * 128 + 128 <= p.rows && first >= 0 && first + (KV8 ? 16 : 8) <= p.span, p.err)) continue;
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        __nv_bfloat16* at = (v ? p.v_out : p.k_out) + to + (long long)i * kAt * 128;
+        __nv_bfloat16* at = (v ? p.v_out : p.k_out) + first;
         if constexpr (KV8) {
           const uint32_t w[4] = {x[v][i].x, x[v][i].y, x[v][i].z, x[v][i].w};
           uint32_t o[8];
