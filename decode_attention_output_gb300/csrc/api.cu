@@ -140,6 +140,22 @@ int workspace_get(size_t scratch, cudaStream_t stream, char** out) {
   return DA_OK;
 }
 
+// Held while a call that keeps anything in the workspace enqueues its launches: two threads may call on one stream, and
+// what one launch leaves there for the next must not have another call's launch between (of 200 calls of each of two
+// threads 30 to 46 gave wrong results). The current device's, as the workspace is.
+class Enqueue {
+ public:
+  Enqueue() {
+    static std::mutex mu[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;  // (workspace_get fails then)
+    lk_ = std::unique_lock<std::mutex>(mu[dev]);
+  }
+
+ private:
+  std::unique_lock<std::mutex> lk_;
+};
+
 // --------------------------------------------------------------- device info
 int sm_count() {
   static int cache[kMaxDevices] = {0};
@@ -1044,6 +1060,7 @@ int only_checked(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_t* 
   const bool fp8 = kv8 || (paged && paged->scales);
   const AttnPlan pl = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_only(o), paged && paged->scales);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Enqueue in_one_go;
   char* ws = nullptr;
   DA_TRY(workspace_get(pl.bytes, st, &ws));
   return run_attention(q, k, v, seq_lens, s, pl, ws, ws + kHeaderBytes,
@@ -1069,6 +1086,7 @@ int fwd_checked(const da_tensor_t* q, const da_tensor_t* k_cache, const da_tenso
   const AttnPlan ap = plan_attention(s, o, fp8 ? kTileFp8 : 0, false, cluster_use_fwd(o), paged && paged->scales, true);
   const size_t attn_bytes = align_up((size_t)s.B * K * 2, 256);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Enqueue in_one_go;
   const AttnPlan fap = plan_attention(s, o, 0, true);
   const FusedPlan fp = (paged || kv8) ? FusedPlan() : plan_fused(s, (int)K, (int)N, fap, o);
   if (fp.ok) {  // one launch: attention, grid barrier, projection
@@ -1400,6 +1418,7 @@ int prefill_checked(const da_tensor_t* q, const da_tensor_t* k, const da_tensor_
   p.Tk = (int)Tk;
   // (a ragged sequence may be twice the average: of whole tiles, in keys)
   const int64_t longest = std::min<int64_t>(Tk, 256 * ((Tk / B + 127) / 128));
+  const Enqueue in_one_go;
   return run_prefill(p, window ? kPromptWindow : kPrompt, q, out, B, Hkv, longest, scale, window, sinks, stream);
 }
 
@@ -1659,6 +1678,7 @@ int decode_attn_scores(const da_tensor_t* q, const da_tensor_t* k_cache, const d
   const Options o = options_snapshot();
   const AttnPlan pl = plan_attention(s, o);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Enqueue in_one_go;
   char* ws = nullptr;
   DA_TRY(workspace_get(pl.bytes, st, &ws));
   return run_attention(q, k_cache, nullptr, seq_lens, s, pl, ws, ws + kHeaderBytes, nullptr, 0, 0,
@@ -1678,6 +1698,7 @@ int decode_attn_oproj(const da_tensor_t* attn_flat, const da_tensor_t* o_weight,
   const Options o = options_snapshot();
   const ProjPlan pl = plan_projection((int)B, (int)K, (int)N, o);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Enqueue in_one_go;
   char* ws = nullptr;
   DA_TRY(workspace_get(pl.bytes, st, &ws));
   return run_projection(static_cast<const __nv_bfloat16*>(attn_flat->data), B > 1 ? attn_flat->stride[0] : K,
@@ -1791,6 +1812,7 @@ int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da
     if (reinterpret_cast<uintptr_t>(table->data) % 4 || reinterpret_cast<uintptr_t>(lens->data) % 4) return DA_ERR_ALIGN;
   }
   if (B == 0 || Tq == 0) return DA_OK;
+  const Enqueue in_one_go;
   const bool gathered = kv8 || BS < 64;  // (below 64 tokens a block TMA takes four copies and more a tile)
   if (Tq * (Hq / Hkv) <= (gathered ? kRowsGathered : kRowsDirect) * B && Hkv <= 256 && !(gathered && mixed_rows(Tq, Hq / Hkv, B, Hkv)))
     return run_few(q, kp, vp, kv_scales, table, cu, lens, out, scale, window, sinks, stream);

@@ -45,6 +45,7 @@
  *    returns DA_ERR_NOMEM: the first call with the largest shapes must precede the
  *    capture. Calls on different streams of the same device share it, graph replays
  *    among them: the caller must order them (their work must not overlap on the GPU).
+ *    Host threads may call at the same time; each call's launches are enqueued in one go.
  *  - seq_lens lives on the device. Each length is clamped to [0, Lcap] on the
  *    device; a length of 0 gives an all-zero attention row.
  *  - Bounded device waits: every wait inside a kernel gives up after about
