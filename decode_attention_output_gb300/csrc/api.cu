@@ -1214,10 +1214,10 @@ int run_prefill(PrefillParams& p, PrefillOver over, const da_tensor_t* q, const 
 // heads, 32 rows 53 and 68, 40 rows 71 and 69.
 constexpr int kRowsDirect = 16, kRowsGathered = 48;
 // From and up to how many a call that lays tokens out may be a batch of prompts' chunks and single tokens, of which each kernel takes
-// its own. 512 new tokens of one sequence and one each of 31 others over 8k, 32 / 8 heads, e4m3: 508 us by the kernel of many rows alone, 221
-// by both (of 63 others: 712 by that of few rows alone, 385). Sequences all alike pay for the other's launches (100 tokens each of
-// 32: 336 -> 341; 8 each: 248 -> 276). Where all items find an SM at once the long chunk's time hides the others'
-// (512 and 3 others: 130 alone, 144 by both).
+// its own. 512 new tokens of one sequence and one each of 31 others over 8k, 32 / 8 heads, e4m3: 508 us by the kernel of many rows alone, 222
+// by both (of 63 others: 712 by that of few rows alone, 351). Sequences all alike pay for the other's launches (100 tokens each of
+// 32: 336 -> 341; 8 each by 28 when this came in, 246 now). Where all items find an SM at once the long chunk's time hides the others'
+// (512 and 3 others: 130 alone, 144 by both; not measured by both: 512 and 7 others 168 alone, and 15 others 290).
 constexpr int kRowsMixedFrom = 24, kRowsMixed = 4096;
 bool mixed_rows(int64_t Tq, int64_t group, int64_t B, int64_t Hkv) {
   return B * Hkv > sm_count() && Hkv <= 256 && Tq * group > kRowsMixedFrom * B && Tq * group <= kRowsMixed * B;

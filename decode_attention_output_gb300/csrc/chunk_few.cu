@@ -24,8 +24,9 @@
 //    largest under 2^15 (exact down to 2^-32 of it). V's scale joins the weight, w v f as f16: f, a power of two a row, keeps the
 //    largest w v (of rows of V that are not all zero: those have a scale of 1 whatever the others have) between 1 and 2^8,
 //    so that smaller ones are off by 2^-25 of it at most. The products are taken as (w v) f: v f can be infinite where w is 0.
-// Measured (32 / 8 heads): four drafted tokens of each of 32 sequences over 8k, bf16 166 us (6.5 TB/s), e4m3 122; one token each of 64
-// sequences over 16k, 64 / 8 heads, 605 us (7.1 TB/s) and 331; of 256 sequences of 100 tokens 39 and 34; of one over 2k 10 and 11.
+// Measured (32 / 8 heads): four drafted tokens of each of 32 sequences over 8k, bf16 168 us (6.5 TB/s), e4m3 122, eight of each 170
+// and 246 (two items of 16 rows, each of which widens all codes); one token each of 64 sequences over 16k, 64 / 8 heads, 615 us
+// (7.0 TB/s) and 335; of 64 over 1k 56 and 43; of 256 sequences of 100 tokens 33 and 34; of one over 2k 10 and 11.
 #include "kernels.h"
 #include "packed.cuh"
 #include "ptx.cuh"
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) chunk_few_kernel(const 
   const int longest = last[0];
   // As many CTAs take part as leave each 256 keys, and the longest item in 48 parts at most: one CTA joins them
   int workers = (int)min((long long)gridDim.x, max(total / max(p.least, longest / kMostParts), 1ll));
-  // Items all alike (one sequence's) and few: so many CTAs that none has parts of two, of which each costs it 5 us, if that leaves
+  // Items all alike to the unit (one sequence's, or sequences of one length) and few: so many CTAs that none has parts of two, of which each costs it 5 us, if that leaves
   // none many units more (one token over 2k, e4m3, 65 units of each of 8 heads: 16.1 -> 10.7 us)
   const int items = last[1], whole = items > 0 ? workers / items * items : 0;
   if (whole > 0 && total == (long long)longest * items && total / whole - total / workers <= kAlignedMore) workers = whole;

@@ -44,8 +44,8 @@
 // lowers the clock, 581 us); four chunks of 512 over 7.7k 180 us (1.48); 16 ragged prompts of up
 // to 2048 112 us (1.09): a step costs 1.2 us, an item 2.8 us more (its output, the diagonal's
 // masks, the hand-over), of which 16 ragged prompts have 11 on each SM. In a window: 16384 tokens, 64 / 8 heads, window 1024,
-// 4 first keys 447 us under the power limit, 16 ragged prompts of up to 2048, 32 / 8 heads,
-// window 777 166: nine and seven steps an item, and the softmax warps, which also store the last item's
+// 4 first keys 446 to 454 us under the power limit, 16 ragged prompts of up to 2048, 32 / 8 heads,
+// window 777 167 to 169: nine and seven steps an item, and the softmax warps, which also store the last item's
 // output, are busy for nine tenths of them.
 #pragma once
 #include "kernels.h"

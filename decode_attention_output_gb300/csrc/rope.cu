@@ -12,12 +12,13 @@
 // kv_cache.cu does for values; the values are its rows unchanged. Queries go to packed rows.
 //
 // A row is read and written once, 4 D bytes (a key into an e4m3 cache 3 D + 4), which bounds rows without a norm; with one, and with
-// positions of several axes, instruction issue does (75% of the slots in a profile). A lane holds dims 4 l .. 4 l + 3 and
+// positions of several axes, instruction issue does (70% of the slots in a profile). A lane holds dims 4 l .. 4 l + 3 and
 // their partners, so that neither pairing needs a shuffle and a call may work in place; the norm's sum is four shuffles a row, four
 // rows side by side. A warp takes one token and eight rows of its heads (two where tokens are few), so that the token's place,
 // its position and its cosines and sines are found once, while the rows are already on their way.
-// Measured (32 / 8 heads): 8191 tokens without norms 27 us (6.3 TB/s), with them 32, and positions of three axes 35; 46.6k
-// tokens with norms into a bf16 cache 179 (6.1 TB/s), into an e4m3 one 218; one token of each of 64 sequences 3.8.
+// Measured (32 / 8 heads), over rows that are not in L2: 8191 tokens without norms 29 us (5.9 TB/s), with them 36, and positions of
+// three axes 38 (the same rows again and again: 27, 32, 35); 46.6k tokens with norms into a bf16 cache 181 (6.0 TB/s), into an e4m3
+// one 219; four chunks of 509 to 512 tokens into an e4m3 one 11.1 (again and again 10.4); one token of each of 64 sequences 3.8.
 #include "kernels.h"
 #include "packed.cuh"
 #include "ptx.cuh"

@@ -18,7 +18,7 @@
  * N = hidden). Head dim 256 is the page's other GQA decode (section "仓库源码
  * 佐证": QK^T contracts D = 256 in two halves of 128, attn.V has N = D = 256);
  * every entry point takes D = 128 or D = 256, read from q's last extent (those over an
- * fp8 cache and decode_attn_prefill: D = 128).
+ * fp8 cache, decode_attn_prefill, decode_attn_prefill_window and decode_attn_chunk: D = 128).
  *
  * Conventions shared by every entry point
  *  - Every tensor argument is a da_tensor_t descriptor. Its data pointer is a
@@ -313,7 +313,9 @@ int decode_attn_prefill_window(const da_tensor_t* q, const da_tensor_t* k, const
  * key or value that some query of a sequence sees can make any output row of that sequence and KV head non-finite.
  * block_size: a power of two from 8 (e4m3: 16) to 2^20. Other limits as decode_attn_prefill. The softmax weights enter
  * P.V unnormalised as bf16, or (e4m3, few rows) with V's scale as f16, off by 2^-25 of the row's largest product
- * of weight and scale at most.
+ * of weight and scale at most; weights below 2^-126 of the row's largest count as 0. A score has to stay in fp32's range, and so
+ * have its product with codes before their scale and a row's sum of values times weights (up to 2^8 each before the division; values
+ * up to 2^90 always do).
  *
  * By Tq * G / B (rows of a sequence and KV head on average) and the pool: few rows are taken 8 or 16 at a time over
  * K and V as they lie, and items that several CTAs share meet in the workspace; many rows 256 at a time, over
@@ -321,7 +323,10 @@ int decode_attn_prefill_window(const da_tensor_t* q, const da_tensor_t* k, const
  * the workspace: so much of the tables' capacity at a time as a block of 4 GiB holds (or one head of one sequence, if that has more), the
  * rest after it. Where the device or the option "workspace_mib" has no such block, half as much at a time, and so on; a size that the device
  * did not have is not asked for again until decode_attn_release or a larger block. DA_ERR_NOMEM where one head of one sequence does not fit.
- * Of a large batch over such a copy each sequence goes the way of its own rows.
+ * Of a batch over such a copy, of more than 24 rows on average and of more (sequence, KV head) pairs than SMs, each sequence goes
+ * the way of its own rows. Else the average decides for all: a long chunk among very many single tokens is then taken 16 rows at a
+ * time (1280 new tokens and 255 single ones over 8k, e4m3, 32 / 8 heads: 1977 us; in two calls 184 + 658), and single tokens among few
+ * long chunks 256 at a time. Where the host knows the lengths, such a batch is better called in two.
  */
 int decode_attn_chunk(const da_tensor_t* q, const da_tensor_t* k_pages, const da_tensor_t* v_pages, const da_tensor_t* kv_scales,
                       const da_tensor_t* block_table, const da_tensor_t* cu_seqlens, const da_tensor_t* seq_lens,
